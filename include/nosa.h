@@ -458,6 +458,94 @@ nosa_status nosa_attend_noalloc(const uint16_t* q, const uint16_t* cache, const 
                                 int cache_slots, int context_len, float softmax_scale, uint16_t* out,
                                 int32_t* err_out, void* stream);
 
+/* ------------------------------------------------------------ 4-bit KV block store
+ * A store of the blocks above in 4 bits: 3.2 times smaller than bf16, so that whole contexts
+ * can stay on the device.  The pages describe no such store: it stands beside the bf16 layouts for
+ * callers whose contexts do not fit or whose attention is bound by their bytes.  Context-free;
+ * nothing here allocates, and every call can be captured in a CUDA graph.  A store is caller-owned
+ * device memory, uint8 [units][max_blocks][NOSA_QUANT_BLOCK_BYTES], 16-byte aligned, for units
+ * (sequence, kv head) as everywhere in this header.
+ *
+ * The 128 values of a token's K (or V) row fall into four groups of 32 consecutive dims.  A group
+ * x_0 .. x_31 is held as
+ *     m = f16(min x),   s = f16((max x - min x) / 15),   n_i = clamp(rint((x_i - m) / s), 0, 15)
+ * (f16(), rint(): to nearest, ties to even; differences in float32; s = 0: n_i = 0) and stands for
+ *     x^_i = n_i s + m.
+ * A group where m or s is not finite in f16 (a NaN or an infinity in it, a minimum beyond f16's
+ * range, a range beyond 15 times f16's) has m = s = NaN (bits 0x7E00) and reads as NaN in all its dims.
+ *
+ * A block of 64 tokens is four tiles of 16 tokens, 2560 bytes each:
+ *   [0, 1024)     K codes: token i (of the tile) has 64 bytes at 64 i; dim d is in byte
+ *                 16 ((d % 32) / 8) + 4 (d / 32) + (d % 8) / 2 of them, even d in the low half
+ *   [1024, 2048)  V codes: dim d of token i is in byte
+ *                 512 (i / 8) + 64 ((d % 32) / 4) + 16 ((i % 8) / 2) + 4 (d / 32) + 2 (i % 2) + (d % 4) / 2
+ *   [2048, 2304)  K: f16 [16 tokens][s of groups 0..3, m of groups 0..3]
+ *   [2304, 2560)  V: f16 [s, m][8 token pairs][4 groups][2 tokens]
+ * (a lane of the attention kernels finds its tensor-core operands in 16 consecutive bytes). */
+#define NOSA_QUANT_BLOCK_BYTES 10240
+
+/* Quantises tokens as they are written to a store.
+ *   k, v     device bf16 [units][n_tokens][d], 16-byte aligned
+ *   pos      device int32 [units]: position of each unit's first token (NULL: 0 for all)
+ *   count    device int32 [units]: tokens of each unit to write, 0 .. n_tokens (NULL: n_tokens);
+ *            the tokens behind them (a padded batch) are not looked at
+ * Positions need no alignment; everything else in the store is left as it was.  err_out (optional
+ * device int32, 4-byte aligned) gets bit 0 set when a token's position lies outside
+ * [0, 64 max_blocks) (the token is not written) or a count outside [0, n_tokens] (clamped); it is
+ * not cleared.  Two calls that write the same unit at the same time race unless they write
+ * different tiles.  Asynchronous on `stream`. */
+nosa_status nosa_quant_append(const uint16_t* k, const uint16_t* v, uint8_t* store, int units, int n_tokens,
+                              int max_blocks, const int32_t* pos, const int32_t* count, int32_t* err_out,
+                              void* stream);
+
+/* Reads blocks of a store back to bf16 (x^ rounded to nearest even), in the layout of the block
+ * cache and of nosa_dense_attend.
+ *   blocks   device int32 [units][n_blocks]: the blocks to read, any order, repeats allowed;
+ *            negative: none (zeros).  NULL: blocks 0 .. n_blocks - 1 of every unit
+ *   lens     device int32 [units]: tokens of each unit; rows at or behind them are written as
+ *            zeros whatever the store holds there (NULL: every row is read)
+ *   kv       device bf16 [units][n_blocks][2][64][d], 16-byte aligned
+ * err_out as above: bit 0 when a listed block is max_blocks or more (written as zeros). */
+nosa_status nosa_quant_read(const uint8_t* store, int units, int max_blocks, const int32_t* blocks, int n_blocks,
+                            const int32_t* lens, uint16_t* kv, int32_t* err_out, void* stream);
+
+/* Attention over every token of a 4-bit store, for one query token or a few (drafted) ones.
+ *   q, out   device bf16 [units][group][n_queries][d], 16-byte aligned; 1 <= group <= 8 q heads per
+ *            kv head, 1 <= n_queries, group * n_queries <= 32
+ *   lens     device int32 [units]: tokens of each unit, the query tokens' own among them: query i
+ *            sees tokens 0 .. lens - n_queries + i.  A query that sees none gets zeros
+ *   max_len  upper bound of lens, at most 64 max_blocks and 1,048,576 (it sizes the launch)
+ *   softmax_scale  0 => 1/sqrt(128)
+ *   scratch  device memory of at least nosa_quant_scratch_bytes(units, group * n_queries,
+ *            ceil(max_len / 64)) bytes, 256-byte aligned; its first 4 bytes receive device-side
+ *            error bits (zero them before the call to read them after it): bit 0 a length outside
+ *            [0, max_len] (clamped), bit 1 a bounded wait for a staged tile gave up (outputs are
+ *            NaN).  Calls that may run at the same time (other streams, graphs) need a scratch each.
+ * The sums are float32.  q is exact (values below 2^-23 of their row's largest are rounded); the
+ * weights exp(logit - reference) and their products with s are rounded to f16, 2^-11 relative each.
+ * Asynchronous on `stream`.  NOSA_ERR_CAPACITY if the scratch is too small. */
+nosa_status nosa_quant_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group, int n_queries,
+                                    int max_blocks, const int32_t* lens, int max_len, float softmax_scale,
+                                    uint16_t* out, void* scratch, size_t scratch_bytes, void* stream);
+
+/* The same over listed blocks: what nosa_attend_noalloc is to a bf16 block cache.
+ *   sel      device int32 [units][max_sel] block ids in any order, negative: none (so the sel_out of
+ *            nosa_select can be passed as it is); block b holds tokens 64 b .. 64 b + 63, of which
+ *            those a query sees (as above) are attended.  A block listed twice counts twice
+ *   sel_slot device int32 [units][max_sel]: the row of the store, 0 .. max_blocks - 1, that holds each
+ *            listed block (a block cache).  NULL: row b of the unit holds block b
+ * 1 <= max_sel <= 16384.  Scratch as above with nosa_quant_scratch_bytes(units, group * n_queries,
+ * max_sel).  Bit 0 of the error word: a row outside [0, max_blocks) (the block is left out), or a
+ * length below 0 (taken as 0). */
+nosa_status nosa_quant_attend(const uint16_t* q, const uint8_t* store, const int32_t* sel, const int32_t* sel_slot,
+                              int units, int group, int n_queries, int max_blocks, int max_sel, const int32_t* lens,
+                              float softmax_scale, uint16_t* out, void* scratch, size_t scratch_bytes, void* stream);
+
+/* Scratch bytes of the two attention calls for `rows` = group * n_queries query rows per unit and at
+ * most `blocks` blocks per unit: never more than 256 + 520 rows (units + 16 SMs).  0 on a bad
+ * argument or without a device. */
+size_t nosa_quant_scratch_bytes(int units, int rows, int blocks);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,7 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnosa.so")
-SOURCES = ["api.cu", "append.cu", "select.cu", "fetch.cu", "attend.cu", "decode.cu", "dense.cu", "noalloc.cu", "prefill.cu"]
+SOURCES = ["api.cu", "append.cu", "select.cu", "fetch.cu", "attend.cu", "decode.cu", "dense.cu", "noalloc.cu", "prefill.cu",
+           "quant.cu", "quant_attend.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]

@@ -24,6 +24,7 @@ NOSA_F_UNFUSED_STEP = 4
 NOSA_F_DMA_BIAS = 8
 NOSA_F_TEST_RADIX_TOPK = 16
 NOSA_F_TEST_PREFILL_WIDE = 32
+NOSA_QUANT_BLOCK_BYTES = 10240
 NOSA_MERGE_AUTO, NOSA_MERGE_KERNEL, NOSA_MERGE_TICKET, NOSA_MERGE_CLUSTER = 0, 1, 2, 3
 
 # every entry point declared in include/nosa.h
@@ -33,7 +34,8 @@ EXPORTS = ["nosa_validate_config", "nosa_query_sizes", "nosa_create", "nosa_dest
            "nosa_reset_stats", "nosa_debug_scores", "nosa_export_state", "nosa_status_string",
            "nosa_attend_noalloc", "nosa_step_plan", "nosa_forecast_select", "nosa_step_forecast",
            "nosa_forecast_join", "nosa_dense_attend", "nosa_dense_scratch_bytes", "nosa_prefill",
-           "nosa_prefill_scratch_bytes"]
+           "nosa_prefill_scratch_bytes", "nosa_quant_append", "nosa_quant_read", "nosa_quant_dense_attend",
+           "nosa_quant_attend", "nosa_quant_scratch_bytes"]
 
 
 class nosa_config(ctypes.Structure):
@@ -117,6 +119,11 @@ def lib() -> ctypes.CDLL:
             "nosa_debug_scores": [vp, i32, p, p],
             "nosa_export_state": [vp, i32, ctypes.POINTER(nosa_state_view)],
             "nosa_attend_noalloc": [p, p, p, p, p, i32, i32, i32, i32, ctypes.c_float, p, p, vp],
+            "nosa_quant_append": [p, p, p, i32, i32, i32, p, p, p, vp],
+            "nosa_quant_read": [p, i32, i32, p, i32, p, p, p, vp],
+            "nosa_quant_dense_attend": [p, p, i32, i32, i32, i32, p, i32, ctypes.c_float, p, p, ctypes.c_size_t, vp],
+            "nosa_quant_attend": [p, p, p, p, i32, i32, i32, i32, i32, p, ctypes.c_float, p, p, ctypes.c_size_t, vp],
+            "nosa_quant_scratch_bytes": [i32, i32, i32],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -126,6 +133,7 @@ def lib() -> ctypes.CDLL:
         L.nosa_status_string.restype = ctypes.c_char_p
         L.nosa_dense_scratch_bytes.restype = ctypes.c_size_t
         L.nosa_prefill_scratch_bytes.restype = ctypes.c_size_t
+        L.nosa_quant_scratch_bytes.restype = ctypes.c_size_t
         _lib = L
     return _lib
 
@@ -312,3 +320,35 @@ def nosa_attend_noalloc(q, cache, sel, sel_slot, n_sel, units, group, cache_slot
                                      cache_slots, context_len, softmax_scale, _ptr(out), _ptr(err_out),
                                      stream or None),
            "nosa_attend_noalloc")
+
+
+def nosa_quant_append(k, v, store, units, n_tokens, max_blocks, pos=None, count=None, err_out=None, stream=0) -> None:
+    """Quantises tokens k, v [units][n_tokens][d] into a 4-bit store [units][max_blocks][10240] (see include/nosa.h)."""
+    _check(lib().nosa_quant_append(_ptr(k), _ptr(v), _ptr(store), units, n_tokens, max_blocks, _ptr(pos), _ptr(count),
+                                   _ptr(err_out), stream or None), "nosa_quant_append")
+
+
+def nosa_quant_read(store, units, max_blocks, blocks, n_blocks, kv, lens=None, err_out=None, stream=0) -> None:
+    """Reads blocks of a 4-bit store back to bf16 kv [units][n_blocks][2][64][d] (see include/nosa.h)."""
+    _check(lib().nosa_quant_read(_ptr(store), units, max_blocks, _ptr(blocks), n_blocks, _ptr(lens), _ptr(kv),
+                                 _ptr(err_out), stream or None), "nosa_quant_read")
+
+
+def nosa_quant_scratch_bytes(units, rows, blocks) -> int:
+    return int(lib().nosa_quant_scratch_bytes(units, rows, blocks))
+
+
+def nosa_quant_dense_attend(q, store, units, group, n_queries, max_blocks, lens, max_len, out, scratch, scratch_bytes,
+                            softmax_scale=0.0, stream=0) -> None:
+    """Attention over every token of a 4-bit store, q/out [units][group][n_queries][d] (see include/nosa.h)."""
+    _check(lib().nosa_quant_dense_attend(_ptr(q), _ptr(store), units, group, n_queries, max_blocks, _ptr(lens), max_len,
+                                         softmax_scale, _ptr(out), _ptr(scratch), scratch_bytes, stream or None),
+           "nosa_quant_dense_attend")
+
+
+def nosa_quant_attend(q, store, sel, sel_slot, units, group, n_queries, max_blocks, max_sel, lens, out, scratch,
+                      scratch_bytes, softmax_scale=0.0, stream=0) -> None:
+    """Attention over listed blocks sel [units][max_sel] of a 4-bit store (see include/nosa.h)."""
+    _check(lib().nosa_quant_attend(_ptr(q), _ptr(store), _ptr(sel), _ptr(sel_slot), units, group, n_queries, max_blocks,
+                                   max_sel, _ptr(lens), softmax_scale, _ptr(out), _ptr(scratch), scratch_bytes,
+                                   stream or None), "nosa_quant_attend")
