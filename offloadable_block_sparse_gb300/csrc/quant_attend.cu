@@ -9,8 +9,9 @@
 // codes.  The terms in m are one more MMA each: the row sums of q, split into two f16 against the
 // K minima, and a 16-row operand of the V minima with a row of ones that yields the softmax sum too.
 //
-// grid: one CTA per (unit, chunk of tiles), four warps.  A warp takes every fourth tile of 16 tokens
-// of the chunk on its own (mma.sync m16n8k16, f16 in, fp32 accumulate):
+// grid: one CTA per (unit, chunk of blocks), four warps.  A warp takes half (two tiles) of every second block of
+// the chunk, through a ring of its own of bulk copies to shared memory, so that no warp waits for
+// another; per tile (mma.sync m16n8k16, f16 in, fp32 accumulate):
 //   S^T (16 tokens x 8 rows) = K codes . q^T       8 MMAs, one accumulator per group, + 1 for m
 //   P^T by movmatrix of the f16-packed weights, times s per group
 //   O^T (128 dims x 8 rows) += V codes^T . P^T      8 MMAs, + 1 for m and the sum
@@ -27,10 +28,19 @@ namespace nosa {
 
 constexpr int kQaWarps = 4;
 constexpr int kQaThreads = kQaWarps * 32;
+constexpr int kQaStages = 2;          // half blocks in flight per warp
+constexpr int kStageTokens = 32, kStageBytes4 = 2 * kTileBytes;
+constexpr int kQaList = 256;          // listed blocks looked up at a time
 constexpr int kQaMaxRows = 32;
 constexpr int kQaRowStride = 132;     // floats per row of a warp's partial in shared memory (no bank conflicts)
 constexpr size_t kQaErrBytes = 256;   // the scratch starts with the device error word
-constexpr float kNoRef = -3e38f;      // R of a row that has seen no token
+constexpr float kNoRef = -3e38f;      // reference of a row that has seen no token
+
+// Shared memory of the rings, which the warps' partials reuse.
+__host__ __device__ constexpr int quant_ring_bytes(int nt) {
+  const int ring = kQaWarps * kQaStages * kStageBytes4, partials = kQaWarps * 8 * nt * kQaRowStride * 4;
+  return ring > partials ? ring : partials;
+}
 
 struct QuantArgs {
   const uint16_t* q;
@@ -42,7 +52,7 @@ struct QuantArgs {
   float* part;  // [unit][chunk][row][2 + 128]
   int* err;
   int group, nq, rows, max_blocks, max_sel, max_len;
-  int chunk_tiles, chunks;
+  int chunk_blocks, chunks;
   float scale;  // softmax scale x log2(e)
 };
 
@@ -85,12 +95,13 @@ __device__ __forceinline__ float ex2(float x) {
 struct QueryTile {
   uint32_t b[8][2];  // [2 group + half]: dims 32 gr + 8 t + {0,4}, {1,5} 2^-4 | {2,6}, {3,7} 2^-4 of row g
   uint32_t sums;     // t = 0, 1: high halves of the sums of groups 2t, 2t + 1; t = 2, 3: the low halves
-  float alpha[2];    // logit factor of rows 2t, 2t + 1 (softmax scale, log2 e, the row's power of two)
 };
 
 // Rows 8 nt + g of q: scaled by a power of two that brings the row's largest magnitude into [2^9, 2^10)
 // (bf16 values down to 2^-23 of it stay exact in f16, and a group's sum stays in range).
-__device__ __forceinline__ void load_query(QueryTile& Q, const uint16_t* q, int row, int rows, int lane, float scale) {
+// alpha: the factors that turn the scores of rows 2t, 2t + 1, in units of 2^-24, into logits in base 2.
+__device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], const uint16_t* q, int row, int rows, int lane,
+                                           float scale) {
   const int t = lane & 3;
   uint4 x[4];
   uint32_t big = 0;  // the largest magnitude's bf16 bits
@@ -105,7 +116,7 @@ __device__ __forceinline__ void load_query(QueryTile& Q, const uint16_t* q, int 
   big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
   // 2^(9 - e) for the exponent e of the largest value; 1 where the row is zero or not finite
   const int e = (int)(big >> 7) - 127;
-  const int shift = big == 0 || big >= 0x7f80u ? 0 : min(9 - e, 126);
+  const int shift = big == 0 || big >= 0x7f80u ? 0 : min(9 - e, 126);  // (alpha is infinite from |q| = 2^116 on)
   const float f = __uint_as_float((uint32_t)(127 + shift) << 23), inv = __uint_as_float((uint32_t)(127 - shift) << 23);
   float sum[4];
 #pragma unroll
@@ -129,95 +140,103 @@ __device__ __forceinline__ void load_query(QueryTile& Q, const uint16_t* q, int 
   const uint32_t l01 = pack_half2(sum[0] - half_lo(h01), sum[1] - half_hi(h01));
   const uint32_t l23 = pack_half2(sum[2] - half_lo(h23), sum[3] - half_hi(h23));
   Q.sums = t == 0 ? h01 : t == 1 ? h23 : t == 2 ? l01 : l23;
-  Q.alpha[0] = scale * __shfl_sync(0xffffffffu, inv, 8 * t);      // row 2t's lanes are 8t .. 8t + 3
-  Q.alpha[1] = scale * __shfl_sync(0xffffffffu, inv, 8 * t + 4);
+  alpha[0] = scale * 0x1p24f * __shfl_sync(0xffffffffu, inv, 8 * t);  // row 2t's lanes are 8t .. 8t + 3
+  alpha[1] = scale * 0x1p24f * __shfl_sync(0xffffffffu, inv, 8 * t + 4);
 }
 
-// One warp's running state for a tile of 8 rows: references of rows 2t, 2t + 1, O^T (codes' part, in units
-// of 2^-24, or 2^-20 for odd dims), and the m part: rows 0..3 the groups, row 4 the softmax sum.
+// One warp's running state for a tile of 8 rows: references of rows 2t, 2t + 1 in units of the scores (an
+// exponent is (z - r) alpha, so that a huge score less itself is zero), O^T (codes' part, in units of 2^-24,
+// or 2^-20 for odd dims), and the m part: rows 0..3 the groups, row 4 the softmax sum.
 struct RowTile {
   float r[2];
   float o[8][4];
   float c[4];
 };
 
-// A tile's operands as a lane holds them.
-struct TileRegs {
-  uint4 kc[2], vc[2];  // codes: tokens g, g + 8; token pairs t, t + 4
-  uint2 ks[2];         // K scales of tokens g, g + 8
-  uint32_t km[2];      // K minima of groups 2 (t % 2), + 1 of tokens g, g + 8
-  uint4 vs[2];         // V scales of the four groups, token pairs t, t + 4
-  uint32_t vm[2];      // rows of the m operand: group g's minima (g < 4), ones (g = 4), zeros
-};
-
-__device__ __forceinline__ void load_tile(TileRegs& T, const uint8_t* src, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    T.kc[h] = *reinterpret_cast<const uint4*>(src + 64 * (g + 8 * h) + 16 * t);
-    T.vc[h] = *reinterpret_cast<const uint4*>(src + kTileV + 512 * h + 16 * lane);
-    T.ks[h] = *reinterpret_cast<const uint2*>(src + kTileKs + 16 * (g + 8 * h));
-    T.km[h] = *reinterpret_cast<const uint32_t*>(src + kTileKs + 16 * (g + 8 * h) + 8 + 4 * (t & 1));
-    T.vs[h] = *reinterpret_cast<const uint4*>(src + kTileVs + 16 * (4 * h + t));
-    const uint32_t m = *reinterpret_cast<const uint32_t*>(src + kTileVm + 16 * (4 * h + t) + 4 * (g & 3));
-    T.vm[h] = g < 4 ? m : g == 4 ? 0x3C003C00u : 0u;
-  }
-}
-
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Keeps the halves of w whose token (2 pair, 2 pair + 1) is below `n`.
+// Keeps the halves of w whose token (first, first + 1) is below n.
 __device__ __forceinline__ uint32_t keep_tokens(uint32_t w, int first, int n) {
   return first + 1 < n ? w : first < n ? w & 0xffffu : 0u;
 }
 
-// Adds the V side of a tile to one row tile: p[h] = weights of token pairs t + 4 h as f16x2.
-__device__ __forceinline__ void add_values(RowTile& A, const TileRegs& T, const uint32_t (&p)[2]) {
+// The V side of a tile as a lane holds it: codes and scales of token pairs t, t + 4, and the rows of the m
+// operand (group g's minima for g < 4, ones for g = 4, zeros).
+struct ValueRegs {
+  uint4 c[2], s[2];
+  uint32_t m[2];
+};
+__device__ __forceinline__ void load_values(ValueRegs& V, const unsigned char* tile, int lane) {
+  const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int gr = 0; gr < 4; ++gr) {
-    const uint32_t b0 = mul_half2(p[0], word(T.vs[0], gr)), b1 = mul_half2(p[1], word(T.vs[1], gr));
-    const uint32_t w0 = word(T.vc[0], gr), w1 = word(T.vc[1], gr), x0 = w0 >> 8, x1 = w1 >> 8;
-    mma_f16(A.o[2 * gr], w0 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x000F000Fu, w1 & 0x00F000F0u, b0, b1);
-    mma_f16(A.o[2 * gr + 1], x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u, b0, b1);
+  for (int h = 0; h < 2; ++h) {
+    V.c[h] = *reinterpret_cast<const uint4*>(tile + kTileV + 512 * h + 16 * lane);
+    V.s[h] = *reinterpret_cast<const uint4*>(tile + kTileVs + 16 * (4 * h + t));
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(tile + kTileVm + 16 * (4 * h + t) + 4 * (g & 3));
+    V.m[h] = g < 4 ? m : g == 4 ? 0x3C003C00u : 0u;
   }
-  mma_f16(A.c, T.vm[0], 0u, T.vm[1], 0u, p[0], p[1]);
 }
 
-// The rare tile at the end of a context with several query tokens where a token that only some of the
-// rows see has a NaN group: 0 x NaN must not reach the others, so each token from `from` on is added
-// alone, into the rows that gave it a weight.  p as above, zero for the tokens a row does not see.
-__device__ __noinline__ void add_values_by_token(RowTile& A, const TileRegs& T, const uint32_t (&p)[2], int from) {
-  const int lane = threadIdx.x & 31, t = lane & 3;
-  for (int tok = from; tok < kTileTokens; ++tok) {
-    const int h = tok >> 3, owner = (tok & 7) >> 1, par = tok & 1;
-    TileRegs S = T;
-    uint32_t w[2];
+// O^T += V^T . P^T for NT row tiles; p[nt][h] = weights of row g, token pair t + 4 h, as f16x2.
+template <int NT>
+__device__ __forceinline__ void add_values(RowTile (&A)[NT], const ValueRegs& V, const uint32_t (&p)[NT][2]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t keep = i == h && t == owner ? (par ? 0xffff0000u : 0x0000ffffu) : 0u;
-      w[i] = p[i] & keep;
-      S.vs[i] = make_uint4(T.vs[i].x & keep, T.vs[i].y & keep, T.vs[i].z & keep, T.vs[i].w & keep);
-      S.vm[i] = T.vm[i] & keep;
+  for (int gr = 0; gr < 4; ++gr) {
+    const uint32_t w0 = word(V.c[0], gr), w1 = word(V.c[1], gr), x0 = w0 >> 8, x1 = w1 >> 8;
+    const uint32_t a[8] = {w0 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x000F000Fu, w1 & 0x00F000F0u,
+                           x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t b0 = mul_half2(p[nt][0], word(V.s[0], gr)), b1 = mul_half2(p[nt][1], word(V.s[1], gr));
+      mma_f16(A[nt].o[2 * gr], a[0], a[1], a[2], a[3], b0, b1);
+      mma_f16(A[nt].o[2 * gr + 1], a[4], a[5], a[6], a[7], b0, b1);
     }
-    RowTile D;
+  }
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) D.o[mt][0] = D.o[mt][1] = D.o[mt][2] = D.o[mt][3] = 0.f;
-    D.c[0] = D.c[1] = D.c[2] = D.c[3] = 0.f;
-    add_values(D, S, w);
-    // the token's weight for rows 2t, 2t + 1: held by lane (row, owner)
-    const uint32_t mine = h ? w[1] : w[0];
-    const uint32_t p0 = __shfl_sync(0xffffffffu, mine, 8 * t + owner), p1 = __shfl_sync(0xffffffffu, mine, 8 * t + 4 + owner);
+  for (int nt = 0; nt < NT; ++nt) mma_f16(A[nt].c, V.m[0], 0u, V.m[1], 0u, p[nt][0], p[nt][1]);
+}
+
+// The rare tile at the end of a context with several query tokens where a token that only some of the rows
+// see has a NaN group: 0 x NaN must not reach the others, so the tokens from `from` on are added one at a
+// time, each into the rows that gave it a weight, after those before them together.
+__device__ __noinline__ void add_values_by_token(RowTile& A, const unsigned char* tile, uint32_t p0, uint32_t p1, int from) {
+  const int lane = threadIdx.x & 31, t = lane & 3;
+  ValueRegs V;
+  load_values(V, tile, lane);
+  for (int tok = max(from, 0) - 1; tok < kTileTokens; ++tok) {
+    ValueRegs S = V;
+    RowTile D[1];
+    uint32_t w[1][2];
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) D[0].o[mt][0] = D[0].o[mt][1] = D[0].o[mt][2] = D[0].o[mt][3] = 0.f;
+    D[0].c[0] = D[0].c[1] = D[0].c[2] = D[0].c[3] = 0.f;
+    const bool together = tok < from;  // the first round: the tokens below `from`
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int first = 2 * t + 8 * h;
+      const uint32_t keep = together ? keep_tokens(0xffffffffu, first, from)
+                                     : (tok == first ? 0x0000ffffu : tok == first + 1 ? 0xffff0000u : 0u);
+      w[0][h] = (h ? p1 : p0) & keep;
+      S.s[h] = make_uint4(V.s[h].x & keep, V.s[h].y & keep, V.s[h].z & keep, V.s[h].w & keep);
+      S.m[h] = V.m[h] & keep;
+    }
+    add_values<1>(D, S, w);
+    // the token's weight for rows 2t, 2t + 1 is held by lane (row, pair of the token)
+    const uint32_t mine = (tok >> 3) == 1 ? w[0][1] : w[0][0];
+    const int owner = (max(tok, 0) & 7) >> 1;
+    const bool in0 = __shfl_sync(0xffffffffu, mine, 8 * t + owner) != 0 || together;
+    const bool in1 = __shfl_sync(0xffffffffu, mine, 8 * t + 4 + owner) != 0 || together;
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
-      A.o[mt][0] += p0 ? D.o[mt][0] : 0.f;
-      A.o[mt][1] += p1 ? D.o[mt][1] : 0.f;
-      A.o[mt][2] += p0 ? D.o[mt][2] : 0.f;
-      A.o[mt][3] += p1 ? D.o[mt][3] : 0.f;
+      A.o[mt][0] += in0 ? D[0].o[mt][0] : 0.f;
+      A.o[mt][1] += in1 ? D[0].o[mt][1] : 0.f;
+      A.o[mt][2] += in0 ? D[0].o[mt][2] : 0.f;
+      A.o[mt][3] += in1 ? D[0].o[mt][3] : 0.f;
     }
-    A.c[0] += p0 ? D.c[0] : 0.f;
-    A.c[1] += p1 ? D.c[1] : 0.f;
-    A.c[2] += p0 ? D.c[2] : 0.f;
-    A.c[3] += p1 ? D.c[3] : 0.f;
+    A.c[0] += in0 ? D[0].c[0] : 0.f;
+    A.c[1] += in1 ? D[0].c[1] : 0.f;
+    A.c[2] += in0 ? D[0].c[2] : 0.f;
+    A.c[3] += in1 ? D[0].c[3] : 0.f;
   }
 }
 
@@ -226,128 +245,177 @@ __device__ __forceinline__ bool not_finite2(uint32_t w) {
   return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
 }
 
-// One tile of 16 tokens for all row tiles.  left: tokens of the context from the tile's first on (may exceed 16).
+// Clears the V scales and minima of the stage's tokens from `left` on: behind the context the store may hold
+// anything, and 0 x NaN is a NaN (the codes are finite as they stand).  Returns whether a token that only some
+// rows see, from `seen` on, has a NaN group.
+__device__ __noinline__ bool clear_tail(unsigned char* stage, int left, int seen) {
+  const int lane = threadIdx.x & 31;
+  bool odd = false;
+  for (int i = lane; i < kStageTokens / 2 * 8; i += 32) {  // [tile][s, m][token pair][group] words of two tokens
+    const int first = (i >> 6) * kTileTokens + 2 * ((i >> 2) & 7);
+    uint32_t* w = reinterpret_cast<uint32_t*>(stage + (i >> 6) * kTileBytes + kTileVs) + (i & 63);
+    const uint32_t x = keep_tokens(*w, first, left);
+    *w = x;
+    odd |= not_finite2(x & ~keep_tokens(0xffffffffu, first, seen));
+  }
+  fence_proxy_async_smem();  // the next bulk copy into the stage comes after these writes
+  __syncwarp();
+  return __any_sync(0xffffffffu, odd);
+}
+
+// One stage (two tiles, 32 tokens) for all row tiles.  left: tokens of the context from the stage's first on.
+// q: the query operands, in registers (NT = 1) or in shared memory (uint4 [nt][group][lane]).
 template <int NT>
-__device__ __forceinline__ void process_tile(RowTile (&A)[NT], const QueryTile (&Q)[NT], TileRegs& T, int left, int nq,
-                                             int rows, int lane) {
+__device__ __forceinline__ void process_stage(RowTile (&A)[NT], const float (&alpha)[NT][2], const QueryTile& Q, const uint4* qs,
+                                              const uint32_t (&sums)[NT], unsigned char* stage, int left, int nq, int rows,
+                                              int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const bool tail = left - (nq - 1) < kTileTokens;  // some row does not see the whole tile
-  int odd_from = kTileTokens;                       // first token that has to be added alone
-  if (tail) {
-    // behind the context the store may hold anything: its codes are finite as they stand, its scales go
+  const bool tail = left - (nq - 1) < kStageTokens;  // some row does not see the whole stage
+  bool odd = false;
+  if (tail) odd = clear_tail(stage, left, left - (nq - 1));
+
+  // scores in units of 2^-24
+  float z[2][NT][4];
+  uint4 kc[2][2];
+  float ks[2][2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const unsigned char* tile = stage + i * kTileBytes;
+    uint32_t km[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int first = 2 * t + 8 * h;
-      T.vs[h].x = keep_tokens(T.vs[h].x, first, left);
-      T.vs[h].y = keep_tokens(T.vs[h].y, first, left);
-      T.vs[h].z = keep_tokens(T.vs[h].z, first, left);
-      T.vs[h].w = keep_tokens(T.vs[h].w, first, left);
-      if (g < 4) T.vm[h] = keep_tokens(T.vm[h], first, left);
+      kc[i][h] = *reinterpret_cast<const uint4*>(tile + 64 * (g + 8 * h) + 16 * t);
+      const uint2 s = *reinterpret_cast<const uint2*>(tile + kTileKs + 16 * (g + 8 * h));
+      km[h] = *reinterpret_cast<const uint32_t*>(tile + kTileKs + 16 * (g + 8 * h) + 8 + 4 * (t & 1));
+      ks[i][h][0] = half_lo(s.x);
+      ks[i][h][1] = half_hi(s.x);
+      ks[i][h][2] = half_lo(s.y);
+      ks[i][h][3] = half_hi(s.y);
     }
-    if (nq > 1) {
-      bool odd = false;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t late = ~keep_tokens(0xffffffffu, 2 * t + 8 * h, left - (nq - 1));
-        odd |= not_finite2(T.vs[h].x & late) || not_finite2(T.vs[h].y & late) || not_finite2(T.vs[h].z & late) ||
-               not_finite2(T.vs[h].w & late);
-      }
-      if (__any_sync(0xffffffffu, odd)) odd_from = max(left - (nq - 1), 0);
+    for (int nt = 0; nt < NT; ++nt) {
+      float m[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_f16_k8(m, km[0], km[1], sums[nt]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[i][nt][e] = m[e] * 0x1p-24f;
     }
   }
-  // the largest V scale of the lane's tokens (the lanes of one t agree)
-  const uint32_t vmax2 = max_half2(max_half2(max_half2(T.vs[0].x, T.vs[0].y), max_half2(T.vs[0].z, T.vs[0].w)),
-                                   max_half2(max_half2(T.vs[1].x, T.vs[1].y), max_half2(T.vs[1].z, T.vs[1].w)));
-  const bool large = (vmax2 & 0x7fffu) >= 0x4000u || (vmax2 >> 16 & 0x7fffu) >= 0x4000u;  // 2 or more
-
-  // K scales as floats, times the 2^24 that the codes lack
-  float ks[2][4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    ks[h][0] = half_lo(T.ks[h].x) * 16777216.f;
-    ks[h][1] = half_hi(T.ks[h].x) * 16777216.f;
-    ks[h][2] = half_lo(T.ks[h].y) * 16777216.f;
-    ks[h][3] = half_hi(T.ks[h].y) * 16777216.f;
-  }
+  for (int gr = 0; gr < 4; ++gr) {
+    uint32_t a[2][8];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float z[4] = {0.f, 0.f, 0.f, 0.f};
-    mma_f16_k8(z, T.km[0], T.km[1], Q[nt].sums);
-#pragma unroll
-    for (int gr = 0; gr < 4; ++gr) {
-      const uint32_t w0 = word(T.kc[0], gr), w1 = word(T.kc[1], gr), x0 = w0 >> 8, x1 = w1 >> 8;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_f16(acc, w0 & 0x000F000Fu, w1 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x00F000F0u, Q[nt].b[2 * gr][0], Q[nt].b[2 * gr][1]);
-      mma_f16(acc, x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u, Q[nt].b[2 * gr + 1][0],
-              Q[nt].b[2 * gr + 1][1]);
-      z[0] = fmaf(acc[0], ks[0][gr], z[0]);
-      z[1] = fmaf(acc[1], ks[0][gr], z[1]);
-      z[2] = fmaf(acc[2], ks[1][gr], z[2]);
-      z[3] = fmaf(acc[3], ks[1][gr], z[3]);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w0 = word(kc[i][0], gr), w1 = word(kc[i][1], gr), x0 = w0 >> 8, x1 = w1 >> 8;
+      a[i][0] = w0 & 0x000F000Fu;
+      a[i][1] = w1 & 0x000F000Fu;
+      a[i][2] = w0 & 0x00F000F0u;
+      a[i][3] = w1 & 0x00F000F0u;
+      a[i][4] = x0 & 0x000F000Fu;
+      a[i][5] = x1 & 0x000F000Fu;
+      a[i][6] = x0 & 0x00F000F0u;
+      a[i][7] = x1 & 0x00F000F0u;
     }
-    z[0] *= Q[nt].alpha[0];
-    z[1] *= Q[nt].alpha[1];
-    z[2] *= Q[nt].alpha[0];
-    z[3] *= Q[nt].alpha[1];
-    if (tail) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 8 * nt + 2 * t + (i & 1), token = g + 8 * (i >> 1);
-        if (row >= rows || token >= left - (nq - 1) + row % nq) z[i] = -INFINITY;
-      }
-    }
-    RowTile& S = A[nt];
-    const float mx0 = fmaxf(z[0], z[2]), mx1 = fmaxf(z[1], z[3]);
-    if (__any_sync(0xffffffffu, mx0 - S.r[0] > 14.f || mx1 - S.r[1] > 14.f || large)) {
-      // a row's maximum has outgrown its reference, or weight x scale might leave f16
-      float top[2] = {mx0, mx1}, vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
-        top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
-      }
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-      // vmax < 2^e: weights up to 2^limit keep the products below 2^15 (a NaN scale sets no limit)
-      if (!(vmax <= 65504.f)) vmax = 0.f;
-      const int e = (int)(__float_as_uint(vmax) >> 23) - 126;
-      const float limit = (float)(14 - max(e - 1, 0));
+    for (int nt = 0; nt < NT; ++nt) {
+      uint4 b;
+      if constexpr (NT == 1)
+        b = make_uint4(Q.b[2 * gr][0], Q.b[2 * gr][1], Q.b[2 * gr + 1][0], Q.b[2 * gr + 1][1]);
+      else
+        b = qs[(4 * nt + gr) * 32 + lane];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (top[i] - S.r[i] > limit) {
-          const float r = top[i] - (limit - 4.f), f = ex2(S.r[i] - r);
-          S.r[i] = r;
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt) {
-            S.o[mt][i] *= f;
-            S.o[mt][i + 2] *= f;
-          }
-          S.c[i] *= f;
-          S.c[i + 2] *= f;
-        }
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16(acc, a[i][0], a[i][1], a[i][2], a[i][3], b.x, b.y);
+        mma_f16(acc, a[i][4], a[i][5], a[i][6], a[i][7], b.z, b.w);
+        z[i][nt][0] = fmaf(acc[0], ks[i][0][gr], z[i][nt][0]);
+        z[i][nt][1] = fmaf(acc[1], ks[i][0][gr], z[i][nt][1]);
+        z[i][nt][2] = fmaf(acc[2], ks[i][1][gr], z[i][nt][2]);
+        z[i][nt][3] = fmaf(acc[3], ks[i][1][gr], z[i][nt][3]);
       }
     }
-    // weights of tokens g (+ 8), rows 2t, 2t + 1; transposed: of row g, token pairs t, t + 4
-    uint32_t p[2] = {movmatrix_trans(pack_half2(ex2(z[0] - S.r[0]), ex2(z[1] - S.r[1]))),
-                     movmatrix_trans(pack_half2(ex2(z[2] - S.r[0]), ex2(z[3] - S.r[1])))};
-    if (odd_from < kTileTokens) {
-      RowTile B = S;  // a copy, so that S itself stays in registers
-      add_values_by_token(B, T, p, odd_from);
-      S = B;
-      TileRegs U = T;
+  }
+  if (tail) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int first = 2 * t + 8 * h;
-        U.vs[h].x = keep_tokens(T.vs[h].x, first, odd_from);
-        U.vs[h].y = keep_tokens(T.vs[h].y, first, odd_from);
-        U.vs[h].z = keep_tokens(T.vs[h].z, first, odd_from);
-        U.vs[h].w = keep_tokens(T.vs[h].w, first, odd_from);
-        U.vm[h] = keep_tokens(T.vm[h], first, odd_from);  // the row of ones too: those tokens are counted
-        p[h] = keep_tokens(p[h], first, odd_from);
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 8 * nt + 2 * t + (e & 1), token = kTileTokens * i + g + 8 * (e >> 1);
+          if (row >= rows || token >= left - (nq - 1) + row % nq) z[i][nt][e] = -INFINITY;
+        }
+  }
+
+  // exponents against the references, and whether they hold: no row's maximum has outgrown its reference by
+  // 14, and no V scale of the stage is 2 or more (then weights up to 2^14 times scales stay within f16)
+  const uint4 vs = *reinterpret_cast<const uint4*>(stage + (lane >> 3 & 1) * kTileBytes + kTileVs + 16 * (lane & 7));
+  const uint32_t vmax2 = max_half2(max_half2(vs.x, vs.y), max_half2(vs.z, vs.w));
+  bool raise = (vmax2 & 0x40004000u) != 0;  // exponent bit 14: 2 or more (scales have no sign)
+  float ex[2][NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ex[i][nt][e] = (z[i][nt][e] - A[nt].r[e & 1]) * alpha[nt][e & 1];
+    const float top = fmaxf(fmaxf(fmaxf(ex[0][nt][0], ex[0][nt][1]), fmaxf(ex[0][nt][2], ex[0][nt][3])),
+                            fmaxf(fmaxf(ex[1][nt][0], ex[1][nt][1]), fmaxf(ex[1][nt][2], ex[1][nt][3])));
+    raise |= top > 14.f;
+  }
+  if (__any_sync(0xffffffffu, raise)) {
+    float vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+    // vmax < 2^e: weights up to 2^limit keep the products below 2^15 (a NaN scale sets no limit)
+    if (!(vmax <= 65504.f)) vmax = 0.f;
+    const float limit = (float)(14 - max((int)(__float_as_uint(vmax) >> 23) - 127, 0));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float best = fmaxf(fmaxf(z[0][nt][e], z[0][nt][e + 2]), fmaxf(z[1][nt][e], z[1][nt][e + 2]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+        const float old = A[nt].r[e];
+        if ((best - old) * alpha[nt][e] > limit) {  // the row's lanes agree; rows differ
+          const float r = best - (limit - 4.f) / alpha[nt][e], f = ex2((old - r) * alpha[nt][e]);
+          A[nt].r[e] = r;
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) {
+            A[nt].o[mt][e] *= f;
+            A[nt].o[mt][e + 2] *= f;
+          }
+          A[nt].c[e] *= f;
+          A[nt].c[e + 2] *= f;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            ex[i][nt][e] = (z[i][nt][e] - r) * alpha[nt][e];
+            ex[i][nt][e + 2] = (z[i][nt][e + 2] - r) * alpha[nt][e];
+          }
+        }
       }
-      add_values(S, U, p);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // weights of tokens g, g + 8 and rows 2t, 2t + 1; transposed: of row g and token pairs t, t + 4
+    uint32_t p[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      p[nt][0] = movmatrix_trans(pack_half2(ex2(ex[i][nt][0]), ex2(ex[i][nt][1])));
+      p[nt][1] = movmatrix_trans(pack_half2(ex2(ex[i][nt][2]), ex2(ex[i][nt][3])));
+    }
+    if (odd) {
+      const int from = min(max(left - (nq - 1) - kTileTokens * i, 0), kTileTokens);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        RowTile B = A[nt];  // a copy, so that A itself stays in registers
+        add_values_by_token(B, stage + i * kTileBytes, p[nt][0], p[nt][1], from);
+        A[nt] = B;
+      }
     } else {
-      add_values(S, T, p);
+      ValueRegs V;
+      load_values(V, stage + i * kTileBytes, lane);
+      add_values<NT>(A, V, p);
     }
   }
 }
@@ -359,45 +427,111 @@ __device__ __forceinline__ uint16_t finish(float o, float l) {
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kQaThreads) quant_attend_kernel(const __grid_constant__ QuantArgs a) {
-  extern __shared__ __align__(16) float smem[];  // [warp][8 NT rows][kQaRowStride], the merge's
+__global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kernel(const __grid_constant__ QuantArgs a) {
+  // the warps' rings, then [warp][8 NT rows][kQaRowStride], their partials; behind them the query operands (NT > 1)
+  extern __shared__ __align__(16) float smem[];
+  __shared__ __align__(8) uint64_t bars[kQaWarps][kQaStages];
+  __shared__ int tokens[kQaWarps][kQaStages];
+  __shared__ int2 list[kQaList];  // (row of the store, tokens of the context from the block on)
   __shared__ float wr[kQaWarps][8 * NT], wl[kQaWarps][8 * NT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int u = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
+  if (lane == 0) {
+#pragma unroll
+    for (int st = 0; st < kQaStages; ++st) mbar_init(&bars[warp][st], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
   pdl_wait();
   pdl_launch_dependents();
   const int len0 = a.lens[u];
   const int len = a.sel ? max(len0, 0) : min(max(len0, 0), a.max_len);
   if (len != len0 && threadIdx.x == 0 && chunk == 0) atomicOr(a.err, kErrBounds);
-  QueryTile Q[NT];
+
+  QueryTile Q;
+  uint4* qs = reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(smem) + quant_ring_bytes(NT));
   RowTile A[NT];
+  float alpha[NT][2];
+  uint32_t sums[NT];
+  auto load_queries = [&]() {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    load_query(Q[nt], a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale);
-    A[nt].r[0] = A[nt].r[1] = kNoRef;
+    for (int nt = 0; nt < NT; ++nt) {
+      load_query(Q, alpha[nt], a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale);
+      sums[nt] = Q.sums;
+      if (NT > 1 && warp == nt % kQaWarps) {
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) A[nt].o[mt][0] = A[nt].o[mt][1] = A[nt].o[mt][2] = A[nt].o[mt][3] = 0.f;
-    A[nt].c[0] = A[nt].c[1] = A[nt].c[2] = A[nt].c[3] = 0.f;
-  }
-  const int tiles = a.sel ? 4 * a.max_sel : (len + kTileTokens - 1) / kTileTokens;
-  const int end = min((chunk + 1) * a.chunk_tiles, tiles);
-  for (int i = chunk * a.chunk_tiles + warp; i < end; i += kQaWarps) {
-    int block = i >> 2, slot = block;
-    if (a.sel) {
-      block = a.sel[(size_t)u * a.max_sel + (i >> 2)];
-      if (block < 0) continue;
-      slot = a.sel_slot ? a.sel_slot[(size_t)u * a.max_sel + (i >> 2)] : block;
-      if (slot < 0 || slot >= a.max_blocks) {
-        if (lane == 0) atomicOr(a.err, kErrBounds);
-        continue;
+        for (int gr = 0; gr < 4; ++gr)
+          qs[(4 * nt + gr) * 32 + lane] = make_uint4(Q.b[2 * gr][0], Q.b[2 * gr][1], Q.b[2 * gr + 1][0], Q.b[2 * gr + 1][1]);
       }
+      A[nt].r[0] = A[nt].r[1] = kNoRef;
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) A[nt].o[mt][0] = A[nt].o[mt][1] = A[nt].o[mt][2] = A[nt].o[mt][3] = 0.f;
+      A[nt].c[0] = A[nt].c[1] = A[nt].c[2] = A[nt].c[3] = 0.f;
     }
-    const long long left = (long long)len - ((long long)block * kBlock + (i & 3) * kTileTokens);
-    if (left <= 0) continue;
-    TileRegs T;
-    load_tile(T, a.store + ((size_t)u * a.max_blocks + slot) * kQuantBlockBytes + (i & 3) * kTileBytes, lane);
-    process_tile<NT>(A, Q, T, (int)min(left, 1ll << 20), a.nq, a.rows, lane);
+    if (NT > 1) __syncthreads();
+  };
+
+  // The chunk's blocks, looked up kQaList at a time (a dense call needs no list).  Warp w takes half w % 2 of the
+  // blocks w / 2, w / 2 + 2, ...
+  const int first = chunk * a.chunk_blocks;
+  const int end = min(first + a.chunk_blocks, a.sel ? a.max_sel : (len + kBlock - 1) / kBlock);
+  const int batch = a.sel ? kQaList : a.chunk_blocks, half = (warp & 1) * kStageTokens;
+  const uint8_t* base = a.store + (size_t)u * a.max_blocks * kQuantBlockBytes + (warp & 1) * kStageBytes4;
+  unsigned char* ring = reinterpret_cast<unsigned char*>(smem) + warp * kQaStages * kStageBytes4;
+  int issued = 0, done = 0;
+  bool late = false;
+  for (int b0 = first; b0 < end || b0 == first; b0 += batch) {
+    const int n = min(batch, end - b0);
+    if (a.sel) {
+      if (b0 > first) __syncthreads();  // the list before is used up
+      for (int j = threadIdx.x; j < n; j += kQaThreads) {
+        const size_t at = (size_t)u * a.max_sel + b0 + j;
+        const int block = a.sel[at];
+        const int slot = block < 0 ? 0 : a.sel_slot ? a.sel_slot[at] : block;
+        const bool held = slot >= 0 && slot < a.max_blocks;
+        if (!held) atomicOr(a.err, kErrBounds);
+        const long long left = block < 0 || !held ? 0 : (long long)len - (long long)block * kBlock;
+        list[j] = make_int2(slot, (int)min(max(left, 0ll), 2ll * kBlock));  // 128 or more: every row sees the whole block
+      }
+      __syncthreads();
+    }
+    int j = warp >> 1;
+    auto issue = [&]() {  // the next half block into the stage whose turn it is; false when there is none
+      int2 e = make_int2(0, 0);
+      for (; j < n; j += kQaWarps / 2) {
+        e = a.sel ? list[j] : make_int2(b0 + j, min(len - (b0 + j) * kBlock, 2 * kBlock));
+        if (e.y > half) break;
+      }
+      if (j >= n || late) return false;
+      j += kQaWarps / 2;
+      if (lane == 0) {
+        const int st = issued % kQaStages;
+        tokens[warp][st] = e.y - half;
+        mbar_arrive_expect_tx(&bars[warp][st], kStageBytes4);
+        bulk_copy_g2s(smem_u32(ring + st * kStageBytes4), base + (size_t)e.x * kQuantBlockBytes, kStageBytes4, &bars[warp][st]);
+      }
+      return true;
+    };
+#pragma unroll
+    for (int i = 0; i < kQaStages; ++i)
+      if (issue()) ++issued;
+    if (b0 == first) load_queries();  // while the first stages arrive
+    __syncwarp();
+    for (; done < issued; ++done) {
+      const int st = done % kQaStages;
+      late |= !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][st], done / kQaStages & 1, kWaitCycles));
+      if (late) continue;  // let what is in flight land, and start no more
+      process_stage<NT>(A, alpha, Q, qs, sums, ring + st * kStageBytes4, tokens[warp][st], a.nq, a.rows, lane);
+      __syncwarp();  // the stage is read
+      if (issue()) ++issued;
+    }
   }
+  if (late) {  // a wait gave up: poison the outputs
+    if (lane == 0) atomicOr(a.err, kErrTimeout);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) A[nt].c[0] = A[nt].c[1] = __int_as_float(0x7fc00000);
+  }
+  __syncthreads();  // the rings become the warps' partials
 
   // the warp's partial: O of rows 2t, 2t + 1, dims 32 gr + 4 g .. + 3
 #pragma unroll
@@ -417,7 +551,7 @@ __global__ void __launch_bounds__(kQaThreads) quant_attend_kernel(const __grid_c
     if (g == 4) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        wr[warp][8 * nt + 2 * t + i] = S.r[i];
+        wr[warp][8 * nt + 2 * t + i] = fmaxf(S.r[i] * alpha[nt][i], kNoRef);  // from here on in base-2 logits
         wl[warp][8 * nt + 2 * t + i] = S.c[i];
       }
     }
@@ -476,15 +610,15 @@ __global__ void __launch_bounds__(kHeadDim) quant_merge_kernel(const float* __re
   out[((size_t)u * rows + row) * kHeadDim + x] = finish(O, L);
 }
 
-// How a call is split: about four CTAs of at least four tiles per SM and unit's share.
+// How a call is split: about four CTAs per SM.
 struct QuantPlan {
-  int chunk_tiles, chunks;
+  int chunk_blocks, chunks;
 };
-static QuantPlan quant_plan(int units, int tiles, int sms) {
+static QuantPlan quant_plan(int units, int blocks, int sms) {
   const long long most = 1 + 16ll * sms / units;  // units x chunks <= units + 16 SMs
   const long long want = std::min<long long>(most, std::max<long long>(1, (4ll * sms + units - 1) / units));
-  const int chunk = std::max<int>(kQaWarps, (int)((tiles + want - 1) / want));
-  return {chunk, (tiles + chunk - 1) / chunk};
+  const int chunk = (int)((blocks + want - 1) / want);
+  return {chunk, (blocks + chunk - 1) / chunk};
 }
 
 static int quant_sms() {
@@ -499,7 +633,7 @@ static int quant_sms() {
 
 template <int NT>
 static cudaError_t launch_quant_attend(const QuantArgs& a, int units, cudaStream_t st) {
-  const int smem = kQaWarps * 8 * NT * kQaRowStride * (int)sizeof(float);
+  const int smem = quant_ring_bytes(NT) + (NT > 1 ? NT * 4 * 32 * (int)sizeof(uint4) : 0);
   cudaError_t e = cudaFuncSetAttribute(quant_attend_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_ex(quant_attend_kernel<NT>, dim3((unsigned)(units * a.chunks)), dim3(kQaThreads), smem, st, true, 0, a);
@@ -508,9 +642,9 @@ static cudaError_t launch_quant_attend(const QuantArgs& a, int units, cudaStream
 static nosa_status quant_attend(QuantArgs& a, int units, int blocks, void* scratch, size_t scratch_bytes, cudaStream_t st) {
   const int sms = quant_sms();
   if (sms <= 0) return NOSA_ERR_CUDA;
-  const QuantPlan plan = quant_plan(units, 4 * blocks, sms);
+  const QuantPlan plan = quant_plan(units, blocks, sms);
   if (scratch_bytes < nosa_quant_scratch_bytes(units, a.rows, blocks)) return NOSA_ERR_CAPACITY;
-  a.chunk_tiles = plan.chunk_tiles;
+  a.chunk_blocks = plan.chunk_blocks;
   a.chunks = plan.chunks;
   a.err = reinterpret_cast<int*>(scratch);
   a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + kQaErrBytes);
@@ -544,7 +678,7 @@ using namespace nosa;
 extern "C" size_t nosa_quant_scratch_bytes(int units, int rows, int blocks) {
   const int sms = quant_sms();
   if (sms <= 0 || units < 1 || units > (1 << 20) || rows < 1 || rows > kQaMaxRows || blocks < 1 || blocks > 16384) return 0;
-  return kQaErrBytes + (size_t)units * quant_plan(units, 4 * blocks, sms).chunks * rows * kPartStride * sizeof(float);
+  return kQaErrBytes + (size_t)units * quant_plan(units, blocks, sms).chunks * rows * kPartStride * sizeof(float);
 }
 
 extern "C" nosa_status nosa_quant_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group,
