@@ -9,17 +9,19 @@
 // codes.  The terms in m are one more MMA each: the row sums of q, split into two f16 against the
 // K minima, and a 16-row operand of the V minima with a row of ones that yields the softmax sum too.
 //
-// grid: one CTA per (unit, chunk of blocks), four warps.  A warp takes half (two tiles) of every second block of
-// the chunk, through a ring of its own of bulk copies to shared memory, so that no warp waits for
-// another; per tile (mma.sync m16n8k16, f16 in, fp32 accumulate):
+// grid: one wave of CTAs of four warps; the units' blocks in one line are cut into equal pieces, one per CTA, so
+// that ragged lengths balance.  A warp takes half (two tiles) of every second block through a ring of its own of
+// bulk copies to shared memory, so that no warp waits for another; per tile (mma.sync m16n8k16, f16 in, fp32
+// accumulate):
 //   S^T (16 tokens x 8 rows) = K codes . q^T       8 MMAs, one accumulator per group, + 1 for m
 //   P^T by movmatrix of the f16-packed weights, times s per group
 //   O^T (128 dims x 8 rows) += V codes^T . P^T      8 MMAs, + 1 for m and the sum
 // The query rows of a unit (q heads x query tokens, at most 32) are NT tiles of 8.  Weights are
 // exp2(logit - R): R follows a row's maximum only when that outgrows it by 2^14, so the usual tile needs
 // no rescaling, and is set so that weight x s stays within f16 (R rises with a scale of 2 or more).
-// The CTA merges its warps in shared memory; chunks merge in a second kernel.
+// A CTA merges its warps in shared memory; a unit's parts, where several CTAs share it, merge in a second kernel.
 #include <algorithm>
+#include <mutex>
 
 #include "host.h"
 #include "quant_core.cuh"
@@ -30,6 +32,7 @@ constexpr int kQaWarps = 4;
 constexpr int kQaThreads = kQaWarps * 32;
 constexpr int kQaStages = 2;          // half blocks in flight per warp
 constexpr int kStageTokens = 32, kStageBytes4 = 2 * kTileBytes;
+constexpr int kQaSplitUnits = 2048;   // beyond, one CTA per unit
 constexpr int kQaList = 256;          // listed blocks looked up at a time
 constexpr int kQaMaxRows = 32;
 constexpr int kQaRowStride = 132;     // floats per row of a warp's partial in shared memory (no bank conflicts)
@@ -42,6 +45,10 @@ __host__ __device__ constexpr int quant_ring_bytes(int nt) {
   return ring > partials ? ring : partials;
 }
 
+__host__ __device__ constexpr int quant_smem_bytes(int nt) {
+  return quant_ring_bytes(nt) + (nt > 1 ? nt * 4 * 32 * 16 : 0);  // and the query operands
+}
+
 struct QuantArgs {
   const uint16_t* q;
   const uint8_t* store;
@@ -49,11 +56,13 @@ struct QuantArgs {
   const int32_t* sel_slot;  // null: row b holds block b
   const int32_t* lens;
   uint16_t* out;
-  float* part;  // [unit][chunk][row][2 + 128]
   int* err;
-  int group, nq, rows, max_blocks, max_sel, max_len;
-  int chunk_blocks, chunks;
-  float scale;  // softmax scale x log2(e)
+  int2* meta;     // [unit]: its first part and how many there are (1: the output is written already)
+  float2* stats;  // [part][row]: reference and softmax sum
+  float* part;    // [part][row][128]
+  int units, nq, rows, max_blocks, max_sel, max_len;
+  int split;      // 0: one CTA per unit
+  float scale;    // softmax scale x log2(e)
 };
 
 // D (16 x 8, f32) += A (16 x 16, row) . B (16 x 8, col), f16 inputs.
@@ -420,11 +429,16 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const float (&al
   }
 }
 
-// Stores output element x of a unit's row: zero where no token was seen.
-__device__ __forceinline__ uint16_t finish(float o, float l) {
-  const __nv_bfloat16 v = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-  return __bfloat16_as_ushort(v);
+// Four dims of an output row: zeros where no token was seen.
+__device__ __forceinline__ void store_out(uint16_t* out, const float4& o, float l) {
+  uint2 v = make_uint2(0, 0);
+  if (l != 0.f) v = make_uint2(pack_bf16x2(o.x / l, o.y / l), pack_bf16x2(o.z / l, o.w / l));
+  *reinterpret_cast<uint2*>(out) = v;
 }
+
+// The blocks that CTA i of n takes of `total`: [first(i), first(i + 1)), and the CTA that takes block b.
+__device__ __forceinline__ long long cta_first(long long total, int i, int n) { return total * i / n; }
+__device__ __forceinline__ int cta_of(long long total, long long b, int n) { return (int)(((b + 1) * n - 1) / total); }
 
 template <int NT>
 __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kernel(const __grid_constant__ QuantArgs a) {
@@ -434,8 +448,8 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
   __shared__ int tokens[kQaWarps][kQaStages];
   __shared__ int2 list[kQaList];  // (row of the store, tokens of the context from the block on)
   __shared__ float wr[kQaWarps][8 * NT], wl[kQaWarps][8 * NT];
+  __shared__ int scan[32], found[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int u = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
   if (lane == 0) {
 #pragma unroll
     for (int st = 0; st < kQaStages; ++st) mbar_init(&bars[warp][st], 1);
@@ -444,216 +458,312 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
   __syncwarp();
   pdl_wait();
   pdl_launch_dependents();
-  const int len0 = a.lens[u];
-  const int len = a.sel ? max(len0, 0) : min(max(len0, 0), a.max_len);
-  if (len != len0 && threadIdx.x == 0 && chunk == 0) atomicOr(a.err, kErrBounds);
 
-  QueryTile Q;
-  uint4* qs = reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(smem) + quant_ring_bytes(NT));
-  RowTile A[NT];
-  float alpha[NT][2];
-  uint32_t sums[NT];
-  auto load_queries = [&]() {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      load_query(Q, alpha[nt], a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale);
-      sums[nt] = Q.sums;
-      if (NT > 1 && warp == nt % kQaWarps) {
-#pragma unroll
-        for (int gr = 0; gr < 4; ++gr)
-          qs[(4 * nt + gr) * 32 + lane] = make_uint4(Q.b[2 * gr][0], Q.b[2 * gr][1], Q.b[2 * gr + 1][0], Q.b[2 * gr + 1][1]);
-      }
-      A[nt].r[0] = A[nt].r[1] = kNoRef;
-#pragma unroll
-      for (int mt = 0; mt < 8; ++mt) A[nt].o[mt][0] = A[nt].o[mt][1] = A[nt].o[mt][2] = A[nt].o[mt][3] = 0.f;
-      A[nt].c[0] = A[nt].c[1] = A[nt].c[2] = A[nt].c[3] = 0.f;
-    }
-    if (NT > 1) __syncthreads();
+  auto length = [&](int u) { return a.sel ? max(a.lens[u], 0) : min(max(a.lens[u], 0), a.max_len); };
+  // blocks of a unit's work; an empty unit counts as one, so that somebody writes its zeros
+  auto blocks_of = [&](int u) { return a.sel ? a.max_sel : max((length(u) + kBlock - 1) / kBlock, 1); };
+
+  // The units' blocks in one line, cut into one piece per CTA: this CTA's are `todo` blocks from block `at` of
+  // unit u on, and unit u's begin at `begin` of `total`.
+  int u = blockIdx.x, at = 0, pieces = gridDim.x;
+  long long todo = 1, total = 1, begin = 0;
+  auto cut = [&]() {  // two blocks a piece at least (a stage per warp); further CTAs have nothing to do
+    pieces = (int)min((long long)gridDim.x, (total + 1) / 2);
+    const long long lo = blockIdx.x < pieces ? cta_first(total, blockIdx.x, pieces) : total;
+    todo = blockIdx.x < pieces ? cta_first(total, blockIdx.x + 1, pieces) - lo : 0;
+    return lo;
   };
+  if (a.split) {
+    if (a.sel) {
+      total = (long long)a.units * a.max_sel;
+      begin = cut();
+      u = (int)(begin / a.max_sel);
+      at = (int)(begin % a.max_sel);
+    } else {
+      const int per = (a.units + kQaThreads - 1) / kQaThreads, u0 = threadIdx.x * per, u1 = min(u0 + per, a.units);
+      int mine = 0, sum;
+      for (int i = u0; i < u1; ++i) mine += blocks_of(i);
+      int before = block_scan_excl(mine, scan, &sum);
+      total = sum;
+      const long long lo = begin = cut();
+      for (int i = u0; i < u1; ++i) {  // the one thread whose units hold block lo
+        const int n = blocks_of(i);
+        if (before <= lo && lo < before + n) {
+          found[0] = i;
+          found[1] = before;
+        }
+        before += n;
+      }
+      __syncthreads();
+      if (todo == 0) return;
+      u = found[0];
+      at = (int)lo - found[1];
+    }
+    begin -= at;
+  }
 
-  // The chunk's blocks, looked up kQaList at a time (a dense call needs no list).  Warp w takes half w % 2 of the
-  // blocks w / 2, w / 2 + 2, ...
-  const int first = chunk * a.chunk_blocks;
-  const int end = min(first + a.chunk_blocks, a.sel ? a.max_sel : (len + kBlock - 1) / kBlock);
-  const int batch = a.sel ? kQaList : a.chunk_blocks, half = (warp & 1) * kStageTokens;
-  const uint8_t* base = a.store + (size_t)u * a.max_blocks * kQuantBlockBytes + (warp & 1) * kStageBytes4;
+  uint4* qs = reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(smem) + quant_ring_bytes(NT));
   unsigned char* ring = reinterpret_cast<unsigned char*>(smem) + warp * kQaStages * kStageBytes4;
   int issued = 0, done = 0;
   bool late = false;
-  for (int b0 = first; b0 < end || b0 == first; b0 += batch) {
-    const int n = min(batch, end - b0);
-    if (a.sel) {
-      if (b0 > first) __syncthreads();  // the list before is used up
-      for (int j = threadIdx.x; j < n; j += kQaThreads) {
-        const size_t at = (size_t)u * a.max_sel + b0 + j;
-        const int block = a.sel[at];
-        const int slot = block < 0 ? 0 : a.sel_slot ? a.sel_slot[at] : block;
-        const bool held = slot >= 0 && slot < a.max_blocks;
-        if (!held) atomicOr(a.err, kErrBounds);
-        const long long left = block < 0 || !held ? 0 : (long long)len - (long long)block * kBlock;
-        list[j] = make_int2(slot, (int)min(max(left, 0ll), 2ll * kBlock));  // 128 or more: every row sees the whole block
+  for (; todo > 0; ++u, at = 0) {
+    const int len = length(u), whole = blocks_of(u);
+    const int first = at, end = a.split ? (int)min((long long)whole, at + todo) : whole;
+    todo -= end - first;
+    if (threadIdx.x == 0 && first == 0 && len != a.lens[u]) atomicOr(a.err, kErrBounds);
+    QueryTile Q;
+    RowTile A[NT];
+    float alpha[NT][2];
+    uint32_t sums[NT];
+    auto load_queries = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        load_query(Q, alpha[nt], a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale);
+        sums[nt] = Q.sums;
+        if (NT > 1 && warp == nt % kQaWarps) {
+#pragma unroll
+          for (int gr = 0; gr < 4; ++gr)
+            qs[(4 * nt + gr) * 32 + lane] = make_uint4(Q.b[2 * gr][0], Q.b[2 * gr][1], Q.b[2 * gr + 1][0], Q.b[2 * gr + 1][1]);
+        }
+        A[nt].r[0] = A[nt].r[1] = kNoRef;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) A[nt].o[mt][0] = A[nt].o[mt][1] = A[nt].o[mt][2] = A[nt].o[mt][3] = 0.f;
+        A[nt].c[0] = A[nt].c[1] = A[nt].c[2] = A[nt].c[3] = 0.f;
       }
+      if (NT > 1) __syncthreads();
+    };
+
+    // The blocks, listed ones looked up kQaList at a time.  Warp w takes half w % 2 of the blocks w / 2, w / 2 + 2, ...
+    const int batch = a.sel ? kQaList : end - first, half = (warp & 1) * kStageTokens;
+    const uint8_t* base = a.store + (size_t)u * a.max_blocks * kQuantBlockBytes + (warp & 1) * kStageBytes4;
+    for (int b0 = first; b0 < end; b0 += batch) {
+      const int n = min(batch, end - b0);
+      if (a.sel) {
+        if (b0 > first) __syncthreads();  // the list before is used up
+        for (int j = threadIdx.x; j < n; j += kQaThreads) {
+          const size_t i = (size_t)u * a.max_sel + b0 + j;
+          const int block = a.sel[i];
+          const int slot = block < 0 ? 0 : a.sel_slot ? a.sel_slot[i] : block;
+          const bool held = slot >= 0 && slot < a.max_blocks;
+          if (!held) atomicOr(a.err, kErrBounds);
+          const long long left = block < 0 || !held ? 0 : (long long)len - (long long)block * kBlock;
+          list[j] = make_int2(slot, (int)min(max(left, 0ll), 2ll * kBlock));  // 128 or more: every row sees the whole block
+        }
+        __syncthreads();
+      }
+      int j = warp >> 1;
+      auto issue = [&]() {  // the next half block into the stage whose turn it is; false when there is none
+        int2 e = make_int2(0, 0);
+        for (; j < n; j += kQaWarps / 2) {
+          e = a.sel ? list[j] : make_int2(b0 + j, min(len - (b0 + j) * kBlock, 2 * kBlock));
+          if (e.y > half) break;
+        }
+        if (j >= n || late) return false;
+        j += kQaWarps / 2;
+        if (lane == 0) {
+          const int st = issued % kQaStages;
+          tokens[warp][st] = e.y - half;
+          mbar_arrive_expect_tx(&bars[warp][st], kStageBytes4);
+          bulk_copy_g2s(smem_u32(ring + st * kStageBytes4), base + (size_t)e.x * kQuantBlockBytes, kStageBytes4, &bars[warp][st]);
+        }
+        return true;
+      };
+#pragma unroll
+      for (int i = 0; i < kQaStages; ++i)
+        if (issue()) ++issued;
+      if (b0 == first) load_queries();  // while the first stages arrive
+      __syncwarp();
+      for (; done < issued; ++done) {
+        const int st = done % kQaStages;
+        late |= !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][st], done / kQaStages & 1, kWaitCycles));
+        if (late) continue;  // let what is in flight land, and start no more
+        process_stage<NT>(A, alpha, Q, qs, sums, ring + st * kStageBytes4, tokens[warp][st], a.nq, a.rows, lane);
+        __syncwarp();  // the stage is read
+        if (issue()) ++issued;
+      }
+    }
+    if (late) {  // a wait gave up: poison the outputs
+      if (lane == 0) atomicOr(a.err, kErrTimeout);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) A[nt].c[0] = A[nt].c[1] = __int_as_float(0x7fc00000);
+    }
+    __syncthreads();  // the rings become the warps' partials
+
+    // the warp's partial: O of rows 2t, 2t + 1, dims 32 gr + 4 g .. + 3
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const RowTile& S = A[nt];
+      float* w = smem + (warp * 8 * NT + 8 * nt + 2 * t) * kQaRowStride;
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float m = __shfl_sync(0xffffffffu, S.c[i], 4 * gr + t);
+          *reinterpret_cast<float4*>(w + i * kQaRowStride + 32 * gr + 4 * g) =
+              make_float4(fmaf(S.o[2 * gr][i], 0x1p24f, m), fmaf(S.o[2 * gr][i + 2], 0x1p20f, m),
+                          fmaf(S.o[2 * gr + 1][i], 0x1p24f, m), fmaf(S.o[2 * gr + 1][i + 2], 0x1p20f, m));
+        }
+      }
+      if (g == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          wr[warp][8 * nt + 2 * t + i] = fmaxf(S.r[i] * alpha[nt][i], kNoRef);  // from here on in base-2 logits
+          wl[warp][8 * nt + 2 * t + i] = S.c[i];
+        }
+      }
+    }
+    __syncthreads();
+    const bool complete = first == 0 && end == whole;
+    const int part = blockIdx.x + u;  // a piece's end and a unit's each move on by one: no two segments share a part
+    for (int idx = threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += kQaThreads) {
+      const int row = idx >> 5, x = 4 * (idx & 31);
+      float R = wr[0][row];
+#pragma unroll
+      for (int w = 1; w < kQaWarps; ++w) R = fmaxf(R, wr[w][row]);
+      float L = 0.f;
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kQaWarps; ++w) {
+        const float f = ex2(wr[w][row] - R);
+        const float4 o = *reinterpret_cast<const float4*>(smem + (w * 8 * NT + row) * kQaRowStride + x);
+        L = fmaf(wl[w][row], f, L);
+        O.x = fmaf(o.x, f, O.x);
+        O.y = fmaf(o.y, f, O.y);
+        O.z = fmaf(o.z, f, O.z);
+        O.w = fmaf(o.w, f, O.w);
+      }
+      if (complete) {
+        store_out(a.out + ((size_t)u * a.rows + row) * kHeadDim + x, O, L);
+      } else {
+        const size_t i = (size_t)part * a.rows + row;
+        if (x == 0) a.stats[i] = make_float2(R, L);
+        *reinterpret_cast<float4*>(a.part + i * kHeadDim + x) = O;
+      }
+    }
+    if (a.split && first == 0 && threadIdx.x == 0)
+      a.meta[u] = make_int2(part, cta_of(total, begin + whole - 1, pieces) - blockIdx.x + 1);
+    begin += whole;
+    if (todo > 0) {
+      fence_proxy_async_smem();  // the next segment's copies come after these reads and writes
       __syncthreads();
     }
-    int j = warp >> 1;
-    auto issue = [&]() {  // the next half block into the stage whose turn it is; false when there is none
-      int2 e = make_int2(0, 0);
-      for (; j < n; j += kQaWarps / 2) {
-        e = a.sel ? list[j] : make_int2(b0 + j, min(len - (b0 + j) * kBlock, 2 * kBlock));
-        if (e.y > half) break;
-      }
-      if (j >= n || late) return false;
-      j += kQaWarps / 2;
-      if (lane == 0) {
-        const int st = issued % kQaStages;
-        tokens[warp][st] = e.y - half;
-        mbar_arrive_expect_tx(&bars[warp][st], kStageBytes4);
-        bulk_copy_g2s(smem_u32(ring + st * kStageBytes4), base + (size_t)e.x * kQuantBlockBytes, kStageBytes4, &bars[warp][st]);
-      }
-      return true;
-    };
-#pragma unroll
-    for (int i = 0; i < kQaStages; ++i)
-      if (issue()) ++issued;
-    if (b0 == first) load_queries();  // while the first stages arrive
-    __syncwarp();
-    for (; done < issued; ++done) {
-      const int st = done % kQaStages;
-      late |= !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][st], done / kQaStages & 1, kWaitCycles));
-      if (late) continue;  // let what is in flight land, and start no more
-      process_stage<NT>(A, alpha, Q, qs, sums, ring + st * kStageBytes4, tokens[warp][st], a.nq, a.rows, lane);
-      __syncwarp();  // the stage is read
-      if (issue()) ++issued;
-    }
-  }
-  if (late) {  // a wait gave up: poison the outputs
-    if (lane == 0) atomicOr(a.err, kErrTimeout);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) A[nt].c[0] = A[nt].c[1] = __int_as_float(0x7fc00000);
-  }
-  __syncthreads();  // the rings become the warps' partials
-
-  // the warp's partial: O of rows 2t, 2t + 1, dims 32 gr + 4 g .. + 3
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const RowTile& S = A[nt];
-    float* w = smem + (warp * 8 * NT + 8 * nt + 2 * t) * kQaRowStride;
-#pragma unroll
-    for (int gr = 0; gr < 4; ++gr) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float m = __shfl_sync(0xffffffffu, S.c[i], 4 * gr + t);
-        *reinterpret_cast<float4*>(w + i * kQaRowStride + 32 * gr + 4 * g) =
-            make_float4(fmaf(S.o[2 * gr][i], 0x1p24f, m), fmaf(S.o[2 * gr][i + 2], 0x1p20f, m),
-                        fmaf(S.o[2 * gr + 1][i], 0x1p24f, m), fmaf(S.o[2 * gr + 1][i + 2], 0x1p20f, m));
-      }
-    }
-    if (g == 4) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        wr[warp][8 * nt + 2 * t + i] = fmaxf(S.r[i] * alpha[nt][i], kNoRef);  // from here on in base-2 logits
-        wl[warp][8 * nt + 2 * t + i] = S.c[i];
-      }
-    }
-  }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += kQaThreads) {
-    const int row = idx >> 5, x = 4 * (idx & 31);
-    float R = wr[0][row];
-#pragma unroll
-    for (int w = 1; w < kQaWarps; ++w) R = fmaxf(R, wr[w][row]);
-    float L = 0.f;
-    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kQaWarps; ++w) {
-      const float f = ex2(wr[w][row] - R);
-      const float4 o = *reinterpret_cast<const float4*>(smem + (w * 8 * NT + row) * kQaRowStride + x);
-      L = fmaf(wl[w][row], f, L);
-      O.x = fmaf(o.x, f, O.x);
-      O.y = fmaf(o.y, f, O.y);
-      O.z = fmaf(o.z, f, O.z);
-      O.w = fmaf(o.w, f, O.w);
-    }
-    if (a.chunks == 1) {
-      uint2 v;
-      v.x = finish(O.x, L) | (uint32_t)finish(O.y, L) << 16;
-      v.y = finish(O.z, L) | (uint32_t)finish(O.w, L) << 16;
-      *reinterpret_cast<uint2*>(a.out + ((size_t)u * a.rows + row) * kHeadDim + x) = v;
-    } else {
-      float* part = a.part + ((size_t)blockIdx.x * a.rows + row) * kPartStride;
-      if (x == 0) {
-        part[0] = R;
-        part[1] = L;
-      }
-      *reinterpret_cast<float2*>(part + 2 + x) = make_float2(O.x, O.y);
-      *reinterpret_cast<float2*>(part + 4 + x) = make_float2(O.z, O.w);
-    }
   }
 }
 
-// Merges a unit row's chunks: one CTA of 128 threads per (unit, row), thread x its dim x.
-__global__ void __launch_bounds__(kHeadDim) quant_merge_kernel(const float* __restrict__ part, uint16_t* __restrict__ out,
-                                                               int rows, int chunks) {
+// Merges the parts of a unit's row, where there are several: one CTA of four warps per (unit, row), each warp
+// every fourth part, each lane four dims.
+__global__ void __launch_bounds__(kQaThreads) quant_merge_kernel(const __grid_constant__ QuantArgs a) {
+  __shared__ float4 so[kQaWarps][32];
+  __shared__ float2 ss[kQaWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int u = blockIdx.x / a.rows, row = blockIdx.x % a.rows;
   pdl_wait();
   pdl_launch_dependents();
-  const int u = blockIdx.x / rows, row = blockIdx.x % rows, x = threadIdx.x;
-  const float* p = part + ((size_t)u * chunks * rows + row) * kPartStride;
-  const size_t step = (size_t)rows * kPartStride;
-  float R = kNoRef;
-  for (int c = 0; c < chunks; ++c) R = fmaxf(R, p[c * step]);
-  float L = 0.f, O = 0.f;
-  for (int c = 0; c < chunks; ++c) {
-    const float f = ex2(p[c * step] - R);
-    L = fmaf(p[c * step + 1], f, L);
-    O = fmaf(p[c * step + 2 + x], f, O);
+  const int2 m = a.meta[u];
+  if (m.y == 1) return;
+  float R = kNoRef, L = 0.f;
+  float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float r, float l, const float4& o) {
+    const float top = fmaxf(R, r), f = ex2(R - top), h = ex2(r - top);
+    R = top;
+    L = L * f + l * h;
+    O.x = O.x * f + o.x * h;
+    O.y = O.y * f + o.y * h;
+    O.z = O.z * f + o.z * h;
+    O.w = O.w * f + o.w * h;
+  };
+#pragma unroll 4
+  for (int c = warp; c < m.y; c += kQaWarps) {
+    const size_t i = (size_t)(m.x + c) * a.rows + row;
+    const float2 s = a.stats[i];
+    add(s.x, s.y, *reinterpret_cast<const float4*>(a.part + i * kHeadDim + 4 * lane));
   }
-  out[((size_t)u * rows + row) * kHeadDim + x] = finish(O, L);
+  so[warp][lane] = O;
+  if (lane == 0) ss[warp] = make_float2(R, L);
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
+    for (int w = 1; w < kQaWarps; ++w) add(ss[w].x, ss[w].y, so[w][lane]);
+    store_out(a.out + ((size_t)u * a.rows + row) * kHeadDim + 4 * lane, O, L);
+  }
 }
 
-// How a call is split: about four CTAs per SM.
-struct QuantPlan {
-  int chunk_blocks, chunks;
+// What the launches need of a device, looked up once (a call costs more in look-ups than in launching otherwise).
+struct QuantDevice {
+  int sms, ctas[3];  // resident CTAs of the kernel for 1, 2, 4 row tiles on the whole device
 };
-static QuantPlan quant_plan(int units, int blocks, int sms) {
-  const long long most = 1 + 16ll * sms / units;  // units x chunks <= units + 16 SMs
-  const long long want = std::min<long long>(most, std::max<long long>(1, (4ll * sms + units - 1) / units));
-  const int chunk = (int)((blocks + want - 1) / want);
-  return {chunk, (blocks + chunk - 1) / chunk};
+static std::mutex g_quant_mutex;
+static QuantDevice g_quant_device[64] = {};
+
+template <int NT>
+static cudaError_t set_up_quant_attend(int sms, int* ctas) {
+  const int smem = quant_smem_bytes(NT);
+  cudaError_t e = cudaFuncSetAttribute(quant_attend_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, quant_attend_kernel<NT>, kQaThreads, smem);
+  *ctas *= sms;
+  return e;
 }
 
-static int quant_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+static bool quant_device(QuantDevice* out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
     (void)cudaGetLastError();
-    return 0;
+    return false;
   }
-  return sms;
+  std::lock_guard<std::mutex> lock(g_quant_mutex);
+  QuantDevice& d = g_quant_device[dev];
+  if (!d.sms) {
+    QuantDevice n = {};
+    if (cudaDeviceGetAttribute(&n.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        set_up_quant_attend<1>(n.sms, &n.ctas[0]) != cudaSuccess || set_up_quant_attend<2>(n.sms, &n.ctas[1]) != cudaSuccess ||
+        set_up_quant_attend<4>(n.sms, &n.ctas[2]) != cudaSuccess || n.sms < 1 || n.ctas[0] < 1 || n.ctas[1] < 1 || n.ctas[2] < 1) {
+      (void)cudaGetLastError();
+      return false;
+    }
+    d = n;
+  }
+  *out = d;
+  return true;
+}
+
+// How many CTAs a call takes.  Units are split into equal pieces over one wave of resident CTAs, of two blocks
+// (a stage per warp) at least; with so many units that whole ones balance by themselves, one CTA each.
+struct QuantPlan {
+  int ctas;
+  bool split;
+  size_t bytes;  // of the scratch
+};
+static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks) {
+  const int wave = std::min(d.ctas[rows <= 8 ? 0 : rows <= 16 ? 1 : 2], 8 * d.sms);
+  if (units > kQaSplitUnits) return {units, false, kQaErrBytes};
+  const long long pieces = ((long long)units * blocks + 1) / 2;
+  const int ctas = (int)std::min<long long>(wave, pieces);
+  const size_t parts = (size_t)ctas + units;
+  return {ctas, true, kQaErrBytes + (size_t)units * sizeof(int2) + parts * rows * (kHeadDim + 2) * sizeof(float) + 16};
 }
 
 template <int NT>
-static cudaError_t launch_quant_attend(const QuantArgs& a, int units, cudaStream_t st) {
-  const int smem = quant_ring_bytes(NT) + (NT > 1 ? NT * 4 * 32 * (int)sizeof(uint4) : 0);
-  cudaError_t e = cudaFuncSetAttribute(quant_attend_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return launch_ex(quant_attend_kernel<NT>, dim3((unsigned)(units * a.chunks)), dim3(kQaThreads), smem, st, true, 0, a);
+static cudaError_t launch_quant_attend(const QuantArgs& a, int ctas, cudaStream_t st) {
+  return launch_ex(quant_attend_kernel<NT>, dim3((unsigned)ctas), dim3(kQaThreads), quant_smem_bytes(NT), st, true, 0, a);
 }
 
-static nosa_status quant_attend(QuantArgs& a, int units, int blocks, void* scratch, size_t scratch_bytes, cudaStream_t st) {
-  const int sms = quant_sms();
-  if (sms <= 0) return NOSA_ERR_CUDA;
-  const QuantPlan plan = quant_plan(units, blocks, sms);
-  if (scratch_bytes < nosa_quant_scratch_bytes(units, a.rows, blocks)) return NOSA_ERR_CAPACITY;
-  a.chunk_blocks = plan.chunk_blocks;
-  a.chunks = plan.chunks;
-  a.err = reinterpret_cast<int*>(scratch);
-  a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(scratch) + kQaErrBytes);
-  cudaError_t e = a.rows <= 8    ? launch_quant_attend<1>(a, units, st)
-                  : a.rows <= 16 ? launch_quant_attend<2>(a, units, st)
-                                 : launch_quant_attend<4>(a, units, st);
-  if (e == cudaSuccess && plan.chunks > 1)
-    e = launch_ex(quant_merge_kernel, dim3((unsigned)(units * a.rows)), dim3(kHeadDim), 0, st, true, 0,
-                  (const float*)a.part, a.out, a.rows, plan.chunks);
+static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t scratch_bytes, cudaStream_t st) {
+  QuantDevice d;
+  if (!quant_device(&d)) return NOSA_ERR_CUDA;
+  const QuantPlan plan = quant_plan(d, a.units, a.rows, blocks);
+  if (scratch_bytes < plan.bytes) return NOSA_ERR_CAPACITY;
+  const size_t parts = (size_t)plan.ctas + a.units;
+  unsigned char* p = static_cast<unsigned char*>(scratch);
+  a.split = plan.split;
+  a.err = reinterpret_cast<int*>(p);
+  a.part = reinterpret_cast<float*>(p + kQaErrBytes);
+  a.stats = reinterpret_cast<float2*>(a.part + parts * a.rows * kHeadDim);
+  a.meta = reinterpret_cast<int2*>(a.stats + parts * a.rows);
+  cudaError_t e = a.rows <= 8    ? launch_quant_attend<1>(a, plan.ctas, st)
+                  : a.rows <= 16 ? launch_quant_attend<2>(a, plan.ctas, st)
+                                 : launch_quant_attend<4>(a, plan.ctas, st);
+  if (e == cudaSuccess && plan.split)
+    e = launch_ex(quant_merge_kernel, dim3((unsigned)(a.units * a.rows)), dim3(kQaThreads), 0, st, true, 0, a);
   if (e == cudaSuccess) return NOSA_OK;
   (void)cudaGetLastError();
   return NOSA_ERR_CUDA;
@@ -676,9 +786,10 @@ static bool bad_args(const void* q, const void* store, const void* lens, const v
 using namespace nosa;
 
 extern "C" size_t nosa_quant_scratch_bytes(int units, int rows, int blocks) {
-  const int sms = quant_sms();
-  if (sms <= 0 || units < 1 || units > (1 << 20) || rows < 1 || rows > kQaMaxRows || blocks < 1 || blocks > 16384) return 0;
-  return kQaErrBytes + (size_t)units * quant_plan(units, blocks, sms).chunks * rows * kPartStride * sizeof(float);
+  QuantDevice d;
+  if (units < 1 || units > (1 << 20) || rows < 1 || rows > kQaMaxRows || blocks < 1 || blocks > 16384 || !quant_device(&d))
+    return 0;
+  return quant_plan(d, units, rows, blocks).bytes;
 }
 
 extern "C" nosa_status nosa_quant_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group,
@@ -692,13 +803,13 @@ extern "C" nosa_status nosa_quant_dense_attend(const uint16_t* q, const uint8_t*
   a.store = store;
   a.lens = lens;
   a.out = out;
-  a.group = group;
+  a.units = units;
   a.nq = n_queries;
   a.rows = group * n_queries;
   a.max_blocks = max_blocks;
   a.max_len = max_len;
   a.scale = (softmax_scale > 0.f ? softmax_scale : 1.f / sqrtf((float)kHeadDim)) * 1.4426950408889634f;
-  return quant_attend(a, units, (max_len + kBlock - 1) / kBlock, scratch, scratch_bytes, static_cast<cudaStream_t>(stream));
+  return quant_attend(a, (max_len + kBlock - 1) / kBlock, scratch, scratch_bytes, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" nosa_status nosa_quant_attend(const uint16_t* q, const uint8_t* store, const int32_t* sel,
@@ -715,11 +826,11 @@ extern "C" nosa_status nosa_quant_attend(const uint16_t* q, const uint8_t* store
   a.sel_slot = sel_slot;
   a.lens = lens;
   a.out = out;
-  a.group = group;
+  a.units = units;
   a.nq = n_queries;
   a.rows = group * n_queries;
   a.max_blocks = max_blocks;
   a.max_sel = max_sel;
   a.scale = (softmax_scale > 0.f ? softmax_scale : 1.f / sqrtf((float)kHeadDim)) * 1.4426950408889634f;
-  return quant_attend(a, units, max_sel, scratch, scratch_bytes, static_cast<cudaStream_t>(stream));
+  return quant_attend(a, max_sel, scratch, scratch_bytes, static_cast<cudaStream_t>(stream));
 }

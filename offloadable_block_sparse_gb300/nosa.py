@@ -148,10 +148,14 @@ def _string(status: int) -> str:
 def _ptr(x):
     if x is None:
         return None
+    if type(x) is int:
+        return x
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if hasattr(x, "ctypes"):
         return x.ctypes.data
     raise TypeError(f"cannot pass {type(x)} as a pointer")
