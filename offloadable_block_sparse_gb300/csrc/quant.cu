@@ -11,29 +11,112 @@ namespace nosa {
 
 constexpr int kQuantWarps = 4;
 
-// The range of a group spread over lanes that differ in the lane-index bits lo_bit .. hi_bit:
-// packed (max x, max -x), so that one shuffle and one packed maximum serve both ends.  The maximum
-// hands on NaN.
+// A group's range is kept as one register of two bf16, (max x, max -x), so that one shuffle and one packed
+// maximum serve both ends.  The maximum hands on NaN.
 __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t range_of(uint32_t hi, uint32_t lo) {  // the lane's maxima and minima, two each
+  lo ^= 0x80008000u;
+  return max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
+}
+// One step of a reduction that also deals its results out: of two values the lane keeps one and gives the other
+// to its partner.
+__device__ __forceinline__ uint32_t deal(uint32_t v0, uint32_t v1, bool keep1, int partner) {
+  return max2_nan(keep1 ? v1 : v0, __shfl_xor_sync(0xffffffffu, keep1 ? v0 : v1, partner));
+}
+__device__ __forceinline__ GroupScale range_scale(uint32_t range) {
+  return group_scale(-bf16_to_float((uint16_t)(range >> 16)), bf16_to_float((uint16_t)range));
+}
 
 // Code of x in a group: clamp(rint((x - m) / s), 0, 15), exactly as the IEEE quotient rounds.  r is
 // 1 / s rounded, so rint((x - m) r) is off by at most one, and only next to a border between two
 // codes; the remainder e = (x - m) - n s is exact there (n s has at most 16 bits, and the two terms are
-// within a factor of two of each other, or n = 0) and says which side x is on.  A division per value
-// instead would cost more than the value's share of the memory time.
-__device__ __forceinline__ uint32_t quant_code(float x, float m, float s, float r) {
+// within a factor of two of each other, or n = 0) and says which side x is on.
+__device__ __forceinline__ uint32_t exact_code(float x, float m, float s) {
   const float d = x - m;
-  float n = rintf(d * r);
+  float n = rintf(d * __frcp_rn(s));
   const float e = 2.f * fmaf(-n, s, d);
-  if (fabsf(e) >= s) {  // rare: a border
-    if (fabsf(e) > s || (((int)n) & 1)) n += copysignf(1.f, e);
-  }
+  if (fabsf(e) > s || (fabsf(e) == s && (((int)n) & 1))) n += copysignf(1.f, e);
   n = fminf(fmaxf(n, 0.f), 15.f);
   return s > 0.f ? (uint32_t)n : 0u;  // s = 0 or NaN: code 0
+}
+__device__ __noinline__ uint32_t exact_codes(uint32_t x0, uint32_t x1, float s, float m) {
+  uint32_t w = 0;
+  for (int e = 0; e < 4; ++e)
+    w |= exact_code(bf16_to_float((uint16_t)((e < 2 ? x0 : x1) >> (16 * (e & 1)))), m, s) << (4 * e);
+  return w;
+}
+
+// Two float32 in one 64-bit register, the operands of the packed arithmetic.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A group's scale as the code loop wants it.
+struct CodeScale {
+  float s, m;
+  uint64_t r2, negm2;  // 1 / s (to 2^-23) and -m, twice
+  bool plain;          // s a normal f16: no code can leave 0 .. 15 (s is within 2^-11 of the range's fifteenth)
+};
+__device__ __forceinline__ CodeScale code_scale(uint32_t s_bits, uint32_t m_bits) {
+  CodeScale c;
+  c.s = half_bits_to_float(s_bits);
+  c.m = half_bits_to_float(m_bits);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(c.s));
+  c.r2 = pair(r, r);
+  c.negm2 = pair(-c.m, -c.m);
+  c.plain = s_bits - 0x0400u < 0x7c00u - 0x0400u;
+  return c;
+}
+
+// Codes of four bf16 values, 4 bits each.  t = (x - m) r is within 2^-17 of the quotient, so its rounding is
+// the quotient's unless t is that near to a border: then, and for an odd scale, the codes are taken exactly
+// (a division per value instead would cost more than the value's share of the memory time).  Adding
+// 1.5 x 2^23 rounds t to the integer that then stands in the sum's low bits.
+__device__ __forceinline__ uint32_t codes4(uint32_t x0, uint32_t x1, const CodeScale& c) {
+  const uint64_t magic = pair(12582912.f, 12582912.f), negmagic = pair(-12582912.f, -12582912.f);
+  uint32_t w = 0xC0C00000u;  // what the four constants' bits 0x4B400000 << 4e add up to, negated
+  float off = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = i ? x1 : x0;
+    const uint64_t t = mul2(add2(pair(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), c.negm2), c.r2);
+    const uint64_t u = add2(t, magic);
+    const uint64_t n = add2(u, negmagic);
+    float n0, n1, u0, u1, f0, f1;
+    unpair(n, n0, n1);
+    unpair(add2(t, pair(-n0, -n1)), f0, f1);
+    unpair(u, u0, u1);
+    off = fmaxf(fmaxf(off, fabsf(f0)), fabsf(f1));
+    w += __float_as_uint(u0) << (8 * i);
+    w += __float_as_uint(u1) << (8 * i + 4);
+  }
+  if (!c.plain || off > 0.5f - 0x1p-16f) w = exact_codes(x0, x1, c.s, c.m);
+  return w;
 }
 
 __global__ void __launch_bounds__(kQuantWarps * 32)
@@ -77,73 +160,92 @@ __global__ void __launch_bounds__(kQuantWarps * 32)
     }
   }
 
-  // K: token g + 8 h, dims 32 gr + 8 t + e in word gr
+  // halves of the tile with a new token
+  const bool any[2] = {first < p0 + c && first + 8 > p0, first + 8 < p0 + c && first + 16 > p0};
+
+  // Ranges.  K: token g + 8 h, group gr, over the lanes t; dealt so that lane t ends up with group t.  V: token
+  // 8 h + 2 t + par, group gr, over the lanes g; lane g ends up with half g / 4, group g % 4, both tokens.
+  uint32_t kr[2], vr[2];
+  {
+    uint32_t v[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr) {
+        const uint4& x = kx[h][gr];
+        v[h][gr] = range_of(max2_nan(max2_nan(x.x, x.y), max2_nan(x.z, x.w)), min2_nan(min2_nan(x.x, x.y), min2_nan(x.z, x.w)));
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      kr[h] = deal(deal(v[h][0], v[h][2], t & 2, 2), deal(v[h][1], v[h][3], t & 2, 2), t & 1, 1);
+  }
+#pragma unroll
+  for (int par = 0; par < 2; ++par) {
+    uint32_t v[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr)
+        v[h][gr] = range_of(max2_nan(vx[h][par][gr].x, vx[h][par][gr].y), min2_nan(vx[h][par][gr].x, vx[h][par][gr].y));
+    uint32_t w[4];
+#pragma unroll
+    for (int gr = 0; gr < 4; ++gr) w[gr] = deal(v[0][gr], v[1][gr], g & 4, 16);
+    vr[par] = deal(deal(w[0], w[2], g & 2, 8), deal(w[1], w[3], g & 2, 8), g & 1, 4);
+  }
+
+  // K: dims 32 gr + 8 t + e of token g + 8 h in word gr
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t w[4], sc[4], mn[4];
+    if (!any[h]) continue;
+    const GroupScale q = range_scale(kr[h]);
+    uint32_t w[4], sm[4];
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
-      const uint32_t x[4] = {kx[h][gr].x, kx[h][gr].y, kx[h][gr].z, kx[h][gr].w};
-      uint32_t hi = max2_nan(max2_nan(x[0], x[1]), max2_nan(x[2], x[3]));
-      uint32_t lo = max2_nan(max2_nan(x[0] ^ 0x80008000u, x[1] ^ 0x80008000u),
-                             max2_nan(x[2] ^ 0x80008000u, x[3] ^ 0x80008000u));
-      // fold the two halves: (max x, max -x) in one register
-      uint32_t both = max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
-      both = max2_nan(both, __shfl_xor_sync(0xffffffffu, both, 1));
-      both = max2_nan(both, __shfl_xor_sync(0xffffffffu, both, 2));
-      const GroupScale q = group_scale(-bf16_to_float((uint16_t)(both >> 16)), bf16_to_float((uint16_t)both));
-      sc[gr] = q.s;
-      mn[gr] = q.m;
-      const float s = half_bits_to_float(q.s), m = half_bits_to_float(q.m), r = __frcp_rn(s);
-      w[gr] = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        w[gr] |= quant_code(bf16_to_float((uint16_t)(x[e >> 1] >> (16 * (e & 1)))), m, s, r) << (4 * e);
+      sm[gr] = __shfl_sync(0xffffffffu, q.s | q.m << 16, (lane & ~3) | gr);
+      const CodeScale cs = code_scale(sm[gr] & 0xffffu, sm[gr] >> 16);
+      w[gr] = codes4(kx[h][gr].x, kx[h][gr].y, cs) | codes4(kx[h][gr].z, kx[h][gr].w, cs) << 16;
     }
     if (kin[h]) {
       *reinterpret_cast<uint4*>(dst + 64 * (g + 8 * h) + 16 * t) = make_uint4(w[0], w[1], w[2], w[3]);
       if (t == 0)
         *reinterpret_cast<uint4*>(dst + kTileKs + 16 * (g + 8 * h)) =
-            make_uint4(sc[0] | sc[1] << 16, sc[2] | sc[3] << 16, mn[0] | mn[1] << 16, mn[2] | mn[3] << 16);
+            make_uint4(__byte_perm(sm[0], sm[1], 0x5410), __byte_perm(sm[2], sm[3], 0x5410),
+                       __byte_perm(sm[0], sm[1], 0x7632), __byte_perm(sm[2], sm[3], 0x7632));
     }
   }
 
-  // V: tokens 8 h + 2 t + par, dims 32 gr + 4 g + e in word gr
+  // V: dims 32 gr + 4 g + e of token 8 h + 2 t + par in half `par` of word gr
+  const GroupScale q0 = range_scale(vr[0]), q1 = range_scale(vr[1]);
+  const uint32_t sp = q0.s | q1.s << 16, mp = q0.m | q1.m << 16;  // of half g / 4, group g % 4
+  {
+    uint8_t* meta = dst + kTileVs + 16 * (4 * (g >> 2) + t) + 4 * (g & 3);
+    const bool in0 = g & 4 ? vin[1][0] : vin[0][0], in1 = g & 4 ? vin[1][1] : vin[0][1];
+    if (in0 && in1) {
+      *reinterpret_cast<uint32_t*>(meta) = sp;
+      *reinterpret_cast<uint32_t*>(meta + kTileVm - kTileVs) = mp;
+    } else if (in0 || in1) {  // the pair's other token stays as it is
+      *reinterpret_cast<uint16_t*>(meta + 2 * in1) = (uint16_t)(sp >> (16 * in1));
+      *reinterpret_cast<uint16_t*>(meta + kTileVm - kTileVs + 2 * in1) = (uint16_t)(mp >> (16 * in1));
+    }
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t w[4] = {0, 0, 0, 0}, sc[4] = {0, 0, 0, 0}, mn[4] = {0, 0, 0, 0};
+    if (!any[h]) continue;
+    uint32_t w[4];
 #pragma unroll
-    for (int par = 0; par < 2; ++par)
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
-        const uint32_t x[2] = {vx[h][par][gr].x, vx[h][par][gr].y};
-        const uint32_t hi = max2_nan(x[0], x[1]), lo = max2_nan(x[0] ^ 0x80008000u, x[1] ^ 0x80008000u);
-        uint32_t both = max2_nan(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) both = max2_nan(both, __shfl_xor_sync(0xffffffffu, both, o));
-        const GroupScale q = group_scale(-bf16_to_float((uint16_t)(both >> 16)), bf16_to_float((uint16_t)both));
-        const float s = half_bits_to_float(q.s), m = half_bits_to_float(q.m), r = __frcp_rn(s);
-        sc[gr] |= q.s << (16 * par);
-        mn[gr] |= q.m << (16 * par);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[gr] |= quant_code(bf16_to_float((uint16_t)(x[e >> 1] >> (16 * (e & 1)))), m, s, r) << (16 * par + 4 * e);
-      }
-    // lane (0, t) also writes the pair's scales, lane (1, t) its minima
+    for (int gr = 0; gr < 4; ++gr) {
+      const uint32_t s2 = __shfl_sync(0xffffffffu, sp, 16 * h + 4 * gr + t), m2 = __shfl_sync(0xffffffffu, mp, 16 * h + 4 * gr + t);
+      const uint32_t w0 = codes4(vx[h][0][gr].x, vx[h][0][gr].y, code_scale(s2 & 0xffffu, m2 & 0xffffu));
+      const uint32_t w1 = codes4(vx[h][1][gr].x, vx[h][1][gr].y, code_scale(s2 >> 16, m2 >> 16));
+      w[gr] = w0 | w1 << 16;
+    }
     uint8_t* codes = dst + kTileV + 512 * h + 16 * lane;
-    uint8_t* meta = dst + (g == 0 ? kTileVs : kTileVm) + 16 * (4 * h + t);
-    const bool both_in = vin[h][0] && vin[h][1];
-    if (both_in) {
+    if (vin[h][0] && vin[h][1]) {
       *reinterpret_cast<uint4*>(codes) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (g == 0) *reinterpret_cast<uint4*>(meta) = make_uint4(sc[0], sc[1], sc[2], sc[3]);
-      if (g == 1) *reinterpret_cast<uint4*>(meta) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
-    } else if (vin[h][0] || vin[h][1]) {  // the pair's other token stays as it is
+    } else if (vin[h][0] || vin[h][1]) {
       const int par = vin[h][1];
 #pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
-        *reinterpret_cast<uint16_t*>(codes + 4 * gr + 2 * par) = (uint16_t)(w[gr] >> (16 * par));
-        if (g < 2) *reinterpret_cast<uint16_t*>(meta + 4 * gr + 2 * par) = (uint16_t)((g == 0 ? sc[gr] : mn[gr]) >> (16 * par));
-      }
+      for (int gr = 0; gr < 4; ++gr) *reinterpret_cast<uint16_t*>(codes + 4 * gr + 2 * par) = (uint16_t)(w[gr] >> (16 * par));
     }
   }
 }
