@@ -75,6 +75,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) { return fmaxf(a, fmaxf(fabsf(b), fabsf(c))); }
+
 // A group's scale as the code loop wants it.
 struct CodeScale {
   float s, m;
@@ -93,29 +100,30 @@ __device__ __forceinline__ CodeScale code_scale(uint32_t s_bits, uint32_t m_bits
   return c;
 }
 
-// Codes of four bf16 values, 4 bits each.  t = (x - m) r is within 2^-17 of the quotient, so its rounding is
+// Codes of 2 N bf16 values, 4 bits each.  t = (x - m) r is within 2^-17 of the quotient, so its rounding is
 // the quotient's unless t is that near to a border: then, and for an odd scale, the codes are taken exactly
 // (a division per value instead would cost more than the value's share of the memory time).  Adding
 // 1.5 x 2^23 rounds t to the integer that then stands in the sum's low bits.
-__device__ __forceinline__ uint32_t codes4(uint32_t x0, uint32_t x1, const CodeScale& c) {
-  const uint64_t magic = pair(12582912.f, 12582912.f), negmagic = pair(-12582912.f, -12582912.f);
-  uint32_t w = 0xC0C00000u;  // what the four constants' bits 0x4B400000 << 4e add up to, negated
+template <int N>
+__device__ __forceinline__ uint32_t codes(const uint32_t (&x)[N], const CodeScale& c) {
+  const uint64_t magic = pair(12582912.f, 12582912.f), negmagic = pair(-12582912.f, -12582912.f), minus1 = pair(-1.f, -1.f);
+  uint32_t w = 0xC0C00000u;  // what the constants' bits 0x4B400000 << 4 e add up to, negated
   float off = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t x = i ? x1 : x0;
-    const uint64_t t = mul2(add2(pair(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)), c.negm2), c.r2);
+  for (int i = 0; i < N; ++i) {
+    const uint64_t t = mul2(add2(pair(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), c.negm2), c.r2);
     const uint64_t u = add2(t, magic);
-    const uint64_t n = add2(u, negmagic);
-    float n0, n1, u0, u1, f0, f1;
-    unpair(n, n0, n1);
-    unpair(add2(t, pair(-n0, -n1)), f0, f1);
+    float u0, u1, f0, f1;
+    unpair(fma2(add2(u, negmagic), minus1, t), f0, f1);
     unpair(u, u0, u1);
-    off = fmaxf(fmaxf(off, fabsf(f0)), fabsf(f1));
+    off = max3_abs(off, f0, f1);
     w += __float_as_uint(u0) << (8 * i);
     w += __float_as_uint(u1) << (8 * i + 4);
   }
-  if (!c.plain || off > 0.5f - 0x1p-16f) w = exact_codes(x0, x1, c.s, c.m);
+  if (!c.plain || off > 0.5f - 0x1p-16f) {
+    w = exact_codes(x[0], x[1], c.s, c.m);
+    if constexpr (N == 4) w |= exact_codes(x[2], x[3], c.s, c.m) << 16;
+  }
   return w;
 }
 
@@ -136,9 +144,10 @@ __global__ void __launch_bounds__(kQuantWarps * 32)
   if (tile < 0 || first >= cap || first >= p0 + c) return;  // cap is a multiple of 16: a tile is in or out as a whole
   uint8_t* dst = store + (size_t)u * max_blocks * kQuantBlockBytes + (size_t)tile * kTileBytes;
   const size_t row0 = (size_t)u * n;
-  // index of the tile's token i among the new ones, and whether it is one of them
-  auto index = [&](int i) { return first + i - p0; };
-  auto is_new = [&](int i) { return index(i) >= 0 && index(i) < c; };
+  // index of the tile's token i among the new ones (-15 at least), and whether it is one of them
+  const int rel = (int)(first - p0);
+  auto index = [&](int i) { return rel + i; };
+  auto is_new = [&](int i) { return (unsigned)(rel + i) < (unsigned)c; };
 
   // loads of the whole tile, issued together
   uint4 kx[2][4];
@@ -161,7 +170,7 @@ __global__ void __launch_bounds__(kQuantWarps * 32)
   }
 
   // halves of the tile with a new token
-  const bool any[2] = {first < p0 + c && first + 8 > p0, first + 8 < p0 + c && first + 16 > p0};
+  const bool any[2] = {rel < c && rel + 8 > 0, rel + 8 < c};
 
   // Ranges.  K: token g + 8 h, group gr, over the lanes t; dealt so that lane t ends up with group t.  V: token
   // 8 h + 2 t + par, group gr, over the lanes g; lane g ends up with half g / 4, group g % 4, both tokens.
@@ -203,7 +212,8 @@ __global__ void __launch_bounds__(kQuantWarps * 32)
     for (int gr = 0; gr < 4; ++gr) {
       sm[gr] = __shfl_sync(0xffffffffu, q.s | q.m << 16, (lane & ~3) | gr);
       const CodeScale cs = code_scale(sm[gr] & 0xffffu, sm[gr] >> 16);
-      w[gr] = codes4(kx[h][gr].x, kx[h][gr].y, cs) | codes4(kx[h][gr].z, kx[h][gr].w, cs) << 16;
+      const uint32_t x[4] = {kx[h][gr].x, kx[h][gr].y, kx[h][gr].z, kx[h][gr].w};
+      w[gr] = codes<4>(x, cs);
     }
     if (kin[h]) {
       *reinterpret_cast<uint4*>(dst + 64 * (g + 8 * h) + 16 * t) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -235,9 +245,8 @@ __global__ void __launch_bounds__(kQuantWarps * 32)
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
       const uint32_t s2 = __shfl_sync(0xffffffffu, sp, 16 * h + 4 * gr + t), m2 = __shfl_sync(0xffffffffu, mp, 16 * h + 4 * gr + t);
-      const uint32_t w0 = codes4(vx[h][0][gr].x, vx[h][0][gr].y, code_scale(s2 & 0xffffu, m2 & 0xffffu));
-      const uint32_t w1 = codes4(vx[h][1][gr].x, vx[h][1][gr].y, code_scale(s2 >> 16, m2 >> 16));
-      w[gr] = w0 | w1 << 16;
+      const uint32_t x0[2] = {vx[h][0][gr].x, vx[h][0][gr].y}, x1[2] = {vx[h][1][gr].x, vx[h][1][gr].y};
+      w[gr] = codes<2>(x0, code_scale(s2 & 0xffffu, m2 & 0xffffu)) | codes<2>(x1, code_scale(s2 >> 16, m2 >> 16)) << 16;
     }
     uint8_t* codes = dst + kTileV + 512 * h + 16 * lane;
     if (vin[h][0] && vin[h][1]) {
