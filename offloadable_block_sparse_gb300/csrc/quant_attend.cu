@@ -20,6 +20,8 @@
 // exp2(logit - R): R follows a row's maximum only when that outgrows it by 2^14, so the usual tile needs
 // no rescaling, and is set so that weight x s stays within f16 (R rises with a scale of 2 or more).
 // A CTA merges its warps in shared memory; a unit's parts, where several CTAs share it, merge in a second kernel.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <mutex>
 
@@ -28,11 +30,14 @@
 
 namespace nosa {
 
+namespace cg = cooperative_groups;
+
 constexpr int kQaWarps = 4;
 constexpr int kQaThreads = kQaWarps * 32;
 constexpr int kQaStages = 2;          // half blocks in flight per warp
 constexpr int kStageTokens = 32, kStageBytes4 = 2 * kTileBytes;
 constexpr int kQaSplitUnits = 2048;   // beyond, one CTA per unit
+constexpr int kQaCluster = 8, kQaClusterBlocks = 32;
 constexpr int kQaList = 256;          // listed blocks looked up at a time
 constexpr int kQaMaxRows = 32;
 constexpr int kQaRowStride = 132;     // floats per row of a warp's partial in shared memory (no bank conflicts)
@@ -49,6 +54,8 @@ __host__ __device__ constexpr int quant_smem_bytes(int nt) {
   return quant_ring_bytes(nt) + (nt > 1 ? nt * 4 * 32 * 16 : 0);  // and the query operands
 }
 
+enum { kWhole, kPieces, kCluster };
+
 struct QuantArgs {
   const uint16_t* q;
   const uint8_t* store;
@@ -61,7 +68,7 @@ struct QuantArgs {
   float2* stats;  // [part][row]: reference and softmax sum
   float* part;    // [part][row][128]
   int units, nq, rows, max_blocks, max_sel, max_len;
-  int split;      // 0: one CTA per unit
+  int split;      // kWhole: one CTA per unit, kPieces: equal pieces of all units' blocks, kCluster: a cluster per unit
   float scale;    // softmax scale x log2(e)
 };
 
@@ -429,6 +436,17 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const float (&al
   }
 }
 
+// Adds a part (reference r, sum l, four dims o) to a running one.
+__device__ __forceinline__ void merge_part(float& R, float& L, float4& O, float r, float l, const float4& o) {
+  const float top = fmaxf(R, r), f = ex2(R - top), h = ex2(r - top);
+  R = top;
+  L = L * f + l * h;
+  O.x = O.x * f + o.x * h;
+  O.y = O.y * f + o.y * h;
+  O.z = O.z * f + o.z * h;
+  O.w = O.w * f + o.w * h;
+}
+
 // Four dims of an output row: zeros where no token was seen.
 __device__ __forceinline__ void store_out(uint16_t* out, const float4& o, float l) {
   uint2 v = make_uint2(0, 0);
@@ -449,6 +467,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
   __shared__ int2 list[kQaList];  // (row of the store, tokens of the context from the block on)
   __shared__ float wr[kQaWarps][8 * NT], wl[kQaWarps][8 * NT];
   __shared__ int scan[32], found[2];
+  __shared__ float2 merged[8 * NT];  // a cluster CTA's references and sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (lane == 0) {
 #pragma unroll
@@ -465,7 +484,9 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
 
   // The units' blocks in one line, cut into one piece per CTA: this CTA's are `todo` blocks from block `at` of
   // unit u on, and unit u's begin at `begin` of `total`.
-  int u = blockIdx.x, at = 0, pieces = gridDim.x;
+  const int ranks = a.split == kCluster ? (int)cg::this_cluster().num_blocks() : 1;
+  const int rank = a.split == kCluster ? (int)cg::this_cluster().block_rank() : 0;
+  int u = blockIdx.x / ranks, at = 0, pieces = gridDim.x;
   long long todo = 1, total = 1, begin = 0;
   auto cut = [&]() {  // two blocks a piece at least (a stage per warp); further CTAs have nothing to do
     pieces = (int)min((long long)gridDim.x, (total + 1) / 2);
@@ -473,7 +494,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
     todo = blockIdx.x < pieces ? cta_first(total, blockIdx.x + 1, pieces) - lo : 0;
     return lo;
   };
-  if (a.split) {
+  if (a.split == kPieces) {
     if (a.sel) {
       total = (long long)a.units * a.max_sel;
       begin = cut();
@@ -508,9 +529,16 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
   bool late = false;
   for (; todo > 0; ++u, at = 0) {
     const int len = length(u), whole = blocks_of(u);
-    const int first = at, end = a.split ? (int)min((long long)whole, at + todo) : whole;
-    todo -= end - first;
-    if (threadIdx.x == 0 && first == 0 && len != a.lens[u]) atomicOr(a.err, kErrBounds);
+    int first = at, end = whole;
+    if (a.split == kPieces) {
+      end = (int)min((long long)whole, at + todo);
+      todo -= end - first;
+    } else {
+      first = (int)cta_first(whole, rank, ranks);
+      end = (int)cta_first(whole, rank + 1, ranks);
+      todo = 0;
+    }
+    if (threadIdx.x == 0 && first == 0 && rank == 0 && len != a.lens[u]) atomicOr(a.err, kErrBounds);
     QueryTile Q;
     RowTile A[NT];
     float alpha[NT][2];
@@ -534,9 +562,9 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
     };
 
     // The blocks, listed ones looked up kQaList at a time.  Warp w takes half w % 2 of the blocks w / 2, w / 2 + 2, ...
-    const int batch = a.sel ? kQaList : end - first, half = (warp & 1) * kStageTokens;
+    const int batch = a.sel ? kQaList : max(end - first, 1), half = (warp & 1) * kStageTokens;
     const uint8_t* base = a.store + (size_t)u * a.max_blocks * kQuantBlockBytes + (warp & 1) * kStageBytes4;
-    for (int b0 = first; b0 < end; b0 += batch) {
+    for (int b0 = first; b0 < end || b0 == first; b0 += batch) {
       const int n = min(batch, end - b0);
       if (a.sel) {
         if (b0 > first) __syncthreads();  // the list before is used up
@@ -632,7 +660,10 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
         O.z = fmaf(o.z, f, O.z);
         O.w = fmaf(o.w, f, O.w);
       }
-      if (complete) {
+      if (ranks > 1) {  // in the place of warp 0's, which this thread alone has read
+        *reinterpret_cast<float4*>(smem + row * kQaRowStride + x) = O;
+        if (x == 0) merged[row] = make_float2(R, L);
+      } else if (complete) {
         store_out(a.out + ((size_t)u * a.rows + row) * kHeadDim + x, O, L);
       } else {
         const size_t i = (size_t)part * a.rows + row;
@@ -640,7 +671,24 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
         *reinterpret_cast<float4*>(a.part + i * kHeadDim + x) = O;
       }
     }
-    if (a.split && first == 0 && threadIdx.x == 0)
+    if (ranks > 1) {  // each CTA of the cluster merges its share of the outputs through distributed shared memory
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();
+      for (int idx = rank * kQaThreads + threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += ranks * kQaThreads) {
+        const int row = idx >> 5, x = 4 * (idx & 31);
+        float R = kNoRef, L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int r = 0; r < ranks; ++r) {
+          const float2 m = *cluster.map_shared_rank(&merged[row], r);
+          merge_part(R, L, O, m.x, m.y, *reinterpret_cast<const float4*>(cluster.map_shared_rank(smem + row * kQaRowStride + x, r)));
+        }
+        store_out(a.out + ((size_t)u * a.rows + row) * kHeadDim + x, O, L);
+      }
+      cluster.sync();  // keep every CTA's shared memory until all have read it
+      return;
+    }
+    if (a.split == kPieces && first == 0 && threadIdx.x == 0)
       a.meta[u] = make_int2(part, cta_of(total, begin + whole - 1, pieces) - blockIdx.x + 1);
     begin += whole;
     if (todo > 0) {
@@ -663,27 +711,18 @@ __global__ void __launch_bounds__(kQaThreads) quant_merge_kernel(const __grid_co
   if (m.y == 1) return;
   float R = kNoRef, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float r, float l, const float4& o) {
-    const float top = fmaxf(R, r), f = ex2(R - top), h = ex2(r - top);
-    R = top;
-    L = L * f + l * h;
-    O.x = O.x * f + o.x * h;
-    O.y = O.y * f + o.y * h;
-    O.z = O.z * f + o.z * h;
-    O.w = O.w * f + o.w * h;
-  };
 #pragma unroll 4
   for (int c = warp; c < m.y; c += kQaWarps) {
     const size_t i = (size_t)(m.x + c) * a.rows + row;
     const float2 s = a.stats[i];
-    add(s.x, s.y, *reinterpret_cast<const float4*>(a.part + i * kHeadDim + 4 * lane));
+    merge_part(R, L, O, s.x, s.y, *reinterpret_cast<const float4*>(a.part + i * kHeadDim + 4 * lane));
   }
   so[warp][lane] = O;
   if (lane == 0) ss[warp] = make_float2(R, L);
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < kQaWarps; ++w) add(ss[w].x, ss[w].y, so[w][lane]);
+    for (int w = 1; w < kQaWarps; ++w) merge_part(R, L, O, ss[w].x, ss[w].y, so[w][lane]);
     store_out(a.out + ((size_t)u * a.rows + row) * kHeadDim + 4 * lane, O, L);
   }
 }
@@ -699,6 +738,7 @@ template <int NT>
 static cudaError_t set_up_quant_attend(int sms, int* ctas) {
   const int smem = quant_smem_bytes(NT);
   cudaError_t e = cudaFuncSetAttribute(quant_attend_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(quant_attend_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, quant_attend_kernel<NT>, kQaThreads, smem);
   *ctas *= sms;
   return e;
@@ -726,25 +766,26 @@ static bool quant_device(QuantDevice* out) {
   return true;
 }
 
-// How many CTAs a call takes.  Units are split into equal pieces over one wave of resident CTAs, of two blocks
-// (a stage per warp) at least; with so many units that whole ones balance by themselves, one CTA each.
+// How many CTAs a call takes, and how they share it.
 struct QuantPlan {
-  int ctas;
-  bool split;
+  int split, ctas, cluster;
   size_t bytes;  // of the scratch
 };
 static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks) {
   const int wave = std::min(d.ctas[rows <= 8 ? 0 : rows <= 16 ? 1 : 2], 8 * d.sms);
-  if (units > kQaSplitUnits) return {units, false, kQaErrBytes};
+  if (units > kQaSplitUnits) return {kWhole, units, 0, kQaErrBytes};
+  const int cl = std::min(kQaCluster, (blocks + 1) / 2);
+  if ((long long)blocks * units <= (long long)kQaClusterBlocks * wave / 4 && blocks <= kQaCluster * kQaClusterBlocks)
+    return {kCluster, units * cl, cl, kQaErrBytes};
   const long long pieces = ((long long)units * blocks + 1) / 2;
   const int ctas = (int)std::min<long long>(wave, pieces);
   const size_t parts = (size_t)ctas + units;
-  return {ctas, true, kQaErrBytes + (size_t)units * sizeof(int2) + parts * rows * (kHeadDim + 2) * sizeof(float) + 16};
+  return {kPieces, ctas, 0, kQaErrBytes + (size_t)units * sizeof(int2) + parts * rows * (kHeadDim + 2) * sizeof(float) + 16};
 }
 
 template <int NT>
-static cudaError_t launch_quant_attend(const QuantArgs& a, int ctas, cudaStream_t st) {
-  return launch_ex(quant_attend_kernel<NT>, dim3((unsigned)ctas), dim3(kQaThreads), quant_smem_bytes(NT), st, true, 0, a);
+static cudaError_t launch_quant_attend(const QuantArgs& a, const QuantPlan& p, cudaStream_t st) {
+  return launch_ex(quant_attend_kernel<NT>, dim3((unsigned)p.ctas), dim3(kQaThreads), quant_smem_bytes(NT), st, true, p.cluster, a);
 }
 
 static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t scratch_bytes, cudaStream_t st) {
@@ -759,10 +800,10 @@ static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t 
   a.part = reinterpret_cast<float*>(p + kQaErrBytes);
   a.stats = reinterpret_cast<float2*>(a.part + parts * a.rows * kHeadDim);
   a.meta = reinterpret_cast<int2*>(a.stats + parts * a.rows);
-  cudaError_t e = a.rows <= 8    ? launch_quant_attend<1>(a, plan.ctas, st)
-                  : a.rows <= 16 ? launch_quant_attend<2>(a, plan.ctas, st)
-                                 : launch_quant_attend<4>(a, plan.ctas, st);
-  if (e == cudaSuccess && plan.split)
+  cudaError_t e = a.rows <= 8    ? launch_quant_attend<1>(a, plan, st)
+                  : a.rows <= 16 ? launch_quant_attend<2>(a, plan, st)
+                                 : launch_quant_attend<4>(a, plan, st);
+  if (e == cudaSuccess && plan.split == kPieces)
     e = launch_ex(quant_merge_kernel, dim3((unsigned)(a.units * a.rows)), dim3(kQaThreads), 0, st, true, 0, a);
   if (e == cudaSuccess) return NOSA_OK;
   (void)cudaGetLastError();
