@@ -51,7 +51,7 @@ __host__ __device__ constexpr int quant_ring_bytes(int nt) {
 }
 
 __host__ __device__ constexpr int quant_smem_bytes(int nt) {
-  return quant_ring_bytes(nt) + (nt > 1 ? nt * 4 * 32 * 16 : 0);  // and the query operands
+  return quant_ring_bytes(nt) + (nt > 1 ? nt * 2432 : 0);  // and the query operands (QueryShared)
 }
 
 enum { kWhole, kPieces, kCluster };
@@ -279,159 +279,179 @@ __device__ __noinline__ bool clear_tail(unsigned char* stage, int left, int seen
   return __any_sync(0xffffffffu, odd);
 }
 
-// One stage (two tiles, 32 tokens) for all row tiles.  left: tokens of the context from the stage's first on.
-// q: the query operands, in registers (NT = 1) or in shared memory (uint4 [nt][group][lane]).
+// The query side in shared memory, for more than one row tile (registers hold it for one).
+struct QueryShared {
+  uint4 b[4][32];    // [group][lane]: QueryTile::b of the group
+  uint32_t sums[32];
+  float2 alpha[32];
+};
+static_assert(kQaWarps >= 4, "a warp per row tile loads the queries");
+static_assert(sizeof(QueryShared) == 2432, "quant_smem_bytes");
+
+// One stage (two tiles, 32 tokens) for all row tiles; left: tokens of the context from the stage's first on.
+// One row tile takes both tiles at once, so that their chains of dependent operations overlap; more row tiles
+// overlap by themselves and take one tile at a time, which keeps them in registers.
 template <int NT>
-__device__ __forceinline__ void process_stage(RowTile (&A)[NT], const float (&alpha)[NT][2], const QueryTile& Q, const uint4* qs,
-                                              const uint32_t (&sums)[NT], unsigned char* stage, int left, int nq, int rows,
-                                              int lane) {
+__device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile& Q, const float (&alpha1)[2],
+                                              const QueryShared* qs, unsigned char* stage, int left, int nq, int rows, int lane) {
+  constexpr int kTiles = NT == 1 ? 2 : 1;
   const int g = lane >> 2, t = lane & 3;
   const bool tail = left - (nq - 1) < kStageTokens;  // some row does not see the whole stage
   bool odd = false;
   if (tail) odd = clear_tail(stage, left, left - (nq - 1));
+  // the largest V scale of the stage: below 2, weights up to 2^14 times scales stay within f16
+  const uint4 vs = *reinterpret_cast<const uint4*>(stage + (lane >> 3 & 1) * kTileBytes + kTileVs + 16 * (lane & 7));
+  const uint32_t vmax2 = max_half2(max_half2(vs.x, vs.y), max_half2(vs.z, vs.w));
+  const bool large = (vmax2 & 0x40004000u) != 0;  // exponent bit 14: 2 or more (scales have no sign)
 
-  // scores in units of 2^-24
-  float z[2][NT][4];
-  uint4 kc[2][2];
-  float ks[2][2][4];
+#pragma unroll 1
+  for (int i0 = 0; i0 < 2; i0 += kTiles) {
+    unsigned char* tile0 = stage + i0 * kTileBytes;
+    // scores in units of 2^-24
+    float z[kTiles][NT][4], ks[kTiles][2][4];
+    uint4 kc[kTiles][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const unsigned char* tile = stage + i * kTileBytes;
-    uint32_t km[2];
+    for (int i = 0; i < kTiles; ++i) {
+      const unsigned char* tile = tile0 + i * kTileBytes;
+      uint32_t km[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      kc[i][h] = *reinterpret_cast<const uint4*>(tile + 64 * (g + 8 * h) + 16 * t);
-      const uint2 s = *reinterpret_cast<const uint2*>(tile + kTileKs + 16 * (g + 8 * h));
-      km[h] = *reinterpret_cast<const uint32_t*>(tile + kTileKs + 16 * (g + 8 * h) + 8 + 4 * (t & 1));
-      ks[i][h][0] = half_lo(s.x);
-      ks[i][h][1] = half_hi(s.x);
-      ks[i][h][2] = half_lo(s.y);
-      ks[i][h][3] = half_hi(s.y);
-    }
+      for (int h = 0; h < 2; ++h) {
+        kc[i][h] = *reinterpret_cast<const uint4*>(tile + 64 * (g + 8 * h) + 16 * t);
+        const uint2 s = *reinterpret_cast<const uint2*>(tile + kTileKs + 16 * (g + 8 * h));
+        km[h] = *reinterpret_cast<const uint32_t*>(tile + kTileKs + 16 * (g + 8 * h) + 8 + 4 * (t & 1));
+        ks[i][h][0] = half_lo(s.x);
+        ks[i][h][1] = half_hi(s.x);
+        ks[i][h][2] = half_lo(s.y);
+        ks[i][h][3] = half_hi(s.y);
+      }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float m[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_f16_k8(m, km[0], km[1], sums[nt]);
+      for (int nt = 0; nt < NT; ++nt) {
+        float m[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16_k8(m, km[0], km[1], NT == 1 ? Q.sums : qs[nt].sums[lane]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[i][nt][e] = m[e] * 0x1p-24f;
-    }
-  }
-#pragma unroll
-  for (int gr = 0; gr < 4; ++gr) {
-    uint32_t a[2][8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t w0 = word(kc[i][0], gr), w1 = word(kc[i][1], gr), x0 = w0 >> 8, x1 = w1 >> 8;
-      a[i][0] = w0 & 0x000F000Fu;
-      a[i][1] = w1 & 0x000F000Fu;
-      a[i][2] = w0 & 0x00F000F0u;
-      a[i][3] = w1 & 0x00F000F0u;
-      a[i][4] = x0 & 0x000F000Fu;
-      a[i][5] = x1 & 0x000F000Fu;
-      a[i][6] = x0 & 0x00F000F0u;
-      a[i][7] = x1 & 0x00F000F0u;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      uint4 b;
-      if constexpr (NT == 1)
-        b = make_uint4(Q.b[2 * gr][0], Q.b[2 * gr][1], Q.b[2 * gr + 1][0], Q.b[2 * gr + 1][1]);
-      else
-        b = qs[(4 * nt + gr) * 32 + lane];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(acc, a[i][0], a[i][1], a[i][2], a[i][3], b.x, b.y);
-        mma_f16(acc, a[i][4], a[i][5], a[i][6], a[i][7], b.z, b.w);
-        z[i][nt][0] = fmaf(acc[0], ks[i][0][gr], z[i][nt][0]);
-        z[i][nt][1] = fmaf(acc[1], ks[i][0][gr], z[i][nt][1]);
-        z[i][nt][2] = fmaf(acc[2], ks[i][1][gr], z[i][nt][2]);
-        z[i][nt][3] = fmaf(acc[3], ks[i][1][gr], z[i][nt][3]);
+        for (int e = 0; e < 4; ++e) z[i][nt][e] = m[e] * 0x1p-24f;
       }
     }
-  }
-  if (tail) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int gr = 0; gr < 4; ++gr) {
+      uint32_t a[kTiles][8];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        const uint32_t w0 = word(kc[i][0], gr), w1 = word(kc[i][1], gr), x0 = w0 >> 8, x1 = w1 >> 8;
+        a[i][0] = w0 & 0x000F000Fu;
+        a[i][1] = w1 & 0x000F000Fu;
+        a[i][2] = w0 & 0x00F000F0u;
+        a[i][3] = w1 & 0x00F000F0u;
+        a[i][4] = x0 & 0x000F000Fu;
+        a[i][5] = x1 & 0x000F000Fu;
+        a[i][6] = x0 & 0x00F000F0u;
+        a[i][7] = x1 & 0x00F000F0u;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint4 b;
+        if constexpr (NT == 1)
+          b = make_uint4(Q.b[2 * gr][0], Q.b[2 * gr][1], Q.b[2 * gr + 1][0], Q.b[2 * gr + 1][1]);
+        else
+          b = qs[nt].b[gr][lane];
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16(acc, a[i][0], a[i][1], a[i][2], a[i][3], b.x, b.y);
+          mma_f16(acc, a[i][4], a[i][5], a[i][6], a[i][7], b.z, b.w);
+          z[i][nt][0] = fmaf(acc[0], ks[i][0][gr], z[i][nt][0]);
+          z[i][nt][1] = fmaf(acc[1], ks[i][0][gr], z[i][nt][1]);
+          z[i][nt][2] = fmaf(acc[2], ks[i][1][gr], z[i][nt][2]);
+          z[i][nt][3] = fmaf(acc[3], ks[i][1][gr], z[i][nt][3]);
+        }
+      }
+    }
+    if (tail) {
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = 8 * nt + 2 * t + (e & 1), token = kTileTokens * (i0 + i) + g + 8 * (e >> 1);
+            if (row >= rows || token >= left - (nq - 1) + row % nq) z[i][nt][e] = -INFINITY;
+          }
+    }
+
+    // exponents against the references, and whether those hold: no row's maximum has outgrown its own by 14
+    bool raise = large;
+    float ex[kTiles][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          ex[i][nt][e] = (z[i][nt][e] - A[nt].r[e & 1]) * (e & 1 ? al.y : al.x);
+          top = fmaxf(top, ex[i][nt][e]);
+        }
+      raise |= top > 14.f;
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+      float vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+      // vmax < 2^e: weights up to 2^limit keep the products below 2^15 (a NaN scale sets no limit)
+      if (!(vmax <= 65504.f)) vmax = 0.f;
+      const float limit = (float)(14 - max((int)(__float_as_uint(vmax) >> 23) - 127, 0));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = 8 * nt + 2 * t + (e & 1), token = kTileTokens * i + g + 8 * (e >> 1);
-          if (row >= rows || token >= left - (nq - 1) + row % nq) z[i][nt][e] = -INFINITY;
-        }
-  }
-
-  // exponents against the references, and whether they hold: no row's maximum has outgrown its reference by
-  // 14, and no V scale of the stage is 2 or more (then weights up to 2^14 times scales stay within f16)
-  const uint4 vs = *reinterpret_cast<const uint4*>(stage + (lane >> 3 & 1) * kTileBytes + kTileVs + 16 * (lane & 7));
-  const uint32_t vmax2 = max_half2(max_half2(vs.x, vs.y), max_half2(vs.z, vs.w));
-  bool raise = (vmax2 & 0x40004000u) != 0;  // exponent bit 14: 2 or more (scales have no sign)
-  float ex[2][NT][4];
+        for (int e = 0; e < 2; ++e) {
+          const float2 al2 = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
+          const float al = e ? al2.y : al2.x;
+          float best = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
+          if (kTiles == 2) best = fmaxf(best, fmaxf(z[kTiles - 1][nt][e], z[kTiles - 1][nt][e + 2]));
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+          for (int o = 4; o < 32; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+          const float old = A[nt].r[e];
+          if ((best - old) * al > limit) {  // the row's lanes agree; rows differ
+            const float r = best - (limit - 4.f) / al, f = ex2((old - r) * al);
+            A[nt].r[e] = r;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+            for (int mt = 0; mt < 8; ++mt) {
+              A[nt].o[mt][e] *= f;
+              A[nt].o[mt][e + 2] *= f;
+            }
+            A[nt].c[e] *= f;
+            A[nt].c[e + 2] *= f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ex[i][nt][e] = (z[i][nt][e] - A[nt].r[e & 1]) * alpha[nt][e & 1];
-    const float top = fmaxf(fmaxf(fmaxf(ex[0][nt][0], ex[0][nt][1]), fmaxf(ex[0][nt][2], ex[0][nt][3])),
-                            fmaxf(fmaxf(ex[1][nt][0], ex[1][nt][1]), fmaxf(ex[1][nt][2], ex[1][nt][3])));
-    raise |= top > 14.f;
-  }
-  if (__any_sync(0xffffffffu, raise)) {
-    float vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-    // vmax < 2^e: weights up to 2^limit keep the products below 2^15 (a NaN scale sets no limit)
-    if (!(vmax <= 65504.f)) vmax = 0.f;
-    const float limit = (float)(14 - max((int)(__float_as_uint(vmax) >> 23) - 127, 0));
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float best = fmaxf(fmaxf(z[0][nt][e], z[0][nt][e + 2]), fmaxf(z[1][nt][e], z[1][nt][e + 2]));
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-        const float old = A[nt].r[e];
-        if ((best - old) * alpha[nt][e] > limit) {  // the row's lanes agree; rows differ
-          const float r = best - (limit - 4.f) / alpha[nt][e], f = ex2((old - r) * alpha[nt][e]);
-          A[nt].r[e] = r;
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt) {
-            A[nt].o[mt][e] *= f;
-            A[nt].o[mt][e + 2] *= f;
-          }
-          A[nt].c[e] *= f;
-          A[nt].c[e + 2] *= f;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            ex[i][nt][e] = (z[i][nt][e] - r) * alpha[nt][e];
-            ex[i][nt][e + 2] = (z[i][nt][e + 2] - r) * alpha[nt][e];
+            for (int i = 0; i < kTiles; ++i) {
+              ex[i][nt][e] = (z[i][nt][e] - r) * al;
+              ex[i][nt][e + 2] = (z[i][nt][e + 2] - r) * al;
+            }
           }
         }
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    // weights of tokens g, g + 8 and rows 2t, 2t + 1; transposed: of row g and token pairs t, t + 4
-    uint32_t p[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      p[nt][0] = movmatrix_trans(pack_half2(ex2(ex[i][nt][0]), ex2(ex[i][nt][1])));
-      p[nt][1] = movmatrix_trans(pack_half2(ex2(ex[i][nt][2]), ex2(ex[i][nt][3])));
     }
-    if (odd) {
-      const int from = min(max(left - (nq - 1) - kTileTokens * i, 0), kTileTokens);
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      // weights of tokens g, g + 8 and rows 2t, 2t + 1; transposed: of row g and token pairs t, t + 4
+      uint32_t p[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        RowTile B = A[nt];  // a copy, so that A itself stays in registers
-        add_values_by_token(B, stage + i * kTileBytes, p[nt][0], p[nt][1], from);
-        A[nt] = B;
+        p[nt][0] = movmatrix_trans(pack_half2(ex2(ex[i][nt][0]), ex2(ex[i][nt][1])));
+        p[nt][1] = movmatrix_trans(pack_half2(ex2(ex[i][nt][2]), ex2(ex[i][nt][3])));
       }
-    } else {
-      ValueRegs V;
-      load_values(V, stage + i * kTileBytes, lane);
-      add_values<NT>(A, V, p);
+      if (odd) {
+        const int from = min(max(left - (nq - 1) - kTileTokens * (i0 + i), 0), kTileTokens);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          RowTile B = A[nt];  // a copy, so that A itself stays in registers
+          add_values_by_token(B, tile0 + i * kTileBytes, p[nt][0], p[nt][1], from);
+          A[nt] = B;
+        }
+      } else {
+        ValueRegs V;
+        load_values(V, tile0 + i * kTileBytes, lane);
+        add_values<NT>(A, V, p);
+      }
     }
   }
 }
@@ -523,7 +543,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
     begin -= at;
   }
 
-  uint4* qs = reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(smem) + quant_ring_bytes(NT));
+  QueryShared* qs = reinterpret_cast<QueryShared*>(reinterpret_cast<unsigned char*>(smem) + quant_ring_bytes(NT));
   unsigned char* ring = reinterpret_cast<unsigned char*>(smem) + warp * kQaStages * kStageBytes4;
   int issued = 0, done = 0;
   bool late = false;
@@ -541,17 +561,19 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
     if (threadIdx.x == 0 && first == 0 && rank == 0 && len != a.lens[u]) atomicOr(a.err, kErrBounds);
     QueryTile Q;
     RowTile A[NT];
-    float alpha[NT][2];
-    uint32_t sums[NT];
+    float alpha1[2];
     auto load_queries = [&]() {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        load_query(Q, alpha[nt], a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale);
-        sums[nt] = Q.sums;
-        if (NT > 1 && warp == nt % kQaWarps) {
+        if (NT == 1 || warp == nt) {
+          load_query(Q, alpha1, a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale);
+          if (NT > 1) {
 #pragma unroll
-          for (int gr = 0; gr < 4; ++gr)
-            qs[(4 * nt + gr) * 32 + lane] = make_uint4(Q.b[2 * gr][0], Q.b[2 * gr][1], Q.b[2 * gr + 1][0], Q.b[2 * gr + 1][1]);
+            for (int gr = 0; gr < 4; ++gr)
+              qs[nt].b[gr][lane] = make_uint4(Q.b[2 * gr][0], Q.b[2 * gr][1], Q.b[2 * gr + 1][0], Q.b[2 * gr + 1][1]);
+            qs[nt].sums[lane] = Q.sums;
+            qs[nt].alpha[lane] = make_float2(alpha1[0], alpha1[1]);
+          }
         }
         A[nt].r[0] = A[nt].r[1] = kNoRef;
 #pragma unroll
@@ -605,7 +627,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
         const int st = done % kQaStages;
         late |= !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][st], done / kQaStages & 1, kWaitCycles));
         if (late) continue;  // let what is in flight land, and start no more
-        process_stage<NT>(A, alpha, Q, qs, sums, ring + st * kStageBytes4, tokens[warp][st], a.nq, a.rows, lane);
+        process_stage<NT>(A, Q, alpha1, qs, ring + st * kStageBytes4, tokens[warp][st], a.nq, a.rows, lane);
         __syncwarp();  // the stage is read
         if (issue()) ++issued;
       }
@@ -621,6 +643,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const RowTile& S = A[nt];
+      const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
       float* w = smem + (warp * 8 * NT + 8 * nt + 2 * t) * kQaRowStride;
 #pragma unroll
       for (int gr = 0; gr < 4; ++gr) {
@@ -635,7 +658,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
       if (g == 4) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          wr[warp][8 * nt + 2 * t + i] = fmaxf(S.r[i] * alpha[nt][i], kNoRef);  // from here on in base-2 logits
+          wr[warp][8 * nt + 2 * t + i] = fmaxf(S.r[i] * (i ? al.y : al.x), kNoRef);  // from here on in base-2 logits
           wl[warp][8 * nt + 2 * t + i] = S.c[i];
         }
       }
