@@ -37,7 +37,6 @@ constexpr int kQaThreads = kQaWarps * 32;
 constexpr int kQaStages = 2;          // half blocks in flight per warp
 constexpr int kStageTokens = 32, kStageBytes4 = 2 * kTileBytes;
 constexpr int kQaSplitUnits = 2048;   // beyond, one CTA per unit
-constexpr int kQaCluster = 8, kQaClusterBlocks = 32;
 constexpr int kQaList = 256;          // listed blocks looked up at a time
 constexpr int kQaMaxRows = 32;
 constexpr int kQaRowStride = 132;     // floats per row of a warp's partial in shared memory (no bank conflicts)
@@ -80,11 +79,18 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// D (16 x 8, f32) += A (16 x 8, row) . B (8 x 8, col), f16 inputs.
+// The same with D = A . B: a zero operand costs nothing, a zeroed accumulator four moves.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// D (16 x 8, f32) = A (16 x 8, row) . B (8 x 8, col), f16 inputs.
 __device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};\n"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a0), "r"(a1), "r"(b0));
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};\n"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -115,7 +121,7 @@ struct QueryTile {
 
 // Rows 8 nt + g of q: scaled by a power of two that brings the row's largest magnitude into [2^9, 2^10)
 // (bf16 values down to 2^-23 of it stay exact in f16, and a group's sum stays in range).
-// alpha: the factors that turn the scores of rows 2t, 2t + 1, in units of 2^-24, into logits in base 2.
+// alpha: the factors that turn the scores of rows 2t, 2t + 1 into logits in base 2.
 __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], const uint16_t* q, int row, int rows, int lane,
                                            float scale) {
   const int t = lane & 3;
@@ -132,7 +138,7 @@ __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], cons
   big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
   // 2^(9 - e) for the exponent e of the largest value; 1 where the row is zero or not finite
   const int e = (int)(big >> 7) - 127;
-  const int shift = big == 0 || big >= 0x7f80u ? 0 : min(9 - e, 126);  // (alpha is infinite from |q| = 2^116 on)
+  const int shift = big == 0 || big >= 0x7f80u ? 0 : min(9 - e, 126);
   const float f = __uint_as_float((uint32_t)(127 + shift) << 23), inv = __uint_as_float((uint32_t)(127 - shift) << 23);
   float sum[4];
 #pragma unroll
@@ -156,8 +162,8 @@ __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], cons
   const uint32_t l01 = pack_half2(sum[0] - half_lo(h01), sum[1] - half_hi(h01));
   const uint32_t l23 = pack_half2(sum[2] - half_lo(h23), sum[3] - half_hi(h23));
   Q.sums = t == 0 ? h01 : t == 1 ? h23 : t == 2 ? l01 : l23;
-  alpha[0] = scale * 0x1p24f * __shfl_sync(0xffffffffu, inv, 8 * t);  // row 2t's lanes are 8t .. 8t + 3
-  alpha[1] = scale * 0x1p24f * __shfl_sync(0xffffffffu, inv, 8 * t + 4);
+  alpha[0] = scale * __shfl_sync(0xffffffffu, inv, 8 * t);  // row 2t's lanes are 8t .. 8t + 3
+  alpha[1] = scale * __shfl_sync(0xffffffffu, inv, 8 * t + 4);
 }
 
 // One warp's running state for a tile of 8 rows: references of rows 2t, 2t + 1 in units of the scores (an
@@ -307,7 +313,7 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
 #pragma unroll 1
   for (int i0 = 0; i0 < 2; i0 += kTiles) {
     unsigned char* tile0 = stage + i0 * kTileBytes;
-    // scores in units of 2^-24
+    // scores of the scaled queries
     float z[kTiles][NT][4], ks[kTiles][2][4];
     uint4 kc[kTiles][2];
 #pragma unroll
@@ -319,18 +325,14 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
         kc[i][h] = *reinterpret_cast<const uint4*>(tile + 64 * (g + 8 * h) + 16 * t);
         const uint2 s = *reinterpret_cast<const uint2*>(tile + kTileKs + 16 * (g + 8 * h));
         km[h] = *reinterpret_cast<const uint32_t*>(tile + kTileKs + 16 * (g + 8 * h) + 8 + 4 * (t & 1));
-        ks[i][h][0] = half_lo(s.x);
-        ks[i][h][1] = half_hi(s.x);
-        ks[i][h][2] = half_lo(s.y);
-        ks[i][h][3] = half_hi(s.y);
+        // the 2^24 that the codes lack
+        ks[i][h][0] = half_lo(s.x) * 0x1p24f;
+        ks[i][h][1] = half_hi(s.x) * 0x1p24f;
+        ks[i][h][2] = half_lo(s.y) * 0x1p24f;
+        ks[i][h][3] = half_hi(s.y) * 0x1p24f;
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float m[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16_k8(m, km[0], km[1], NT == 1 ? Q.sums : qs[nt].sums[lane]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[i][nt][e] = m[e] * 0x1p-24f;
-      }
+      for (int nt = 0; nt < NT; ++nt) mma_f16_k8(z[i][nt], km[0], km[1], NT == 1 ? Q.sums : qs[nt].sums[lane]);
     }
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
@@ -356,8 +358,8 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
           b = qs[nt].b[gr][lane];
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(acc, a[i][0], a[i][1], a[i][2], a[i][3], b.x, b.y);
+          float acc[4];
+          mma_f16_first(acc, a[i][0], a[i][1], a[i][2], a[i][3], b.x, b.y);
           mma_f16(acc, a[i][4], a[i][5], a[i][6], a[i][7], b.z, b.w);
           z[i][nt][0] = fmaf(acc[0], ks[i][0][gr], z[i][nt][0]);
           z[i][nt][1] = fmaf(acc[1], ks[i][0][gr], z[i][nt][1]);
@@ -378,21 +380,17 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
           }
     }
 
-    // exponents against the references, and whether those hold: no row's maximum has outgrown its own by 14
+    // whether the references hold: no row's maximum has outgrown its own by 14
     bool raise = large;
-    float ex[kTiles][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
-      float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          ex[i][nt][e] = (z[i][nt][e] - A[nt].r[e & 1]) * (e & 1 ? al.y : al.x);
-          top = fmaxf(top, ex[i][nt][e]);
-        }
-      raise |= top > 14.f;
+      for (int e = 0; e < 2; ++e) {
+        float best = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
+        if (kTiles == 2) best = fmaxf(best, fmaxf(z[kTiles - 1][nt][e], z[kTiles - 1][nt][e + 2]));
+        raise |= (best - A[nt].r[e]) * (e ? al.y : al.x) > 14.f;
+      }
     }
     if (__any_sync(0xffffffffu, raise)) {
       float vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
@@ -422,13 +420,17 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
             }
             A[nt].c[e] *= f;
             A[nt].c[e + 2] *= f;
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-              ex[i][nt][e] = (z[i][nt][e] - r) * al;
-              ex[i][nt][e + 2] = (z[i][nt][e + 2] - r) * al;
-            }
           }
         }
+    }
+    // exponents
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[i][nt][e] = (z[i][nt][e] - A[nt].r[e & 1]) * (e & 1 ? al.y : al.x);
     }
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
@@ -436,8 +438,8 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
       uint32_t p[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        p[nt][0] = movmatrix_trans(pack_half2(ex2(ex[i][nt][0]), ex2(ex[i][nt][1])));
-        p[nt][1] = movmatrix_trans(pack_half2(ex2(ex[i][nt][2]), ex2(ex[i][nt][3])));
+        p[nt][0] = movmatrix_trans(pack_half2(ex2(z[i][nt][0]), ex2(z[i][nt][1])));
+        p[nt][1] = movmatrix_trans(pack_half2(ex2(z[i][nt][2]), ex2(z[i][nt][3])));
       }
       if (odd) {
         const int from = min(max(left - (nq - 1) - kTileTokens * (i0 + i), 0), kTileTokens);
@@ -794,11 +796,22 @@ struct QuantPlan {
   int split, ctas, cluster;
   size_t bytes;  // of the scratch
 };
-static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks) {
+
+// Three ways, by what a call would pay (microseconds on GB300, 8 rows a unit, back to back in a graph):
+//  * a cluster per unit, the largest power of two of CTAs whose clusters fit one wave (16 at most, each CTA two
+//    blocks at least): no second kernel, which costs about 5, but a unit cannot spread further, and lengths do not
+//    balance.  2 units of 64 blocks: 6.9 against 8.2; 8 of 256: 14.4 against 17.4; 64 of 64: 13.8 against 17.9;
+//    64 listing 81: 17.3 against 20.2.  (Clusters of 3, 6 or 12 pack badly: 64 of 64 blocks 16.9 with 3, 13.8 with 4.)
+//    So for at most 16 blocks a CTA, and where all units list the same number and fill half a wave, 40.
+//  * equal pieces of all units' blocks over one wave, merged by a second kernel: 8 units of 1024 blocks 28.8 against
+//    41.5 in clusters, 16 of 1024 38.4 against 52.8; ragged lengths balance.
+//  * with thousands of units one CTA each, which balance by themselves.
+static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks, bool listed) {
   const int wave = std::min(d.ctas[rows <= 8 ? 0 : rows <= 16 ? 1 : 2], 8 * d.sms);
   if (units > kQaSplitUnits) return {kWhole, units, 0, kQaErrBytes};
-  const int cl = std::min(kQaCluster, (blocks + 1) / 2);
-  if ((long long)blocks * units <= (long long)kQaClusterBlocks * wave / 4 && blocks <= kQaCluster * kQaClusterBlocks)
+  int cl = 16;
+  while (cl > 1 && ((long long)units * cl > wave || 2 * cl > blocks + 1)) cl /= 2;
+  if (units * cl <= wave && blocks <= (listed && 2 * units * cl > wave ? 40 : 16) * cl)
     return {kCluster, units * cl, cl, kQaErrBytes};
   const long long pieces = ((long long)units * blocks + 1) / 2;
   const int ctas = (int)std::min<long long>(wave, pieces);
@@ -814,7 +827,7 @@ static cudaError_t launch_quant_attend(const QuantArgs& a, const QuantPlan& p, c
 static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t scratch_bytes, cudaStream_t st) {
   QuantDevice d;
   if (!quant_device(&d)) return NOSA_ERR_CUDA;
-  const QuantPlan plan = quant_plan(d, a.units, a.rows, blocks);
+  const QuantPlan plan = quant_plan(d, a.units, a.rows, blocks, a.sel != nullptr);
   if (scratch_bytes < plan.bytes) return NOSA_ERR_CAPACITY;
   const size_t parts = (size_t)plan.ctas + a.units;
   unsigned char* p = static_cast<unsigned char*>(scratch);
@@ -853,7 +866,7 @@ extern "C" size_t nosa_quant_scratch_bytes(int units, int rows, int blocks) {
   QuantDevice d;
   if (units < 1 || units > (1 << 20) || rows < 1 || rows > kQaMaxRows || blocks < 1 || blocks > 16384 || !quant_device(&d))
     return 0;
-  return quant_plan(d, units, rows, blocks).bytes;
+  return std::max(quant_plan(d, units, rows, blocks, false).bytes, quant_plan(d, units, rows, blocks, true).bytes);
 }
 
 extern "C" nosa_status nosa_quant_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group,
