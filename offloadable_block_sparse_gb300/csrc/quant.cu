@@ -1,9 +1,8 @@
 // Writing the 4-bit KV block store (nosa_quant_append) and reading it back (nosa_quant_read).
 //
-// Both move a tile of 16 tokens per warp through registers only: the lanes hold the tile in the
-// store's own layout (quant_core.cuh), so each lane's codes leave (or arrive) as 16-byte words, and
-// the bf16 side is touched in whole 32-byte sectors.  Both are bound by HBM: 512 bytes of bf16 and
-// 160 of the store per token and unit.
+// Both move tiles of 16 tokens through registers only: the lanes hold a tile in the store's own layout
+// (quant_core.cuh), so each lane's codes leave (or arrive) as 16-byte words, and the bf16 side is touched
+// in whole 32-byte sectors.  A token and unit is 512 bytes of bf16 and 160 of the store.
 #include "host.h"
 #include "quant_core.cuh"
 
@@ -127,134 +126,100 @@ __device__ __forceinline__ uint32_t codes(const uint32_t (&x)[N], const CodeScal
   return w;
 }
 
+// One CTA per tile, one warp per half tile (8 tokens) of K or V: short enough for a single token, whose time is one
+// warp's path through the code, and small enough in registers for many warps.
 __global__ void __launch_bounds__(kQuantWarps * 32)
     quant_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, uint8_t* __restrict__ store,
-                        int units, int n, int max_blocks, const int32_t* __restrict__ pos,
-                        const int32_t* __restrict__ count, int tiles, int32_t* err) {
+                        int n, int max_blocks, const int32_t* __restrict__ pos, const int32_t* __restrict__ count,
+                        int tiles, int32_t* err) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int u = blockIdx.x / tiles, i = blockIdx.x % tiles;
   pdl_wait();
   pdl_launch_dependents();
-  const long long job = (long long)blockIdx.x * kQuantWarps + (threadIdx.x >> 5);
-  const int u = (int)(job / tiles), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  if (u >= units) return;
   const long long p0 = pos ? pos[u] : 0, cap = (long long)max_blocks * kBlock;
   const int c0 = count ? count[u] : n, c = min(max(c0, 0), n);
-  const long long tile = (p0 >> 4) + job % tiles;  // an arithmetic shift: negative positions round down
-  if (job % tiles == 0 && lane == 0 && err && (c0 != c || (c > 0 && (p0 < 0 || p0 + c > cap)))) atomicOr(err, kErrBounds);
-  const long long first = tile * kTileTokens;
-  if (tile < 0 || first >= cap || first >= p0 + c) return;  // cap is a multiple of 16: a tile is in or out as a whole
+  const long long tile = (p0 >> 4) + i;  // an arithmetic shift: negative positions round down
+  if (i == 0 && threadIdx.x == 0 && err && (c0 != c || (c > 0 && (p0 < 0 || p0 + c > cap)))) atomicOr(err, kErrBounds);
+  const int half = 8 * (warp >> 1);
+  const long long first = tile * kTileTokens;  // cap is a multiple of 16: a tile is in or out as a whole
+  const int rel = (int)(first - p0) + half;    // the half's first token among the new ones, -15 at least
+  if (tile < 0 || first >= cap || rel >= c || rel + 8 <= 0) return;
   uint8_t* dst = store + (size_t)u * max_blocks * kQuantBlockBytes + (size_t)tile * kTileBytes;
-  const size_t row0 = (size_t)u * n;
-  // index of the tile's token i among the new ones (-15 at least), and whether it is one of them
-  const int rel = (int)(first - p0);
-  auto index = [&](int i) { return rel + i; };
-  auto is_new = [&](int i) { return (unsigned)(rel + i) < (unsigned)c; };
+  auto is_new = [&](int j) { return (unsigned)(rel + j) < (unsigned)c; };  // the half's token j
+  auto row = [&](int j) { return ((size_t)u * n + (is_new(j) ? rel + j : 0)) * kHeadDim; };
 
-  // loads of the whole tile, issued together
-  uint4 kx[2][4];
-  uint2 vx[2][2][4];  // [half][token of the pair][group]
-  bool kin[2], vin[2][2];
+  if ((warp & 1) == 0) {
+    // K: dims 32 gr + 8 t + e of token g in word gr; a group's range over the lanes t, dealt so that lane t ends up
+    // with group t
+    const bool in = is_new(g);
+    const uint16_t* src = k + row(g) + 8 * t;
+    uint4 x[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    kin[h] = is_new(g + 8 * h);
-    const uint16_t* src = k + (row0 + (kin[h] ? index(g + 8 * h) : 0)) * kHeadDim + 8 * t;
+    for (int gr = 0; gr < 4; ++gr) x[gr] = in ? ld_stream_v4(src + 32 * gr) : make_uint4(0, 0, 0, 0);
+    uint32_t r[4], w[4], sm[4];
 #pragma unroll
-    for (int gr = 0; gr < 4; ++gr) kx[h][gr] = kin[h] ? ld_stream_v4(src + 32 * gr) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int par = 0; par < 2; ++par) {
-      vin[h][par] = is_new(8 * h + 2 * t + par);
-      const uint16_t* vs = v + (row0 + (vin[h][par] ? index(8 * h + 2 * t + par) : 0)) * kHeadDim + 4 * g;
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr)
-        vx[h][par][gr] = vin[h][par] ? __ldcs(reinterpret_cast<const uint2*>(vs + 32 * gr)) : make_uint2(0, 0);
-    }
-  }
-
-  // halves of the tile with a new token
-  const bool any[2] = {rel < c && rel + 8 > 0, rel + 8 < c};
-
-  // Ranges.  K: token g + 8 h, group gr, over the lanes t; dealt so that lane t ends up with group t.  V: token
-  // 8 h + 2 t + par, group gr, over the lanes g; lane g ends up with half g / 4, group g % 4, both tokens.
-  uint32_t kr[2], vr[2];
-  {
-    uint32_t v[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
-        const uint4& x = kx[h][gr];
-        v[h][gr] = range_of(max2_nan(max2_nan(x.x, x.y), max2_nan(x.z, x.w)), min2_nan(min2_nan(x.x, x.y), min2_nan(x.z, x.w)));
-      }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      kr[h] = deal(deal(v[h][0], v[h][2], t & 2, 2), deal(v[h][1], v[h][3], t & 2, 2), t & 1, 1);
-  }
-#pragma unroll
-  for (int par = 0; par < 2; ++par) {
-    uint32_t v[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr)
-        v[h][gr] = range_of(max2_nan(vx[h][par][gr].x, vx[h][par][gr].y), min2_nan(vx[h][par][gr].x, vx[h][par][gr].y));
-    uint32_t w[4];
-#pragma unroll
-    for (int gr = 0; gr < 4; ++gr) w[gr] = deal(v[0][gr], v[1][gr], g & 4, 16);
-    vr[par] = deal(deal(w[0], w[2], g & 2, 8), deal(w[1], w[3], g & 2, 8), g & 1, 4);
-  }
-
-  // K: dims 32 gr + 8 t + e of token g + 8 h in word gr
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (!any[h]) continue;
-    const GroupScale q = range_scale(kr[h]);
-    uint32_t w[4], sm[4];
+    for (int gr = 0; gr < 4; ++gr)
+      r[gr] = range_of(max2_nan(max2_nan(x[gr].x, x[gr].y), max2_nan(x[gr].z, x[gr].w)),
+                       min2_nan(min2_nan(x[gr].x, x[gr].y), min2_nan(x[gr].z, x[gr].w)));
+    const GroupScale q = range_scale(deal(deal(r[0], r[2], t & 2, 2), deal(r[1], r[3], t & 2, 2), t & 1, 1));
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
       sm[gr] = __shfl_sync(0xffffffffu, q.s | q.m << 16, (lane & ~3) | gr);
-      const CodeScale cs = code_scale(sm[gr] & 0xffffu, sm[gr] >> 16);
-      const uint32_t x[4] = {kx[h][gr].x, kx[h][gr].y, kx[h][gr].z, kx[h][gr].w};
-      w[gr] = codes<4>(x, cs);
+      const uint32_t y[4] = {x[gr].x, x[gr].y, x[gr].z, x[gr].w};
+      w[gr] = codes<4>(y, code_scale(sm[gr] & 0xffffu, sm[gr] >> 16));
     }
-    if (kin[h]) {
-      *reinterpret_cast<uint4*>(dst + 64 * (g + 8 * h) + 16 * t) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (in) {
+      *reinterpret_cast<uint4*>(dst + 64 * (half + g) + 16 * t) = make_uint4(w[0], w[1], w[2], w[3]);
       if (t == 0)
-        *reinterpret_cast<uint4*>(dst + kTileKs + 16 * (g + 8 * h)) =
+        *reinterpret_cast<uint4*>(dst + kTileKs + 16 * (half + g)) =
             make_uint4(__byte_perm(sm[0], sm[1], 0x5410), __byte_perm(sm[2], sm[3], 0x5410),
                        __byte_perm(sm[0], sm[1], 0x7632), __byte_perm(sm[2], sm[3], 0x7632));
     }
-  }
-
-  // V: dims 32 gr + 4 g + e of token 8 h + 2 t + par in half `par` of word gr
-  const GroupScale q0 = range_scale(vr[0]), q1 = range_scale(vr[1]);
-  const uint32_t sp = q0.s | q1.s << 16, mp = q0.m | q1.m << 16;  // of half g / 4, group g % 4
-  {
-    uint8_t* meta = dst + kTileVs + 16 * (4 * (g >> 2) + t) + 4 * (g & 3);
-    const bool in0 = g & 4 ? vin[1][0] : vin[0][0], in1 = g & 4 ? vin[1][1] : vin[0][1];
-    if (in0 && in1) {
-      *reinterpret_cast<uint32_t*>(meta) = sp;
-      *reinterpret_cast<uint32_t*>(meta + kTileVm - kTileVs) = mp;
-    } else if (in0 || in1) {  // the pair's other token stays as it is
-      *reinterpret_cast<uint16_t*>(meta + 2 * in1) = (uint16_t)(sp >> (16 * in1));
-      *reinterpret_cast<uint16_t*>(meta + kTileVm - kTileVs + 2 * in1) = (uint16_t)(mp >> (16 * in1));
-    }
-  }
+  } else {
+    // V: dims 32 gr + 4 g + e of token 2 t + par in half `par` of word gr; a group's range over the lanes g, dealt so
+    // that lane g ends up with group g % 4 of token g / 4 of the pair
+    const bool in[2] = {is_new(2 * t), is_new(2 * t + 1)};
+    uint2 x[2][4];
+    uint32_t r[2][4], w[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (!any[h]) continue;
-    uint32_t w[4];
+    for (int par = 0; par < 2; ++par) {
+      const uint16_t* src = v + row(2 * t + par) + 4 * g;
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr)
+        x[par][gr] = in[par] ? __ldcs(reinterpret_cast<const uint2*>(src + 32 * gr)) : make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int par = 0; par < 2; ++par)
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr)
+        r[par][gr] = range_of(max2_nan(x[par][gr].x, x[par][gr].y), min2_nan(x[par][gr].x, x[par][gr].y));
+    uint32_t d[4];
+#pragma unroll
+    for (int gr = 0; gr < 4; ++gr) d[gr] = deal(r[0][gr], r[1][gr], g & 4, 16);
+    const GroupScale q = range_scale(deal(deal(d[0], d[2], g & 2, 8), deal(d[1], d[3], g & 2, 8), g & 1, 4));
+    if (g & 4 ? in[1] : in[0]) {
+      uint8_t* meta = dst + kTileVs + 16 * ((half >> 1) + t) + 4 * (g & 3) + 2 * (g >> 2);
+      *reinterpret_cast<uint16_t*>(meta) = (uint16_t)q.s;
+      *reinterpret_cast<uint16_t*>(meta + kTileVm - kTileVs) = (uint16_t)q.m;
+    }
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
-      const uint32_t s2 = __shfl_sync(0xffffffffu, sp, 16 * h + 4 * gr + t), m2 = __shfl_sync(0xffffffffu, mp, 16 * h + 4 * gr + t);
-      const uint32_t x0[2] = {vx[h][0][gr].x, vx[h][0][gr].y}, x1[2] = {vx[h][1][gr].x, vx[h][1][gr].y};
-      w[gr] = codes<2>(x0, code_scale(s2 & 0xffffu, m2 & 0xffffu)) | codes<2>(x1, code_scale(s2 >> 16, m2 >> 16)) << 16;
-    }
-    uint8_t* codes = dst + kTileV + 512 * h + 16 * lane;
-    if (vin[h][0] && vin[h][1]) {
-      *reinterpret_cast<uint4*>(codes) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if (vin[h][0] || vin[h][1]) {
-      const int par = vin[h][1];
+      uint32_t half_word[2];
 #pragma unroll
-      for (int gr = 0; gr < 4; ++gr) *reinterpret_cast<uint16_t*>(codes + 4 * gr + 2 * par) = (uint16_t)(w[gr] >> (16 * par));
+      for (int par = 0; par < 2; ++par) {
+        const uint32_t sm = __shfl_sync(0xffffffffu, q.s | q.m << 16, 16 * par + 4 * gr + t);
+        const uint32_t y[2] = {x[par][gr].x, x[par][gr].y};
+        half_word[par] = codes<2>(y, code_scale(sm & 0xffffu, sm >> 16));
+      }
+      w[gr] = half_word[0] | half_word[1] << 16;
+    }
+    uint8_t* out = dst + kTileV + 64 * half + 16 * lane;
+    if (in[0] && in[1]) {
+      *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if (in[0] || in[1]) {  // the pair's other token stays as it is
+      const int par = in[1];
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr) *reinterpret_cast<uint16_t*>(out + 4 * gr + 2 * par) = (uint16_t)(w[gr] >> (16 * par));
     }
   }
 }
@@ -347,10 +312,10 @@ extern "C" nosa_status nosa_quant_append(const uint16_t* k, const uint16_t* v, u
     return NOSA_ERR_INVALID_ARG;
   // tiles that n tokens touch at most, from any starting position
   const long long tiles = ((long long)n_tokens + 2 * kTileTokens - 2) / kTileTokens;
-  const long long ctas = (units * tiles + kQuantWarps - 1) / kQuantWarps;
+  const long long ctas = units * tiles;
   if (ctas >= (1ll << 31) || (long long)units * max_blocks >= (1ll << 31)) return NOSA_ERR_INVALID_ARG;
   return launched(launch_ex(quant_append_kernel, dim3((unsigned)ctas), dim3(kQuantWarps * 32), 0,
-                            static_cast<cudaStream_t>(stream), true, 0, k, v, store, units, n_tokens, max_blocks, pos,
+                            static_cast<cudaStream_t>(stream), true, 0, k, v, store, n_tokens, max_blocks, pos,
                             count, (int)tiles, err_out));
 }
 
