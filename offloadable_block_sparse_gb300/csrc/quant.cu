@@ -35,17 +35,9 @@ __device__ __forceinline__ GroupScale range_scale(uint32_t range) {
   return group_scale(-bf16_to_float((uint16_t)(range >> 16)), bf16_to_float((uint16_t)range));
 }
 
-// Code of x in a group: clamp(rint((x - m) / s), 0, 15), exactly as the IEEE quotient rounds.  r is
-// 1 / s rounded, so rint((x - m) r) is off by at most one, and only next to a border between two
-// codes; the remainder e = (x - m) - n s is exact there (n s has at most 16 bits, and the two terms are
-// within a factor of two of each other, or n = 0) and says which side x is on.
+// Code of x in a group: clamp(rint((x - m) / s), 0, 15), for s > 0.
 __device__ __forceinline__ uint32_t exact_code(float x, float m, float s) {
-  const float d = x - m;
-  float n = rintf(d * __frcp_rn(s));
-  const float e = 2.f * fmaf(-n, s, d);
-  if (fabsf(e) > s || (fabsf(e) == s && (((int)n) & 1))) n += copysignf(1.f, e);
-  n = fminf(fmaxf(n, 0.f), 15.f);
-  return s > 0.f ? (uint32_t)n : 0u;  // s = 0 or NaN: code 0
+  return (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(x - m, s)), 0.f), 15.f);
 }
 __device__ __noinline__ uint32_t exact_codes(uint32_t x0, uint32_t x1, float s, float m) {
   uint32_t w = 0;
@@ -79,13 +71,14 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ float max3_abs(float a, float b, float c) { return fmaxf(a, fmaxf(fabsf(b), fabsf(c))); }
 
 // A group's scale as the code loop wants it.
 struct CodeScale {
   float s, m;
-  uint64_t r2, negm2;  // 1 / s (to 2^-23) and -m, twice
-  bool plain;          // s a normal f16: no code can leave 0 .. 15 (s is within 2^-11 of the range's fifteenth)
+  uint64_t r2, negs2, negm2;  // 1 / s (to 2^-23), -s and -m, twice
+  // s is a normal f16: no code can leave 0 .. 15 (s is within 2^-11 of the range's fifteenth).  Otherwise it is
+  // subnormal, or zero or a NaN, and then all codes are 0.
+  bool plain;
 };
 __device__ __forceinline__ CodeScale code_scale(uint32_t s_bits, uint32_t m_bits) {
   CodeScale c;
@@ -94,34 +87,37 @@ __device__ __forceinline__ CodeScale code_scale(uint32_t s_bits, uint32_t m_bits
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(c.s));
   c.r2 = pair(r, r);
+  c.negs2 = pair(-c.s, -c.s);
   c.negm2 = pair(-c.m, -c.m);
   c.plain = s_bits - 0x0400u < 0x7c00u - 0x0400u;
   return c;
 }
 
-// Codes of 2 N bf16 values, 4 bits each.  t = (x - m) r is within 2^-17 of the quotient, so its rounding is
-// the quotient's unless t is that near to a border: then, and for an odd scale, the codes are taken exactly
-// (a division per value instead would cost more than the value's share of the memory time).  Adding
-// 1.5 x 2^23 rounds t to the integer that then stands in the sum's low bits.
+// Codes of 2 N bf16 values, 4 bits each, without a division: t = d r for d = x - m, then one Newton step on the
+// remainder, t + (d - t s) r.  The remainder is exact (s has 11 bits, and the terms cancel), so a quotient that lies on
+// a border between two codes, k + 1/2, comes out as just that and goes to the even code; ties are frequent with
+// bf16 values (one in a thousand).  A quotient off the border is at least a unit of d's last place away from it in d,
+// which t resolves unless d fills all of float32's bits (x below 2^-15 of m).  Adding 1.5 x 2^23 rounds t to the
+// integer that then stands in the sum's low bits.
 template <int N>
 __device__ __forceinline__ uint32_t codes(const uint32_t (&x)[N], const CodeScale& c) {
-  const uint64_t magic = pair(12582912.f, 12582912.f), negmagic = pair(-12582912.f, -12582912.f), minus1 = pair(-1.f, -1.f);
+  const uint64_t magic = pair(12582912.f, 12582912.f);
   uint32_t w = 0xC0C00000u;  // what the constants' bits 0x4B400000 << 4 e add up to, negated
-  float off = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const uint64_t t = mul2(add2(pair(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), c.negm2), c.r2);
-    const uint64_t u = add2(t, magic);
-    float u0, u1, f0, f1;
-    unpair(fma2(add2(u, negmagic), minus1, t), f0, f1);
-    unpair(u, u0, u1);
-    off = max3_abs(off, f0, f1);
+    const uint64_t d = add2(pair(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), c.negm2);
+    const uint64_t t = mul2(d, c.r2);
+    float u0, u1;
+    unpair(add2(fma2(fma2(t, c.negs2, d), c.r2, t), magic), u0, u1);
     w += __float_as_uint(u0) << (8 * i);
     w += __float_as_uint(u1) << (8 * i + 4);
   }
-  if (!c.plain || off > 0.5f - 0x1p-16f) {
-    w = exact_codes(x[0], x[1], c.s, c.m);
-    if constexpr (N == 4) w |= exact_codes(x[2], x[3], c.s, c.m) << 16;
+  if (!c.plain) {
+    w = 0;
+    if (c.s > 0.f) {
+      w = exact_codes(x[0], x[1], c.s, c.m);
+      if constexpr (N == 4) w |= exact_codes(x[2], x[3], c.s, c.m) << 16;
+    }
   }
   return w;
 }
@@ -229,7 +225,7 @@ __device__ __forceinline__ float code_float(uint32_t w, int e) {
   return __uint_as_float(((w >> (4 * e)) & 15u) | 0x4B000000u) - 8388608.f;
 }
 
-__global__ void __launch_bounds__(kQuantWarps * 32)
+__global__ void __launch_bounds__(kQuantWarps * 32, 8)
     quant_read_kernel(const uint8_t* __restrict__ store, int units, int max_blocks, const int32_t* __restrict__ blocks,
                       int n_blocks, const int32_t* __restrict__ lens, uint16_t* __restrict__ kv, int32_t* err) {
   pdl_wait();
