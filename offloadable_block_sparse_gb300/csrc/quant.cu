@@ -72,25 +72,29 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// A group's scale as the code loop wants it.
-struct CodeScale {
-  float s, m;
-  uint64_t r2, negs2, negm2;  // 1 / s (to 2^-23), -s and -m, twice
-  // s is a normal f16: no code can leave 0 .. 15 (s is within 2^-11 of the range's fifteenth).  Otherwise it is
-  // subnormal, or zero or a NaN, and then all codes are 0.
-  bool plain;
+// What a group's owner computes and the code loop wants: m and s as f16 bits, and -m, -s and 1 / s (to 2^-23).
+struct GroupCode {
+  GroupScale q;
+  float negm, negs, r;
+  // s is a normal f16: no code can leave 0 .. 15 (s is within 2^-11 of the range's fifteenth)
+  __device__ __forceinline__ bool plain() const { return q.s - 0x0400u < 0x7c00u - 0x0400u; }
 };
-__device__ __forceinline__ CodeScale code_scale(uint32_t s_bits, uint32_t m_bits) {
-  CodeScale c;
-  c.s = half_bits_to_float(s_bits);
-  c.m = half_bits_to_float(m_bits);
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(c.s));
-  c.r2 = pair(r, r);
-  c.negs2 = pair(-c.s, -c.s);
-  c.negm2 = pair(-c.m, -c.m);
-  c.plain = s_bits - 0x0400u < 0x7c00u - 0x0400u;
+__device__ __forceinline__ GroupCode group_code(uint32_t range) {
+  GroupCode c;
+  c.q = range_scale(range);
+  c.negm = -half_bits_to_float(c.q.m);
+  c.negs = -half_bits_to_float(c.q.s);
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(c.r) : "f"(-c.negs));
   return c;
+}
+// The group of lane `owner`, each value twice.
+struct CodeScale {
+  uint64_t negm2, negs2, r2;
+};
+__device__ __forceinline__ CodeScale code_scale(const GroupCode& c, int owner) {
+  const float m = __shfl_sync(0xffffffffu, c.negm, owner), s = __shfl_sync(0xffffffffu, c.negs, owner);
+  const float r = __shfl_sync(0xffffffffu, c.r, owner);
+  return {pair(m, m), pair(s, s), pair(r, r)};
 }
 
 // Codes of 2 N bf16 values, 4 bits each, without a division: t = d r for d = x - m, then one Newton step on the
@@ -99,8 +103,9 @@ __device__ __forceinline__ CodeScale code_scale(uint32_t s_bits, uint32_t m_bits
 // bf16 values (one in a thousand).  A quotient off the border is at least a unit of d's last place away from it in d,
 // which t resolves unless d fills all of float32's bits (x below 2^-15 of m).  Adding 1.5 x 2^23 rounds t to the
 // integer that then stands in the sum's low bits.
+// plain = false (some group of the warp has a subnormal s, zero or a NaN): by division, and zeros for the latter two.
 template <int N>
-__device__ __forceinline__ uint32_t codes(const uint32_t (&x)[N], const CodeScale& c) {
+__device__ __forceinline__ uint32_t codes(const uint32_t (&x)[N], const CodeScale& c, bool plain) {
   const uint64_t magic = pair(12582912.f, 12582912.f);
   uint32_t w = 0xC0C00000u;  // what the constants' bits 0x4B400000 << 4 e add up to, negated
 #pragma unroll
@@ -112,11 +117,14 @@ __device__ __forceinline__ uint32_t codes(const uint32_t (&x)[N], const CodeScal
     w += __float_as_uint(u0) << (8 * i);
     w += __float_as_uint(u1) << (8 * i + 4);
   }
-  if (!c.plain) {
+  if (!plain) {
+    float negs, negm, unused;
+    unpair(c.negs2, negs, unused);
+    unpair(c.negm2, negm, unused);
     w = 0;
-    if (c.s > 0.f) {
-      w = exact_codes(x[0], x[1], c.s, c.m);
-      if constexpr (N == 4) w |= exact_codes(x[2], x[3], c.s, c.m) << 16;
+    if (negs < 0.f) {
+      w = exact_codes(x[0], x[1], -negs, -negm);
+      if constexpr (N == 4) w |= exact_codes(x[2], x[3], -negs, -negm) << 16;
     }
   }
   return w;
@@ -152,24 +160,23 @@ __global__ void __launch_bounds__(kQuantWarps * 32)
     uint4 x[4];
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) x[gr] = in ? ld_stream_v4(src + 32 * gr) : make_uint4(0, 0, 0, 0);
-    uint32_t r[4], w[4], sm[4];
+    uint32_t r[4], w[4];
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr)
       r[gr] = range_of(max2_nan(max2_nan(x[gr].x, x[gr].y), max2_nan(x[gr].z, x[gr].w)),
                        min2_nan(min2_nan(x[gr].x, x[gr].y), min2_nan(x[gr].z, x[gr].w)));
-    const GroupScale q = range_scale(deal(deal(r[0], r[2], t & 2, 2), deal(r[1], r[3], t & 2, 2), t & 1, 1));
+    const GroupCode q = group_code(deal(deal(r[0], r[2], t & 2, 2), deal(r[1], r[3], t & 2, 2), t & 1, 1));
+    const bool plain = __all_sync(0xffffffffu, q.plain() || !in);
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
-      sm[gr] = __shfl_sync(0xffffffffu, q.s | q.m << 16, (lane & ~3) | gr);
       const uint32_t y[4] = {x[gr].x, x[gr].y, x[gr].z, x[gr].w};
-      w[gr] = codes<4>(y, code_scale(sm[gr] & 0xffffu, sm[gr] >> 16));
+      w[gr] = codes<4>(y, code_scale(q, (lane & ~3) | gr), plain);
     }
     if (in) {
       *reinterpret_cast<uint4*>(dst + 64 * (half + g) + 16 * t) = make_uint4(w[0], w[1], w[2], w[3]);
-      if (t == 0)
-        *reinterpret_cast<uint4*>(dst + kTileKs + 16 * (half + g)) =
-            make_uint4(__byte_perm(sm[0], sm[1], 0x5410), __byte_perm(sm[2], sm[3], 0x5410),
-                       __byte_perm(sm[0], sm[1], 0x7632), __byte_perm(sm[2], sm[3], 0x7632));
+      uint8_t* meta = dst + kTileKs + 16 * (half + g) + 2 * t;
+      *reinterpret_cast<uint16_t*>(meta) = (uint16_t)q.q.s;
+      *reinterpret_cast<uint16_t*>(meta + 8) = (uint16_t)q.q.m;
     }
   } else {
     // V: dims 32 gr + 4 g + e of token 2 t + par in half `par` of word gr; a group's range over the lanes g, dealt so
@@ -192,22 +199,23 @@ __global__ void __launch_bounds__(kQuantWarps * 32)
     uint32_t d[4];
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) d[gr] = deal(r[0][gr], r[1][gr], g & 4, 16);
-    const GroupScale q = range_scale(deal(deal(d[0], d[2], g & 2, 8), deal(d[1], d[3], g & 2, 8), g & 1, 4));
-    if (g & 4 ? in[1] : in[0]) {
+    const GroupCode q = group_code(deal(deal(d[0], d[2], g & 2, 8), deal(d[1], d[3], g & 2, 8), g & 1, 4));
+    const bool mine = g & 4 ? in[1] : in[0];
+    const bool plain = __all_sync(0xffffffffu, q.plain() || !mine);
+    if (mine) {
       uint8_t* meta = dst + kTileVs + 16 * ((half >> 1) + t) + 4 * (g & 3) + 2 * (g >> 2);
-      *reinterpret_cast<uint16_t*>(meta) = (uint16_t)q.s;
-      *reinterpret_cast<uint16_t*>(meta + kTileVm - kTileVs) = (uint16_t)q.m;
+      *reinterpret_cast<uint16_t*>(meta) = (uint16_t)q.q.s;
+      *reinterpret_cast<uint16_t*>(meta + kTileVm - kTileVs) = (uint16_t)q.q.m;
     }
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
       uint32_t half_word[2];
 #pragma unroll
       for (int par = 0; par < 2; ++par) {
-        const uint32_t sm = __shfl_sync(0xffffffffu, q.s | q.m << 16, 16 * par + 4 * gr + t);
         const uint32_t y[2] = {x[par][gr].x, x[par][gr].y};
-        half_word[par] = codes<2>(y, code_scale(sm & 0xffffu, sm >> 16));
+        half_word[par] = codes<2>(y, code_scale(q, 16 * par + 4 * gr + t), plain);
       }
-      w[gr] = half_word[0] | half_word[1] << 16;
+      w[gr] = __byte_perm(half_word[0], half_word[1], 0x5410);  // (a token that is not new has any bits)
     }
     uint8_t* out = dst + kTileV + 64 * half + 16 * lane;
     if (in[0] && in[1]) {
