@@ -17,8 +17,8 @@
 //   P^T by movmatrix of the f16-packed weights, times s per group
 //   O^T (128 dims x 8 rows) += V codes^T . P^T      8 MMAs, + 1 for m and the sum
 // The query rows of a unit (q heads x query tokens, at most 32) are NT tiles of 8.  Weights are
-// exp2(logit - R): R follows a row's maximum only when that outgrows it by 2^14, so the usual tile needs
-// no rescaling, and is set so that weight x s stays within f16 (R rises with a scale of 2 or more).
+// exp2(logit - R): R follows a row's maximum only when that would get a weight above 2^14, so the usual tile
+// needs no rescaling, and is set so that weight x s stays within f16 (R rises with a scale of 2 or more).
 // A CTA merges its warps in shared memory; a unit's parts, where several CTAs share it, merge in a second kernel.
 #include <cooperative_groups.h>
 
@@ -105,8 +105,8 @@ __device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
   const __half2 v = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ float half_lo(uint32_t a) { return half_bits_to_float(a & 0xffffu); }
-__device__ __forceinline__ float half_hi(uint32_t a) { return half_bits_to_float(a >> 16); }
+__device__ __forceinline__ float half_lo(uint32_t a) { return __low2float(*reinterpret_cast<const __half2*>(&a)); }
+__device__ __forceinline__ float half_hi(uint32_t a) { return __high2float(*reinterpret_cast<const __half2*>(&a)); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -166,21 +166,17 @@ __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], cons
   alpha[1] = scale * __shfl_sync(0xffffffffu, inv, 8 * t + 4);
 }
 
-// One warp's running state for a tile of 8 rows: references of rows 2t, 2t + 1 in units of the scores (an
-// exponent is (z - r) alpha, so that a huge score less itself is zero), O^T (codes' part, in units of 2^-24,
-// or 2^-20 for odd dims), and the m part: rows 0..3 the groups, row 4 the softmax sum.
+// One warp's running state for a tile of 8 rows: of rows 2t, 2t + 1 the score that has the weight 2^14, the largest
+// allowed (a score z has 2^((z - top) alpha + 14), so that a huge score less itself is zero); O^T (codes' part, in
+// units of 2^-24, or 2^-20 for odd dims); and the m part: rows 0..3 the groups, row 4 the softmax sum.
+constexpr float kTopWeight = 14.f;
 struct RowTile {
-  float r[2];
+  float top[2];
   float o[8][4];
   float c[4];
 };
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-// Keeps the halves of w whose token (first, first + 1) is below n.
-__device__ __forceinline__ uint32_t keep_tokens(uint32_t w, int first, int n) {
-  return first + 1 < n ? w : first < n ? w & 0xffffu : 0u;
-}
 
 // The V side of a tile as a lane holds it: codes and scales of token pairs t, t + 4, and the rows of the m
 // operand (group g's minima for g < 4, ones for g = 4, zeros).
@@ -195,7 +191,7 @@ __device__ __forceinline__ void load_values(ValueRegs& V, const unsigned char* t
     V.c[h] = *reinterpret_cast<const uint4*>(tile + kTileV + 512 * h + 16 * lane);
     V.s[h] = *reinterpret_cast<const uint4*>(tile + kTileVs + 16 * (4 * h + t));
     const uint32_t m = *reinterpret_cast<const uint32_t*>(tile + kTileVm + 16 * (4 * h + t) + 4 * (g & 3));
-    V.m[h] = g < 4 ? m : g == 4 ? 0x3C003C00u : 0u;
+    V.m[h] = (m & (g < 4 ? 0xffffffffu : 0u)) | (g == 4 ? 0x3C003C00u : 0u);
   }
 }
 
@@ -218,71 +214,31 @@ __device__ __forceinline__ void add_values(RowTile (&A)[NT], const ValueRegs& V,
   for (int nt = 0; nt < NT; ++nt) mma_f16(A[nt].c, V.m[0], 0u, V.m[1], 0u, p[nt][0], p[nt][1]);
 }
 
-// The rare tile at the end of a context with several query tokens where a token that only some of the rows
-// see has a NaN group: 0 x NaN must not reach the others, so the tokens from `from` on are added one at a
-// time, each into the rows that gave it a weight, after those before them together.
-__device__ __noinline__ void add_values_by_token(RowTile& A, const unsigned char* tile, uint32_t p0, uint32_t p1, int from) {
-  const int lane = threadIdx.x & 31, t = lane & 3;
-  ValueRegs V;
-  load_values(V, tile, lane);
-  for (int tok = max(from, 0) - 1; tok < kTileTokens; ++tok) {
-    ValueRegs S = V;
-    RowTile D[1];
-    uint32_t w[1][2];
-#pragma unroll
-    for (int mt = 0; mt < 8; ++mt) D[0].o[mt][0] = D[0].o[mt][1] = D[0].o[mt][2] = D[0].o[mt][3] = 0.f;
-    D[0].c[0] = D[0].c[1] = D[0].c[2] = D[0].c[3] = 0.f;
-    const bool together = tok < from;  // the first round: the tokens below `from`
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int first = 2 * t + 8 * h;
-      const uint32_t keep = together ? keep_tokens(0xffffffffu, first, from)
-                                     : (tok == first ? 0x0000ffffu : tok == first + 1 ? 0xffff0000u : 0u);
-      w[0][h] = (h ? p1 : p0) & keep;
-      S.s[h] = make_uint4(V.s[h].x & keep, V.s[h].y & keep, V.s[h].z & keep, V.s[h].w & keep);
-      S.m[h] = V.m[h] & keep;
-    }
-    add_values<1>(D, S, w);
-    // the token's weight for rows 2t, 2t + 1 is held by lane (row, pair of the token)
-    const uint32_t mine = (tok >> 3) == 1 ? w[0][1] : w[0][0];
-    const int owner = (max(tok, 0) & 7) >> 1;
-    const bool in0 = __shfl_sync(0xffffffffu, mine, 8 * t + owner) != 0 || together;
-    const bool in1 = __shfl_sync(0xffffffffu, mine, 8 * t + 4 + owner) != 0 || together;
-#pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
-      A.o[mt][0] += in0 ? D[0].o[mt][0] : 0.f;
-      A.o[mt][1] += in1 ? D[0].o[mt][1] : 0.f;
-      A.o[mt][2] += in0 ? D[0].o[mt][2] : 0.f;
-      A.o[mt][3] += in1 ? D[0].o[mt][3] : 0.f;
-    }
-    A.c[0] += in0 ? D[0].c[0] : 0.f;
-    A.c[1] += in1 ? D[0].c[1] : 0.f;
-    A.c[2] += in0 ? D[0].c[2] : 0.f;
-    A.c[3] += in1 ? D[0].c[3] : 0.f;
-  }
-}
-
-// A half that is infinite or NaN, in either position.
-__device__ __forceinline__ bool not_finite2(uint32_t w) {
-  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
-}
-
-// Clears the V scales and minima of the stage's tokens from `left` on: behind the context the store may hold
-// anything, and 0 x NaN is a NaN (the codes are finite as they stand).  Returns whether a token that only some
-// rows see, from `seen` on, has a NaN group.
-__device__ __noinline__ bool clear_tail(unsigned char* stage, int left, int seen) {
-  const int lane = threadIdx.x & 31;
-  bool odd = false;
+// Prepares a stage that not every row sees as a whole (left: tokens of the context from its first on).  Behind the
+// context the store may hold anything, and 0 x NaN is a NaN, so those tokens' V scales and minima are cleared (codes
+// are finite as they stand).  So is a NaN group of a token that only some rows see: the rows that see it get a bit of
+// `poison`, and their dims of that group a NaN in the end.
+__device__ __forceinline__ void clear_tail(unsigned char* stage, int* poison, int left, int nq, int rows, int lane) {
+#pragma unroll 1
   for (int i = lane; i < kStageTokens / 2 * 8; i += 32) {  // [tile][s, m][token pair][group] words of two tokens
-    const int first = (i >> 6) * kTileTokens + 2 * ((i >> 2) & 7);
     uint32_t* w = reinterpret_cast<uint32_t*>(stage + (i >> 6) * kTileBytes + kTileVs) + (i & 63);
-    const uint32_t x = keep_tokens(*w, first, left);
+    uint32_t x = *w;
+#pragma unroll 1
+    for (int par = 0; par < 2; ++par) {
+      const int token = (i >> 6) * kTileTokens + 2 * ((i >> 2) & 7) + par, late = token - (left - nq);
+      const uint32_t mask = par ? 0xffff0000u : 0x0000ffffu;
+      if (late >= nq) {
+        x &= ~mask;
+      } else if (late > 0 && (x & mask & 0x7c007c00u) == (mask & 0x7c007c00u)) {
+        x &= ~mask;
+        for (int row = 0; row < rows; ++row)
+          if (row % nq >= late) atomicOr(&poison[row], 1 << (i & 3));
+      }
+    }
     *w = x;
-    odd |= not_finite2(x & ~keep_tokens(0xffffffffu, first, seen));
   }
   fence_proxy_async_smem();  // the next bulk copy into the stage comes after these writes
   __syncwarp();
-  return __any_sync(0xffffffffu, odd);
 }
 
 // The query side in shared memory, for more than one row tile (registers hold it for one).
@@ -294,17 +250,22 @@ struct QueryShared {
 static_assert(kQaWarps >= 4, "a warp per row tile loads the queries");
 static_assert(sizeof(QueryShared) == 2432, "quant_smem_bytes");
 
+// The 2^24 that the codes lack go into the K scales (8 products a tile), or for one row tile into alpha and, the
+// other way, into the m part (4).
+__host__ __device__ constexpr float code_unit(int nt) { return nt == 1 ? 1.f : 0x1p24f; }
+
 // One stage (two tiles, 32 tokens) for all row tiles; left: tokens of the context from the stage's first on.
-// One row tile takes both tiles at once, so that their chains of dependent operations overlap; more row tiles
+// One or two row tiles take both tiles at once, so that their chains of dependent operations overlap; four row tiles
 // overlap by themselves and take one tile at a time, which keeps them in registers.
 template <int NT>
 __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile& Q, const float (&alpha1)[2],
-                                              const QueryShared* qs, unsigned char* stage, int left, int nq, int rows, int lane) {
-  constexpr int kTiles = NT == 1 ? 2 : 1;
+                                              const QueryShared* qs, unsigned char* stage, int* poison, int left, int nq,
+                                              int rows, int lane) {
+  constexpr int kTiles = NT <= 2 ? 2 : 1;
+  constexpr float kCodeUnit = code_unit(NT);
   const int g = lane >> 2, t = lane & 3;
   const bool tail = left - (nq - 1) < kStageTokens;  // some row does not see the whole stage
-  bool odd = false;
-  if (tail) odd = clear_tail(stage, left, left - (nq - 1));
+  if (tail) clear_tail(stage, poison, left, nq, rows, lane);
   // the largest V scale of the stage: below 2, weights up to 2^14 times scales stay within f16
   const uint4 vs = *reinterpret_cast<const uint4*>(stage + (lane >> 3 & 1) * kTileBytes + kTileVs + 16 * (lane & 7));
   const uint32_t vmax2 = max_half2(max_half2(vs.x, vs.y), max_half2(vs.z, vs.w));
@@ -325,14 +286,17 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
         kc[i][h] = *reinterpret_cast<const uint4*>(tile + 64 * (g + 8 * h) + 16 * t);
         const uint2 s = *reinterpret_cast<const uint2*>(tile + kTileKs + 16 * (g + 8 * h));
         km[h] = *reinterpret_cast<const uint32_t*>(tile + kTileKs + 16 * (g + 8 * h) + 8 + 4 * (t & 1));
-        // the 2^24 that the codes lack
-        ks[i][h][0] = half_lo(s.x) * 0x1p24f;
-        ks[i][h][1] = half_hi(s.x) * 0x1p24f;
-        ks[i][h][2] = half_lo(s.y) * 0x1p24f;
-        ks[i][h][3] = half_hi(s.y) * 0x1p24f;
+        ks[i][h][0] = half_lo(s.x) * kCodeUnit;
+        ks[i][h][1] = half_hi(s.x) * kCodeUnit;
+        ks[i][h][2] = half_lo(s.y) * kCodeUnit;
+        ks[i][h][3] = half_hi(s.y) * kCodeUnit;
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_f16_k8(z[i][nt], km[0], km[1], NT == 1 ? Q.sums : qs[nt].sums[lane]);
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_f16_k8(z[i][nt], km[0], km[1], NT == 1 ? Q.sums : qs[nt].sums[lane]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[i][nt][e] *= 0x1p-24f * kCodeUnit;
+      }
     }
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
@@ -380,16 +344,15 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
           }
     }
 
-    // whether the references hold: no row's maximum has outgrown its own by 14
+    // whether the references hold: no score above its row's top
     bool raise = large;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float best = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
         if (kTiles == 2) best = fmaxf(best, fmaxf(z[kTiles - 1][nt][e], z[kTiles - 1][nt][e + 2]));
-        raise |= (best - A[nt].r[e]) * (e ? al.y : al.x) > 14.f;
+        raise |= best > A[nt].top[e];
       }
     }
     if (__any_sync(0xffffffffu, raise)) {
@@ -398,7 +361,7 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
       for (int o = 1; o < 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
       // vmax < 2^e: weights up to 2^limit keep the products below 2^15 (a NaN scale sets no limit)
       if (!(vmax <= 65504.f)) vmax = 0.f;
-      const float limit = (float)(14 - max((int)(__float_as_uint(vmax) >> 23) - 127, 0));
+      const float limit = kTopWeight - (float)max((int)(__float_as_uint(vmax) >> 23) - 127, 0);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -409,10 +372,10 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
           if (kTiles == 2) best = fmaxf(best, fmaxf(z[kTiles - 1][nt][e], z[kTiles - 1][nt][e + 2]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-          const float old = A[nt].r[e];
-          if ((best - old) * al > limit) {  // the row's lanes agree; rows differ
-            const float r = best - (limit - 4.f) / al, f = ex2((old - r) * al);
-            A[nt].r[e] = r;
+          const float old = A[nt].top[e];
+          if ((best - old) * al + kTopWeight > limit) {  // the row's lanes agree; rows differ
+            const float top = best + (kTopWeight + 4.f - limit) / al, f = ex2((old - top) * al);
+            A[nt].top[e] = top;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
               A[nt].o[mt][e] *= f;
@@ -430,7 +393,7 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[i][nt][e] = (z[i][nt][e] - A[nt].r[e & 1]) * (e & 1 ? al.y : al.x);
+        for (int e = 0; e < 4; ++e) z[i][nt][e] = fmaf(z[i][nt][e] - A[nt].top[e & 1], e & 1 ? al.y : al.x, kTopWeight);
     }
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
@@ -441,19 +404,9 @@ __device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile&
         p[nt][0] = movmatrix_trans(pack_half2(ex2(z[i][nt][0]), ex2(z[i][nt][1])));
         p[nt][1] = movmatrix_trans(pack_half2(ex2(z[i][nt][2]), ex2(z[i][nt][3])));
       }
-      if (odd) {
-        const int from = min(max(left - (nq - 1) - kTileTokens * (i0 + i), 0), kTileTokens);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          RowTile B = A[nt];  // a copy, so that A itself stays in registers
-          add_values_by_token(B, tile0 + i * kTileBytes, p[nt][0], p[nt][1], from);
-          A[nt] = B;
-        }
-      } else {
-        ValueRegs V;
-        load_values(V, tile0 + i * kTileBytes, lane);
-        add_values<NT>(A, V, p);
-      }
+      ValueRegs V;
+      load_values(V, tile0 + i * kTileBytes, lane);
+      add_values<NT>(A, V, p);
     }
   }
 }
@@ -489,6 +442,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
   __shared__ int2 list[kQaList];  // (row of the store, tokens of the context from the block on)
   __shared__ float wr[kQaWarps][8 * NT], wl[kQaWarps][8 * NT];
   __shared__ int scan[32], found[2];
+  __shared__ int poison[kQaMaxRows];  // [row]: groups that end as NaN
   __shared__ float2 merged[8 * NT];  // a cluster CTA's references and sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (lane == 0) {
@@ -561,6 +515,8 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
       todo = 0;
     }
     if (threadIdx.x == 0 && first == 0 && rank == 0 && len != a.lens[u]) atomicOr(a.err, kErrBounds);
+    if (threadIdx.x < kQaMaxRows) poison[threadIdx.x] = 0;
+    if (a.nq > 1) __syncthreads();
     QueryTile Q;
     RowTile A[NT];
     float alpha1[2];
@@ -568,7 +524,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (NT == 1 || warp == nt) {
-          load_query(Q, alpha1, a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale);
+          load_query(Q, alpha1, a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale * (0x1p24f / code_unit(NT)));
           if (NT > 1) {
 #pragma unroll
             for (int gr = 0; gr < 4; ++gr)
@@ -577,7 +533,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
             qs[nt].alpha[lane] = make_float2(alpha1[0], alpha1[1]);
           }
         }
-        A[nt].r[0] = A[nt].r[1] = kNoRef;
+        A[nt].top[0] = A[nt].top[1] = kNoRef;
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) A[nt].o[mt][0] = A[nt].o[mt][1] = A[nt].o[mt][2] = A[nt].o[mt][3] = 0.f;
         A[nt].c[0] = A[nt].c[1] = A[nt].c[2] = A[nt].c[3] = 0.f;
@@ -629,7 +585,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
         const int st = done % kQaStages;
         late |= !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][st], done / kQaStages & 1, kWaitCycles));
         if (late) continue;  // let what is in flight land, and start no more
-        process_stage<NT>(A, Q, alpha1, qs, ring + st * kStageBytes4, tokens[warp][st], a.nq, a.rows, lane);
+        process_stage<NT>(A, Q, alpha1, qs, ring + st * kStageBytes4, poison, tokens[warp][st], a.nq, a.rows, lane);
         __syncwarp();  // the stage is read
         if (issue()) ++issued;
       }
@@ -660,7 +616,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
       if (g == 4) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          wr[warp][8 * nt + 2 * t + i] = fmaxf(S.r[i] * (i ? al.y : al.x), kNoRef);  // from here on in base-2 logits
+          wr[warp][8 * nt + 2 * t + i] = fmaxf(S.top[i] * (i ? al.y : al.x) - kTopWeight, kNoRef);  // from here on in base-2 logits
           wl[warp][8 * nt + 2 * t + i] = S.c[i];
         }
       }
@@ -685,6 +641,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
         O.z = fmaf(o.z, f, O.z);
         O.w = fmaf(o.w, f, O.w);
       }
+      if (poison[row] >> (x >> 5) & 1) O.x = O.y = O.z = O.w = __int_as_float(0x7fc00000);
       if (ranks > 1) {  // in the place of warp 0's, which this thread alone has read
         *reinterpret_cast<float4*>(smem + row * kQaRowStride + x) = O;
         if (x == 0) merged[row] = make_float2(R, L);
