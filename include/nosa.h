@@ -516,6 +516,7 @@ nosa_status nosa_quant_read(const uint8_t* store, int units, int max_blocks, con
  *            sees tokens 0 .. lens - n_queries + i.  A query that sees none gets zeros
  *   max_len  upper bound of lens, at most 64 max_blocks and 1,048,576 (it sizes the launch)
  *   softmax_scale  0 => 1/sqrt(128)
+ *   q and out must not overlap
  *   scratch  device memory of at least nosa_quant_scratch_bytes(units, group * n_queries,
  *            ceil(max_len / 64)) bytes, 256-byte aligned; its first 4 bytes receive device-side
  *            error bits (zero them before the call to read them after it): bit 0 a length outside

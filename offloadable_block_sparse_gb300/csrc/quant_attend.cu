@@ -32,8 +32,7 @@ namespace nosa {
 
 namespace cg = cooperative_groups;
 
-constexpr int kQaWarps = 4;
-constexpr int kQaThreads = kQaWarps * 32;
+constexpr int kMergeWarps = 8;
 constexpr int kQaStages = 2;          // half blocks in flight per warp
 constexpr int kStageTokens = 32, kStageBytes4 = 2 * kTileBytes;
 constexpr int kQaSplitUnits = 2048;   // beyond, one CTA per unit
@@ -43,14 +42,14 @@ constexpr int kQaRowStride = 132;     // floats per row of a warp's partial in s
 constexpr size_t kQaErrBytes = 256;   // the scratch starts with the device error word
 constexpr float kNoRef = -3e38f;      // reference of a row that has seen no token
 
-// Shared memory of the rings, which the warps' partials reuse.
-__host__ __device__ constexpr int quant_ring_bytes(int nt) {
-  const int ring = kQaWarps * kQaStages * kStageBytes4, partials = kQaWarps * 8 * nt * kQaRowStride * 4;
+// Shared memory of the rings of a CTA's warps, which their partials (nt row tiles) reuse.
+__host__ __device__ constexpr int quant_ring_bytes(int nt, int warps) {
+  const int ring = warps * kQaStages * kStageBytes4, partials = warps * 8 * nt * kQaRowStride * 4;
   return ring > partials ? ring : partials;
 }
 
-__host__ __device__ constexpr int quant_smem_bytes(int nt) {
-  return quant_ring_bytes(nt) + (nt > 1 ? nt * 2432 : 0);  // and the query operands (QueryShared)
+__host__ __device__ constexpr int quant_smem_bytes(int nt, int warps) {
+  return quant_ring_bytes(nt, warps) + (nt > 1 ? nt * 2432 : 0);  // and the query operands (QueryShared)
 }
 
 enum { kWhole, kPieces, kCluster };
@@ -162,8 +161,10 @@ __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], cons
   const uint32_t l01 = pack_half2(sum[0] - half_lo(h01), sum[1] - half_hi(h01));
   const uint32_t l23 = pack_half2(sum[2] - half_lo(h23), sum[3] - half_hi(h23));
   Q.sums = t == 0 ? h01 : t == 1 ? h23 : t == 2 ? l01 : l23;
-  alpha[0] = scale * __shfl_sync(0xffffffffu, inv, 8 * t);  // row 2t's lanes are 8t .. 8t + 3
-  alpha[1] = scale * __shfl_sync(0xffffffffu, inv, 8 * t + 4);
+  // Kept away from zero and infinity: scores stay below 2^50, so below 2^-100 all weights are equal, and at the upper
+  // end any score but the largest has none.
+  alpha[0] = fminf(fmaxf(scale * __shfl_sync(0xffffffffu, inv, 8 * t), 0x1p-100f), 0x1p127f);  // row 2t's lanes: 8t ..
+  alpha[1] = fminf(fmaxf(scale * __shfl_sync(0xffffffffu, inv, 8 * t + 4), 0x1p-100f), 0x1p127f);
 }
 
 // One warp's running state for a tile of 8 rows: of rows 2t, 2t + 1 the score that has the weight 2^14, the largest
@@ -247,7 +248,6 @@ struct QueryShared {
   uint32_t sums[32];
   float2 alpha[32];
 };
-static_assert(kQaWarps >= 4, "a warp per row tile loads the queries");
 static_assert(sizeof(QueryShared) == 2432, "quant_smem_bytes");
 
 // The 2^24 that the codes lack go into the K scales (8 products a tile), or for one row tile into alpha and, the
@@ -433,14 +433,16 @@ __device__ __forceinline__ void store_out(uint16_t* out, const float4& o, float 
 __device__ __forceinline__ long long cta_first(long long total, int i, int n) { return total * i / n; }
 __device__ __forceinline__ int cta_of(long long total, long long b, int n) { return (int)(((b + 1) * n - 1) / total); }
 
-template <int NT>
-__global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kernel(const __grid_constant__ QuantArgs a) {
+template <int NT, int W>
+__global__ void __launch_bounds__(W * 32, (NT == 1 ? 16 : 8) / W) quant_attend_kernel(const __grid_constant__ QuantArgs a) {
+  constexpr int kThreads = W * 32;
+  static_assert(W >= NT, "a warp per row tile loads the queries");
   // the warps' rings, then [warp][8 NT rows][kQaRowStride], their partials; behind them the query operands (NT > 1)
   extern __shared__ __align__(16) float smem[];
-  __shared__ __align__(8) uint64_t bars[kQaWarps][kQaStages];
-  __shared__ int tokens[kQaWarps][kQaStages];
+  __shared__ __align__(8) uint64_t bars[W][kQaStages];
+  __shared__ int tokens[W][kQaStages];
   __shared__ int2 list[kQaList];  // (row of the store, tokens of the context from the block on)
-  __shared__ float wr[kQaWarps][8 * NT], wl[kQaWarps][8 * NT];
+  __shared__ float wr[W][8 * NT], wl[W][8 * NT];
   __shared__ int scan[32], found[2];
   __shared__ int poison[kQaMaxRows];  // [row]: groups that end as NaN
   __shared__ float2 merged[8 * NT];  // a cluster CTA's references and sums
@@ -464,8 +466,8 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
   const int rank = a.split == kCluster ? (int)cg::this_cluster().block_rank() : 0;
   int u = blockIdx.x / ranks, at = 0, pieces = gridDim.x;
   long long todo = 1, total = 1, begin = 0;
-  auto cut = [&]() {  // two blocks a piece at least (a stage per warp); further CTAs have nothing to do
-    pieces = (int)min((long long)gridDim.x, (total + 1) / 2);
+  auto cut = [&]() {  // a stage per warp at least; further CTAs have nothing to do
+    pieces = (int)min((long long)gridDim.x, (total + W / 2 - 1) / (W / 2));
     const long long lo = blockIdx.x < pieces ? cta_first(total, blockIdx.x, pieces) : total;
     todo = blockIdx.x < pieces ? cta_first(total, blockIdx.x + 1, pieces) - lo : 0;
     return lo;
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
       u = (int)(begin / a.max_sel);
       at = (int)(begin % a.max_sel);
     } else {
-      const int per = (a.units + kQaThreads - 1) / kQaThreads, u0 = threadIdx.x * per, u1 = min(u0 + per, a.units);
+      const int per = (a.units + kThreads - 1) / kThreads, u0 = threadIdx.x * per, u1 = min(u0 + per, a.units);
       int mine = 0, sum;
       for (int i = u0; i < u1; ++i) mine += blocks_of(i);
       int before = block_scan_excl(mine, scan, &sum);
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
     begin -= at;
   }
 
-  QueryShared* qs = reinterpret_cast<QueryShared*>(reinterpret_cast<unsigned char*>(smem) + quant_ring_bytes(NT));
+  QueryShared* qs = reinterpret_cast<QueryShared*>(reinterpret_cast<unsigned char*>(smem) + quant_ring_bytes(NT, W));
   unsigned char* ring = reinterpret_cast<unsigned char*>(smem) + warp * kQaStages * kStageBytes4;
   int issued = 0, done = 0;
   bool late = false;
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
       const int n = min(batch, end - b0);
       if (a.sel) {
         if (b0 > first) __syncthreads();  // the list before is used up
-        for (int j = threadIdx.x; j < n; j += kQaThreads) {
+        for (int j = threadIdx.x; j < n; j += kThreads) {
           const size_t i = (size_t)u * a.max_sel + b0 + j;
           const int block = a.sel[i];
           const int slot = block < 0 ? 0 : a.sel_slot ? a.sel_slot[i] : block;
@@ -562,12 +564,12 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
       int j = warp >> 1;
       auto issue = [&]() {  // the next half block into the stage whose turn it is; false when there is none
         int2 e = make_int2(0, 0);
-        for (; j < n; j += kQaWarps / 2) {
+        for (; j < n; j += W / 2) {
           e = a.sel ? list[j] : make_int2(b0 + j, min(len - (b0 + j) * kBlock, 2 * kBlock));
           if (e.y > half) break;
         }
         if (j >= n || late) return false;
-        j += kQaWarps / 2;
+        j += W / 2;
         if (lane == 0) {
           const int st = issued % kQaStages;
           tokens[warp][st] = e.y - half;
@@ -624,15 +626,15 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
     __syncthreads();
     const bool complete = first == 0 && end == whole;
     const int part = blockIdx.x + u;  // a piece's end and a unit's each move on by one: no two segments share a part
-    for (int idx = threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += kQaThreads) {
+    for (int idx = threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += kThreads) {
       const int row = idx >> 5, x = 4 * (idx & 31);
       float R = wr[0][row];
 #pragma unroll
-      for (int w = 1; w < kQaWarps; ++w) R = fmaxf(R, wr[w][row]);
+      for (int w = 1; w < W; ++w) R = fmaxf(R, wr[w][row]);
       float L = 0.f;
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kQaWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float f = ex2(wr[w][row] - R);
         const float4 o = *reinterpret_cast<const float4*>(smem + (w * 8 * NT + row) * kQaRowStride + x);
         L = fmaf(wl[w][row], f, L);
@@ -656,7 +658,7 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
     if (ranks > 1) {  // each CTA of the cluster merges its share of the outputs through distributed shared memory
       cg::cluster_group cluster = cg::this_cluster();
       cluster.sync();
-      for (int idx = rank * kQaThreads + threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += ranks * kQaThreads) {
+      for (int idx = rank * kThreads + threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += ranks * kThreads) {
         const int row = idx >> 5, x = 4 * (idx & 31);
         float R = kNoRef, L = 0.f;
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -680,11 +682,11 @@ __global__ void __launch_bounds__(kQaThreads, NT == 1 ? 4 : 2) quant_attend_kern
   }
 }
 
-// Merges the parts of a unit's row, where there are several: one CTA of four warps per (unit, row), each warp
-// every fourth part, each lane four dims.
-__global__ void __launch_bounds__(kQaThreads) quant_merge_kernel(const __grid_constant__ QuantArgs a) {
-  __shared__ float4 so[kQaWarps][32];
-  __shared__ float2 ss[kQaWarps];
+// Merges the parts of a unit's row, where there are several: one CTA of eight warps per (unit, row), each warp
+// every eighth part, each lane four dims.
+__global__ void __launch_bounds__(kMergeWarps * 32) quant_merge_kernel(const __grid_constant__ QuantArgs a) {
+  __shared__ float4 so[kMergeWarps][32];
+  __shared__ float2 ss[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int u = blockIdx.x / a.rows, row = blockIdx.x % a.rows;
   pdl_wait();
@@ -694,7 +696,7 @@ __global__ void __launch_bounds__(kQaThreads) quant_merge_kernel(const __grid_co
   float R = kNoRef, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int c = warp; c < m.y; c += kQaWarps) {
+  for (int c = warp; c < m.y; c += kMergeWarps) {
     const size_t i = (size_t)(m.x + c) * a.rows + row;
     const float2 s = a.stats[i];
     merge_part(R, L, O, s.x, s.y, *reinterpret_cast<const float4*>(a.part + i * kHeadDim + 4 * lane));
@@ -704,24 +706,29 @@ __global__ void __launch_bounds__(kQaThreads) quant_merge_kernel(const __grid_co
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < kQaWarps; ++w) merge_part(R, L, O, ss[w].x, ss[w].y, so[w][lane]);
+    for (int w = 1; w < kMergeWarps; ++w) merge_part(R, L, O, ss[w].x, ss[w].y, so[w][lane]);
     store_out(a.out + ((size_t)u * a.rows + row) * kHeadDim + 4 * lane, O, L);
   }
 }
 
+// The kernel's forms: row tiles and warps.  One row tile: eight warps a CTA (fewer parts to merge), or four for small
+// calls (a shorter merge); more row tiles take the registers of eight warps an SM, two CTAs of four.
+enum { kForm1x8, kForm1x4, kForm2x4, kForm4x4, kForms };
+
 // What the launches need of a device, looked up once (a call costs more in look-ups than in launching otherwise).
 struct QuantDevice {
-  int sms, ctas[3];  // resident CTAs of the kernel for 1, 2, 4 row tiles on the whole device
+  int sms, ctas[kForms];  // resident CTAs of each form on the whole device
 };
 static std::mutex g_quant_mutex;
 static QuantDevice g_quant_device[64] = {};
 
-template <int NT>
+template <int NT, int W>
 static cudaError_t set_up_quant_attend(int sms, int* ctas) {
-  const int smem = quant_smem_bytes(NT);
-  cudaError_t e = cudaFuncSetAttribute(quant_attend_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(quant_attend_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, quant_attend_kernel<NT>, kQaThreads, smem);
+  const int smem = quant_smem_bytes(NT, W);
+  cudaError_t e = cudaFuncSetAttribute(quant_attend_kernel<NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(quant_attend_kernel<NT, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, quant_attend_kernel<NT, W>, W * 32, smem);
+  if (e == cudaSuccess && *ctas < 1) e = cudaErrorInvalidConfiguration;
   *ctas *= sms;
   return e;
 }
@@ -736,9 +743,11 @@ static bool quant_device(QuantDevice* out) {
   QuantDevice& d = g_quant_device[dev];
   if (!d.sms) {
     QuantDevice n = {};
-    if (cudaDeviceGetAttribute(&n.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        set_up_quant_attend<1>(n.sms, &n.ctas[0]) != cudaSuccess || set_up_quant_attend<2>(n.sms, &n.ctas[1]) != cudaSuccess ||
-        set_up_quant_attend<4>(n.sms, &n.ctas[2]) != cudaSuccess || n.sms < 1 || n.ctas[0] < 1 || n.ctas[1] < 1 || n.ctas[2] < 1) {
+    if (cudaDeviceGetAttribute(&n.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n.sms < 1 ||
+        set_up_quant_attend<1, 8>(n.sms, &n.ctas[kForm1x8]) != cudaSuccess ||
+        set_up_quant_attend<1, 4>(n.sms, &n.ctas[kForm1x4]) != cudaSuccess ||
+        set_up_quant_attend<2, 4>(n.sms, &n.ctas[kForm2x4]) != cudaSuccess ||
+        set_up_quant_attend<4, 4>(n.sms, &n.ctas[kForm4x4]) != cudaSuccess) {
       (void)cudaGetLastError();
       return false;
     }
@@ -750,35 +759,60 @@ static bool quant_device(QuantDevice* out) {
 
 // How many CTAs a call takes, and how they share it.
 struct QuantPlan {
-  int split, ctas, cluster;
+  int form, split, ctas, cluster;
   size_t bytes;  // of the scratch
 };
 
-// Three ways, by what a call would pay (microseconds on GB300, 8 rows a unit, back to back in a graph):
-//  * a cluster per unit, the largest power of two of CTAs whose clusters fit one wave (16 at most, each CTA two
-//    blocks at least): no second kernel, which costs about 5, but a unit cannot spread further, and lengths do not
-//    balance.  2 units of 64 blocks: 6.9 against 8.2; 8 of 256: 14.4 against 17.4; 64 of 64: 13.8 against 17.9;
-//    64 listing 81: 17.3 against 20.2.  (Clusters of 3, 6 or 12 pack badly: 64 of 64 blocks 16.9 with 3, 13.8 with 4.)
-//    So for at most 16 blocks a CTA, and where all units list the same number and fill half a wave, 40.
-//  * equal pieces of all units' blocks over one wave, merged by a second kernel: 8 units of 1024 blocks 28.8 against
-//    41.5 in clusters, 16 of 1024 38.4 against 52.8; ragged lengths balance.
-//  * with thousands of units one CTA each, which balance by themselves.
-static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks, bool listed) {
-  const int wave = std::min(d.ctas[rows <= 8 ? 0 : rows <= 16 ? 1 : 2], 8 * d.sms);
-  if (units > kQaSplitUnits) return {kWhole, units, 0, kQaErrBytes};
-  int cl = 16;
-  while (cl > 1 && ((long long)units * cl > wave || 2 * cl > blocks + 1)) cl /= 2;
-  if (units * cl <= wave && blocks <= (listed && 2 * units * cl > wave ? 40 : 16) * cl)
-    return {kCluster, units * cl, cl, kQaErrBytes};
-  const long long pieces = ((long long)units * blocks + 1) / 2;
-  const int ctas = (int)std::min<long long>(wave, pieces);
-  const size_t parts = (size_t)ctas + units;
-  return {kPieces, ctas, 0, kQaErrBytes + (size_t)units * sizeof(int2) + parts * rows * (kHeadDim + 2) * sizeof(float) + 16};
+// The largest power of two of CTAs per unit, `most` at most, that fits all units into one wave and leaves each warp a
+// stage (clusters of 3, 6 or 12 pack badly).
+static int cluster_size(int units, int blocks, int wave, int warps, int most) {
+  int cl = most;
+  while (cl > 1 && ((long long)units * cl > wave || (cl - 1) * (warps / 2) >= blocks)) cl /= 2;
+  return cl;
 }
 
-template <int NT>
+// Three ways, by what a call pays (microseconds on GB300, back to back in a graph):
+//  * a cluster per unit, merged through distributed shared memory: no second kernel (about 5), but a unit cannot
+//    spread further, and ragged lengths do not balance.
+//  * equal pieces of all units' blocks over one wave, merged by a second kernel.
+//  * one CTA per unit, where they are more than a wave and the last round is not too empty for their length: 512 units
+//    of 64 blocks 63.3 against 63.8 in pieces, of 8 blocks 15.0 against 21.1; 1024 of 64 109 against 117.
+// 8 rows a unit:               cluster, 4 warps   cluster, 8 warps   pieces, 8 warps
+//    2 units of 64 blocks            6.9                 6.9               7.8
+//    8 units of 256                 14.0                14.0              12.1
+//   16 units of 64                   9.2                14.9               9.9
+//   16 units of 256                 16.9                22.3              14.7
+//   64 units of 64                  13.6                13.1              16.8
+//  256 units of 32                  21.0                20.2              24.8
+//  256 units listing 81             45.5                42.5              45.8
+// So clusters of eight warps where they fill most of a wave and the units are not long (listed blocks balance, lengths
+// may not), clusters of four for small calls.  With 16 or 32 rows pieces win from 64 blocks on.
+static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks, bool listed) {
+  int form = rows <= 8 ? kForm1x8 : rows <= 16 ? kForm2x4 : kForm4x4;
+  const int warps = form == kForm1x8 ? 8 : 4, wave = std::min(d.ctas[form], 8 * d.sms);
+  const int rounds = (units + wave - 1) / wave;
+  if (units > kQaSplitUnits || (units > wave && (long long)(rounds * wave - units) * blocks <= 24ll * units))
+    return {form, kWhole, units, 0, kQaErrBytes};
+  const int cl = cluster_size(units, blocks, wave, warps, 8);
+  if (form != kForm1x8) {
+    if (units * cl <= wave && blocks <= 4 * cl) return {form, kCluster, units * cl, cl, kQaErrBytes};
+  } else {
+    if (units * cl <= wave && 2 * units * cl > wave && blocks <= (listed ? 100 : 32) * cl)
+      return {form, kCluster, units * cl, cl, kQaErrBytes};
+    const int wave4 = std::min(d.ctas[kForm1x4], 8 * d.sms), cl4 = cluster_size(units, blocks, wave4, 4, 16);
+    if (units * cl4 <= wave4 && blocks <= 6 * cl4) return {kForm1x4, kCluster, units * cl4, cl4, kQaErrBytes};
+  }
+  const long long pieces = ((long long)units * blocks + warps / 2 - 1) / (warps / 2);
+  const int ctas = (int)std::min<long long>(wave, pieces);
+  const size_t parts = (size_t)ctas + units;
+  return {form, kPieces, ctas, 0,
+          kQaErrBytes + (size_t)units * sizeof(int2) + parts * rows * (kHeadDim + 2) * sizeof(float) + 16};
+}
+
+template <int NT, int W>
 static cudaError_t launch_quant_attend(const QuantArgs& a, const QuantPlan& p, cudaStream_t st) {
-  return launch_ex(quant_attend_kernel<NT>, dim3((unsigned)p.ctas), dim3(kQaThreads), quant_smem_bytes(NT), st, true, p.cluster, a);
+  return launch_ex(quant_attend_kernel<NT, W>, dim3((unsigned)p.ctas), dim3(W * 32), quant_smem_bytes(NT, W), st, true,
+                   p.cluster, a);
 }
 
 static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t scratch_bytes, cudaStream_t st) {
@@ -793,11 +827,12 @@ static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t 
   a.part = reinterpret_cast<float*>(p + kQaErrBytes);
   a.stats = reinterpret_cast<float2*>(a.part + parts * a.rows * kHeadDim);
   a.meta = reinterpret_cast<int2*>(a.stats + parts * a.rows);
-  cudaError_t e = a.rows <= 8    ? launch_quant_attend<1>(a, plan, st)
-                  : a.rows <= 16 ? launch_quant_attend<2>(a, plan, st)
-                                 : launch_quant_attend<4>(a, plan, st);
+  cudaError_t e = plan.form == kForm1x8   ? launch_quant_attend<1, 8>(a, plan, st)
+                  : plan.form == kForm1x4 ? launch_quant_attend<1, 4>(a, plan, st)
+                  : plan.form == kForm2x4 ? launch_quant_attend<2, 4>(a, plan, st)
+                                          : launch_quant_attend<4, 4>(a, plan, st);
   if (e == cudaSuccess && plan.split == kPieces)
-    e = launch_ex(quant_merge_kernel, dim3((unsigned)(a.units * a.rows)), dim3(kQaThreads), 0, st, true, 0, a);
+    e = launch_ex(quant_merge_kernel, dim3((unsigned)(a.units * a.rows)), dim3(kMergeWarps * 32), 0, st, true, 0, a);
   if (e == cudaSuccess) return NOSA_OK;
   (void)cudaGetLastError();
   return NOSA_ERR_CUDA;

@@ -539,3 +539,94 @@ def test_a_context_selects_and_the_store_is_attended():
             assert (sparse.float() - plain.float()).abs().max().item() <= 2e-2
     finally:
         N.nosa_destroy(ctx)
+
+
+@pytest.mark.parametrize("units,nb,group,nq", [(700, 20, 2, 1), (330, 40, 8, 1), (2100, 3, 1, 1), (400, 12, 4, 5), (310, 30, 8, 2)],
+                         ids=["whole", "pieces", "thousands", "32-rows", "16-rows"])
+def test_many_units_with_ragged_lengths(units, nb, group, nq):
+    """More units than one wave of CTAs, with empty ones among them; pieces that span several units."""
+    few = _random_store(8, nb, 77)
+    host = np.tile(few, (-(-units // 8), 1, 1))[:units]
+    rng = np.random.default_rng(units)
+    lens = rng.integers(0, 64 * nb + 1, units)
+    lens[::7] = 0
+    lens[5] = 64 * nb
+    store = torch.from_numpy(host).cuda()
+    q = _queries(rng, units, group, nq)
+    sel = np.full((units, nb + 3), -1, np.int32)
+    for u in range(units):
+        sel[u, :nb] = rng.permutation(nb)
+    dense, sc = _dense(q, store, _i32(lens), 64 * nb)
+    sparse, sc2 = _sparse(q, store, torch.from_numpy(sel).cuda(), None, _i32(lens))  # every block, in any order
+    torch.cuda.synchronize()
+    assert int(sc[:4].view(torch.int32).item()) == 0 and int(sc2[:4].view(torch.int32).item()) == 0
+    at = np.arange(64 * nb).reshape(nb, 64)
+    for u in list(range(0, 40)) + list(range(40, units, 37)) + [units - 1]:
+        for got in (dense, sparse):
+            _check_unit(_f64(got[u]), _f64(q[u]), host[u], at, int(lens[u]), nq, 1 / math.sqrt(128))
+    # every unit of both is finite, and the two agree within their roundings to bf16 and f16
+    assert torch.isfinite(dense).all() and torch.isfinite(sparse).all()
+    assert (dense.float() - sparse.float()).abs().max().item() <= 2 * (2.0 ** -8 + 2.0 ** -9) * 8
+
+
+@pytest.mark.parametrize("scale,size", [(1e-30, 1e-30), (1e-38, 1.0), (1e30, 1.0), (3e38, 1e30), (0.0, 3e38)])
+def test_extreme_scales_give_a_mean_or_the_largest(scale, size):
+    """Logits of (almost) zero weigh all tokens alike; logits of any size leave the token with the largest."""
+    n = 200
+    host = _random_store(1, 4, 3)
+    store = torch.from_numpy(host).cuda()
+    q = torch.zeros((1, 8, 1, 128), dtype=torch.bfloat16, device="cuda")
+    q[..., 5] = size
+    out, _ = _dense(q, store, _i32([n]), n, scale=scale)
+    torch.cuda.synchronize()
+    kk, vv, _, sv = (x.reshape(-1, 128)[:n] for x in Q.unpack(host[0]))
+    if scale and scale * size < 1e-3:
+        best = np.arange(n)
+    else:
+        best = np.nonzero(kk[:, 5] == kk[:, 5].max())[0]
+        assert best.size == 1
+    err = np.abs(_f64(out[0]).reshape(8, 128) - vv[best].mean(0))
+    # weights alike: rounding of the products with s (2^-11 of the largest |n s| + |m|) and of the result
+    assert (err <= 2.0 ** -8 * np.abs(vv[best].mean(0)) + 2.0 ** -9 * sv.max()).all()
+
+
+def test_a_selection_of_nothing_gives_zeros():
+    store = torch.from_numpy(_random_store(2, 3, 1)).cuda()
+    q = _queries(np.random.default_rng(1), 2, 8, 2)
+    sel = torch.full((2, 5), -1, dtype=torch.int32, device="cuda")
+    sel[1, 3] = 2  # behind the context
+    out, sc = _sparse(q, store, sel, None, _i32([192, 100]))
+    torch.cuda.synchronize()
+    assert not out.any() and int(sc[:4].view(torch.int32).item()) == 0
+
+
+def test_first_calls_may_be_made_under_capture():
+    """A process whose first use of the store is inside a graph capture (nothing is set up before)."""
+    code = """
+import torch
+from offloadable_block_sparse_gb300 import nosa as N
+k = torch.randn(3, 70, 128, device="cuda").to(torch.bfloat16); q = torch.randn(3, 8, 128, device="cuda").to(torch.bfloat16)
+store = torch.zeros(3, 2, 10240, dtype=torch.uint8, device="cuda"); lens = torch.full((3,), 70, dtype=torch.int32, device="cuda")
+kv = torch.empty(3, 2, 2, 64, 128, dtype=torch.bfloat16, device="cuda"); sel = torch.tensor([[0, 1]] * 3, dtype=torch.int32, device="cuda")
+a, b = torch.empty_like(q), torch.empty_like(q); sc = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    s = torch.cuda.current_stream().cuda_stream
+    N.nosa_quant_append(k, k, store, 3, 70, 2, stream=s)
+    N.nosa_quant_read(store, 3, 2, None, 2, kv, lens=lens, stream=s)
+    N.nosa_quant_dense_attend(q, store, 3, 8, 1, 2, lens, 70, a, sc, sc.numel(), stream=s)
+    N.nosa_quant_attend(q, store, sel, None, 3, 8, 1, 2, 2, lens, b, sc, sc.numel(), stream=s)
+g.replay()
+torch.cuda.synchronize()
+x = kv[:, :, 0].reshape(3, 128, 128)
+assert (x[:, :70].float() - k.float()).abs().max() < 0.6 and not x[:, 70:].any()
+assert torch.isfinite(a).all() and a.any() and (a.float() - b.float()).abs().max() < 0.1
+print("ok")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr[-2000:]
