@@ -33,7 +33,6 @@ namespace nosa {
 namespace cg = cooperative_groups;
 
 constexpr int kMergeWarps = 8;
-constexpr int kQaStages = 2;          // half blocks in flight per warp
 constexpr int kStageTokens = 32, kStageBytes4 = 2 * kTileBytes;
 constexpr int kQaSplitUnits = 2048;   // beyond, one CTA per unit
 constexpr int kQaList = 256;          // listed blocks looked up at a time
@@ -42,14 +41,13 @@ constexpr int kQaRowStride = 132;     // floats per row of a warp's partial in s
 constexpr size_t kQaErrBytes = 256;   // the scratch starts with the device error word
 constexpr float kNoRef = -3e38f;      // reference of a row that has seen no token
 
-// Shared memory of the rings of a CTA's warps, which their partials (nt row tiles) reuse.
-__host__ __device__ constexpr int quant_ring_bytes(int nt, int warps) {
-  const int ring = warps * kQaStages * kStageBytes4, partials = warps * 8 * nt * kQaRowStride * 4;
-  return ring > partials ? ring : partials;
-}
+// Half blocks in flight per worker.  A pair of warps frees a stage one late.
+__host__ __device__ constexpr int stages(int nt) { return nt == 4 ? 3 : 2; }
 
-__host__ __device__ constexpr int quant_smem_bytes(int nt, int warps) {
-  return quant_ring_bytes(nt, warps) + (nt > 1 ? nt * 2432 : 0);  // and the query operands (QueryShared)
+// Shared memory of the rings of n workers, which their partials (nt row tiles) reuse.
+__host__ __device__ constexpr int quant_ring_bytes(int nt, int n) {
+  const int ring = n * stages(nt) * kStageBytes4, partials = n * 8 * nt * kQaRowStride * 4;
+  return ring > partials ? ring : partials;
 }
 
 enum { kWhole, kPieces, kCluster };
@@ -73,7 +71,7 @@ struct QuantArgs {
 // D (16 x 8, f32) += A (16 x 16, row) . B (16 x 8, col), f16 inputs.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -81,13 +79,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 // The same with D = A . B: a zero operand costs nothing, a zeroed accumulator four moves.
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // D (16 x 8, f32) = A (16 x 8, row) . B (8 x 8, col), f16 inputs.
 __device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};\n"
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};\n"
                : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
@@ -170,43 +168,56 @@ __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], cons
 // One warp's running state for a tile of 8 rows: of rows 2t, 2t + 1 the score that has the weight 2^14, the largest
 // allowed (a score z has 2^((z - top) alpha + 14), so that a huge score less itself is zero); O^T (codes' part, in
 // units of 2^-24, or 2^-20 for odd dims); and the m part: rows 0..3 the groups, row 4 the softmax sum.
+// A warp of a pair (process_pair) holds half the dims: GR = 2 groups, rows 0, 1 of the m part.
 constexpr float kTopWeight = 14.f;
+template <int GR>
 struct RowTile {
   float top[2];
-  float o[8][4];
+  float o[2 * GR][4];
   float c[4];
 };
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// The V side of a tile as a lane holds it: codes and scales of token pairs t, t + 4, and the rows of the m
-// operand (group g's minima for g < 4, ones for g = 4, zeros).
+// The V side of a tile as a lane holds it, GR groups from group g0 on: codes and scales of token pairs t, t + 4, and the
+// rows of the m operand (group g0 + g's minima for g < GR, ones for g = 4, zeros).
+template <int GR>
 struct ValueRegs {
-  uint4 c[2], s[2];
-  uint32_t m[2];
+  uint32_t c[2][GR], s[2][GR], m[2];
 };
-__device__ __forceinline__ void load_values(ValueRegs& V, const unsigned char* tile, int lane) {
+template <int GR>
+__device__ __forceinline__ void load_words(uint32_t (&w)[GR], const unsigned char* p) {
+  if constexpr (GR == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+}
+template <int GR>
+__device__ __forceinline__ void load_values(ValueRegs<GR>& V, const unsigned char* tile, int g0, int lane) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    V.c[h] = *reinterpret_cast<const uint4*>(tile + kTileV + 512 * h + 16 * lane);
-    V.s[h] = *reinterpret_cast<const uint4*>(tile + kTileVs + 16 * (4 * h + t));
-    const uint32_t m = *reinterpret_cast<const uint32_t*>(tile + kTileVm + 16 * (4 * h + t) + 4 * (g & 3));
-    V.m[h] = (m & (g < 4 ? 0xffffffffu : 0u)) | (g == 4 ? 0x3C003C00u : 0u);
+    load_words<GR>(V.c[h], tile + kTileV + 512 * h + 16 * lane + 4 * g0);
+    load_words<GR>(V.s[h], tile + kTileVs + 16 * (4 * h + t) + 4 * g0);
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(tile + kTileVm + 16 * (4 * h + t) + 4 * (g0 + (g & (GR - 1))));
+    V.m[h] = (m & (g < GR ? 0xffffffffu : 0u)) | (g == 4 ? 0x3C003C00u : 0u);
   }
 }
 
 // O^T += V^T . P^T for NT row tiles; p[nt][h] = weights of row g, token pair t + 4 h, as f16x2.
-template <int NT>
-__device__ __forceinline__ void add_values(RowTile (&A)[NT], const ValueRegs& V, const uint32_t (&p)[NT][2]) {
+template <int NT, int GR>
+__device__ __forceinline__ void add_values(RowTile<GR> (&A)[NT], const ValueRegs<GR>& V, const uint32_t (&p)[NT][2]) {
 #pragma unroll
-  for (int gr = 0; gr < 4; ++gr) {
-    const uint32_t w0 = word(V.c[0], gr), w1 = word(V.c[1], gr), x0 = w0 >> 8, x1 = w1 >> 8;
+  for (int gr = 0; gr < GR; ++gr) {
+    const uint32_t w0 = V.c[0][gr], w1 = V.c[1][gr], x0 = w0 >> 8, x1 = w1 >> 8;
     const uint32_t a[8] = {w0 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x000F000Fu, w1 & 0x00F000F0u,
                            x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const uint32_t b0 = mul_half2(p[nt][0], word(V.s[0], gr)), b1 = mul_half2(p[nt][1], word(V.s[1], gr));
+      const uint32_t b0 = mul_half2(p[nt][0], V.s[0][gr]), b1 = mul_half2(p[nt][1], V.s[1][gr]);
       mma_f16(A[nt].o[2 * gr], a[0], a[1], a[2], a[3], b0, b1);
       mma_f16(A[nt].o[2 * gr + 1], a[4], a[5], a[6], a[7], b0, b1);
     }
@@ -215,18 +226,18 @@ __device__ __forceinline__ void add_values(RowTile (&A)[NT], const ValueRegs& V,
   for (int nt = 0; nt < NT; ++nt) mma_f16(A[nt].c, V.m[0], 0u, V.m[1], 0u, p[nt][0], p[nt][1]);
 }
 
-// Prepares a stage that not every row sees as a whole (left: tokens of the context from its first on).  Behind the
-// context the store may hold anything, and 0 x NaN is a NaN, so those tokens' V scales and minima are cleared (codes
-// are finite as they stand).  So is a NaN group of a token that only some rows see: the rows that see it get a bit of
-// `poison`, and their dims of that group a NaN in the end.
-__device__ __forceinline__ void clear_tail(unsigned char* stage, int* poison, int left, int nq, int rows, int lane) {
+// Prepares a tile that not every row sees as a whole (left: tokens of the context from its first on, possibly none).
+// Behind the context the store may hold anything, and 0 x NaN is a NaN, so those tokens' V scales and minima are
+// cleared (codes are finite as they stand).  So is a NaN group of a token that only some rows see: the rows that see
+// it get a bit of `poison`, and their dims of that group a NaN in the end.
+__device__ __forceinline__ void clear_tail(unsigned char* tile, int* poison, int left, int nq, int rows, int lane) {
 #pragma unroll 1
-  for (int i = lane; i < kStageTokens / 2 * 8; i += 32) {  // [tile][s, m][token pair][group] words of two tokens
-    uint32_t* w = reinterpret_cast<uint32_t*>(stage + (i >> 6) * kTileBytes + kTileVs) + (i & 63);
+  for (int i = lane; i < kTileTokens / 2 * 8; i += 32) {  // [s, m][token pair][group] words of two tokens
+    uint32_t* w = reinterpret_cast<uint32_t*>(tile + kTileVs) + i;
     uint32_t x = *w;
 #pragma unroll 1
     for (int par = 0; par < 2; ++par) {
-      const int token = (i >> 6) * kTileTokens + 2 * ((i >> 2) & 7) + par, late = token - (left - nq);
+      const int late = 2 * ((i >> 2) & 7) + par - (left - nq);  // rows of query tokens from `late` on see the token
       const uint32_t mask = par ? 0xffff0000u : 0x0000ffffu;
       if (late >= nq) {
         x &= ~mask;
@@ -248,167 +259,276 @@ struct QueryShared {
   uint32_t sums[32];
   float2 alpha[32];
 };
-static_assert(sizeof(QueryShared) == 2432, "quant_smem_bytes");
 
 // The 2^24 that the codes lack go into the K scales (8 products a tile), or for one row tile into alpha and, the
 // other way, into the m part (4).
 __host__ __device__ constexpr float code_unit(int nt) { return nt == 1 ? 1.f : 0x1p24f; }
 
-// One stage (two tiles, 32 tokens) for all row tiles; left: tokens of the context from the stage's first on.
-// One or two row tiles take both tiles at once, so that their chains of dependent operations overlap; four row tiles
-// overlap by themselves and take one tile at a time, which keeps them in registers.
-template <int NT>
-__device__ __forceinline__ void process_stage(RowTile (&A)[NT], const QueryTile& Q, const float (&alpha1)[2],
-                                              const QueryShared* qs, unsigned char* stage, int* poison, int left, int nq,
-                                              int rows, int lane) {
-  constexpr int kTiles = NT <= 2 ? 2 : 1;
+// Scores of kTiles tiles from `tile0` on for all row tiles: z[tile][row tile] of tokens g, g + 8 and rows 2t, 2t + 1.
+// A token that a row does not see (left: tokens of the context from the first tile's first on) gets -inf.
+template <int NT, int kTiles>
+__device__ __forceinline__ void score_tiles(float (&z)[kTiles][NT][4], const QueryTile& Q, const QueryShared* qs,
+                                            const unsigned char* tile0, bool tail, int left, int nq, int rows, int lane) {
   constexpr float kCodeUnit = code_unit(NT);
   const int g = lane >> 2, t = lane & 3;
-  const bool tail = left - (nq - 1) < kStageTokens;  // some row does not see the whole stage
-  if (tail) clear_tail(stage, poison, left, nq, rows, lane);
-  // the largest V scale of the stage: below 2, weights up to 2^14 times scales stay within f16
-  const uint4 vs = *reinterpret_cast<const uint4*>(stage + (lane >> 3 & 1) * kTileBytes + kTileVs + 16 * (lane & 7));
-  const uint32_t vmax2 = max_half2(max_half2(vs.x, vs.y), max_half2(vs.z, vs.w));
-  const bool large = (vmax2 & 0x40004000u) != 0;  // exponent bit 14: 2 or more (scales have no sign)
-
-#pragma unroll 1
-  for (int i0 = 0; i0 < 2; i0 += kTiles) {
-    unsigned char* tile0 = stage + i0 * kTileBytes;
-    // scores of the scaled queries
-    float z[kTiles][NT][4], ks[kTiles][2][4];
-    uint4 kc[kTiles][2];
+  float ks[kTiles][2][4];
+  uint4 kc[kTiles][2];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const unsigned char* tile = tile0 + i * kTileBytes;
-      uint32_t km[2];
+  for (int i = 0; i < kTiles; ++i) {
+    const unsigned char* tile = tile0 + i * kTileBytes;
+    uint32_t km[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        kc[i][h] = *reinterpret_cast<const uint4*>(tile + 64 * (g + 8 * h) + 16 * t);
-        const uint2 s = *reinterpret_cast<const uint2*>(tile + kTileKs + 16 * (g + 8 * h));
-        km[h] = *reinterpret_cast<const uint32_t*>(tile + kTileKs + 16 * (g + 8 * h) + 8 + 4 * (t & 1));
-        ks[i][h][0] = half_lo(s.x) * kCodeUnit;
-        ks[i][h][1] = half_hi(s.x) * kCodeUnit;
-        ks[i][h][2] = half_lo(s.y) * kCodeUnit;
-        ks[i][h][3] = half_hi(s.y) * kCodeUnit;
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mma_f16_k8(z[i][nt], km[0], km[1], NT == 1 ? Q.sums : qs[nt].sums[lane]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[i][nt][e] *= 0x1p-24f * kCodeUnit;
-      }
+    for (int h = 0; h < 2; ++h) {
+      kc[i][h] = *reinterpret_cast<const uint4*>(tile + 64 * (g + 8 * h) + 16 * t);
+      const uint2 s = *reinterpret_cast<const uint2*>(tile + kTileKs + 16 * (g + 8 * h));
+      km[h] = *reinterpret_cast<const uint32_t*>(tile + kTileKs + 16 * (g + 8 * h) + 8 + 4 * (t & 1));
+      ks[i][h][0] = half_lo(s.x) * kCodeUnit;
+      ks[i][h][1] = half_hi(s.x) * kCodeUnit;
+      ks[i][h][2] = half_lo(s.y) * kCodeUnit;
+      ks[i][h][3] = half_hi(s.y) * kCodeUnit;
     }
-#pragma unroll
-    for (int gr = 0; gr < 4; ++gr) {
-      uint32_t a[kTiles][8];
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        const uint32_t w0 = word(kc[i][0], gr), w1 = word(kc[i][1], gr), x0 = w0 >> 8, x1 = w1 >> 8;
-        a[i][0] = w0 & 0x000F000Fu;
-        a[i][1] = w1 & 0x000F000Fu;
-        a[i][2] = w0 & 0x00F000F0u;
-        a[i][3] = w1 & 0x00F000F0u;
-        a[i][4] = x0 & 0x000F000Fu;
-        a[i][5] = x1 & 0x000F000Fu;
-        a[i][6] = x0 & 0x00F000F0u;
-        a[i][7] = x1 & 0x00F000F0u;
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint4 b;
-        if constexpr (NT == 1)
-          b = make_uint4(Q.b[2 * gr][0], Q.b[2 * gr][1], Q.b[2 * gr + 1][0], Q.b[2 * gr + 1][1]);
-        else
-          b = qs[nt].b[gr][lane];
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          float acc[4];
-          mma_f16_first(acc, a[i][0], a[i][1], a[i][2], a[i][3], b.x, b.y);
-          mma_f16(acc, a[i][4], a[i][5], a[i][6], a[i][7], b.z, b.w);
-          z[i][nt][0] = fmaf(acc[0], ks[i][0][gr], z[i][nt][0]);
-          z[i][nt][1] = fmaf(acc[1], ks[i][0][gr], z[i][nt][1]);
-          z[i][nt][2] = fmaf(acc[2], ks[i][1][gr], z[i][nt][2]);
-          z[i][nt][3] = fmaf(acc[3], ks[i][1][gr], z[i][nt][3]);
-        }
-      }
-    }
-    if (tail) {
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = 8 * nt + 2 * t + (e & 1), token = kTileTokens * (i0 + i) + g + 8 * (e >> 1);
-            if (row >= rows || token >= left - (nq - 1) + row % nq) z[i][nt][e] = -INFINITY;
-          }
-    }
-
-    // whether the references hold: no score above its row's top
-    bool raise = large;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      mma_f16_k8(z[i][nt], km[0], km[1], NT == 1 ? Q.sums : qs[nt].sums[lane]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float best = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
-        if (kTiles == 2) best = fmaxf(best, fmaxf(z[kTiles - 1][nt][e], z[kTiles - 1][nt][e + 2]));
-        raise |= best > A[nt].top[e];
+      for (int e = 0; e < 4; ++e) z[i][nt][e] *= 0x1p-24f * kCodeUnit;
+    }
+  }
+#pragma unroll
+  for (int gr = 0; gr < 4; ++gr) {
+    uint32_t a[kTiles][8];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const uint32_t w0 = word(kc[i][0], gr), w1 = word(kc[i][1], gr), x0 = w0 >> 8, x1 = w1 >> 8;
+      a[i][0] = w0 & 0x000F000Fu;
+      a[i][1] = w1 & 0x000F000Fu;
+      a[i][2] = w0 & 0x00F000F0u;
+      a[i][3] = w1 & 0x00F000F0u;
+      a[i][4] = x0 & 0x000F000Fu;
+      a[i][5] = x1 & 0x000F000Fu;
+      a[i][6] = x0 & 0x00F000F0u;
+      a[i][7] = x1 & 0x00F000F0u;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      uint4 b;
+      if constexpr (NT == 1)
+        b = make_uint4(Q.b[2 * gr][0], Q.b[2 * gr][1], Q.b[2 * gr + 1][0], Q.b[2 * gr + 1][1]);
+      else
+        b = qs[nt].b[gr][lane];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        float acc[4];
+        mma_f16_first(acc, a[i][0], a[i][1], a[i][2], a[i][3], b.x, b.y);
+        mma_f16(acc, a[i][4], a[i][5], a[i][6], a[i][7], b.z, b.w);
+        z[i][nt][0] = fmaf(acc[0], ks[i][0][gr], z[i][nt][0]);
+        z[i][nt][1] = fmaf(acc[1], ks[i][0][gr], z[i][nt][1]);
+        z[i][nt][2] = fmaf(acc[2], ks[i][1][gr], z[i][nt][2]);
+        z[i][nt][3] = fmaf(acc[3], ks[i][1][gr], z[i][nt][3]);
       }
     }
-    if (__any_sync(0xffffffffu, raise)) {
-      float vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
+  }
+  if (tail) {
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-      // vmax < 2^e: weights up to 2^limit keep the products below 2^15 (a NaN scale sets no limit)
-      if (!(vmax <= 65504.f)) vmax = 0.f;
-      const float limit = kTopWeight - (float)max((int)(__float_as_uint(vmax) >> 23) - 127, 0);
+    for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 al2 = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
-          const float al = e ? al2.y : al2.x;
-          float best = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
-          if (kTiles == 2) best = fmaxf(best, fmaxf(z[kTiles - 1][nt][e], z[kTiles - 1][nt][e + 2]));
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-          const float old = A[nt].top[e];
-          if ((best - old) * al + kTopWeight > limit) {  // the row's lanes agree; rows differ
-            const float top = best + (kTopWeight + 4.f - limit) / al, f = ex2((old - top) * al);
-            A[nt].top[e] = top;
-#pragma unroll
-            for (int mt = 0; mt < 8; ++mt) {
-              A[nt].o[mt][e] *= f;
-              A[nt].o[mt][e + 2] *= f;
-            }
-            A[nt].c[e] *= f;
-            A[nt].c[e + 2] *= f;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int row = 8 * nt + 2 * t + (e & 1), token = kTileTokens * i + g + 8 * (e >> 1);
+          if (row >= rows || token >= left - (nq - 1) + row % nq) z[i][nt][e] = -INFINITY;
         }
+  }
+}
+
+// The lane's best score of row 2t + e over its tokens.
+template <int NT, int kTiles>
+__device__ __forceinline__ float lane_best(const float (&z)[kTiles][NT][4], int nt, int e) {
+  float best = fmaxf(z[0][nt][e], z[0][nt][e + 2]);
+  if constexpr (kTiles == 2) best = fmaxf(best, fmaxf(z[1][nt][e], z[1][nt][e + 2]));
+  return best;
+}
+
+// The weight (as a power of two) up to which weights x V scales below vmax stay within f16: products below 2^15.
+__device__ __forceinline__ float weight_limit(float vmax) {
+  if (!(vmax <= 65504.f)) vmax = 0.f;  // a NaN scale sets no limit
+  return kTopWeight - (float)max((int)(__float_as_uint(vmax) >> 23) - 127, 0);
+}
+
+// Raises row 2t + e's top so that `best` weighs 2^(limit - 4), where it would weigh more than 2^limit.
+template <int GR>
+__device__ __forceinline__ void raise_top(RowTile<GR>& S, int e, float best, float al, float limit) {
+  const float old = S.top[e];
+  if ((best - old) * al + kTopWeight > limit) {  // the row's lanes agree; rows differ
+    const float top = best + (kTopWeight + 4.f - limit) / al, f = ex2((old - top) * al);
+    S.top[e] = top;
+#pragma unroll
+    for (int mt = 0; mt < 2 * GR; ++mt) {
+      S.o[mt][e] *= f;
+      S.o[mt][e + 2] *= f;
     }
-    // exponents
+    S.c[e] *= f;
+    S.c[e + 2] *= f;
+  }
+}
+
+// Weights of tokens g, g + 8 and rows 2t, 2t + 1 as f16, transposed: of row g and token pairs t, t + 4.
+__device__ __forceinline__ void weights(uint32_t (&p)[2], const float (&z)[4], const float (&top)[2], float al0, float al1) {
+  float w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(z[e] - top[e & 1], e & 1 ? al1 : al0, kTopWeight));
+  p[0] = movmatrix_trans(pack_half2(w[0], w[1]));
+  p[1] = movmatrix_trans(pack_half2(w[2], w[3]));
+}
+
+// One or two row tiles: a warp takes a stage (two tiles, 32 tokens) by itself, both tiles at once so that their chains
+// of dependent operations overlap.  left: tokens of the context from the stage's first on.
+template <int NT>
+__device__ __forceinline__ void process_stage(RowTile<4> (&A)[NT], const QueryTile& Q, const float (&alpha1)[2],
+                                              const QueryShared* qs, unsigned char* stage, int* poison, int left, int nq,
+                                              int rows, int lane) {
+  const bool tail = left - (nq - 1) < kStageTokens;  // some row does not see the whole stage
+  if (tail) {
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) clear_tail(stage + i * kTileBytes, poison, left - i * kTileTokens, nq, rows, lane);
+  }
+  // the largest V scale of the stage: below 2, weights up to 2^14 times scales stay within f16
+  const uint4 vs = *reinterpret_cast<const uint4*>(stage + (lane >> 3 & 1) * kTileBytes + kTileVs + 16 * (lane & 7));
+  const uint32_t vmax2 = max_half2(max_half2(vs.x, vs.y), max_half2(vs.z, vs.w));
+  bool raise = (vmax2 & 0x40004000u) != 0;  // exponent bit 14: 2 or more (scales have no sign)
+  float z[2][NT][4];
+  score_tiles<NT, 2>(z, Q, qs, stage, tail, left, nq, rows, lane);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) raise |= lane_best<NT, 2>(z, nt, e) > A[nt].top[e];
+  if (__any_sync(0xffffffffu, raise)) {
+    float vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+    const float limit = weight_limit(vmax);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
+      for (int e = 0; e < 2; ++e) {
+        float best = lane_best<NT, 2>(z, nt, e);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[i][nt][e] = fmaf(z[i][nt][e] - A[nt].top[e & 1], e & 1 ? al.y : al.x, kTopWeight);
-    }
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      // weights of tokens g, g + 8 and rows 2t, 2t + 1; transposed: of row g and token pairs t, t + 4
-      uint32_t p[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        p[nt][0] = movmatrix_trans(pack_half2(ex2(z[i][nt][0]), ex2(z[i][nt][1])));
-        p[nt][1] = movmatrix_trans(pack_half2(ex2(z[i][nt][2]), ex2(z[i][nt][3])));
+        for (int o = 4; o < 32; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+        raise_top(A[nt], e, best, e ? al.y : al.x, limit);
       }
-      ValueRegs V;
-      load_values(V, tile0 + i * kTileBytes, lane);
-      add_values<NT>(A, V, p);
     }
   }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t p[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
+      weights(p[nt], z[i][nt], A[nt].top, al.x, al.y);
+    }
+    ValueRegs<4> V;
+    load_values(V, stage + i * kTileBytes, 0, lane);
+    add_values(A, V, p);
+  }
+}
+
+// Four row tiles: their accumulators would take half a thread's registers, and a stage's chain of operations is long, so
+// two warps share a stage.  Each scores one of its two tiles for all rows and hands its weights to the other through shared memory; then
+// each adds both tiles' values for its half of the dims.  The two keep the same tops: a warp that wants one raised says
+// so with its weights, and then both take the better of their rows' best scores and weigh again.
+template <int NT>
+struct PairShared {
+  uint4 p[2][2][(NT + 1) / 2][32];  // [turn][warp of the pair]: the weights, two row tiles each
+  int flags[2][2];            // [turn][warp]: kRaise, kLate
+  float best[2][8 * NT];      // [warp]: the rows' best scores, and the largest V scale, when a top is raised
+  float vmax[2];
+};
+enum { kRaise = 1, kLate = 2 };
+
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;\n" ::"r"(pair + 1) : "memory"); }
+
+// Returns whether the stage has arrived (late: this warp has seen that it has not; then the other is told).
+template <int NT>
+__device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], const QueryShared* qs, PairShared<NT>& X, int turn, int pair,
+                                             int role, bool late, unsigned char* stage, int* poison, int left, int nq,
+                                             int rows, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  unsigned char* tile = stage + role * kTileBytes;
+  float z[1][NT][4];
+  uint32_t p[NT][2], vmax2 = 0;
+  auto weigh = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 al = qs[nt].alpha[lane];
+      weights(p[nt], z[0][nt], A[nt].top, al.x, al.y);
+    }
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) X.p[turn][role][i][lane] = make_uint4(p[2 * i][0], p[2 * i][1], p[2 * i + 1][0], p[2 * i + 1][1]);
+  };
+  int flags = late ? kLate : 0;
+  if (!late) {
+    left -= role * kTileTokens;
+    const bool tail = left - (nq - 1) < kTileTokens;
+    if (tail) clear_tail(tile, poison, left, nq, rows, lane);
+    const uint4 vs = *reinterpret_cast<const uint4*>(tile + kTileVs + 16 * (lane & 7));
+    vmax2 = max_half2(max_half2(vs.x, vs.y), max_half2(vs.z, vs.w));
+    bool raise = (vmax2 & 0x40004000u) != 0;  // as in process_stage
+    score_tiles<NT, 1>(z, QueryTile(), qs, tile, tail, left, nq, rows, lane);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) raise |= lane_best<NT, 1>(z, nt, e) > A[nt].top[e];
+    if (__any_sync(0xffffffffu, raise)) flags = kRaise;
+    weigh();
+  }
+  if (lane == 0) X.flags[turn][role] = flags;
+  pair_sync(pair);
+  flags = X.flags[turn][0] | X.flags[turn][1];
+  if (flags & kLate) return false;
+  if (flags) {
+    float vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+    if (lane == 0) X.vmax[role] = vmax;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float best = lane_best<NT, 1>(z, nt, e);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+        if (g == 0) X.best[role][8 * nt + 2 * t + e] = best;
+      }
+    pair_sync(pair);
+    const float limit = weight_limit(fmaxf(X.vmax[0], X.vmax[1]));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 al = qs[nt].alpha[lane];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * nt + 2 * t + e;
+        raise_top(A[nt], e, fmaxf(X.best[0][row], X.best[1][row]), e ? al.y : al.x, limit);
+      }
+    }
+    weigh();
+    pair_sync(pair);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // the warp's own tile, then the other's
+    const int at = role ^ i;
+    if (i == 1) {
+#pragma unroll
+      for (int k = 0; k < NT / 2; ++k) {
+        const uint4 v = X.p[turn][at][k][lane];
+        p[2 * k][0] = v.x, p[2 * k][1] = v.y, p[2 * k + 1][0] = v.z, p[2 * k + 1][1] = v.w;
+      }
+    }
+    ValueRegs<2> V;
+    load_values(V, stage + at * kTileBytes, 2 * role, lane);
+    add_values(A, V, p);
+  }
+  return true;
 }
 
 // Adds a part (reference r, sum l, four dims o) to a running one.
@@ -433,26 +553,37 @@ __device__ __forceinline__ void store_out(uint16_t* out, const float4& o, float 
 __device__ __forceinline__ long long cta_first(long long total, int i, int n) { return total * i / n; }
 __device__ __forceinline__ int cta_of(long long total, long long b, int n) { return (int)(((b + 1) * n - 1) / total); }
 
+// Workers of a CTA: warps, or pairs of them for four row tiles.
+__host__ __device__ constexpr int workers(int nt, int warps) { return nt == 4 ? warps / 2 : warps; }
+// Warps an SM by registers: 128 a thread for one row tile, 255 for more.
+__host__ __device__ constexpr int warps_per_sm(int nt) { return nt == 1 ? 16 : 8; }
+
 template <int NT, int W>
-__global__ void __launch_bounds__(W * 32, (NT == 1 ? 16 : 8) / W) quant_attend_kernel(const __grid_constant__ QuantArgs a) {
-  constexpr int kThreads = W * 32;
+__global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_kernel(const __grid_constant__ QuantArgs a) {
+  constexpr int kThreads = W * 32, N = workers(NT, W), S = stages(NT);
+  constexpr bool kPair = NT == 4;
   static_assert(W >= NT, "a warp per row tile loads the queries");
-  // the warps' rings, then [warp][8 NT rows][kQaRowStride], their partials; behind them the query operands (NT > 1)
+  static_assert(N % 2 == 0 && N <= 15, "halves of blocks are dealt to the workers; a named barrier per pair");
+  // the workers' rings, then [worker][8 NT rows][kQaRowStride], their partials; behind them, for pairs, the query
+  // operands and what the warps of a pair exchange
   extern __shared__ __align__(16) float smem[];
-  __shared__ __align__(8) uint64_t bars[W][kQaStages];
-  __shared__ int tokens[W][kQaStages];
+  __shared__ __align__(8) uint64_t bars[N][S];
   __shared__ int2 list[kQaList];  // (row of the store, tokens of the context from the block on)
-  __shared__ float wr[W][8 * NT], wl[W][8 * NT];
+  __shared__ float wr[N][8 * NT], wl[N][8 * NT];
   __shared__ int scan[32], found[2];
   __shared__ int poison[kQaMaxRows];  // [row]: groups that end as NaN
   __shared__ float2 merged[8 * NT];  // a cluster CTA's references and sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  if (lane == 0) {
+  const int me = kPair ? warp >> 1 : warp, role = kPair ? warp & 1 : 0;  // the warp's worker, and its part in the pair
+  if (lane == 0 && role == 0) {
 #pragma unroll
-    for (int st = 0; st < kQaStages; ++st) mbar_init(&bars[warp][st], 1);
+    for (int st = 0; st < S; ++st) mbar_init(&bars[me][st], 1);
     fence_mbar_init();
   }
-  __syncwarp();
+  if (kPair)
+    __syncthreads();
+  else
+    __syncwarp();
   pdl_wait();
   pdl_launch_dependents();
 
@@ -466,8 +597,8 @@ __global__ void __launch_bounds__(W * 32, (NT == 1 ? 16 : 8) / W) quant_attend_k
   const int rank = a.split == kCluster ? (int)cg::this_cluster().block_rank() : 0;
   int u = blockIdx.x / ranks, at = 0, pieces = gridDim.x;
   long long todo = 1, total = 1, begin = 0;
-  auto cut = [&]() {  // a stage per warp at least; further CTAs have nothing to do
-    pieces = (int)min((long long)gridDim.x, (total + W / 2 - 1) / (W / 2));
+  auto cut = [&]() {  // a stage per worker at least; further CTAs have nothing to do
+    pieces = (int)min((long long)gridDim.x, (total + N / 2 - 1) / (N / 2));
     const long long lo = blockIdx.x < pieces ? cta_first(total, blockIdx.x, pieces) : total;
     todo = blockIdx.x < pieces ? cta_first(total, blockIdx.x + 1, pieces) - lo : 0;
     return lo;
@@ -501,9 +632,10 @@ __global__ void __launch_bounds__(W * 32, (NT == 1 ? 16 : 8) / W) quant_attend_k
     begin -= at;
   }
 
-  QueryShared* qs = reinterpret_cast<QueryShared*>(reinterpret_cast<unsigned char*>(smem) + quant_ring_bytes(NT, W));
-  unsigned char* ring = reinterpret_cast<unsigned char*>(smem) + warp * kQaStages * kStageBytes4;
-  int issued = 0, done = 0;
+  QueryShared* qs = reinterpret_cast<QueryShared*>(reinterpret_cast<unsigned char*>(smem) + quant_ring_bytes(NT, N));
+  PairShared<NT>* pairs = reinterpret_cast<PairShared<NT>*>(qs + (NT > 1 ? NT : 0));
+  unsigned char* ring = reinterpret_cast<unsigned char*>(smem) + me * S * kStageBytes4;
+  int in = 0, out = 0, phase = 0, turn = 0;  // the ring's next stage to fill and to use, and that one's phase
   bool late = false;
   for (; todo > 0; ++u, at = 0) {
     const int len = length(u), whole = blocks_of(u);
@@ -520,7 +652,7 @@ __global__ void __launch_bounds__(W * 32, (NT == 1 ? 16 : 8) / W) quant_attend_k
     if (threadIdx.x < kQaMaxRows) poison[threadIdx.x] = 0;
     if (a.nq > 1) __syncthreads();
     QueryTile Q;
-    RowTile A[NT];
+    RowTile<kPair ? 2 : 4> A[NT];
     float alpha1[2];
     auto load_queries = [&]() {
 #pragma unroll
@@ -537,59 +669,73 @@ __global__ void __launch_bounds__(W * 32, (NT == 1 ? 16 : 8) / W) quant_attend_k
         }
         A[nt].top[0] = A[nt].top[1] = kNoRef;
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt) A[nt].o[mt][0] = A[nt].o[mt][1] = A[nt].o[mt][2] = A[nt].o[mt][3] = 0.f;
+        for (int mt = 0; mt < (kPair ? 4 : 8); ++mt) A[nt].o[mt][0] = A[nt].o[mt][1] = A[nt].o[mt][2] = A[nt].o[mt][3] = 0.f;
         A[nt].c[0] = A[nt].c[1] = A[nt].c[2] = A[nt].c[3] = 0.f;
       }
       if (NT > 1) __syncthreads();
     };
 
-    // The blocks, listed ones looked up kQaList at a time.  Warp w takes half w % 2 of the blocks w / 2, w / 2 + 2, ...
-    const int batch = a.sel ? kQaList : max(end - first, 1), half = (warp & 1) * kStageTokens;
-    const uint8_t* base = a.store + (size_t)u * a.max_blocks * kQuantBlockBytes + (warp & 1) * kStageBytes4;
+    // The blocks, listed ones looked up kQaList at a time and those without a token left out.  Worker w takes half
+    // w % 2 of the blocks w / 2, w / 2 + N / 2, ...  (an empty second half of the last block too: it adds nothing).
+    const int batch = a.sel ? kQaList : max(end - first, 1), half = (me & 1) * kStageTokens;
+    const uint8_t* base = a.store + (size_t)u * a.max_blocks * kQuantBlockBytes + (me & 1) * kStageBytes4;
     for (int b0 = first; b0 < end || b0 == first; b0 += batch) {
-      const int n = min(batch, end - b0);
+      int n = max(min(batch, end - b0), 0);
       if (a.sel) {
         if (b0 > first) __syncthreads();  // the list before is used up
-        for (int j = threadIdx.x; j < n; j += kThreads) {
-          const size_t i = (size_t)u * a.max_sel + b0 + j;
-          const int block = a.sel[i];
-          const int slot = block < 0 ? 0 : a.sel_slot ? a.sel_slot[i] : block;
-          const bool held = slot >= 0 && slot < a.max_blocks;
-          if (!held) atomicOr(a.err, kErrBounds);
-          const long long left = block < 0 || !held ? 0 : (long long)len - (long long)block * kBlock;
-          list[j] = make_int2(slot, (int)min(max(left, 0ll), 2ll * kBlock));  // 128 or more: every row sees the whole block
+        int kept = 0;
+        for (int j0 = 0; j0 < n; j0 += kThreads) {
+          int2 e = make_int2(0, 0);
+          if (j0 + (int)threadIdx.x < n) {
+            const size_t i = (size_t)u * a.max_sel + b0 + j0 + threadIdx.x;
+            const int block = a.sel[i];
+            const int slot = block < 0 ? 0 : a.sel_slot ? a.sel_slot[i] : block;
+            const bool held = slot >= 0 && slot < a.max_blocks;
+            if (!held) atomicOr(a.err, kErrBounds);
+            const long long left = block < 0 || !held ? 0 : (long long)len - (long long)block * kBlock;
+            e = make_int2(slot, (int)min(max(left, 0ll), 2ll * kBlock));  // 128 or more: every row sees the whole block
+          }
+          int sum;
+          const int at = block_scan_excl(e.y > 0, scan, &sum);
+          if (e.y > 0) list[kept + at] = e;
+          kept += sum;
         }
+        n = kept;
         __syncthreads();
+      } else if (len == 0) {
+        n = 0;
       }
-      int j = warp >> 1;
-      auto issue = [&]() {  // the next half block into the stage whose turn it is; false when there is none
-        int2 e = make_int2(0, 0);
-        for (; j < n; j += W / 2) {
-          e = a.sel ? list[j] : make_int2(b0 + j, min(len - (b0 + j) * kBlock, 2 * kBlock));
-          if (e.y > half) break;
+      const int step = N / 2, mine = (n - (me >> 1) + step - 1) / step;  // the worker's halves
+      int started = 0;
+      auto issue = [&]() {  // the next half into the stage whose turn it is
+        if (started >= mine || late) return;
+        if (lane == 0 && role == 0) {
+          const int j = (me >> 1) + started * step, row = a.sel ? list[j].x : b0 + j;
+          mbar_arrive_expect_tx(&bars[me][in], kStageBytes4);
+          bulk_copy_g2s(smem_u32(ring + in * kStageBytes4), base + (size_t)row * kQuantBlockBytes, kStageBytes4, &bars[me][in]);
         }
-        if (j >= n || late) return false;
-        j += W / 2;
-        if (lane == 0) {
-          const int st = issued % kQaStages;
-          tokens[warp][st] = e.y - half;
-          mbar_arrive_expect_tx(&bars[warp][st], kStageBytes4);
-          bulk_copy_g2s(smem_u32(ring + st * kStageBytes4), base + (size_t)e.x * kQuantBlockBytes, kStageBytes4, &bars[warp][st]);
-        }
-        return true;
+        in = in + 1 == S ? 0 : in + 1;
+        ++started;
       };
 #pragma unroll
-      for (int i = 0; i < kQaStages; ++i)
-        if (issue()) ++issued;
+      for (int i = 0; i < S; ++i) issue();
       if (b0 == first) load_queries();  // while the first stages arrive
-      __syncwarp();
-      for (; done < issued; ++done) {
-        const int st = done % kQaStages;
-        late |= !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][st], done / kQaStages & 1, kWaitCycles));
-        if (late) continue;  // let what is in flight land, and start no more
-        process_stage<NT>(A, Q, alpha1, qs, ring + st * kStageBytes4, poison, tokens[warp][st], a.nq, a.rows, lane);
-        __syncwarp();  // the stage is read
-        if (issue()) ++issued;
+      for (int done = 0; done < started; ++done) {
+        late |= !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[me][out], phase, kWaitCycles));
+        unsigned char* stage = ring + out * kStageBytes4;
+        const int j = (me >> 1) + done * step, left = (a.sel ? list[j].y : len - (b0 + j) * kBlock) - half;
+        if constexpr (kPair) {
+          // beyond the sync inside, both warps are through with the stage before, and its place is free
+          late = !process_pair<NT>(A, qs, pairs[me], turn, me, role, late, stage, poison, left, a.nq, a.rows, lane);
+          turn ^= 1;
+          if (started - done < S) issue();
+        } else if (!late) {  // otherwise let what is in flight land, and start no more
+          process_stage<NT>(A, Q, alpha1, qs, stage, poison, left, a.nq, a.rows, lane);
+          __syncwarp();  // the stage is read
+          issue();
+        }
+        out = out + 1 == S ? 0 : out + 1;
+        if (out == 0) phase ^= 1;
       }
     }
     if (late) {  // a wait gave up: poison the outputs
@@ -599,27 +745,27 @@ __global__ void __launch_bounds__(W * 32, (NT == 1 ? 16 : 8) / W) quant_attend_k
     }
     __syncthreads();  // the rings become the warps' partials
 
-    // the warp's partial: O of rows 2t, 2t + 1, dims 32 gr + 4 g .. + 3
+    // the worker's partial: O of rows 2t, 2t + 1, dims 32 gr + 4 g .. + 3 of the warp's groups
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const RowTile& S = A[nt];
-      const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
-      float* w = smem + (warp * 8 * NT + 8 * nt + 2 * t) * kQaRowStride;
+      const auto& T = A[nt];
+      const float2 al = NT > 1 ? qs[nt].alpha[lane] : make_float2(alpha1[0], alpha1[1]);
+      float* w = smem + (me * 8 * NT + 8 * nt + 2 * t) * kQaRowStride + 64 * role;
 #pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
+      for (int gr = 0; gr < (kPair ? 2 : 4); ++gr) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float m = __shfl_sync(0xffffffffu, S.c[i], 4 * gr + t);
+          const float m = __shfl_sync(0xffffffffu, T.c[i], 4 * gr + t);
           *reinterpret_cast<float4*>(w + i * kQaRowStride + 32 * gr + 4 * g) =
-              make_float4(fmaf(S.o[2 * gr][i], 0x1p24f, m), fmaf(S.o[2 * gr][i + 2], 0x1p20f, m),
-                          fmaf(S.o[2 * gr + 1][i], 0x1p24f, m), fmaf(S.o[2 * gr + 1][i + 2], 0x1p20f, m));
+              make_float4(fmaf(T.o[2 * gr][i], 0x1p24f, m), fmaf(T.o[2 * gr][i + 2], 0x1p20f, m),
+                          fmaf(T.o[2 * gr + 1][i], 0x1p24f, m), fmaf(T.o[2 * gr + 1][i + 2], 0x1p20f, m));
         }
       }
-      if (g == 4) {
+      if (g == 4 && role == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          wr[warp][8 * nt + 2 * t + i] = fmaxf(S.top[i] * (i ? al.y : al.x) - kTopWeight, kNoRef);  // from here on in base-2 logits
-          wl[warp][8 * nt + 2 * t + i] = S.c[i];
+          wr[me][8 * nt + 2 * t + i] = fmaxf(T.top[i] * (i ? al.y : al.x) - kTopWeight, kNoRef);  // in base-2 logits
+          wl[me][8 * nt + 2 * t + i] = T.c[i];
         }
       }
     }
@@ -630,11 +776,11 @@ __global__ void __launch_bounds__(W * 32, (NT == 1 ? 16 : 8) / W) quant_attend_k
       const int row = idx >> 5, x = 4 * (idx & 31);
       float R = wr[0][row];
 #pragma unroll
-      for (int w = 1; w < W; ++w) R = fmaxf(R, wr[w][row]);
+      for (int w = 1; w < N; ++w) R = fmaxf(R, wr[w][row]);
       float L = 0.f;
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
+      for (int w = 0; w < N; ++w) {
         const float f = ex2(wr[w][row] - R);
         const float4 o = *reinterpret_cast<const float4*>(smem + (w * 8 * NT + row) * kQaRowStride + x);
         L = fmaf(wl[w][row], f, L);
@@ -644,7 +790,7 @@ __global__ void __launch_bounds__(W * 32, (NT == 1 ? 16 : 8) / W) quant_attend_k
         O.w = fmaf(o.w, f, O.w);
       }
       if (poison[row] >> (x >> 5) & 1) O.x = O.y = O.z = O.w = __int_as_float(0x7fc00000);
-      if (ranks > 1) {  // in the place of warp 0's, which this thread alone has read
+      if (ranks > 1) {  // in the place of worker 0's, which this thread alone has read
         *reinterpret_cast<float4*>(smem + row * kQaRowStride + x) = O;
         if (x == 0) merged[row] = make_float2(R, L);
       } else if (complete) {
@@ -711,6 +857,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) quant_merge_kernel(const __g
   }
 }
 
+template <int NT, int W>
+constexpr int quant_smem_bytes() {
+  return quant_ring_bytes(NT, workers(NT, W)) +
+         (NT > 1 ? NT * (int)sizeof(QueryShared) : 0) + (NT == 4 ? workers(NT, W) * (int)sizeof(PairShared<NT>) : 0);
+}
+
 // The kernel's forms: row tiles and warps.  One row tile: eight warps a CTA (fewer parts to merge), or four for small
 // calls (a shorter merge); more row tiles take the registers of eight warps an SM, two CTAs of four.
 enum { kForm1x8, kForm1x4, kForm2x4, kForm4x4, kForms };
@@ -724,7 +876,7 @@ static QuantDevice g_quant_device[64] = {};
 
 template <int NT, int W>
 static cudaError_t set_up_quant_attend(int sms, int* ctas) {
-  const int smem = quant_smem_bytes(NT, W);
+  const int smem = quant_smem_bytes<NT, W>();
   cudaError_t e = cudaFuncSetAttribute(quant_attend_kernel<NT, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(quant_attend_kernel<NT, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, quant_attend_kernel<NT, W>, W * 32, smem);
@@ -763,11 +915,11 @@ struct QuantPlan {
   size_t bytes;  // of the scratch
 };
 
-// The largest power of two of CTAs per unit, `most` at most, that fits all units into one wave and leaves each warp a
-// stage (clusters of 3, 6 or 12 pack badly).
-static int cluster_size(int units, int blocks, int wave, int warps, int most) {
+// The largest power of two of CTAs per unit, `most` at most, that fits all units into one wave and leaves each worker
+// a stage (clusters of 3, 6 or 12 pack badly).
+static int cluster_size(int units, int blocks, int wave, int n, int most) {
   int cl = most;
-  while (cl > 1 && ((long long)units * cl > wave || (cl - 1) * (warps / 2) >= blocks)) cl /= 2;
+  while (cl > 1 && ((long long)units * cl > wave || (cl - 1) * (n / 2) >= blocks)) cl /= 2;
   return cl;
 }
 
@@ -789,11 +941,11 @@ static int cluster_size(int units, int blocks, int wave, int warps, int most) {
 // may not), clusters of four for small calls.  With 16 or 32 rows pieces win from 64 blocks on.
 static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks, bool listed) {
   int form = rows <= 8 ? kForm1x8 : rows <= 16 ? kForm2x4 : kForm4x4;
-  const int warps = form == kForm1x8 ? 8 : 4, wave = std::min(d.ctas[form], 8 * d.sms);
+  const int n = form == kForm1x8 ? 8 : form == kForm2x4 ? 4 : 2, wave = std::min(d.ctas[form], 8 * d.sms);
   const int rounds = (units + wave - 1) / wave;
   if (units > kQaSplitUnits || (units > wave && (long long)(rounds * wave - units) * blocks <= 24ll * units))
     return {form, kWhole, units, 0, kQaErrBytes};
-  const int cl = cluster_size(units, blocks, wave, warps, 8);
+  const int cl = cluster_size(units, blocks, wave, n, 8);
   if (form != kForm1x8) {
     if (units * cl <= wave && blocks <= 4 * cl) return {form, kCluster, units * cl, cl, kQaErrBytes};
   } else {
@@ -802,7 +954,7 @@ static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int block
     const int wave4 = std::min(d.ctas[kForm1x4], 8 * d.sms), cl4 = cluster_size(units, blocks, wave4, 4, 16);
     if (units * cl4 <= wave4 && blocks <= 6 * cl4) return {kForm1x4, kCluster, units * cl4, cl4, kQaErrBytes};
   }
-  const long long pieces = ((long long)units * blocks + warps / 2 - 1) / (warps / 2);
+  const long long pieces = ((long long)units * blocks + n / 2 - 1) / (n / 2);
   const int ctas = (int)std::min<long long>(wave, pieces);
   const size_t parts = (size_t)ctas + units;
   return {form, kPieces, ctas, 0,
@@ -811,7 +963,7 @@ static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int block
 
 template <int NT, int W>
 static cudaError_t launch_quant_attend(const QuantArgs& a, const QuantPlan& p, cudaStream_t st) {
-  return launch_ex(quant_attend_kernel<NT, W>, dim3((unsigned)p.ctas), dim3(W * 32), quant_smem_bytes(NT, W), st, true,
+  return launch_ex(quant_attend_kernel<NT, W>, dim3((unsigned)p.ctas), dim3(W * 32), quant_smem_bytes<NT, W>(), st, true,
                    p.cluster, a);
 }
 
