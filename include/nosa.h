@@ -523,7 +523,8 @@ nosa_status nosa_quant_read(const uint8_t* store, int units, int max_blocks, con
  *            [0, max_len] (clamped), bit 1 a bounded wait for a staged tile gave up (outputs are
  *            NaN).  Calls that may run at the same time (other streams, graphs) need a scratch each.
  * The sums are float32.  q is exact (values below 2^-23 of their row's largest are rounded); the
- * weights exp(logit - reference) and their products with s are rounded to f16, 2^-11 relative each.
+ * weights exp(logit - reference), their products with s and V's group maxima m + 15 s are rounded to f16,
+ * 2^-11 relative each.
  * Asynchronous on `stream`.  NOSA_ERR_CAPACITY if the scratch is too small. */
 nosa_status nosa_quant_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group, int n_queries,
                                     int max_blocks, const int32_t* lens, int max_len, float softmax_scale,

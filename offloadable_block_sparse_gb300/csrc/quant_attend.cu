@@ -3,23 +3,24 @@
 // With K^ = n s + m (codes n, a scale s and a minimum m per token and group of 32 dims; quant_core.cuh),
 //   q . K^_t = sum_gr s_{t,gr} (q_gr . n_{t,gr}) + sum_gr m_{t,gr} sum(q_gr)
 //   sum_t p_t V^_t = sum_t (p_t s_{t,gr}) n_{t,gr} + sum_t p_t m_{t,gr}
-// so codes enter the tensor cores as they are and are never turned into values: a masked code in the
-// low mantissa bits of an f16 is the subnormal n 2^-24 (n 2^-20 four bits further up, which the other
-// operand or the result makes good by an exact 2^-4), two instructions' worth of masking per four
-// codes.  The terms in m are one more MMA each: the row sums of q, split into two f16 against the
-// K minima, and a 16-row operand of the V minima with a row of ones that yields the softmax sum too.
+// so codes enter the tensor cores without being turned into values: a masked code in the low mantissa bits of
+// an f16 is the subnormal n 2^-24 (n 2^-20 four bits further up, which the other operand or the result makes
+// good by an exact 2^-4): five instructions for eight codes.  The other terms are one more MMA each: the row
+// sums of q, split into two f16, against the K minima, and a 16-row operand of V's minima with a row of ones that
+// yields the softmax sum too.
 //
-// grid: one wave of CTAs of four warps; the units' blocks in one line are cut into equal pieces, one per CTA, so
-// that ragged lengths balance.  A warp takes half (two tiles) of every second block through a ring of its own of
-// bulk copies to shared memory, so that no warp waits for another; per tile (mma.sync m16n8k16, f16 in, fp32
-// accumulate):
-//   S^T (16 tokens x 8 rows) = K codes . q^T       8 MMAs, one accumulator per group, + 1 for m
+// grid (quant_plan): one wave of CTAs; the units' blocks in one line are cut into equal pieces, one per CTA, so that
+// ragged lengths balance, or a cluster of CTAs takes a unit.  A warp takes half (two tiles of 16 tokens) of every
+// second block or so through a ring of its own of bulk copies to shared memory, so that no warp waits for another;
+// per tile (mma.sync m16n8k16, f16 in, fp32 accumulate; with at most 32 rows a unit tcgen05's tiles of 64 rows and
+// more would be mostly empty, and the codes would have to be written out as f16 to shared memory first):
+//   S^T (16 tokens x 8 rows) = K codes . q^T        8 MMAs, one accumulator per group, + 1 for m
 //   P^T by movmatrix of the f16-packed weights, times s per group
-//   O^T (128 dims x 8 rows) += V codes^T . P^T      8 MMAs, + 1 for m and the sum
-// The query rows of a unit (q heads x query tokens, at most 32) are NT tiles of 8.  Weights are
-// exp2(logit - R): R follows a row's maximum only when that would get a weight above 2^14, so the usual tile
-// needs no rescaling, and is set so that weight x s stays within f16 (R rises with a scale of 2 or more).
-// A CTA merges its warps in shared memory; a unit's parts, where several CTAs share it, merge in a second kernel.
+//   O^T (128 dims x 8 rows) += V codes^T . P^T       8 MMAs, + 1 for m and the sum
+// The query rows of a unit (q heads x query tokens, at most 32) are NT tiles of 8.  Weights are 2^(logit - R): R
+// follows a row's maximum only when that would get a weight above 2^14, so the usual tile needs no rescaling, and is
+// set so that weight x s stays within f16 (R rises with a scale of 2 or more).  A CTA merges its warps in shared
+// memory; a unit's parts, where several CTAs share it, merge through the cluster or in a second kernel.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -98,6 +99,11 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 v = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
+                            *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 __device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
   const __half2 v = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -167,8 +173,8 @@ __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], cons
 
 // One warp's running state for a tile of 8 rows: of rows 2t, 2t + 1 the score that has the weight 2^14, the largest
 // allowed (a score z has 2^((z - top) alpha + 14), so that a huge score less itself is zero); O^T (codes' part, in
-// units of 2^-24, or 2^-20 for odd dims); and the m part: rows 0..3 the groups, row 4 the softmax sum.
-// A warp of a pair (process_pair) holds half the dims: GR = 2 groups, rows 0, 1 of the m part.
+// units of 2^-24, or 2^-20 for odd dims); and the minima's part: rows 0..3 the groups, row 4 the softmax sum,
+// rows 8..11 the groups' sixteenths.  A warp of a pair (process_pair) holds half the dims: GR = 2 groups.
 constexpr float kTopWeight = 14.f;
 template <int GR>
 struct RowTile {
@@ -180,10 +186,17 @@ struct RowTile {
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // The V side of a tile as a lane holds it, GR groups from group g0 on: codes and scales of token pairs t, t + 4, and the
-// rows of the m operand (group g0 + g's minima for g < GR, ones for g = 4, zeros).
+// rows of the operand that goes with the weights alone: row g group g0 + g's minimum (g < GR), row 4 ones (the softmax
+// sum), and rows 8 + g a sixteenth of the minimum instead where the stage has scales of 2 or more (`large`).
+//
+// flip (all ones in a stage's second tile, else zero): the tile enters as -(15 - n) s and m + 15 s, its codes
+// complemented, its products negated and its maxima in the place of the minima.  Sums over codes of 0 .. 15 and over
+// minima alone would each be far larger than their total, and so would the rounding of long sums, which the tensor
+// cores cut off rather than round; with tiles taken from either end the sums stay near their totals.  (Taking 8 off each
+// code did the same for 3 to 7 % more time.)
 template <int GR>
 struct ValueRegs {
-  uint32_t c[2][GR], s[2][GR], m[2];
+  uint32_t c[2][GR], s[2][GR], m[2], m16[2];
 };
 template <int GR>
 __device__ __forceinline__ void load_words(uint32_t (&w)[GR], const unsigned char* p) {
@@ -196,34 +209,47 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[GR], const unsigned cha
   }
 }
 template <int GR>
-__device__ __forceinline__ void load_values(ValueRegs<GR>& V, const unsigned char* tile, int g0, int lane) {
+__device__ __forceinline__ void load_values(ValueRegs<GR>& V, const unsigned char* tile, int g0, uint32_t flip, bool large,
+                                            int lane) {
   const int g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     load_words<GR>(V.c[h], tile + kTileV + 512 * h + 16 * lane + 4 * g0);
     load_words<GR>(V.s[h], tile + kTileVs + 16 * (4 * h + t) + 4 * g0);
-    const uint32_t m = *reinterpret_cast<const uint32_t*>(tile + kTileVm + 16 * (4 * h + t) + 4 * (g0 + (g & (GR - 1))));
-    V.m[h] = (m & (g < GR ? 0xffffffffu : 0u)) | (g == 4 ? 0x3C003C00u : 0u);
+    const unsigned char* w = tile + kTileVs + 16 * (4 * h + t) + 4 * (g0 + (g & (GR - 1)));
+    uint32_t m = *reinterpret_cast<const uint32_t*>(w + kTileVm - kTileVs);
+    const uint32_t keep = g < GR ? 0xffffffffu : 0u, ones = g == 4 ? 0x3C003C00u : 0u;
+    V.m16[h] = 0u;
+    if (large) {
+      m = mul_half2(m, 0x2C002C00u);                                                                // m / 16
+      if (flip) m = fma_half2(*reinterpret_cast<const uint32_t*>(w), 0x3B803B80u, m);                // + 15 s / 16
+      V.m16[h] = m & keep;
+      V.m[h] = ones;
+    } else {
+      if (flip) m = fma_half2(*reinterpret_cast<const uint32_t*>(w), 0x4B804B80u, m);                // + 15 s
+      V.m[h] = (m & keep) | ones;
+    }
   }
 }
 
 // O^T += V^T . P^T for NT row tiles; p[nt][h] = weights of row g, token pair t + 4 h, as f16x2.
 template <int NT, int GR>
-__device__ __forceinline__ void add_values(RowTile<GR> (&A)[NT], const ValueRegs<GR>& V, const uint32_t (&p)[NT][2]) {
+__device__ __forceinline__ void add_values(RowTile<GR> (&A)[NT], const ValueRegs<GR>& V, uint32_t flip, const uint32_t (&p)[NT][2]) {
+  const uint32_t sign = flip & 0x80008000u;
 #pragma unroll
   for (int gr = 0; gr < GR; ++gr) {
     const uint32_t w0 = V.c[0][gr], w1 = V.c[1][gr], x0 = w0 >> 8, x1 = w1 >> 8;
-    const uint32_t a[8] = {w0 & 0x000F000Fu, w0 & 0x00F000F0u, w1 & 0x000F000Fu, w1 & 0x00F000F0u,
-                           x0 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x000F000Fu, x1 & 0x00F000F0u};
+    const uint32_t a[8] = {(w0 ^ flip) & 0x000F000Fu, (w0 ^ flip) & 0x00F000F0u, (w1 ^ flip) & 0x000F000Fu, (w1 ^ flip) & 0x00F000F0u,
+                           (x0 ^ flip) & 0x000F000Fu, (x0 ^ flip) & 0x00F000F0u, (x1 ^ flip) & 0x000F000Fu, (x1 ^ flip) & 0x00F000F0u};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const uint32_t b0 = mul_half2(p[nt][0], V.s[0][gr]), b1 = mul_half2(p[nt][1], V.s[1][gr]);
+      const uint32_t b0 = mul_half2(p[nt][0] ^ sign, V.s[0][gr]), b1 = mul_half2(p[nt][1] ^ sign, V.s[1][gr]);
       mma_f16(A[nt].o[2 * gr], a[0], a[1], a[2], a[3], b0, b1);
       mma_f16(A[nt].o[2 * gr + 1], a[4], a[5], a[6], a[7], b0, b1);
     }
   }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) mma_f16(A[nt].c, V.m[0], 0u, V.m[1], 0u, p[nt][0], p[nt][1]);
+  for (int nt = 0; nt < NT; ++nt) mma_f16(A[nt].c, V.m[0], V.m16[0], V.m[1], V.m16[1], p[nt][0], p[nt][1]);
 }
 
 // Prepares a tile that not every row sees as a whole (left: tokens of the context from its first on, possibly none).
@@ -402,11 +428,13 @@ __device__ __forceinline__ void process_stage(RowTile<4> (&A)[NT], const QueryTi
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) raise |= lane_best<NT, 2>(z, nt, e) > A[nt].top[e];
+  bool large = false;
   if (__any_sync(0xffffffffu, raise)) {
     float vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
     const float limit = weight_limit(vmax);
+    large = limit < kTopWeight;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
@@ -428,8 +456,8 @@ __device__ __forceinline__ void process_stage(RowTile<4> (&A)[NT], const QueryTi
       weights(p[nt], z[i][nt], A[nt].top, al.x, al.y);
     }
     ValueRegs<4> V;
-    load_values(V, stage + i * kTileBytes, 0, lane);
-    add_values(A, V, p);
+    load_values(V, stage + i * kTileBytes, 0, i ? ~0u : 0u, large, lane);
+    add_values(A, V, i ? ~0u : 0u, p);
   }
 }
 
@@ -486,6 +514,7 @@ __device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], const QuerySha
   pair_sync(pair);
   flags = X.flags[turn][0] | X.flags[turn][1];
   if (flags & kLate) return false;
+  bool large = false;
   if (flags) {
     float vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
 #pragma unroll
@@ -502,6 +531,7 @@ __device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], const QuerySha
       }
     pair_sync(pair);
     const float limit = weight_limit(fmaxf(X.vmax[0], X.vmax[1]));
+    large = limit < kTopWeight;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 al = qs[nt].alpha[lane];
@@ -515,18 +545,15 @@ __device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], const QuerySha
     pair_sync(pair);
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {  // the warp's own tile, then the other's
-    const int at = role ^ i;
-    if (i == 1) {
+  for (int i = 0; i < 2; ++i) {  // (the warp's own weights too come back from there: fewer registers in between)
 #pragma unroll
-      for (int k = 0; k < NT / 2; ++k) {
-        const uint4 v = X.p[turn][at][k][lane];
-        p[2 * k][0] = v.x, p[2 * k][1] = v.y, p[2 * k + 1][0] = v.z, p[2 * k + 1][1] = v.w;
-      }
+    for (int k = 0; k < NT / 2; ++k) {
+      const uint4 v = X.p[turn][i][k][lane];
+      p[2 * k][0] = v.x, p[2 * k][1] = v.y, p[2 * k + 1][0] = v.z, p[2 * k + 1][1] = v.w;
     }
     ValueRegs<2> V;
-    load_values(V, stage + at * kTileBytes, 2 * role, lane);
-    add_values(A, V, p);
+    load_values(V, stage + i * kTileBytes, 2 * role, i ? ~0u : 0u, large, lane);
+    add_values(A, V, i ? ~0u : 0u, p);
   }
   return true;
 }
@@ -550,8 +577,9 @@ __device__ __forceinline__ void store_out(uint16_t* out, const float4& o, float 
 }
 
 // The blocks that CTA i of n takes of `total`: [first(i), first(i + 1)), and the CTA that takes block b.
-__device__ __forceinline__ long long cta_first(long long total, int i, int n) { return total * i / n; }
-__device__ __forceinline__ int cta_of(long long total, long long b, int n) { return (int)(((b + 1) * n - 1) / total); }
+// (total is at most kQaSplitUnits x 16384.)
+__device__ __forceinline__ int cta_first(int total, int i, int n) { return (int)((long long)total * i / n); }
+__device__ __forceinline__ int cta_of(int total, int b, int n) { return (int)(((long long)(b + 1) * n - 1) / total); }
 
 // Workers of a CTA: warps, or pairs of them for four row tiles.
 __host__ __device__ constexpr int workers(int nt, int warps) { return nt == 4 ? warps / 2 : warps; }
@@ -596,26 +624,26 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
   const int ranks = a.split == kCluster ? (int)cg::this_cluster().num_blocks() : 1;
   const int rank = a.split == kCluster ? (int)cg::this_cluster().block_rank() : 0;
   int u = blockIdx.x / ranks, at = 0, pieces = gridDim.x;
-  long long todo = 1, total = 1, begin = 0;
+  int todo = 1, total = 1, begin = 0;
   auto cut = [&]() {  // a stage per worker at least; further CTAs have nothing to do
-    pieces = (int)min((long long)gridDim.x, (total + N / 2 - 1) / (N / 2));
-    const long long lo = blockIdx.x < pieces ? cta_first(total, blockIdx.x, pieces) : total;
+    pieces = min((int)gridDim.x, (total + N / 2 - 1) / (N / 2));
+    const int lo = blockIdx.x < pieces ? cta_first(total, blockIdx.x, pieces) : total;
     todo = blockIdx.x < pieces ? cta_first(total, blockIdx.x + 1, pieces) - lo : 0;
     return lo;
   };
   if (a.split == kPieces) {
     if (a.sel) {
-      total = (long long)a.units * a.max_sel;
+      total = a.units * a.max_sel;
       begin = cut();
-      u = (int)(begin / a.max_sel);
-      at = (int)(begin % a.max_sel);
+      u = begin / a.max_sel;
+      at = begin % a.max_sel;
     } else {
       const int per = (a.units + kThreads - 1) / kThreads, u0 = threadIdx.x * per, u1 = min(u0 + per, a.units);
       int mine = 0, sum;
       for (int i = u0; i < u1; ++i) mine += blocks_of(i);
       int before = block_scan_excl(mine, scan, &sum);
       total = sum;
-      const long long lo = begin = cut();
+      const int lo = begin = cut();
       for (int i = u0; i < u1; ++i) {  // the one thread whose units hold block lo
         const int n = blocks_of(i);
         if (before <= lo && lo < before + n) {
@@ -627,7 +655,7 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
       __syncthreads();
       if (todo == 0) return;
       u = found[0];
-      at = (int)lo - found[1];
+      at = lo - found[1];
     }
     begin -= at;
   }
@@ -641,11 +669,11 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
     const int len = length(u), whole = blocks_of(u);
     int first = at, end = whole;
     if (a.split == kPieces) {
-      end = (int)min((long long)whole, at + todo);
+      end = min(whole, at + todo);
       todo -= end - first;
     } else {
-      first = (int)cta_first(whole, rank, ranks);
-      end = (int)cta_first(whole, rank + 1, ranks);
+      first = cta_first(whole, rank, ranks);
+      end = cta_first(whole, rank + 1, ranks);
       todo = 0;
     }
     if (threadIdx.x == 0 && first == 0 && rank == 0 && len != a.lens[u]) atomicOr(a.err, kErrBounds);
@@ -755,7 +783,7 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
       for (int gr = 0; gr < (kPair ? 2 : 4); ++gr) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float m = __shfl_sync(0xffffffffu, T.c[i], 4 * gr + t);
+          const float m = fmaf(__shfl_sync(0xffffffffu, T.c[i + 2], 4 * gr + t), 16.f, __shfl_sync(0xffffffffu, T.c[i], 4 * gr + t));
           *reinterpret_cast<float4*>(w + i * kQaRowStride + 32 * gr + 4 * g) =
               make_float4(fmaf(T.o[2 * gr][i], 0x1p24f, m), fmaf(T.o[2 * gr][i + 2], 0x1p20f, m),
                           fmaf(T.o[2 * gr + 1][i], 0x1p24f, m), fmaf(T.o[2 * gr + 1][i + 2], 0x1p20f, m));

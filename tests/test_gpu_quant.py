@@ -630,3 +630,28 @@ print("ok")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "ok" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("units,group,nq", [(320, 8, 1), (16, 8, 2), (16, 8, 4)], ids=["8-rows", "16-rows", "32-rows"])
+def test_long_means_lose_no_more_than_roundings(units, group, nq):
+    """65,536 tokens that nearly cancel (a result of 0.006 from values of 1), a unit's tokens in few long sums.
+
+    The error's norm over the result's: rounding to bf16 is at most 2^-8 of each value (2^-9.8 in the mean square);
+    a token's weight and its product with s are rounded by 2^-11 at most, independently, so that their errors add up as
+    the tokens' values themselves do: sqrt(2 / 3) 2^-11 times the size of a code's part against its value's, 8.7 against
+    3.7 in units of s, 2^-10.1.  Together 2^-9; a sum that drifts by 2^-24 of its codes' part a step, 500 steps long, would
+    be off by 2^-6."""
+    nb = 1024
+    one = torch.from_numpy(_random_store(1, nb, 99)).cuda()
+    store = one.expand(units, -1, -1).contiguous()
+    q = _queries(np.random.default_rng(4), units, group, nq)
+    out, _ = _dense(q, store, _i32([64 * nb] * units), 64 * nb)
+    torch.cuda.synchronize()
+    kk, vv, _, _ = Q.unpack(one[0].cpu().numpy())
+    k, v = torch.from_numpy(kk).cuda().view(-1, 128), torch.from_numpy(vv).cuda().view(-1, 128)
+    at = torch.arange(64 * nb, device="cuda")
+    for u in (0, 3, units - 1):
+        for i in range(nq):
+            z = (q[u, :, i].double() @ k.T / math.sqrt(128)).masked_fill(at >= 64 * nb - (nq - 1 - i), -math.inf)
+            ref = torch.softmax(z, -1) @ v
+            assert ((out[u, :, i].double() - ref).norm() / ref.norm()).item() <= 2.0 ** -8
