@@ -655,3 +655,24 @@ def test_long_means_lose_no_more_than_roundings(units, group, nq):
             z = (q[u, :, i].double() @ k.T / math.sqrt(128)).masked_fill(at >= 64 * nb - (nq - 1 - i), -math.inf)
             ref = torch.softmax(z, -1) @ v
             assert ((out[u, :, i].double() - ref).norm() / ref.norm()).item() <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("group,nq", [(8, 1), (8, 2), (8, 4)])
+def test_rows_of_q_do_not_touch_each_other(group, nq):
+    """A NaN or an infinity in one row of q, and a row of zeros (the mean), leave the other rows as they are."""
+    n = 300
+    store = torch.from_numpy(_random_store(1, 5, 8)).cuda()
+    q = _queries(np.random.default_rng(3), 1, group, nq)
+    clean, _ = _dense(q, store, _i32([n]), n)
+    clean = clean.clone()
+    odd = q.clone()
+    odd[0, 1, 0, 7], odd[0, 3, nq - 1, 100], odd[0, 5, 0] = float("nan"), float("inf"), 0
+    out, _ = _dense(odd, store, _i32([n]), n)
+    torch.cuda.synchronize()
+    same = torch.ones((group, nq), dtype=torch.bool)
+    same[1, 0] = same[3, nq - 1] = same[5, 0] = False
+    assert torch.equal(out[0].cpu()[same], clean[0].cpu()[same])
+    assert out[0, 1, 0].isnan().all() and out[0, 3, nq - 1].isnan().all()
+    _, vv, _, sv = (x.reshape(-1, 128)[:n - (nq - 1)] for x in Q.unpack(store[0].cpu().numpy()))
+    err = np.abs(_f64(out[0, 5, 0]) - vv.mean(0))
+    assert (err <= 2.0 ** -8 * np.abs(vv.mean(0)) + 2.0 ** -9 * sv.max()).all()
