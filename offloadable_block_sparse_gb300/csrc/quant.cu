@@ -3,12 +3,15 @@
 // Both move tiles of 16 tokens through registers only: the lanes hold a tile in the store's own layout
 // (quant_core.cuh), so each lane's codes leave (or arrive) as 16-byte words, and the bf16 side is touched
 // in whole 32-byte sectors.  A token and unit is 512 bytes of bf16 and 160 of the store.
+#include <algorithm>
+
 #include "host.h"
 #include "quant_core.cuh"
 
 namespace nosa {
 
 constexpr int kQuantWarps = 4;
+constexpr int kAppendTiles = 4, kAppendCtas = 3000;
 
 // A group's range is kept as one register of two bf16, (max x, max -x), so that one shuffle and one packed
 // maximum serve both ends.  The maximum hands on NaN.
@@ -97,19 +100,18 @@ __device__ __forceinline__ CodeScale code_scale(const GroupCode& c, int owner) {
   return {pair(m, m), pair(s, s), pair(r, r)};
 }
 
-// Codes of 2 N bf16 values, 4 bits each, without a division: t = d r for d = x - m, then one Newton step on the
+// Codes of eight bf16 values, 4 bits each, without a division: t = d r for d = x - m, then one Newton step on the
 // remainder, t + (d - t s) r.  The remainder is exact (s has 11 bits, and the terms cancel), so a quotient that lies on
 // a border between two codes, k + 1/2, comes out as just that and goes to the even code; ties are frequent with
 // bf16 values (one in a thousand).  A quotient off the border is at least a unit of d's last place away from it in d,
 // which t resolves unless d fills all of float32's bits (x below 2^-15 of m).  Adding 1.5 x 2^23 rounds t to the
 // integer that then stands in the sum's low bits.
 // plain = false (some group of the warp has a subnormal s, zero or a NaN): by division, and zeros for the latter two.
-template <int N>
-__device__ __forceinline__ uint32_t codes(const uint32_t (&x)[N], const CodeScale& c, bool plain) {
+__device__ __forceinline__ uint32_t codes(const uint32_t (&x)[4], const CodeScale& c, bool plain) {
   const uint64_t magic = pair(12582912.f, 12582912.f);
   uint32_t w = 0xC0C00000u;  // what the constants' bits 0x4B400000 << 4 e add up to, negated
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const uint64_t d = add2(pair(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), c.negm2);
     const uint64_t t = mul2(d, c.r2);
     float u0, u1;
@@ -122,44 +124,42 @@ __device__ __forceinline__ uint32_t codes(const uint32_t (&x)[N], const CodeScal
     unpair(c.negs2, negs, unused);
     unpair(c.negm2, negm, unused);
     w = 0;
-    if (negs < 0.f) {
-      w = exact_codes(x[0], x[1], -negs, -negm);
-      if constexpr (N == 4) w |= exact_codes(x[2], x[3], -negs, -negm) << 16;
-    }
+    if (negs < 0.f) w = exact_codes(x[0], x[1], -negs, -negm) | exact_codes(x[2], x[3], -negs, -negm) << 16;
   }
   return w;
 }
 
-// One CTA per tile, one warp per half tile (8 tokens) of K or V: short enough for a single token, whose time is one
-// warp's path through the code, and small enough in registers for many warps.
+// A CTA takes `per` tiles in turn, a warp half a tile (8 tokens) of K or V: short enough for a single token, whose time
+// is one warp's path through the code, and small enough in registers for many warps.
 __global__ void __launch_bounds__(kQuantWarps * 32)
     quant_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, uint8_t* __restrict__ store,
                         int n, int max_blocks, const int32_t* __restrict__ pos, const int32_t* __restrict__ count,
-                        int tiles, int32_t* err) {
+                        int tiles, int per, int32_t* err) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int u = blockIdx.x / tiles, i = blockIdx.x % tiles;
+  const int ctas = (tiles + per - 1) / per, u = blockIdx.x / ctas, i0 = blockIdx.x % ctas * per;
   pdl_wait();
   pdl_launch_dependents();
   const long long p0 = pos ? pos[u] : 0, cap = (long long)max_blocks * kBlock;
   const int c0 = count ? count[u] : n, c = min(max(c0, 0), n);
-  const long long tile = (p0 >> 4) + i;  // an arithmetic shift: negative positions round down
-  if (i == 0 && threadIdx.x == 0 && err && (c0 != c || (c > 0 && (p0 < 0 || p0 + c > cap)))) atomicOr(err, kErrBounds);
+  if (i0 == 0 && threadIdx.x == 0 && err && (c0 != c || (c > 0 && (p0 < 0 || p0 + c > cap)))) atomicOr(err, kErrBounds);
   const int half = 8 * (warp >> 1);
-  const long long first = tile * kTileTokens;  // cap is a multiple of 16: a tile is in or out as a whole
-  const int rel = (int)(first - p0) + half;    // the half's first token among the new ones, -15 at least
-  if (tile < 0 || first >= cap || rel >= c || rel + 8 <= 0) return;
-  uint8_t* dst = store + (size_t)u * max_blocks * kQuantBlockBytes + (size_t)tile * kTileBytes;
-  auto is_new = [&](int j) { return (unsigned)(rel + j) < (unsigned)c; };  // the half's token j
-  auto row = [&](int j) { return ((size_t)u * n + (is_new(j) ? rel + j : 0)) * kHeadDim; };
+  const bool is_v = warp & 1;
+  long long tile = (p0 >> 4) + i0;                     // an arithmetic shift: negative positions round down
+  int rel = (int)(tile * kTileTokens - p0) + half;     // the half's first token among the new ones, -15 at least
+  uint8_t* dst = store + ((size_t)u * max_blocks * 4 + tile) * kTileBytes;  // (not used outside the store)
+  for (int done = 0; done < per && rel < c; ++done, ++tile, rel += kTileTokens, dst += kTileBytes) {
+    // cap is a multiple of 16: a tile is in or out as a whole
+    if (tile < 0 || tile * kTileTokens >= cap || rel + 8 <= 0) continue;
+    auto is_new = [&](int j) { return (unsigned)(rel + j) < (unsigned)c; };  // the half's token j
+    auto row = [&](int j) { return ((size_t)u * n + (is_new(j) ? rel + j : 0)) * kHeadDim; };
 
-  if ((warp & 1) == 0) {
-    // K: dims 32 gr + 8 t + e of token g in word gr; a group's range over the lanes t, dealt so that lane t ends up
-    // with group t
+    // the lane's part: dims 32 gr + 8 t + e of token g in word gr, which is K's own layout
     const bool in = is_new(g);
-    const uint16_t* src = k + row(g) + 8 * t;
+    const uint16_t* src = (is_v ? v : k) + row(g) + 8 * t;
     uint4 x[4];
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) x[gr] = in ? ld_stream_v4(src + 32 * gr) : make_uint4(0, 0, 0, 0);
+    // ranges over the lanes t, dealt so that lane t ends up with group t
     uint32_t r[4], w[4];
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr)
@@ -170,60 +170,37 @@ __global__ void __launch_bounds__(kQuantWarps * 32)
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
       const uint32_t y[4] = {x[gr].x, x[gr].y, x[gr].z, x[gr].w};
-      w[gr] = codes<4>(y, code_scale(q, (lane & ~3) | gr), plain);
+      w[gr] = codes(y, code_scale(q, (lane & ~3) | gr), plain);
     }
-    if (in) {
-      *reinterpret_cast<uint4*>(dst + 64 * (half + g) + 16 * t) = make_uint4(w[0], w[1], w[2], w[3]);
-      uint8_t* meta = dst + kTileKs + 16 * (half + g) + 2 * t;
-      *reinterpret_cast<uint16_t*>(meta) = (uint16_t)q.q.s;
-      *reinterpret_cast<uint16_t*>(meta + 8) = (uint16_t)q.q.m;
+    if (!is_v) {
+      if (in) {
+        *reinterpret_cast<uint4*>(dst + 64 * (half + g) + 16 * t) = make_uint4(w[0], w[1], w[2], w[3]);
+        uint8_t* meta = dst + kTileKs + 16 * (half + g) + 2 * t;
+        *reinterpret_cast<uint16_t*>(meta) = (uint16_t)q.q.s;
+        *reinterpret_cast<uint16_t*>(meta + 8) = (uint16_t)q.q.m;
+      }
+      continue;
     }
-  } else {
-    // V: dims 32 gr + 4 g + e of token 2 t + par in half `par` of word gr; a group's range over the lanes g, dealt so
-    // that lane g ends up with group g % 4 of token g / 4 of the pair
-    const bool in[2] = {is_new(2 * t), is_new(2 * t + 1)};
-    uint2 x[2][4];
-    uint32_t r[2][4], w[4];
-#pragma unroll
-    for (int par = 0; par < 2; ++par) {
-      const uint16_t* src = v + row(2 * t + par) + 4 * g;
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr)
-        x[par][gr] = in[par] ? __ldcs(reinterpret_cast<const uint2*>(src + 32 * gr)) : make_uint2(0, 0);
-    }
-#pragma unroll
-    for (int par = 0; par < 2; ++par)
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr)
-        r[par][gr] = range_of(max2_nan(x[par][gr].x, x[par][gr].y), min2_nan(x[par][gr].x, x[par][gr].y));
-    uint32_t d[4];
-#pragma unroll
-    for (int gr = 0; gr < 4; ++gr) d[gr] = deal(r[0][gr], r[1][gr], g & 4, 16);
-    const GroupCode q = group_code(deal(deal(d[0], d[2], g & 2, 8), deal(d[1], d[3], g & 2, 8), g & 1, 4));
-    const bool mine = g & 4 ? in[1] : in[0];
-    const bool plain = __all_sync(0xffffffffu, q.plain() || !mine);
-    if (mine) {
-      uint8_t* meta = dst + kTileVs + 16 * ((half >> 1) + t) + 4 * (g & 3) + 2 * (g >> 2);
-      *reinterpret_cast<uint16_t*>(meta) = (uint16_t)q.q.s;
-      *reinterpret_cast<uint16_t*>(meta + kTileVm - kTileVs) = (uint16_t)q.q.m;
-    }
+    // V's words hold four dims of a token pair: the pair's lanes (g even and odd) swap halves of theirs, and the even one
+    // keeps dims 8 t .. + 3 of both tokens, the odd one dims 8 t + 4 .. + 7
+    const int odd = g & 1;
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
-      uint32_t half_word[2];
-#pragma unroll
-      for (int par = 0; par < 2; ++par) {
-        const uint32_t y[2] = {x[par][gr].x, x[par][gr].y};
-        half_word[par] = codes<2>(y, code_scale(q, 16 * par + 4 * gr + t), plain);
-      }
-      w[gr] = __byte_perm(half_word[0], half_word[1], 0x5410);  // (a token that is not new has any bits)
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, w[gr], 4);
+      w[gr] = odd ? __byte_perm(other, w[gr], 0x7632) : __byte_perm(w[gr], other, 0x5410);
     }
-    uint8_t* out = dst + kTileV + 64 * half + 16 * lane;
-    if (in[0] && in[1]) {
+    uint8_t* out = dst + kTileV + 64 * half + 16 * (4 * (2 * t + odd) + (g >> 1));
+    const bool in0 = is_new(g & ~1), in1 = is_new(g | 1);
+    if (in0 && in1) {
       *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if (in[0] || in[1]) {  // the pair's other token stays as it is
-      const int par = in[1];
+    } else if (in0 || in1) {  // the pair's other token stays as it is
 #pragma unroll
-      for (int gr = 0; gr < 4; ++gr) *reinterpret_cast<uint16_t*>(out + 4 * gr + 2 * par) = (uint16_t)(w[gr] >> (16 * par));
+      for (int gr = 0; gr < 4; ++gr) *reinterpret_cast<uint16_t*>(out + 4 * gr + 2 * in1) = (uint16_t)(w[gr] >> (16 * in1));
+    }
+    if (in) {
+      uint8_t* meta = dst + kTileVs + 16 * ((half + g) >> 1) + 4 * t + 2 * odd;
+      *reinterpret_cast<uint16_t*>(meta) = (uint16_t)q.q.s;
+      *reinterpret_cast<uint16_t*>(meta + kTileVm - kTileVs) = (uint16_t)q.q.m;
     }
   }
 }
@@ -316,11 +293,13 @@ extern "C" nosa_status nosa_quant_append(const uint16_t* k, const uint16_t* v, u
     return NOSA_ERR_INVALID_ARG;
   // tiles that n tokens touch at most, from any starting position
   const long long tiles = ((long long)n_tokens + 2 * kTileTokens - 2) / kTileTokens;
-  const long long ctas = units * tiles;
+  // Up to kAppendTiles tiles a CTA, which saves the others' set-up, as long as every SM keeps a few CTAs' worth.
+  const int per = (int)std::min<long long>(kAppendTiles, std::max<long long>(1, units * tiles / kAppendCtas));
+  const long long ctas = units * ((tiles + per - 1) / per);
   if (ctas >= (1ll << 31) || (long long)units * max_blocks >= (1ll << 31)) return NOSA_ERR_INVALID_ARG;
   return launched(launch_ex(quant_append_kernel, dim3((unsigned)ctas), dim3(kQuantWarps * 32), 0,
                             static_cast<cudaStream_t>(stream), true, 0, k, v, store, n_tokens, max_blocks, pos,
-                            count, (int)tiles, err_out));
+                            count, (int)tiles, per, err_out));
 }
 
 extern "C" nosa_status nosa_quant_read(const uint8_t* store, int units, int max_blocks, const int32_t* blocks,
