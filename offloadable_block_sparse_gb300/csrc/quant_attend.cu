@@ -956,17 +956,18 @@ static int cluster_size(int units, int blocks, int wave, int n, int most) {
 //    spread further, and ragged lengths do not balance.
 //  * equal pieces of all units' blocks over one wave, merged by a second kernel.
 //  * one CTA per unit, where they are more than a wave and the last round is not too empty for their length: 512 units
-//    of 64 blocks 63.3 against 63.8 in pieces, of 8 blocks 15.0 against 21.1; 1024 of 64 109 against 117.
+//    of 64 blocks 64.5 against 65.2 in pieces, of 8 blocks 15.3 against 21.2; 1024 of 64 111 against 119.
 // 8 rows a unit:               cluster, 4 warps   cluster, 8 warps   pieces, 8 warps
-//    2 units of 64 blocks            6.9                 6.9               7.8
-//    8 units of 256                 14.0                14.0              12.1
-//   16 units of 64                   9.2                14.9               9.9
-//   16 units of 256                 16.9                22.3              14.7
-//   64 units of 64                  13.6                13.1              16.8
-//  256 units of 32                  21.0                20.2              24.8
-//  256 units listing 81             45.5                42.5              45.8
+//    2 units of 64 blocks            6.7                 7.4               7.6
+//    8 units of 256                 14.0                14.0              12.4
+//   16 units of 64                   9.1                 9.5              10.0
+//   16 units of 256                 17.1                19.7              14.9
+//   64 units of 64                  14.0                13.5              17.4
+//  256 units of 32                  21.4                20.4              25.3
+//  256 units listing 81             45.2                43.9              47.5
 // So clusters of eight warps where they fill most of a wave and the units are not long (listed blocks balance, lengths
-// may not), clusters of four for small calls.  With 16 or 32 rows pieces win from 64 blocks on.
+// may not), clusters of four for small calls.  With 16 or 32 rows pieces win from a few blocks a CTA on (32 rows, 16
+// units of 64 blocks: 17.6 against 23.0).
 static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks, bool listed) {
   int form = rows <= 8 ? kForm1x8 : rows <= 16 ? kForm2x4 : kForm4x4;
   const int n = form == kForm1x8 ? 8 : form == kForm2x4 ? 4 : 2, wave = std::min(d.ctas[form], 8 * d.sms);

@@ -676,3 +676,25 @@ def test_rows_of_q_do_not_touch_each_other(group, nq):
     _, vv, _, sv = (x.reshape(-1, 128)[:n - (nq - 1)] for x in Q.unpack(store[0].cpu().numpy()))
     err = np.abs(_f64(out[0, 5, 0]) - vv.mean(0))
     assert (err <= 2.0 ** -8 * np.abs(vv.mean(0)) + 2.0 ** -9 * sv.max()).all()
+
+
+def test_calls_on_two_streams_with_a_scratch_each():
+    """Calls that overlap share nothing but the store: every result is that of the call alone."""
+    host = _random_store(12, 60, 5)
+    store = torch.from_numpy(host).cuda()
+    rng = np.random.default_rng(9)
+    work = []
+    for nq in (1, 4):
+        q = _queries(rng, 12, 8, nq)
+        lens = _i32(rng.integers(1, 64 * 60 + 1, 12))
+        work.append((q, lens, _scratch(12, 8 * nq, 60), torch.empty_like(q), _dense(q, store, lens, 64 * 60)[0].clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    for _ in range(30):
+        for s, (q, lens, scratch, out, _) in zip(streams, work):
+            with torch.cuda.stream(s):
+                out.zero_()
+                _dense(q, store, lens, 64 * 60, scratch=scratch, out=out)
+        torch.cuda.synchronize()
+        for _, _, _, out, alone in work:
+            assert torch.equal(out, alone)
