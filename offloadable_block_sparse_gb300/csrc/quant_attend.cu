@@ -219,15 +219,19 @@ __device__ __forceinline__ void load_values(ValueRegs<GR>& V, const unsigned cha
     const unsigned char* w = tile + kTileVs + 16 * (4 * h + t) + 4 * (g0 + (g & (GR - 1)));
     uint32_t m = *reinterpret_cast<const uint32_t*>(w + kTileVm - kTileVs);
     const uint32_t keep = g < GR ? 0xffffffffu : 0u, ones = g == 4 ? 0x3C003C00u : 0u;
-    V.m16[h] = 0u;
-    if (large) {
-      m = mul_half2(m, 0x2C002C00u);                                                                // m / 16
-      if (flip) m = fma_half2(*reinterpret_cast<const uint32_t*>(w), 0x3B803B80u, m);                // + 15 s / 16
-      V.m16[h] = m & keep;
-      V.m[h] = ones;
+    const uint32_t s = flip ? *reinterpret_cast<const uint32_t*>(w) : 0u;
+    // m, or m / 16; + 15 s, or 15 s / 16.  By selects in the single warps' form (a branch cost it 2 %), by a branch in
+    // the pairs' (there the selects cost 3 %).
+    if (GR == 4 || !large) {
+      if (GR == 4) m = mul_half2(m, large ? 0x2C002C00u : 0x3C003C00u);
+      if (flip) m = fma_half2(s, GR == 4 && large ? 0x3B803B80u : 0x4B804B80u, m);
+      V.m[h] = (m & (GR == 4 && large ? 0u : keep)) | ones;
+      V.m16[h] = m & (GR == 4 && large ? keep : 0u);
     } else {
-      if (flip) m = fma_half2(*reinterpret_cast<const uint32_t*>(w), 0x4B804B80u, m);                // + 15 s
-      V.m[h] = (m & keep) | ones;
+      m = mul_half2(m, 0x2C002C00u);
+      if (flip) m = fma_half2(s, 0x3B803B80u, m);
+      V.m[h] = ones;
+      V.m16[h] = m & keep;
     }
   }
 }
