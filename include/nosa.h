@@ -469,7 +469,8 @@ nosa_status nosa_attend_noalloc(const uint16_t* q, const uint16_t* cache, const 
  * The 128 values of a token's K (or V) row fall into four groups of 32 consecutive dims.  A group
  * x_0 .. x_31 is held as
  *     m = f16(min x),   s = f16((max x - min x) / 15),   n_i = clamp(rint((x_i - m) / s), 0, 15)
- * (f16(), rint(): to nearest, ties to even; differences in float32; s = 0: n_i = 0) and stands for
+ * (f16(), rint(): to nearest, ties to even; differences in float32, and a quotient within 2^-20 of
+ * a border between two codes but not on it may take either; s = 0: n_i = 0) and stands for
  *     x^_i = n_i s + m.
  * A group where m or s is not finite in f16 (a NaN or an infinity in it, a minimum beyond f16's
  * range, a range beyond 15 times f16's) has m = s = NaN (bits 0x7E00) and reads as NaN in all its dims.

@@ -21,6 +21,11 @@
 // follows a row's maximum only when that would get a weight above 2^14, so the usual tile needs no rescaling, and is
 // set so that weight x s stays within f16 (R rises with a scale of 2 or more).  A CTA merges its warps in shared
 // memory; a unit's parts, where several CTAs share it, merge through the cluster or in a second kernel.
+//
+// Bound by HBM where a call is long: 256 units of 32,768 tokens and 4 rows (1.34 GB) in 198 us, 1.01 of measured HBM.
+// A tile takes 265 instructions with one row tile, at 16 warps an SM about the time of its 2,560 bytes, so shorter calls
+// pay for their start and end: 256 units listing 81 blocks (212 MB) 42.8 us, 0.74.  With four row tiles 568 instructions,
+// 76 of them MMAs: 16 units of 65,521 tokens and 32 rows 82.5 us against 25 of HBM and 33 of the tensor pipe.
 #include <cooperative_groups.h>
 
 #include <algorithm>
