@@ -974,23 +974,25 @@ static int cluster_size(int units, int blocks, int wave, int n, int most) {
 //   64 units of 64                  14.0                13.5              17.4
 //  256 units of 32                  21.4                20.4              25.3
 //  256 units listing 81             45.2                43.9              47.5
-// So clusters of eight warps where they fill most of a wave and the units are not long (listed blocks balance, lengths
-// may not), clusters of four for small calls.  With 16 or 32 rows pieces win from a few blocks a CTA on (32 rows, 16
-// units of 64 blocks: 17.6 against 23.0).
+// So clusters (of eight warps a CTA) where they fill most of a wave and the units are not long (listed blocks balance,
+// lengths may not), clusters of four warps a CTA for small calls.  16 and 32 rows: the same where clusters fill a wave (64
+// units of 64 blocks 19.1 against 23.4 and 31.0 against 35.6, 256 of 32 29.3 against 36.5 and 52.2 against 60.8), pieces
+// from a few blocks a CTA on where they do not (16 units of 64 blocks, 32 rows 19.3 against 17.6), and 16 CTAs for very few
+// units (2 of 32 blocks, 16 rows 9.1 against 10.0 with 8 and 10.2 in pieces).
 static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks, bool listed) {
   int form = rows <= 8 ? kForm1x8 : rows <= 16 ? kForm2x4 : kForm4x4;
   const int n = form == kForm1x8 ? 8 : form == kForm2x4 ? 4 : 2, wave = std::min(d.ctas[form], 8 * d.sms);
   const int rounds = (units + wave - 1) / wave;
   if (units > kQaSplitUnits || (units > wave && (long long)(rounds * wave - units) * blocks <= 24ll * units))
     return {form, kWhole, units, 0, kQaErrBytes};
-  const int cl = cluster_size(units, blocks, wave, n, 8);
-  if (form != kForm1x8) {
-    if (units * cl <= wave && blocks <= 4 * cl) return {form, kCluster, units * cl, cl, kQaErrBytes};
-  } else {
-    if (units * cl <= wave && 2 * units * cl > wave && blocks <= (listed ? 100 : 32) * cl)
-      return {form, kCluster, units * cl, cl, kQaErrBytes};
+  const int cl = cluster_size(units, blocks, wave, n, form != kForm1x8 && 64 * units <= wave ? 16 : 8);
+  if (units * cl <= wave && 2 * units * cl > wave && blocks <= (listed ? 100 : 32) * cl)
+    return {form, kCluster, units * cl, cl, kQaErrBytes};
+  if (form == kForm1x8) {
     const int wave4 = std::min(d.ctas[kForm1x4], 8 * d.sms), cl4 = cluster_size(units, blocks, wave4, 4, 16);
     if (units * cl4 <= wave4 && blocks <= 6 * cl4) return {kForm1x4, kCluster, units * cl4, cl4, kQaErrBytes};
+  } else if (units * cl <= wave && blocks <= 4 * cl) {
+    return {form, kCluster, units * cl, cl, kQaErrBytes};
   }
   const long long pieces = ((long long)units * blocks + n / 2 - 1) / (n / 2);
   const int ctas = (int)std::min<long long>(wave, pieces);
