@@ -698,3 +698,30 @@ def test_calls_on_two_streams_with_a_scratch_each():
         torch.cuda.synchronize()
         for _, _, _, out, alone in work:
             assert torch.equal(out, alone)
+
+
+def test_attention_past_32_bit_offsets_and_at_the_longest_context():
+    nb = 2 ** 32 // BB + 3  # the last blocks of the first unit start beyond 4 GiB
+    store = torch.zeros((2, nb, BB), dtype=torch.uint8, device="cuda")
+    few = _random_store(2, 2, 6)
+    store[:, nb - 2:] = torch.from_numpy(few).cuda()
+    q = _queries(np.random.default_rng(1), 2, 8, 1)
+    sel = torch.tensor([[nb - 1, nb - 2]] * 2, dtype=torch.int32, device="cuda")
+    lens = [64 * nb - 3, 64 * nb - 70]
+    out, sc = _sparse(q, store, sel, None, _i32(lens))
+    torch.cuda.synchronize()
+    assert int(sc[:4].view(torch.int32).item()) == 0
+    at = np.arange(64 * (nb - 2), 64 * nb).reshape(2, 64)
+    for u in range(2):
+        _check_unit(_f64(out[u]), _f64(q[u]), few[u], at, lens[u], 1, 1 / math.sqrt(128))
+    del store
+    # 1,048,576 tokens: sixteen copies of 65,536, which give what one copy gives
+    one = torch.from_numpy(_random_store(1, 1024, 21)).cuda()
+    long = one.repeat(1, 16, 1)
+    q = _queries(np.random.default_rng(2), 1, 4, 1)
+    a, _ = _dense(q, one, _i32([65536]), 65536)
+    b, sc = _dense(q, long, _i32([1 << 20]), 1 << 20)
+    with pytest.raises(N.NosaError):
+        _dense(q, long, _i32([1 << 20]), (1 << 20) + 1, scratch=(sc, sc.numel()))
+    torch.cuda.synchronize()
+    assert ((a.double() - b.double()).norm() / a.double().norm()).item() <= 2 * 2.0 ** -8  # each as in the test of means
