@@ -18,8 +18,9 @@
 //   P^T by movmatrix of the f16-packed weights, times s per group
 //   O^T (128 dims x 8 rows) += V codes^T . P^T       8 MMAs, + 1 for m and the sum
 // The query rows of a unit (q heads x query tokens, at most 32) are NT tiles of 8.  Weights are 2^(logit - R): R
-// follows a row's maximum only when that would get a weight above 2^14, so the usual tile needs no rescaling, and is
-// set so that weight x s stays within f16 (R rises with a scale of 2 or more).  A CTA merges its warps in shared
+// follows a row's maximum only when that would get a weight above 2^14, so the usual tile needs no rescaling; where a
+// scale of 2 or more could take weight x s out of f16, all of a warp's weights shrink by a power of two for good.  A CTA
+// merges its warps in shared
 // memory; a unit's parts, where several CTAs share it, merge through the cluster or in a second kernel.
 //
 // Bound by HBM where a call is long: 256 units of 32,768 tokens and 4 rows (1.34 GB) in 198 us, 1.01 of measured HBM.
@@ -176,11 +177,12 @@ __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], cons
   alpha[1] = fminf(fmaxf(scale * __shfl_sync(0xffffffffu, inv, 8 * t + 4), 0x1p-100f), 0x1p127f);
 }
 
-// One warp's running state for a tile of 8 rows: of rows 2t, 2t + 1 the score that has the weight 2^14, the largest
-// allowed (a score z has 2^((z - top) alpha + 14), so that a huge score less itself is zero); O^T (codes' part, in
+// One warp's running state for a tile of 8 rows: of rows 2t, 2t + 1 the score that has the largest weight allowed, 2^lift
+// (a score z has 2^((z - top) alpha + lift), so that a huge score less itself is zero; lift is the warp's, 14 until a V
+// scale of 2 or more calls for less, and no part of top, where a huge score would swallow it); O^T (codes' part, in
 // units of 2^-24, or 2^-20 for odd dims); and the minima's part: rows 0..3 the groups, row 4 the softmax sum,
 // rows 8..11 the groups' sixteenths.  A warp of a pair (process_pair) holds half the dims: GR = 2 groups.
-constexpr float kTopWeight = 14.f;
+constexpr float kTopWeight = 14.f;  // lift at the start
 template <int GR>
 struct RowTile {
   float top[2];
@@ -384,34 +386,52 @@ __device__ __forceinline__ float lane_best(const float (&z)[kTiles][NT][4], int 
   return best;
 }
 
-// The weight (as a power of two) up to which weights x V scales below vmax stay within f16: products below 2^15.
+// The weight (as a power of two) up to which weights x V scales up to vmax stay within f16: products below 2^15.
 __device__ __forceinline__ float weight_limit(float vmax) {
   if (!(vmax <= 65504.f)) vmax = 0.f;  // a NaN scale sets no limit
   return kTopWeight - (float)max((int)(__float_as_uint(vmax) >> 23) - 127, 0);
 }
 
-// Raises row 2t + e's top so that `best` weighs 2^(limit - 4), where it would weigh more than 2^limit.
 template <int GR>
-__device__ __forceinline__ void raise_top(RowTile<GR>& S, int e, float best, float al, float limit) {
-  const float old = S.top[e];
-  if ((best - old) * al + kTopWeight > limit) {  // the row's lanes agree; rows differ
-    const float top = best + (kTopWeight + 4.f - limit) / al, f = ex2((old - top) * al);
-    S.top[e] = top;
+__device__ __forceinline__ void rescale_row(RowTile<GR>& S, int e, float f) {
 #pragma unroll
-    for (int mt = 0; mt < 2 * GR; ++mt) {
-      S.o[mt][e] *= f;
-      S.o[mt][e + 2] *= f;
-    }
-    S.c[e] *= f;
-    S.c[e + 2] *= f;
+  for (int mt = 0; mt < 2 * GR; ++mt) {
+    S.o[mt][e] *= f;
+    S.o[mt][e + 2] *= f;
   }
+  S.c[e] *= f;
+  S.c[e + 2] *= f;
+}
+
+// Raises row 2t + e's top so that `best`, its best score, weighs 2^(lift - 4), where it would weigh more than 2^lift.
+// Returns whether it still weighs more than 2^limit.
+template <int GR>
+__device__ __forceinline__ bool raise_top(RowTile<GR>& S, int e, float best, float al, float lift, float limit) {
+  const float old = S.top[e];
+  if (best > old) {  // the row's lanes agree; rows differ
+    S.top[e] = best + 4.f / al;
+    rescale_row(S, e, ex2((old - S.top[e]) * al));
+  }
+  return fmaf(best - S.top[e], al, lift) > limit;
+}
+
+// Shrinks the weights of all rows from 2^lift at most to 2^limit.
+template <int NT, int GR>
+__device__ __forceinline__ void lower_lift(RowTile<GR> (&A)[NT], float& lift, float limit) {
+  const float f = ex2(limit - lift);
+  lift = limit;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) rescale_row(A[nt], e, f);
 }
 
 // Weights of tokens g, g + 8 and rows 2t, 2t + 1 as f16, transposed: of row g and token pairs t, t + 4.
-__device__ __forceinline__ void weights(uint32_t (&p)[2], const float (&z)[4], const float (&top)[2], float al0, float al1) {
+__device__ __forceinline__ void weights(uint32_t (&p)[2], const float (&z)[4], const float (&top)[2], float al0, float al1,
+                                        float lift) {
   float w[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(z[e] - top[e & 1], e & 1 ? al1 : al0, kTopWeight));
+  for (int e = 0; e < 4; ++e) w[e] = ex2(fmaf(z[e] - top[e & 1], e & 1 ? al1 : al0, lift));
   p[0] = movmatrix_trans(pack_half2(w[0], w[1]));
   p[1] = movmatrix_trans(pack_half2(w[2], w[3]));
 }
@@ -419,7 +439,7 @@ __device__ __forceinline__ void weights(uint32_t (&p)[2], const float (&z)[4], c
 // One or two row tiles: a warp takes a stage (two tiles, 32 tokens) by itself, both tiles at once so that their chains
 // of dependent operations overlap.  left: tokens of the context from the stage's first on.
 template <int NT>
-__device__ __forceinline__ void process_stage(RowTile<4> (&A)[NT], const QueryTile& Q, const float (&alpha1)[2],
+__device__ __forceinline__ void process_stage(RowTile<4> (&A)[NT], float& lift, const QueryTile& Q, const float (&alpha1)[2],
                                               const QueryShared* qs, unsigned char* stage, int* poison, int left, int nq,
                                               int rows, int lane) {
   const bool tail = left - (nq - 1) < kStageTokens;  // some row does not see the whole stage
@@ -444,6 +464,7 @@ __device__ __forceinline__ void process_stage(RowTile<4> (&A)[NT], const QueryTi
     for (int o = 1; o < 16; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
     const float limit = weight_limit(vmax);
     large = limit < kTopWeight;
+    bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
@@ -452,9 +473,10 @@ __device__ __forceinline__ void process_stage(RowTile<4> (&A)[NT], const QueryTi
         float best = lane_best<NT, 2>(z, nt, e);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-        raise_top(A[nt], e, best, e ? al.y : al.x, limit);
+        over |= raise_top(A[nt], e, best, e ? al.y : al.x, lift, limit);
       }
     }
+    if (__any_sync(0xffffffffu, over)) lower_lift(A, lift, limit);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -462,7 +484,7 @@ __device__ __forceinline__ void process_stage(RowTile<4> (&A)[NT], const QueryTi
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
-      weights(p[nt], z[i][nt], A[nt].top, al.x, al.y);
+      weights(p[nt], z[i][nt], A[nt].top, al.x, al.y, lift);
     }
     ValueRegs<4> V;
     load_values(V, stage + i * kTileBytes, 0, i ? ~0u : 0u, large, lane);
@@ -487,7 +509,7 @@ __device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0,
 
 // Returns whether the stage has arrived (late: this warp has seen that it has not; then the other is told).
 template <int NT>
-__device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], const QueryShared* qs, PairShared<NT>& X, int turn, int pair,
+__device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], float& lift, const QueryShared* qs, PairShared<NT>& X, int turn, int pair,
                                              int role, bool late, unsigned char* stage, int* poison, int left, int nq,
                                              int rows, int lane) {
   const int g = lane >> 2, t = lane & 3;
@@ -498,7 +520,7 @@ __device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], const QuerySha
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 al = qs[nt].alpha[lane];
-      weights(p[nt], z[0][nt], A[nt].top, al.x, al.y);
+      weights(p[nt], z[0][nt], A[nt].top, al.x, al.y, lift);
     }
 #pragma unroll
     for (int i = 0; i < NT / 2; ++i) X.p[turn][role][i][lane] = make_uint4(p[2 * i][0], p[2 * i][1], p[2 * i + 1][0], p[2 * i + 1][1]);
@@ -541,15 +563,17 @@ __device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], const QuerySha
     pair_sync(pair);
     const float limit = weight_limit(fmaxf(X.vmax[0], X.vmax[1]));
     large = limit < kTopWeight;
+    bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 al = qs[nt].alpha[lane];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int row = 8 * nt + 2 * t + e;
-        raise_top(A[nt], e, fmaxf(X.best[0][row], X.best[1][row]), e ? al.y : al.x, limit);
+        over |= raise_top(A[nt], e, fmaxf(X.best[0][row], X.best[1][row]), e ? al.y : al.x, lift, limit);
       }
     }
+    if (__any_sync(0xffffffffu, over)) lower_lift(A, lift, limit);  // the pair's warps see the same
     weigh();
     pair_sync(pair);
   }
@@ -690,7 +714,7 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
     if (a.nq > 1) __syncthreads();
     QueryTile Q;
     RowTile<kPair ? 2 : 4> A[NT];
-    float alpha1[2];
+    float alpha1[2], lift = kTopWeight;
     auto load_queries = [&]() {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -763,11 +787,11 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
         const int j = (me >> 1) + done * step, left = (a.sel ? list[j].y : len - (b0 + j) * kBlock) - half;
         if constexpr (kPair) {
           // beyond the sync inside, both warps are through with the stage before, and its place is free
-          late = !process_pair<NT>(A, qs, pairs[me], turn, me, role, late, stage, poison, left, a.nq, a.rows, lane);
+          late = !process_pair<NT>(A, lift, qs, pairs[me], turn, me, role, late, stage, poison, left, a.nq, a.rows, lane);
           turn ^= 1;
           if (started - done < S) issue();
         } else if (!late) {  // otherwise let what is in flight land, and start no more
-          process_stage<NT>(A, Q, alpha1, qs, stage, poison, left, a.nq, a.rows, lane);
+          process_stage<NT>(A, lift, Q, alpha1, qs, stage, poison, left, a.nq, a.rows, lane);
           __syncwarp();  // the stage is read
           issue();
         }
@@ -801,7 +825,7 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
       if (g == 4 && role == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          wr[me][8 * nt + 2 * t + i] = fmaxf(T.top[i] * (i ? al.y : al.x) - kTopWeight, kNoRef);  // in base-2 logits
+          wr[me][8 * nt + 2 * t + i] = fmaxf(T.top[i] * (i ? al.y : al.x) - lift, kNoRef);  // in base-2 logits
           wl[me][8 * nt + 2 * t + i] = T.c[i];
         }
       }

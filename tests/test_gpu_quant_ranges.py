@@ -1,0 +1,79 @@
+"""The attention over the 4-bit store at the ends of its types' ranges, in each of its forms (8, 16 and 32 query
+rows a unit), against the float64 oracle's reading of the same store."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import quant_oracle as Q
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from offloadable_block_sparse_gb300 import nosa as N  # noqa: E402
+
+BB = N.NOSA_QUANT_BLOCK_BYTES
+FORMS = [(8, 1), (8, 2), (8, 4)]  # q heads and query tokens a unit: 8, 16 and 32 rows
+
+
+def _stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _store(k, v):
+    """k, v float [units, n, 128]: their store on the device, and what it stands for (K, V, |n s| + |m| of V)."""
+    units, n = k.shape[:2]
+    nb = -(-n // 64)
+    kd, vd = (torch.from_numpy(np.asarray(x, np.float32)).to(torch.bfloat16).cuda() for x in (k, v))
+    store = torch.zeros((units, nb, BB), dtype=torch.uint8, device="cuda")
+    N.nosa_quant_append(kd, vd, store, units, n, nb, stream=_stream())
+    torch.cuda.synchronize()
+    got = Q.unpack(store.cpu().numpy().reshape(-1, BB))
+    kk, vv, _, sv = (x.reshape(units, nb * 64, 128)[:, :n] for x in got)
+    return store, kk, vv, sv
+
+
+def _dense(q, store, lens, scale=0.0):
+    units, group, nq = q.shape[:3]
+    nb = store.shape[1]
+    bytes_ = N.nosa_quant_scratch_bytes(units, group * nq, nb)
+    scratch = torch.zeros(bytes_, dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    N.nosa_quant_dense_attend(q, store, units, group, nq, nb, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                              64 * nb, out, scratch, bytes_, softmax_scale=scale, stream=_stream())
+    torch.cuda.synchronize()
+    assert int(scratch[:4].view(torch.int32).item()) == 0
+    return out.double().cpu().numpy()
+
+
+def _one_token(out, u, n, kk, vv, sv, dim):
+    """Every row of unit u has the values of the token it sees with the largest K in `dim`: one token's weight and
+    its product with s are rounded to f16 (2^-11 each, of the codes' part), m + 15 s too, and the result to bf16."""
+    nq = out.shape[2]
+    for i in range(nq):
+        see = n - (nq - 1 - i)
+        best = np.nonzero(kk[u, :see, dim] == kk[u, :see, dim].max())[0]
+        assert best.size == 1
+        ref = vv[u, best[0]]
+        err = np.abs(out[u, :, i] - ref)
+        assert (err <= 2.0 ** -8 * np.abs(ref) + 3 * 2.0 ** -11 * 16 * sv[u, best[0]]).all(), (i, np.nanmax(err))
+
+
+@pytest.mark.parametrize("group,nq", FORMS)
+@pytest.mark.parametrize("v_size", [1.0, 60.0, 9000.0])
+@pytest.mark.parametrize("q_size", [1e6, 1e9, 1e20])
+def test_huge_logits_leave_one_token_whatever_its_scale(group, nq, v_size, q_size):
+    rng = np.random.default_rng(41)
+    n = 300
+    k, v = rng.standard_normal((2, 2, n, 128))
+    v *= v_size
+    k[0, 251, 5], k[1, 40, 5] = 9.0, 9.0  # far above the others
+    store, kk, vv, sv = _store(k, v)
+    q = torch.zeros((2, group, nq, 128), dtype=torch.bfloat16, device="cuda")
+    q[..., 5] = q_size
+    out = _dense(q, store, [n, n])
+    for u in range(2):
+        _one_token(out, u, n, kk, vv, sv, 5)
