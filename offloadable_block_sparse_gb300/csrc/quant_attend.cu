@@ -130,9 +130,9 @@ struct QueryTile {
 
 // Rows 8 nt + g of q: scaled by a power of two that brings the row's largest magnitude into [2^9, 2^10)
 // (bf16 values down to 2^-23 of it stay exact in f16, and a group's sum stays in range).
-// alpha: the factors that turn the scores of rows 2t, 2t + 1 into logits in base 2.
+// alpha: the factors that turn the scores of rows 2t, 2t + 1, which are counted in 2^-24 / unit, into logits in base 2.
 __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], const uint16_t* q, int row, int rows, int lane,
-                                           float scale) {
+                                           float scale, float unit) {
   const int t = lane & 3;
   uint4 x[4];
   uint32_t big = 0;  // the largest magnitude's bf16 bits
@@ -171,10 +171,13 @@ __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], cons
   const uint32_t l01 = pack_half2(sum[0] - half_lo(h01), sum[1] - half_hi(h01));
   const uint32_t l23 = pack_half2(sum[2] - half_lo(h23), sum[3] - half_hi(h23));
   Q.sums = t == 0 ? h01 : t == 1 ? h23 : t == 2 ? l01 : l23;
-  // Kept away from zero and infinity: scores stay below 2^50, so below 2^-100 all weights are equal, and at the upper
-  // end any score but the largest has none.
-  alpha[0] = fminf(fmaxf(scale * __shfl_sync(0xffffffffu, inv, 8 * t), 0x1p-100f), 0x1p127f);  // row 2t's lanes: 8t ..
-  alpha[1] = fminf(fmaxf(scale * __shfl_sync(0xffffffffu, inv, 8 * t + 4), 0x1p-100f), 0x1p127f);
+  // Kept away from zero and infinity.  128 products of a q below 2^10 and an x^ below 2^20 make a score below 2^37, and
+  // any two differ by 2^-48 (f16's smallest steps) or not at all: below 2^-100 all weights are equal, and from 2^77 on any
+  // score but the largest has none, while score x alpha stays within float32.
+  const float most = 0x1p77f * (0x1p24f / unit);
+  scale *= 0x1p24f / unit;
+  alpha[0] = fminf(fmaxf(scale * __shfl_sync(0xffffffffu, inv, 8 * t), 0x1p-100f), most);  // row 2t's lanes: 8t ..
+  alpha[1] = fminf(fmaxf(scale * __shfl_sync(0xffffffffu, inv, 8 * t + 4), 0x1p-100f), most);
 }
 
 // One warp's running state for a tile of 8 rows: of rows 2t, 2t + 1 the score that has the largest weight allowed, 2^lift
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (NT == 1 || warp == nt) {
-          load_query(Q, alpha1, a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale * (0x1p24f / code_unit(NT)));
+          load_query(Q, alpha1, a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale, code_unit(NT));
           if (NT > 1) {
 #pragma unroll
             for (int gr = 0; gr < 4; ++gr)

@@ -77,3 +77,20 @@ def test_huge_logits_leave_one_token_whatever_its_scale(group, nq, v_size, q_siz
     out = _dense(q, store, [n, n])
     for u in range(2):
         _one_token(out, u, n, kk, vv, sv, 5)
+
+
+@pytest.mark.parametrize("group,nq", FORMS)
+@pytest.mark.parametrize("k_size", [1.0, 3000.0])
+@pytest.mark.parametrize("scale,q_size", [(1e30, 1.0), (3e38, 1e30), (0.0, 3e38), (3e38, 3e38)])
+def test_extreme_scales_leave_one_token_in_every_form(group, nq, k_size, scale, q_size):
+    """Logits up to 2^250 and beyond float32: the token with the largest takes all."""
+    rng = np.random.default_rng(43)
+    n = 300
+    k, v = rng.standard_normal((2, 2, n, 128))
+    k[0, 251, 5], k[1, 40, 5] = 9.0, 9.0
+    store, kk, vv, sv = _store(k * k_size, v)
+    q = torch.zeros((2, group, nq, 128), dtype=torch.bfloat16, device="cuda")
+    q[..., 5] = q_size
+    out = _dense(q, store, [n, n], scale=scale)
+    for u in range(2):
+        _one_token(out, u, n, kk, vv, sv, 5)
