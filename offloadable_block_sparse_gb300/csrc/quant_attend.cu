@@ -114,6 +114,9 @@ __device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
   const __half2 v = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ uint32_t at_least_2(uint32_t a) {  // a mask of the halves that are 2 or more
+  return __hge2_mask(*reinterpret_cast<const __half2*>(&a), __half2half2(__ushort_as_half((unsigned short)0x4000)));
+}
 __device__ __forceinline__ float half_lo(uint32_t a) { return __low2float(*reinterpret_cast<const __half2*>(&a)); }
 __device__ __forceinline__ float half_hi(uint32_t a) { return __high2float(*reinterpret_cast<const __half2*>(&a)); }
 __device__ __forceinline__ float ex2(float x) {
@@ -184,7 +187,7 @@ __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], cons
 // (a score z has 2^((z - top) alpha + lift), so that a huge score less itself is zero; lift is the warp's, 14 until a V
 // scale of 2 or more calls for less, and no part of top, where a huge score would swallow it); O^T (codes' part, in
 // units of 2^-24, or 2^-20 for odd dims); and the minima's part: rows 0..3 the groups, row 4 the softmax sum,
-// rows 8..11 the groups' sixteenths.  A warp of a pair (process_pair) holds half the dims: GR = 2 groups.
+// rows 8..11 the groups' maxima that enter as sixteenths.  A warp of a pair (process_pair) holds half the dims: GR = 2 groups.
 constexpr float kTopWeight = 14.f;  // lift at the start
 template <int GR>
 struct RowTile {
@@ -197,13 +200,16 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 
 
 // The V side of a tile as a lane holds it, GR groups from group g0 on: codes and scales of token pairs t, t + 4, and the
 // rows of the operand that goes with the weights alone: row g group g0 + g's minimum (g < GR), row 4 ones (the softmax
-// sum), and rows 8 + g a sixteenth of the minimum instead where the stage has scales of 2 or more (`large`).
+// sum).
 //
 // flip (all ones in a stage's second tile, else zero): the tile enters as -(15 - n) s and m + 15 s, its codes
 // complemented, its products negated and its maxima in the place of the minima.  Sums over codes of 0 .. 15 and over
 // minima alone would each be far larger than their total, and so would the rounding of long sums, which the tensor
 // cores cut off rather than round; with tiles taken from either end the sums stay near their totals.  (Taking 8 off each
-// code did the same for 3 to 7 % more time.)
+// code did the same for 3 to 7 % more time.)  A maximum with a scale of 2 or more, which may lie beyond f16, enters as its
+// sixteenth in row 8 + g instead (there the subnormals' step, 2^-24, is nothing against s; for smaller scales it could be
+// as large as the values).  large: the stage may have such a scale.  The single warps ask first, which saves them 1 %; the
+// pairs, which that branch would cost 4 %, always say yes.
 template <int GR>
 struct ValueRegs {
   uint32_t c[2][GR], s[2][GR], m[2], m16[2];
@@ -229,20 +235,19 @@ __device__ __forceinline__ void load_values(ValueRegs<GR>& V, const unsigned cha
     const unsigned char* w = tile + kTileVs + 16 * (4 * h + t) + 4 * (g0 + (g & (GR - 1)));
     uint32_t m = *reinterpret_cast<const uint32_t*>(w + kTileVm - kTileVs);
     const uint32_t keep = g < GR ? 0xffffffffu : 0u, ones = g == 4 ? 0x3C003C00u : 0u;
-    const uint32_t s = flip ? *reinterpret_cast<const uint32_t*>(w) : 0u;
-    // m, or m / 16; + 15 s, or 15 s / 16.  By selects in the single warps' form (a branch cost it 2 %), by a branch in
-    // the pairs' (there the selects cost 3 %).
-    if (GR == 4 || !large) {
-      if (GR == 4) m = mul_half2(m, large ? 0x2C002C00u : 0x3C003C00u);
-      if (flip) m = fma_half2(s, GR == 4 && large ? 0x3B803B80u : 0x4B804B80u, m);
-      V.m[h] = (m & (GR == 4 && large ? 0u : keep)) | ones;
-      V.m16[h] = m & (GR == 4 && large ? keep : 0u);
-    } else {
-      m = mul_half2(m, 0x2C002C00u);
-      if (flip) m = fma_half2(s, 0x3B803B80u, m);
-      V.m[h] = ones;
-      V.m16[h] = m & keep;
+    uint32_t m16 = 0;
+    if (flip) {
+      const uint32_t s = *reinterpret_cast<const uint32_t*>(w);
+      if (large) {
+        const uint32_t big = at_least_2(s);
+        m16 = fma_half2(s, 0x3B803B80u, mul_half2(m, 0x2C002C00u)) & big;  // 15 s / 16 + m / 16
+        m = fma_half2(s, 0x4B804B80u, m) & ~big;
+      } else {
+        m = fma_half2(s, 0x4B804B80u, m);
+      }
     }
+    V.m[h] = (m & keep) | ones;
+    V.m16[h] = m16 & keep;
   }
 }
 
@@ -453,7 +458,7 @@ __device__ __forceinline__ void process_stage(RowTile<4> (&A)[NT], float& lift, 
   // the largest V scale of the stage: below 2, weights up to 2^14 times scales stay within f16
   const uint4 vs = *reinterpret_cast<const uint4*>(stage + (lane >> 3 & 1) * kTileBytes + kTileVs + 16 * (lane & 7));
   const uint32_t vmax2 = max_half2(max_half2(vs.x, vs.y), max_half2(vs.z, vs.w));
-  bool raise = (vmax2 & 0x40004000u) != 0;  // exponent bit 14: 2 or more (scales have no sign)
+  bool raise = (vmax2 & 0x40004000u) != 0;  // 2 or more
   float z[2][NT][4];
   score_tiles<NT, 2>(z, Q, qs, stage, tail, left, nq, rows, lane);
 #pragma unroll
@@ -548,7 +553,6 @@ __device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], float& lift, c
   pair_sync(pair);
   flags = X.flags[turn][0] | X.flags[turn][1];
   if (flags & kLate) return false;
-  bool large = false;
   if (flags) {
     float vmax = fmaxf(half_lo(vmax2), half_hi(vmax2));
 #pragma unroll
@@ -565,7 +569,6 @@ __device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], float& lift, c
       }
     pair_sync(pair);
     const float limit = weight_limit(fmaxf(X.vmax[0], X.vmax[1]));
-    large = limit < kTopWeight;
     bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -588,7 +591,7 @@ __device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], float& lift, c
       p[2 * k][0] = v.x, p[2 * k][1] = v.y, p[2 * k + 1][0] = v.z, p[2 * k + 1][1] = v.w;
     }
     ValueRegs<2> V;
-    load_values(V, stage + i * kTileBytes, 2 * role, i ? ~0u : 0u, large, lane);
+    load_values(V, stage + i * kTileBytes, 2 * role, i ? ~0u : 0u, true, lane);
     add_values(A, V, i ? ~0u : 0u, p);
   }
   return true;

@@ -94,3 +94,24 @@ def test_extreme_scales_leave_one_token_in_every_form(group, nq, k_size, scale, 
     out = _dense(q, store, [n, n], scale=scale)
     for u in range(2):
         _one_token(out, u, n, kk, vv, sv, 5)
+
+
+@pytest.mark.parametrize("group,nq", FORMS)
+@pytest.mark.parametrize("scale_of", ["every-token", "one-token"])
+def test_small_groups_keep_their_values_beside_large_ones(group, nq, scale_of):
+    """Groups of one value (s = 0) next to a group with scales of 2 and more: weights and the softmax sum meet the same
+    minima, so that nothing but float32 sums and the result's rounding to bf16 stands between the value and the output."""
+    rng = np.random.default_rng(47)
+    n = 200
+    k, v = rng.standard_normal((2, 1, n, 128))
+    v[..., 0:32] *= 40.0 if scale_of == "every-token" else 1.0
+    v[:, 70, 0:32] *= 40.0
+    v[..., 32:64], v[..., 64:96], v[..., 96:128] = 1e-4, 1e-5, -3e-6
+    store, kk, vv, sv = _store(k, v)
+    q = torch.from_numpy(rng.standard_normal((1, group, nq, 128)).astype(np.float32)).to(torch.bfloat16).cuda()
+    out = _dense(q, store, [n])
+    ref = vv[0, 0, 32:]
+    assert (vv[0, :, 32:] == ref).all()
+    err = np.abs(out[0, :, :, 32:] - ref)
+    # float32 sums over 13 tiles, in units of the sum: less than 2^-16
+    assert (err <= (2.0 ** -8 + 2.0 ** -16) * np.abs(ref)).all(), (err / np.abs(ref)).max()
