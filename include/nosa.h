@@ -549,6 +549,11 @@ nosa_status nosa_quant_attend(const uint16_t* q, const uint8_t* store, const int
  * argument or without a device. */
 size_t nosa_quant_scratch_bytes(int units, int rows, int blocks);
 
+/* Test hook, as NOSA_F_TEST_ZERO_WAIT is for a context's calls: SM cycles that a wait for a staged tile may take in
+ * the two attention calls that this host thread makes from now on (negative: waits give up at once; 0: the built-in
+ * limit, about a second, which is also the most).  Calls captured in a graph keep the limit of their capture. */
+nosa_status nosa_debug_quant_wait(long long cycles);
+
 #ifdef __cplusplus
 }
 #endif

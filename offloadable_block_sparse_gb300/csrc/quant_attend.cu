@@ -73,6 +73,7 @@ struct QuantArgs {
   int units, nq, rows, max_blocks, max_sel, max_len;
   int split;      // kWhole: one CTA per unit, kPieces: equal pieces of all units' blocks, kCluster: a cluster per unit
   float scale;    // softmax scale x log2(e)
+  long long wait_limit;  // SM cycles a wait for a staged half block may take before it gives up (< 0: none)
 };
 
 // D (16 x 8, f32) += A (16 x 16, row) . B (16 x 8, col), f16 inputs.
@@ -597,6 +598,17 @@ __device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], float& lift, c
   return true;
 }
 
+// Waits for a staged half block.  Returns whether it came within `limit` cycles; waits on for those that did not, as long
+// again as the longest limit, so that the copy has landed before the ring has another use or the CTA ends.
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t phase, long long limit) {
+  if (mbar_try_wait(bar, phase)) return limit >= 0;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, phase)) {
+    if (clock64() - t0 > 2 * kWaitCycles) return false;
+  }
+  return clock64() - t0 <= limit;
+}
+
 // Adds a part (reference r, sum l, four dims o) to a running one.
 __device__ __forceinline__ void merge_part(float& R, float& L, float4& O, float r, float l, const float4& o) {
   const float top = fmaxf(R, r), f = ex2(R - top), h = ex2(r - top);
@@ -788,7 +800,7 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
       for (int i = 0; i < S; ++i) issue();
       if (b0 == first) load_queries();  // while the first stages arrive
       for (int done = 0; done < started; ++done) {
-        late |= !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[me][out], phase, kWaitCycles));
+        late |= !__all_sync(0xffffffffu, stage_wait(&bars[me][out], phase, a.wait_limit));
         unsigned char* stage = ring + out * kStageBytes4;
         const int j = (me >> 1) + done * step, left = (a.sel ? list[j].y : len - (b0 + j) * kBlock) - half;
         if constexpr (kPair) {
@@ -796,7 +808,7 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
           late = !process_pair<NT>(A, lift, qs, pairs[me], turn, me, role, late, stage, poison, left, a.nq, a.rows, lane);
           turn ^= 1;
           if (started - done < S) issue();
-        } else if (!late) {  // otherwise let what is in flight land, and start no more
+        } else if (!late) {  // otherwise wait for what is in flight, and start no more
           process_stage<NT>(A, lift, Q, alpha1, qs, stage, poison, left, a.nq, a.rows, lane);
           __syncwarp();  // the stage is read
           issue();
@@ -1037,6 +1049,8 @@ static cudaError_t launch_quant_attend(const QuantArgs& a, const QuantPlan& p, c
                    p.cluster, a);
 }
 
+static thread_local long long g_wait_limit = kWaitCycles;
+
 static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t scratch_bytes, cudaStream_t st) {
   QuantDevice d;
   if (!quant_device(&d)) return NOSA_ERR_CUDA;
@@ -1045,6 +1059,7 @@ static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t 
   const size_t parts = (size_t)plan.ctas + a.units;
   unsigned char* p = static_cast<unsigned char*>(scratch);
   a.split = plan.split;
+  a.wait_limit = g_wait_limit;
   a.err = reinterpret_cast<int*>(p);
   a.part = reinterpret_cast<float*>(p + kQaErrBytes);
   a.stats = reinterpret_cast<float2*>(a.part + parts * a.rows * kHeadDim);
@@ -1075,6 +1090,11 @@ static bool bad_args(const void* q, const void* store, const void* lens, const v
 }  // namespace nosa
 
 using namespace nosa;
+
+extern "C" nosa_status nosa_debug_quant_wait(long long cycles) {
+  g_wait_limit = cycles == 0 ? kWaitCycles : std::min(cycles, kWaitCycles);
+  return NOSA_OK;
+}
 
 extern "C" size_t nosa_quant_scratch_bytes(int units, int rows, int blocks) {
   QuantDevice d;

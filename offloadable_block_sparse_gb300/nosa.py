@@ -35,7 +35,7 @@ EXPORTS = ["nosa_validate_config", "nosa_query_sizes", "nosa_create", "nosa_dest
            "nosa_attend_noalloc", "nosa_step_plan", "nosa_forecast_select", "nosa_step_forecast",
            "nosa_forecast_join", "nosa_dense_attend", "nosa_dense_scratch_bytes", "nosa_prefill",
            "nosa_prefill_scratch_bytes", "nosa_quant_append", "nosa_quant_read", "nosa_quant_dense_attend",
-           "nosa_quant_attend", "nosa_quant_scratch_bytes"]
+           "nosa_quant_attend", "nosa_quant_scratch_bytes", "nosa_debug_quant_wait"]
 
 
 class nosa_config(ctypes.Structure):
@@ -124,6 +124,7 @@ def lib() -> ctypes.CDLL:
             "nosa_quant_dense_attend": [p, p, i32, i32, i32, i32, p, i32, ctypes.c_float, p, p, ctypes.c_size_t, vp],
             "nosa_quant_attend": [p, p, p, p, i32, i32, i32, i32, i32, p, ctypes.c_float, p, p, ctypes.c_size_t, vp],
             "nosa_quant_scratch_bytes": [i32, i32, i32],
+            "nosa_debug_quant_wait": [ctypes.c_longlong],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -356,3 +357,8 @@ def nosa_quant_attend(q, store, sel, sel_slot, units, group, n_queries, max_bloc
     _check(lib().nosa_quant_attend(_ptr(q), _ptr(store), _ptr(sel), _ptr(sel_slot), units, group, n_queries, max_blocks,
                                    max_sel, _ptr(lens), softmax_scale, _ptr(out), _ptr(scratch), scratch_bytes,
                                    stream or None), "nosa_quant_attend")
+
+
+def nosa_debug_quant_wait(cycles: int) -> None:
+    """Test hook: the wait limit of this thread's 4-bit attention calls (see include/nosa.h)."""
+    _check(lib().nosa_debug_quant_wait(cycles), "nosa_debug_quant_wait")
