@@ -545,8 +545,9 @@ nosa_status nosa_quant_attend(const uint16_t* q, const uint8_t* store, const int
                               float softmax_scale, uint16_t* out, void* scratch, size_t scratch_bytes, void* stream);
 
 /* Scratch bytes of the two attention calls for `rows` = group * n_queries query rows per unit and at
- * most `blocks` blocks per unit: never more than 256 + 520 rows (units + 16 SMs).  0 on a bad
- * argument or without a device. */
+ * most `blocks` blocks per unit: never more than 256 + 520 rows (units + 16 SMs), and never less for
+ * more units, rows or blocks, so that a scratch made for a program's largest call serves all of them.
+ * 0 on a bad argument or without a device. */
 size_t nosa_quant_scratch_bytes(int units, int rows, int blocks);
 
 /* Test hook, as NOSA_F_TEST_ZERO_WAIT is for a context's calls: SM cycles that a wait for a staged tile may take in

@@ -991,8 +991,27 @@ static bool quant_device(QuantDevice* out) {
 // How many CTAs a call takes, and how they share it.
 struct QuantPlan {
   int form, split, ctas, cluster;
-  size_t bytes;  // of the scratch
 };
+
+// Query rows' form, its workers a CTA and its CTAs in one wave.
+static int row_form(int rows) { return rows <= 8 ? kForm1x8 : rows <= 16 ? kForm2x4 : kForm4x4; }
+static int form_workers(int form) { return form == kForm1x8 ? 8 : form == kForm2x4 ? 4 : 2; }
+static int form_wave(const QuantDevice& d, int form) { return std::min(d.ctas[form], 8 * d.sms); }
+
+// Bytes of `parts` parts of `units` units behind the error word.
+static size_t parts_bytes(size_t units, size_t parts, int rows) {
+  return kQaErrBytes + units * sizeof(int2) + parts * rows * (kHeadDim + 2) * sizeof(float) + 16;
+}
+
+// What a call wants for its scratch: enough for pieces whether it takes them or not, so that more units, rows or blocks never
+// want less, and a scratch made for the largest call serves them all.  More units than a wave take pieces only where a
+// round's empty places, fewer than a wave, times the blocks are above 24 units (quant_plan).
+static size_t quant_bytes(const QuantDevice& d, int units, int rows, int blocks) {
+  const int form = row_form(rows), n = form_workers(form);
+  const long long wave = std::max({form_wave(d, kForm1x8), form_wave(d, kForm2x4), form_wave(d, kForm4x4)});
+  const long long u = std::min<long long>({units, kQaSplitUnits, std::max(wave, wave * blocks / 24)});
+  return parts_bytes(u, std::min(wave, (u * blocks + n / 2 - 1) / (n / 2)) + u, rows);
+}
 
 // The largest power of two of CTAs per unit, `most` at most, that fits all units into one wave and leaves each worker
 // a stage (clusters of 3, 6 or 12 pack badly).
@@ -1022,25 +1041,21 @@ static int cluster_size(int units, int blocks, int wave, int n, int most) {
 // from a few blocks a CTA on where they do not (16 units of 64 blocks, 32 rows 19.3 against 17.6), and 16 CTAs for very few
 // units (2 of 32 blocks, 16 rows 9.1 against 10.0 with 8 and 10.2 in pieces).
 static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks, bool listed) {
-  int form = rows <= 8 ? kForm1x8 : rows <= 16 ? kForm2x4 : kForm4x4;
-  const int n = form == kForm1x8 ? 8 : form == kForm2x4 ? 4 : 2, wave = std::min(d.ctas[form], 8 * d.sms);
+  const int form = row_form(rows), n = form_workers(form), wave = form_wave(d, form);
   const int rounds = (units + wave - 1) / wave;
   if (units > kQaSplitUnits || (units > wave && (long long)(rounds * wave - units) * blocks <= 24ll * units))
-    return {form, kWhole, units, 0, kQaErrBytes};
+    return {form, kWhole, units, 0};
   const int cl = cluster_size(units, blocks, wave, n, form != kForm1x8 && 64 * units <= wave ? 16 : 8);
   if (units * cl <= wave && 2 * units * cl > wave && blocks <= (listed ? 100 : 32) * cl)
-    return {form, kCluster, units * cl, cl, kQaErrBytes};
+    return {form, kCluster, units * cl, cl};
   if (form == kForm1x8) {
-    const int wave4 = std::min(d.ctas[kForm1x4], 8 * d.sms), cl4 = cluster_size(units, blocks, wave4, 4, 16);
-    if (units * cl4 <= wave4 && blocks <= 6 * cl4) return {kForm1x4, kCluster, units * cl4, cl4, kQaErrBytes};
+    const int wave4 = form_wave(d, kForm1x4), cl4 = cluster_size(units, blocks, wave4, 4, 16);
+    if (units * cl4 <= wave4 && blocks <= 6 * cl4) return {kForm1x4, kCluster, units * cl4, cl4};
   } else if (units * cl <= wave && blocks <= 4 * cl) {
-    return {form, kCluster, units * cl, cl, kQaErrBytes};
+    return {form, kCluster, units * cl, cl};
   }
   const long long pieces = ((long long)units * blocks + n / 2 - 1) / (n / 2);
-  const int ctas = (int)std::min<long long>(wave, pieces);
-  const size_t parts = (size_t)ctas + units;
-  return {form, kPieces, ctas, 0,
-          kQaErrBytes + (size_t)units * sizeof(int2) + parts * rows * (kHeadDim + 2) * sizeof(float) + 16};
+  return {form, kPieces, (int)std::min<long long>(wave, pieces), 0};
 }
 
 template <int NT, int W>
@@ -1055,7 +1070,7 @@ static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t 
   QuantDevice d;
   if (!quant_device(&d)) return NOSA_ERR_CUDA;
   const QuantPlan plan = quant_plan(d, a.units, a.rows, blocks, a.sel != nullptr);
-  if (scratch_bytes < plan.bytes) return NOSA_ERR_CAPACITY;
+  if (scratch_bytes < quant_bytes(d, a.units, a.rows, blocks)) return NOSA_ERR_CAPACITY;
   const size_t parts = (size_t)plan.ctas + a.units;
   unsigned char* p = static_cast<unsigned char*>(scratch);
   a.split = plan.split;
@@ -1100,7 +1115,7 @@ extern "C" size_t nosa_quant_scratch_bytes(int units, int rows, int blocks) {
   QuantDevice d;
   if (units < 1 || units > (1 << 20) || rows < 1 || rows > kQaMaxRows || blocks < 1 || blocks > 16384 || !quant_device(&d))
     return 0;
-  return std::max(quant_plan(d, units, rows, blocks, false).bytes, quant_plan(d, units, rows, blocks, true).bytes);
+  return quant_bytes(d, units, rows, blocks);
 }
 
 extern "C" nosa_status nosa_quant_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group,

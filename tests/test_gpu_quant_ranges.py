@@ -115,3 +115,40 @@ def test_small_groups_keep_their_values_beside_large_ones(group, nq, scale_of):
     err = np.abs(out[0, :, :, 32:] - ref)
     # float32 sums over 13 tiles, in units of the sum: less than 2^-16
     assert (err <= (2.0 ** -8 + 2.0 ** -16) * np.abs(ref)).all(), (err / np.abs(ref)).max()
+
+
+@pytest.mark.parametrize("rows,blocks", [(8, 64), (8, 20), (16, 64), (32, 64), (32, 8), (1, 1)])
+def test_scratch_for_more_is_enough_for_less(rows, blocks):
+    """A program sizes its scratch for its largest batch: fewer units, rows or blocks never want more."""
+    size = N.nosa_quant_scratch_bytes
+    units = [1, 2, 16, 64, 151, 152, 153, 303, 304, 305, 442, 443, 600, 608, 609, 2048, 2049, 5000, 1 << 20]
+    got = [size(u, rows, blocks) for u in units]
+    assert got == sorted(got), list(zip(units, got))
+    for u in units:
+        got = [size(u, r, blocks) for r in range(1, rows + 1)]
+        assert got == sorted(got), (u, got)
+        got = [size(u, rows, b) for b in (1, 2, 3, 7, 20, 26, 27, 64, 65, 100, 101, 1000, 16384)]
+        assert got == sorted(got), (u, got)
+
+
+def test_a_batch_that_shrinks_keeps_its_scratch():
+    store, kk, vv, sv = _store(*np.random.default_rng(5).standard_normal((2, 1, 64 * 64, 128)))
+    store = store.expand(443, -1, -1).contiguous()
+    q = torch.zeros((443, 8, 1, 128), dtype=torch.bfloat16, device="cuda")
+    bytes_ = N.nosa_quant_scratch_bytes(443, 8, 64)
+    scratch = torch.zeros(bytes_, dtype=torch.uint8, device="cuda")
+    lens = torch.full((443,), 64 * 64, dtype=torch.int32, device="cuda")
+    sel = torch.arange(64, dtype=torch.int32, device="cuda").repeat(443, 1)
+    mean = vv[0].mean(0)
+    tol = 2.0 ** -8 * np.abs(mean) + 2.0 ** -9 * sv[0].max()
+    for units in (443, 442, 305, 304, 152, 20, 1):
+        for listed in (False, True):
+            out = torch.full_like(q, float("nan"))
+            if listed:
+                N.nosa_quant_attend(q, store, sel, None, units, 8, 1, 64, 64, lens, out, scratch, bytes_, stream=_stream())
+            else:
+                N.nosa_quant_dense_attend(q, store, units, 8, 1, 64, lens, 64 * 64, out, scratch, bytes_, stream=_stream())
+            torch.cuda.synchronize()
+            got = out.double().cpu().numpy()
+            assert (np.abs(got[:units] - mean) <= tol).all()
+            assert np.isnan(got[units:]).all()
