@@ -523,9 +523,12 @@ nosa_status nosa_quant_read(const uint8_t* store, int units, int max_blocks, con
  *            error bits (zero them before the call to read them after it): bit 0 a length outside
  *            [0, max_len] (clamped), bit 1 a bounded wait for a staged tile gave up (outputs are
  *            NaN).  Calls that may run at the same time (other streams, graphs) need a scratch each.
- * The sums are float32.  q is exact (values below 2^-23 of their row's largest are rounded); the
- * weights exp(logit - reference), their products with s and V's group maxima m + 15 s are rounded to f16,
- * 2^-11 relative each.
+ * The sums are float32.  q is exact (values below 2^-22 of their row's largest are rounded).  The
+ * weights exp(logit - reference), their products with s and the group maxima m + 15 s that stand for the
+ * minima in every second 16 tokens of V are rounded to f16: 2^-11 relative each.  Weights and products
+ * that are small for f16 are off by 2^(e - 35) of the row's largest weight instead, where 2^e <= the
+ * largest s met in V < 2^(e + 1), or e = 0: by 2^-35 for values of usual size, by 2^-20 beside values near f16's ends.
+ * Logits of any size are fine: beyond float32 the largest takes all.
  * Asynchronous on `stream`.  NOSA_ERR_CAPACITY if the scratch is too small. */
 nosa_status nosa_quant_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group, int n_queries,
                                     int max_blocks, const int32_t* lens, int max_len, float softmax_scale,

@@ -133,7 +133,8 @@ struct QueryTile {
 };
 
 // Rows 8 nt + g of q: scaled by a power of two that brings the row's largest magnitude into [2^9, 2^10)
-// (bf16 values down to 2^-23 of it stay exact in f16, and a group's sum stays in range).
+// (bf16 values down to 2^-22 of it stay exact in f16, those of odd dims a sixteenth of their size among its subnormals,
+// and a group's sum stays in range).
 // alpha: the factors that turn the scores of rows 2t, 2t + 1, which are counted in 2^-24 / unit, into logits in base 2.
 __device__ __forceinline__ void load_query(QueryTile& Q, float (&alpha)[2], const uint16_t* q, int row, int rows, int lane,
                                            float scale, float unit) {
@@ -1090,7 +1091,7 @@ static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t 
   return NOSA_ERR_CUDA;
 }
 
-// The checks both calls share; units x rows and units x chunks stay below 2^31 with units <= 2^20.
+// The checks both calls share; units x rows stays below 2^31 with units <= 2^20.
 static bool bad_args(const void* q, const void* store, const void* lens, const void* out, const void* scratch, int units,
                      int group, int nq, int max_blocks, float scale) {
   if (!q || !store || !lens || !out || !scratch) return true;

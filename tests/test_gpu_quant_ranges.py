@@ -152,3 +152,21 @@ def test_a_batch_that_shrinks_keeps_its_scratch():
             got = out.double().cpu().numpy()
             assert (np.abs(got[:units] - mean) <= tol).all()
             assert np.isnan(got[units:]).all()
+
+
+@pytest.mark.parametrize("group,nq", FORMS)
+def test_small_values_of_q_are_exact(group, nq):
+    """Values of 2^-22 of their row's largest in odd and in even dims give exactly the same logits (about 1400, where the
+    last of a value's eight bits is worth 10): two tokens share the weight."""
+    small = 2.0 ** -22 * (1 + 2.0 ** -7)
+    k, v = np.zeros((2, 1, 2 + nq, 128))
+    k[0, 0, 33] = k[0, 1, 64] = 57344.0  # the same code and scale in an odd and in an even dim
+    v[0, 0], v[0, 1] = 1.0, 2.0
+    k[0, 2:] = -1.0  # the query tokens' own: no weight
+    store, kk, _, _ = _store(k, v)
+    assert kk[0, 0, 33] == kk[0, 1, 64] > 57000 and kk[0, 0, 0] == kk[0, 1, 0] == 0
+    q = torch.zeros((1, group, nq, 128), dtype=torch.bfloat16, device="cuda")
+    q[..., 0], q[..., 33], q[..., 64] = 1.0, small, small
+    out = _dense(q, store, [2 + nq], scale=1e5)
+    # groups of one value: weights alike, the sum and the minima exact
+    assert (out == 1.5).all()
