@@ -20,13 +20,16 @@
 // The query rows of a unit (q heads x query tokens, at most 32) are NT tiles of 8.  Weights are 2^(logit - R): R
 // follows a row's maximum only when that would get a weight above 2^14, so the usual tile needs no rescaling; where a
 // scale of 2 or more could take weight x s out of f16, all of a warp's weights shrink by a power of two for good.  A CTA
-// merges its warps in shared
-// memory; a unit's parts, where several CTAs share it, merge through the cluster or in a second kernel.
+// merges its warps in shared memory; a unit's parts, where several CTAs share it, merge through the cluster or in a
+// second kernel.  Weights, their products with s and the maxima of every second tile are f16 because the tensor cores
+// take them so; scores, sums and references are float32.  Against 64 bits results are off by 0.0017 to 0.0018 (root mean
+// square, relative), by 0.0016 to 0.0017 with everything in float32: the rest is the result's rounding to bf16.
 //
-// Bound by HBM where a call is long: 256 units of 32,768 tokens and 4 rows (1.34 GB) in 198 us, 1.01 of measured HBM.
-// A tile takes 265 instructions with one row tile, at 16 warps an SM about the time of its 2,560 bytes, so shorter calls
-// pay for their start and end: 256 units listing 81 blocks (212 MB) 42.8 us, 0.74.  With four row tiles 568 instructions,
-// 76 of them MMAs: 16 units of 65,521 tokens and 32 rows 82.5 us against 25 of HBM and 33 of the tensor pipe.
+// Bound by HBM where a call is long: 256 units of 32,768 tokens and 4 rows (1.34 GB) in 199 us, 1.00 of measured HBM.
+// A tile takes 276 instructions with one row tile, at 16 warps an SM about the time of its 2,560 bytes, so shorter calls
+// pay for their start and end: 256 units listing 81 blocks (212 MB) 43.0 us, 0.74.  With two row tiles 317 instructions:
+// 16 units of 65,521 tokens and 16 rows 45.8 us against 25 of HBM.  With four 566, 76 of them MMAs: the same and 32 rows
+// 85.0 us against 25 of HBM and 33 of the tensor pipe.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -635,7 +638,7 @@ __device__ __forceinline__ int cta_of(int total, int b, int n) { return (int)(((
 
 // Workers of a CTA: warps, or pairs of them for four row tiles.
 __host__ __device__ constexpr int workers(int nt, int warps) { return nt == 4 ? warps / 2 : warps; }
-// Warps an SM by registers: 128 a thread for one row tile, 255 for more.
+// Warps an SM by registers: 128 a thread for one row tile (where the compiler spills 84 bytes a thread), 255 for more.
 __host__ __device__ constexpr int warps_per_sm(int nt) { return nt == 1 ? 16 : 8; }
 
 template <int NT, int W>
@@ -1022,25 +1025,26 @@ static int cluster_size(int units, int blocks, int wave, int n, int most) {
   return cl;
 }
 
-// Three ways, by what a call pays (microseconds on GB300, back to back in a graph):
+// Three ways, by what a call pays (microseconds on GB300, back to back in a graph, all units of one length):
 //  * a cluster per unit, merged through distributed shared memory: no second kernel (about 5), but a unit cannot
 //    spread further, and ragged lengths do not balance.
 //  * equal pieces of all units' blocks over one wave, merged by a second kernel.
 //  * one CTA per unit, where they are more than a wave and the last round is not too empty for their length: 512 units
-//    of 64 blocks 64.5 against 65.2 in pieces, of 8 blocks 15.3 against 21.2; 1024 of 64 111 against 119.
+//    of 64 blocks 64.7 against 67.6 in pieces, of 8 blocks 15.9 against 24.2; 1024 of 64 114 against 124.
 // 8 rows a unit:               cluster, 4 warps   cluster, 8 warps   pieces, 8 warps
-//    2 units of 64 blocks            6.7                 7.4               7.6
-//    8 units of 256                 14.0                14.0              12.4
-//   16 units of 64                   9.1                 9.5              10.0
-//   16 units of 256                 17.1                19.7              14.9
-//   64 units of 64                  14.0                13.5              17.4
-//  256 units of 32                  21.4                20.4              25.3
-//  256 units listing 81             45.2                43.9              47.5
+//    2 units of 64 blocks            7.0                 7.5               7.9
+//    8 units of 256                 14.0                14.0              12.3
+//   16 units of 64                   9.1                 9.4              10.0
+//   16 units of 256                 17.1                19.3              14.8
+//   64 units of 64                  13.9                13.3              17.3
+//  256 units of 32                  21.6                20.7              27.4
+//  256 units listing 81             44.7                43.0              46.9
 // So clusters (of eight warps a CTA) where they fill most of a wave and the units are not long (listed blocks balance,
-// lengths may not), clusters of four warps a CTA for small calls.  16 and 32 rows: the same where clusters fill a wave (64
-// units of 64 blocks 19.1 against 23.4 and 31.0 against 35.6, 256 of 32 29.3 against 36.5 and 52.2 against 60.8), pieces
-// from a few blocks a CTA on where they do not (16 units of 64 blocks, 32 rows 19.3 against 17.6), and 16 CTAs for very few
-// units (2 of 32 blocks, 16 rows 9.1 against 10.0 with 8 and 10.2 in pieces).
+// lengths may not; the border of 100 listed blocks a CTA has no measurement of its own but the 81 below it), clusters of
+// four warps a CTA for small calls.  16 and 32 rows: the same where clusters fill a wave (64 units of 64 blocks 18.8
+// against 23.3 and 31.8 against 35.9, 256 of 32 29.5 against 36.6 and 53.4 against 61.5), pieces from a few blocks a CTA on
+// where they do not (16 units of 64 blocks, 32 rows 19.6 against 17.8), and 16 CTAs for very few units (2 of 32 blocks,
+// 16 rows 9.2 against 10.2 in pieces).
 static QuantPlan quant_plan(const QuantDevice& d, int units, int rows, int blocks, bool listed) {
   const int form = row_form(rows), n = form_workers(form), wave = form_wave(d, form);
   const int rounds = (units + wave - 1) / wave;
