@@ -828,7 +828,9 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
     }
     __syncthreads();  // the rings become the warps' partials
 
-    // the worker's partial: O of rows 2t, 2t + 1, dims 32 gr + 4 g .. + 3 of the warp's groups
+    // the worker's partial: O of rows 2t, 2t + 1, dims 32 gr + 4 g .. + 3 of the warp's groups, without the lift (a huge
+    // reference would swallow it)
+    const float unit = ex2(-lift);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const auto& T = A[nt];
@@ -838,17 +840,19 @@ __global__ void __launch_bounds__(W * 32, warps_per_sm(NT) / W) quant_attend_ker
       for (int gr = 0; gr < (kPair ? 2 : 4); ++gr) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float m = fmaf(__shfl_sync(0xffffffffu, T.c[i + 2], 4 * gr + t), 16.f, __shfl_sync(0xffffffffu, T.c[i], 4 * gr + t));
+          const float m =
+              fmaf(__shfl_sync(0xffffffffu, T.c[i + 2], 4 * gr + t), 16.f, __shfl_sync(0xffffffffu, T.c[i], 4 * gr + t)) * unit;
+          const float even = 0x1p24f * unit, odd = 0x1p20f * unit;
           *reinterpret_cast<float4*>(w + i * kQaRowStride + 32 * gr + 4 * g) =
-              make_float4(fmaf(T.o[2 * gr][i], 0x1p24f, m), fmaf(T.o[2 * gr][i + 2], 0x1p20f, m),
-                          fmaf(T.o[2 * gr + 1][i], 0x1p24f, m), fmaf(T.o[2 * gr + 1][i + 2], 0x1p20f, m));
+              make_float4(fmaf(T.o[2 * gr][i], even, m), fmaf(T.o[2 * gr][i + 2], odd, m),
+                          fmaf(T.o[2 * gr + 1][i], even, m), fmaf(T.o[2 * gr + 1][i + 2], odd, m));
         }
       }
       if (g == 4 && role == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          wr[me][8 * nt + 2 * t + i] = fmaxf(T.top[i] * (i ? al.y : al.x) - lift, kNoRef);  // in base-2 logits
-          wl[me][8 * nt + 2 * t + i] = T.c[i];
+          wr[me][8 * nt + 2 * t + i] = fmaxf(T.top[i] * (i ? al.y : al.x), kNoRef);  // in base-2 logits
+          wl[me][8 * nt + 2 * t + i] = T.c[i] * unit;
         }
       }
     }

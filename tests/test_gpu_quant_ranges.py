@@ -170,3 +170,26 @@ def test_small_values_of_q_are_exact(group, nq):
     out = _dense(q, store, [2 + nq], scale=1e5)
     # groups of one value: weights alike, the sum and the minima exact
     assert (out == 1.5).all()
+
+
+@pytest.mark.parametrize("group,nq", FORMS)
+@pytest.mark.parametrize("q_size", [1.0, 1e6, 1e10, 1e20])
+def test_equal_scores_share_the_weight_whatever_their_scales(group, nq, q_size):
+    """Two tokens with the same key, far above the others, in different warps' shares; the V scales beside one of them are
+    large.  Logits of 13 to 1e21."""
+    rng = np.random.default_rng(53)
+    n = 64 * 8 - 5
+    k, v = rng.standard_normal((2, 1, n, 128))
+    v[0, 64 * 5:64 * 5 + 64] *= 3000.0
+    k[0, 64 * 5 + 9] = k[0, 20]
+    k[0, [20, 64 * 5 + 9], 5] = 300.0
+    store, kk, vv, sv = _store(k, v)
+    a, b = 20, 64 * 5 + 9
+    assert np.array_equal(kk[0, a], kk[0, b])
+    q = torch.zeros((1, group, nq, 128), dtype=torch.bfloat16, device="cuda")
+    q[..., 5] = q_size
+    out = _dense(q, store, [n])
+    ref = (vv[0, a] + vv[0, b]) / 2
+    # weights, products with s and maxima rounded to f16, 2^-11 each of at most 16 |x^|'s parts, and the result to bf16
+    err = np.abs(out[0] - ref)
+    assert (err <= 2.0 ** -8 * np.abs(ref) + 3 * 2.0 ** -11 * 16 * (sv[0, a] + sv[0, b]) / 2).all(), np.nanmax(err / np.abs(ref))
