@@ -4,7 +4,7 @@ store, attending over it with each block's attention mass, and dropping the bloc
 An 8-bit store holds units x rows blocks of 64 tokens of one (sequence, kv head) each.  Values are e4m3
 codes times a power of two, one for the block's K and one for its V: the smallest s with max|x| <= 448 s.
 A block is four tiles of 16 tokens (2048 bytes of K codes, 2048 of V codes) and 128 bytes that begin with
-the two scales as float32.  include/nosa.h (nosa_fp8_append) gives the place of every code.
+the two scales as float32.  include/nosa.h (nosa_byte_append) gives the place of every code.
 
 The sizes are this repository's workloads (synth/inputs.py): 2 kv heads with 8 query heads each at 16K
 and 64K tokens, 8 kv heads with 4 query heads each at 32K, and the one-sequence 4K case.
@@ -275,8 +275,8 @@ def prepare(case, seed):
     st["out"] = torch.zeros((units, rows, D), dtype=torch.bfloat16, device="cuda")
     st["mass"] = torch.zeros((units, case["blocks"]), dtype=torch.float32, device="cuda") if op == "mass" else None
     st |= dict(group=case["group"], queries=case["queries"])
-    # the header's bound of nosa_fp8_scratch_bytes for 256 SMs
-    need = 512 + 536 * rows * (units + 4096) + (16 * rows * units * case["blocks"] if op == "mass" else 0)
+    # the header's bound of nosa_byte_scratch_bytes for 256 SMs
+    need = 512 + 536 * rows * (units + 4096) + (16 * (rows + 1) * units * case["blocks"] if op == "mass" else 0)
     st["scratch"] = torch.zeros(need, dtype=torch.uint8, device="cuda")
     return st
 
@@ -308,15 +308,15 @@ def _run_own(st):
         return st["acc_out"], st["slot_out"], st["row"]
     nb = st["nb"]
     if op == "append":
-        N.nosa_fp8_append(st["k"], st["v"], st["store"], units, st["n"], nb, pos=st["pos"], count=st["count"],
+        N.nosa_byte_append(st["k"], st["v"], st["store"], units, st["n"], nb, pos=st["pos"], count=st["count"],
                           stream=stream)
-        N.nosa_fp8_read(st["store"], units, nb, st["blocks"], st["n_blocks"], st["kv"], lens=st["lens"], stream=stream)
+        N.nosa_byte_read(st["store"], units, nb, st["blocks"], st["n_blocks"], st["kv"], lens=st["lens"], stream=stream)
         return st["kv"]
     if op == "dense":
-        N.nosa_fp8_dense_attend(st["q"], st["store"], units, st["group"], st["queries"], nb, st["lens"], st["context"],
+        N.nosa_byte_dense_attend(st["q"], st["store"], units, st["group"], st["queries"], nb, st["lens"], st["context"],
                                 st["out"], st["scratch"], st["scratch"].numel(), stream=stream)
         return st["out"]
-    N.nosa_fp8_attend(st["q"], st["store"], st["sel"], st["slots"], units, st["group"], st["queries"], nb,
+    N.nosa_byte_attend(st["q"], st["store"], st["sel"], st["slots"], units, st["group"], st["queries"], nb,
                       st["n_blocks"], st["lens"], st["out"], st["scratch"], st["scratch"].numel(), mass=st["mass"],
                       stream=stream)
     return st["out"] if st["mass"] is None else (st["out"], st["mass"])
