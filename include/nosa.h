@@ -554,9 +554,172 @@ nosa_status nosa_quant_attend(const uint16_t* q, const uint8_t* store, const int
 size_t nosa_quant_scratch_bytes(int units, int rows, int blocks);
 
 /* Test hook, as NOSA_F_TEST_ZERO_WAIT is for a context's calls: SM cycles that a wait for a staged tile may take in
- * the two attention calls that this host thread makes from now on (negative: waits give up at once; 0: the built-in
+ * the attention calls over 4-bit and 8-bit stores that this host thread makes from now on (negative: waits give up at once; 0: the built-in
  * limit, about a second, which is also the most).  Calls captured in a graph keep the limit of their capture. */
 nosa_status nosa_debug_quant_wait(long long cycles);
+
+/* ------------------------------------------------------------ 8-bit KV block store
+ * The same blocks in 8 bits, half of bf16: between the host store's precision and the 4-bit store's size, and, with
+ * nosa_evict, of a bounded size for any context.  The pages describe no such store.  Context-free; nothing here
+ * allocates, and every call can be captured in a CUDA graph.  A store is caller-owned device memory,
+ * uint8 [units][max_blocks][NOSA_BYTE_BLOCK_BYTES], 16-byte aligned: rows of one block of 64 tokens each.
+ *
+ * A block has a scale s_K for its 64 x 128 K values and s_V for its V values, each a power of two 2^e with
+ * -118 <= e <= 119, or 0 where all values are zero.  A value is held as an e4m3 code c (sign, 4 bits of exponent with
+ * bias 7, 3 of mantissa; 0x7F and 0xFF are NaN; the largest is 448) and stands for s c.  Writing a value takes c =
+ * e4m3(x / s), to nearest, ties to even, with the smallest s that makes |x| <= 448 s (values beyond 448 2^119 become that):
+ * |x - s c| <= max(2^-4 |x|, 2^-10 s).  A NaN or an infinity becomes a NaN and has no part in the scale.
+ *
+ * Bytes of a block: four tiles of 16 tokens, 4096 bytes each, then s_K and s_V as float32, then 120 unused ones.
+ *   [0, 2048)     of a tile: K code of token i, dim d at 1024 (i / 8) + 512 ((d % 32) / 16) + 16 (4 (i % 8) + d / 32) + d % 16
+ *   [2048, 4096)  V code of token i, dim d at 2048 + 512 ((d % 16) / 4) + 16 (4 (d / 16) + (i % 8) / 2) + 8 ((d % 4) / 2)
+ *                 + 4 (i / 8) + 2 (d % 2) + i % 2
+ * (a lane of the attention kernels finds its tensor-core operands in 16 consecutive bytes). */
+#define NOSA_BYTE_BLOCK_BYTES 16512
+
+/* Quantises tokens as they are written to an 8-bit store.
+ *   k, v     device bf16 [units][n_tokens][d], 16-byte aligned
+ *   pos      device int32 [units]: position of each unit's first token (NULL: 0 for all)
+ *   count    device int32 [units]: tokens of each unit to write, 0 .. n_tokens (NULL: n_tokens);
+ *            the tokens behind them (a padded batch) are not looked at
+ *   slot_blk device int32 [units][max_blocks]: the block that each row holds, -1 for none (nosa_evict keeps such a
+ *            table); a token's block is written to the lowest row that holds it.  NULL: row b holds block b
+ * A call that writes a block's first token begins the block: its scales come from the new tokens alone, and rows
+ * behind these hold nothing until they are written.  Otherwise the block keeps its scales, or takes larger ones
+ * if the new tokens need them; then the codes c of all its other rows become e4m3(c s_old / s_new).  Each such step
+ * halves s_old / s_new at least, so it rounds only codes whose values are below 2^-6 s_new.  Everything else
+ * in the store is left as it was.
+ * err_out (optional device int32, 4-byte aligned) gets bit 0 set when a count lies outside [0, n_tokens] (clamped),
+ * or a token's position is negative, at or behind 64 max_blocks (without slot_blk) or in a block that no row holds:
+ * that token is not written.  It is not cleared.  Two calls that write the same block at the same time race.
+ * Asynchronous on `stream`. */
+nosa_status nosa_byte_append(const uint16_t* k, const uint16_t* v, uint8_t* store, int units, int n_tokens,
+                             int max_blocks, const int32_t* pos, const int32_t* count, const int32_t* slot_blk,
+                             int32_t* err_out, void* stream);
+
+/* Reads blocks of an 8-bit store back to bf16 (s c, which bf16 holds exactly), in the layout of the block cache and of
+ * nosa_dense_attend.
+ *   blocks   device int32 [units][n_blocks]: the blocks to read, any order, repeats allowed; negative: none (zeros).
+ *            NULL: blocks 0 .. n_blocks - 1 of every unit
+ *   slots    device int32 [units][n_blocks]: the row that holds each listed block (NULL: row b holds block b); not
+ *            without blocks
+ *   lens     device int32 [units]: tokens of each unit; rows at or behind them are written as zeros whatever the
+ *            store holds there (NULL: every row is read)
+ *   kv       device bf16 [units][n_blocks][2][64][d], 16-byte aligned
+ * err_out as above: bit 0 when a listed block's row lies outside [0, max_blocks) (written as zeros). */
+nosa_status nosa_byte_read(const uint8_t* store, int units, int max_blocks, const int32_t* blocks, const int32_t* slots,
+                           int n_blocks, const int32_t* lens, uint16_t* kv, int32_t* err_out, void* stream);
+
+/* Attention over every token of an 8-bit store, for one query token or a few (drafted) ones.  Arguments as for
+ * nosa_quant_dense_attend, and
+ *   mass     device float32 [units][ceil(max_len / 64)] or NULL: receives the attention weight that each block of the
+ *            unit gets, summed over its tokens and the unit's rows (so a unit's masses add up to its rows that see a
+ *            token); 0 for blocks without a token.  What nosa_evict accumulates
+ *   scratch  device memory of at least nosa_byte_scratch_bytes(units, group * n_queries, ceil(max_len / 64), mass != NULL)
+ *            bytes, 256-byte aligned, its first 4 bytes as for nosa_quant_dense_attend
+ * A query that sees no token gets zeros; one with a value that is not finite, NaN.
+ * The sums, the weights' among them, are float32.  q is exact (values below 2^-22 of their row's largest are rounded).
+ * The weights exp(logit - reference) that multiply V are rounded to f16: 2^-11 relative each, 2^-35 of the row's
+ * largest weight at least.  Logits of any size are fine: beyond float32 the largest takes all.
+ * Asynchronous on `stream`.  NOSA_ERR_CAPACITY if the scratch is too small. */
+nosa_status nosa_byte_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group, int n_queries,
+                                   int max_blocks, const int32_t* lens, int max_len, float softmax_scale, uint16_t* out,
+                                   float* mass, void* scratch, size_t scratch_bytes, void* stream);
+
+/* The same over listed blocks.  Arguments as for nosa_quant_attend; mass is [units][max_sel], 0 for entries that are
+ * not attended.  With nosa_evict's table sel = slot_blk and sel_slot = 0, 1, 2, ... for every unit. */
+nosa_status nosa_byte_attend(const uint16_t* q, const uint8_t* store, const int32_t* sel, const int32_t* sel_slot,
+                             int units, int group, int n_queries, int max_blocks, int max_sel, const int32_t* lens,
+                             float softmax_scale, uint16_t* out, float* mass, void* scratch, size_t scratch_bytes,
+                             void* stream);
+
+/* Scratch bytes of the two attention calls for `rows` = group * n_queries query rows per unit and at most `blocks`
+ * blocks per unit, with their masses (mass != 0) or without: never more than 512 + 536 rows (units + 16 SMs), and
+ * 16 (rows + 1) units blocks more with masses; never less for more units, rows or blocks or with masses.  0 on a
+ * bad argument or without a device. */
+size_t nosa_byte_scratch_bytes(int units, int rows, int blocks, int mass);
+
+/* Eviction from a store by accumulated attention weight, for stores whose rows hold any block (slot_blk).  For
+ * each unit, with a_i the accumulated weight of row i:
+ *   1. a_i = decay a_i + mass_i (two float32 roundings; a NaN counts as 0) for rows that hold a block, 0 for the others
+ *   2. while more than `budget` rows would hold a block, next_block's among them, the block with the smallest a_i goes
+ *      (of equal ones the one with the higher number): its row is empty, a_i = 0.  Never dropped are the blocks below
+ *      sink_blocks, the last window_blocks of the unit's ceil(lens / 64), those behind them, and next_block
+ *   3. next_block, if no row holds it, takes the lowest empty row, with a_i = 0
+ * acc, slot_blk   device float32, int32 [units][slots]: a_i, and the block of each row (negative: none); a block
+ *                 has one row (of a block with several, all go or none)
+ * mass            device float32 [units][slots] (nosa_byte_attend's, with sel = slot_blk), or NULL: none
+ * lens            device int32 [units]: tokens of each unit; may be NULL if window_blocks is 0
+ * acc_out, slot_blk_out  as acc and slot_blk, which they may be (each its own; no other overlap)
+ * next_block      device int32 [units], or NULL: the block that the unit writes next (negative: none)
+ * next_slot       device int32 [units], or NULL: receives the row that holds next_block, -1 if none
+ * 1 <= slots <= 16384, 0 <= budget <= slots, 0 <= sink_blocks, 0 <= window_blocks, decay finite, >= 0.
+ * err_out (optional device int32, 4-byte aligned) gets bit 2 set when a next_block found no row (all rows hold blocks
+ * that are never dropped); it is not cleared.  Allocates nothing; asynchronous on `stream`. */
+nosa_status nosa_evict(const float* acc, const int32_t* slot_blk, const float* mass, int units, int slots,
+                       const int32_t* lens, int budget, int sink_blocks, int window_blocks, float decay, float* acc_out,
+                       int32_t* slot_blk_out, const int32_t* next_block, int32_t* next_slot, int32_t* err_out,
+                       void* stream);
+
+/* ------------------------------------------------------------ rotary positions
+ * The entry points above take q and k as they are attended; these calls turn a projection's output into that.  Of a
+ * head's d = 128 dims the first r (rot_dims) are rotated in r / 2 pairs, the others copied.  Pair i of a token at
+ * position p, (x_i, x_{i + r/2}) or (x_{2i}, x_{2i + 1}) if interleaved, becomes
+ *     attention_factor (x cos(p f_i) - x' sin(p f_i), x' cos(p f_i) + x sin(p f_i)),    f_i = base^(-2i / r)
+ * with f_i changed for contexts longer than the trained ones:
+ *     NOSA_ROPE_LINEAR  f_i / factor
+ *     NOSA_ROPE_BASE    base factor^(r / (r - 2)) in place of base (r = 2: no change), so that the slowest pair
+ *                       turns `factor` times slower and the fastest as before
+ *     NOSA_ROPE_PARTS   f_i (g + (1 - g) / factor), g = clamp((original f_i / 2 pi - low) / (high - low), 0, 1): pairs that
+ *                       turn more than `high` times over the `original` length as before, those that turn fewer than
+ *                       `low` times `factor` times slower */
+#define NOSA_ROPE_PLAIN 0
+#define NOSA_ROPE_LINEAR 1
+#define NOSA_ROPE_BASE 2
+#define NOSA_ROPE_PARTS 3
+typedef struct {
+  uint32_t struct_size;    /* sizeof(nosa_rope_config) */
+  int32_t rot_dims;        /* r: even, 2 .. 128 */
+  int32_t interleaved;     /* 0: pairs (i, i + r/2); 1: pairs (2i, 2i + 1) */
+  int32_t scaling;         /* NOSA_ROPE_* */
+  double base;             /* >= 1 */
+  double factor;           /* >= 1; not looked at by NOSA_ROPE_PLAIN */
+  double low, high;        /* NOSA_ROPE_PARTS: 0 <= low < high, turns */
+  double original;         /* NOSA_ROPE_PARTS: > 0, tokens */
+  double attention_factor; /* > 0; 0 => 1 */
+} nosa_rope_config;
+
+/* What nosa_rope takes: made once, on the host, plain data. */
+typedef struct {
+  uint32_t struct_size; /* sizeof(nosa_rope_table) */
+  int32_t rot_dims, interleaved;
+  float attention_factor;
+  uint64_t turn[64]; /* f_i / 2 pi in units of 2^-64 turns: p turn[i] modulo 2^64 is the angle at p, however far */
+} nosa_rope_table;
+nosa_status nosa_rope_make(const nosa_rope_config* cfg, nosa_rope_table* out);
+
+/* A tensor to rotate, of batch x heads x n_tokens rows of d values: row (b, h, t) begins at value
+ * b stride[0] + h stride[1] + t stride[2] of x (and of y, which receives it). */
+typedef struct {
+  const uint16_t* x;  /* device bf16 */
+  uint16_t* y;        /* device bf16; x itself with the same strides (in place), else no overlap */
+  int32_t heads;
+  int32_t pad_;
+  int64_t x_stride[3]; /* >= 0 */
+  int64_t y_stride[3]; /* >= d where that extent is above 1 */
+} nosa_rope_view;
+
+/* Rotates one or two tensors (q and k of a layer) in one launch.
+ *   pos      device int32 [batch]: position of each sequence's first token (NULL: 0 for all; any int32)
+ *   count    device int32 [batch]: tokens of each sequence, 0 .. n_tokens (NULL: n_tokens); rows behind them are
+ *            neither read nor written
+ *   inverse  != 0: turns the other way, attention_factor as before: the gradient of the rotation
+ * Angles are exact to 2^-24 of a half turn (and 2^-54 |p|, the table's own rounding), arithmetic is float32, the result
+ * is rounded once.  Rows that begin at multiples of 16 bytes with r a multiple of 16 are fastest.
+ * err_out (optional device int32, 4-byte aligned) gets bit 0 set when a count lies outside [0, n_tokens] (clamped);
+ * it is not cleared.  Allocates nothing, keeps nothing of `table` or `views`; asynchronous on `stream`. */
+nosa_status nosa_rope(const nosa_rope_table* table, const nosa_rope_view* views, int n_views, int batch, int n_tokens,
+                      const int32_t* pos, const int32_t* count, int inverse, int32_t* err_out, void* stream);
 
 #ifdef __cplusplus
 }

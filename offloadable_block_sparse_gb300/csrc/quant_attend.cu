@@ -37,19 +37,13 @@
 
 #include "host.h"
 #include "quant_core.cuh"
+#include "store_core.cuh"
 
 namespace nosa {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMergeWarps = 8;
 constexpr int kStageTokens = 32, kStageBytes4 = 2 * kTileBytes;
-constexpr int kQaSplitUnits = 2048;   // beyond, one CTA per unit
-constexpr int kQaList = 256;          // listed blocks looked up at a time
-constexpr int kQaMaxRows = 32;
-constexpr int kQaRowStride = 132;     // floats per row of a warp's partial in shared memory (no bank conflicts)
-constexpr size_t kQaErrBytes = 256;   // the scratch starts with the device error word
-constexpr float kNoRef = -3e38f;      // reference of a row that has seen no token
 
 // Half blocks in flight per worker.  A pair of warps frees a stage one late.
 __host__ __device__ constexpr int stages(int nt) { return nt == 4 ? 3 : 2; }
@@ -59,8 +53,6 @@ __host__ __device__ constexpr int quant_ring_bytes(int nt, int n) {
   const int ring = n * stages(nt) * kStageBytes4, partials = n * 8 * nt * kQaRowStride * 4;
   return ring > partials ? ring : partials;
 }
-
-enum { kWhole, kPieces, kCluster };
 
 struct QuantArgs {
   const uint16_t* q;
@@ -79,21 +71,6 @@ struct QuantArgs {
   long long wait_limit;  // SM cycles a wait for a staged half block may take before it gives up (< 0: none)
 };
 
-// D (16 x 8, f32) += A (16 x 16, row) . B (16 x 8, col), f16 inputs.
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// The same with D = A . B: a zero operand costs nothing, a zeroed accumulator four moves.
-__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                              uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
-               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
 // D (16 x 8, f32) = A (16 x 8, row) . B (8 x 8, col), f16 inputs.
 __device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};\n"
@@ -101,10 +78,6 @@ __device__ __forceinline__ void mma_f16_k8(float (&d)[4], uint32_t a0, uint32_t 
                : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -123,11 +96,6 @@ __device__ __forceinline__ uint32_t at_least_2(uint32_t a) {  // a mask of the h
 }
 __device__ __forceinline__ float half_lo(uint32_t a) { return __low2float(*reinterpret_cast<const __half2*>(&a)); }
 __device__ __forceinline__ float half_hi(uint32_t a) { return __high2float(*reinterpret_cast<const __half2*>(&a)); }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // The query rows of one tile of 8 as MMA operands, and the factors that undo their scaling.
 struct QueryTile {
@@ -602,40 +570,6 @@ __device__ __forceinline__ bool process_pair(RowTile<2> (&A)[NT], float& lift, c
   return true;
 }
 
-// Waits for a staged half block.  Returns whether it came within `limit` cycles; waits on for those that did not, as long
-// again as the longest limit, so that the copy has landed before the ring has another use or the CTA ends.
-__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t phase, long long limit) {
-  if (mbar_try_wait(bar, phase)) return limit >= 0;
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, phase)) {
-    if (clock64() - t0 > 2 * kWaitCycles) return false;
-  }
-  return clock64() - t0 <= limit;
-}
-
-// Adds a part (reference r, sum l, four dims o) to a running one.
-__device__ __forceinline__ void merge_part(float& R, float& L, float4& O, float r, float l, const float4& o) {
-  const float top = fmaxf(R, r), f = ex2(R - top), h = ex2(r - top);
-  R = top;
-  L = L * f + l * h;
-  O.x = O.x * f + o.x * h;
-  O.y = O.y * f + o.y * h;
-  O.z = O.z * f + o.z * h;
-  O.w = O.w * f + o.w * h;
-}
-
-// Four dims of an output row: zeros where no token was seen.
-__device__ __forceinline__ void store_out(uint16_t* out, const float4& o, float l) {
-  uint2 v = make_uint2(0, 0);
-  if (l != 0.f) v = make_uint2(pack_bf16x2(o.x / l, o.y / l), pack_bf16x2(o.z / l, o.w / l));
-  *reinterpret_cast<uint2*>(out) = v;
-}
-
-// The blocks that CTA i of n takes of `total`: [first(i), first(i + 1)), and the CTA that takes block b.
-// (total is at most kQaSplitUnits x 16384.)
-__device__ __forceinline__ int cta_first(int total, int i, int n) { return (int)((long long)total * i / n); }
-__device__ __forceinline__ int cta_of(int total, int b, int n) { return (int)(((long long)(b + 1) * n - 1) / total); }
-
 // Workers of a CTA: warps, or pairs of them for four row tiles.
 __host__ __device__ constexpr int workers(int nt, int warps) { return nt == 4 ? warps / 2 : warps; }
 // Warps an SM by registers: 128 a thread for one row tile (where the compiler spills 84 bytes a thread), 255 for more.
@@ -1073,7 +1007,7 @@ static cudaError_t launch_quant_attend(const QuantArgs& a, const QuantPlan& p, c
                    p.cluster, a);
 }
 
-static thread_local long long g_wait_limit = kWaitCycles;
+thread_local long long g_wait_limit = kWaitCycles;
 
 static nosa_status quant_attend(QuantArgs& a, int blocks, void* scratch, size_t scratch_bytes, cudaStream_t st) {
   QuantDevice d;

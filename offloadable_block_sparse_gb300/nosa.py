@@ -25,6 +25,8 @@ NOSA_F_DMA_BIAS = 8
 NOSA_F_TEST_RADIX_TOPK = 16
 NOSA_F_TEST_PREFILL_WIDE = 32
 NOSA_QUANT_BLOCK_BYTES = 10240
+NOSA_BYTE_BLOCK_BYTES = 16512
+NOSA_ROPE_PLAIN, NOSA_ROPE_LINEAR, NOSA_ROPE_BASE, NOSA_ROPE_PARTS = 0, 1, 2, 3
 NOSA_MERGE_AUTO, NOSA_MERGE_KERNEL, NOSA_MERGE_TICKET, NOSA_MERGE_CLUSTER = 0, 1, 2, 3
 
 # every entry point declared in include/nosa.h
@@ -35,7 +37,9 @@ EXPORTS = ["nosa_validate_config", "nosa_query_sizes", "nosa_create", "nosa_dest
            "nosa_attend_noalloc", "nosa_step_plan", "nosa_forecast_select", "nosa_step_forecast",
            "nosa_forecast_join", "nosa_dense_attend", "nosa_dense_scratch_bytes", "nosa_prefill",
            "nosa_prefill_scratch_bytes", "nosa_quant_append", "nosa_quant_read", "nosa_quant_dense_attend",
-           "nosa_quant_attend", "nosa_quant_scratch_bytes", "nosa_debug_quant_wait"]
+           "nosa_quant_attend", "nosa_quant_scratch_bytes", "nosa_debug_quant_wait", "nosa_byte_append",
+           "nosa_byte_read", "nosa_byte_dense_attend", "nosa_byte_attend", "nosa_byte_scratch_bytes", "nosa_evict",
+           "nosa_rope_make", "nosa_rope"]
 
 
 class nosa_config(ctypes.Structure):
@@ -70,6 +74,22 @@ class nosa_state_view(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("sel", "sel_kind", "sel_slot", "n_sel", "fetch", "n_fetch",
                                                "slot_blk", "evicted", "kt", "se_win", "se_blk", "gamma",
                                                "last_used")]
+
+
+class nosa_rope_config(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("rot_dims", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32)] + [(n, ctypes.c_double) for n in ("base", "factor", "low", "high", "original",
+                                                                                "attention_factor")]
+
+
+class nosa_rope_table(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("rot_dims", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("attention_factor", ctypes.c_float), ("turn", ctypes.c_uint64 * 64)]
+
+
+class nosa_rope_view(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int32), ("pad_", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
 
 
 class NosaError(RuntimeError):
@@ -125,6 +145,14 @@ def lib() -> ctypes.CDLL:
             "nosa_quant_attend": [p, p, p, p, i32, i32, i32, i32, i32, p, ctypes.c_float, p, p, ctypes.c_size_t, vp],
             "nosa_quant_scratch_bytes": [i32, i32, i32],
             "nosa_debug_quant_wait": [ctypes.c_longlong],
+            "nosa_byte_append": [p, p, p, i32, i32, i32, p, p, p, p, vp],
+            "nosa_byte_read": [p, i32, i32, p, p, i32, p, p, p, vp],
+            "nosa_byte_dense_attend": [p, p, i32, i32, i32, i32, p, i32, ctypes.c_float, p, p, p, ctypes.c_size_t, vp],
+            "nosa_byte_attend": [p, p, p, p, i32, i32, i32, i32, i32, p, ctypes.c_float, p, p, p, ctypes.c_size_t, vp],
+            "nosa_byte_scratch_bytes": [i32, i32, i32, i32],
+            "nosa_evict": [p, p, p, i32, i32, p, i32, i32, i32, ctypes.c_float, p, p, p, p, p, vp],
+            "nosa_rope_make": [ctypes.POINTER(nosa_rope_config), ctypes.POINTER(nosa_rope_table)],
+            "nosa_rope": [ctypes.POINTER(nosa_rope_table), ctypes.POINTER(nosa_rope_view), i32, i32, i32, p, p, i32, p, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -135,6 +163,7 @@ def lib() -> ctypes.CDLL:
         L.nosa_dense_scratch_bytes.restype = ctypes.c_size_t
         L.nosa_prefill_scratch_bytes.restype = ctypes.c_size_t
         L.nosa_quant_scratch_bytes.restype = ctypes.c_size_t
+        L.nosa_byte_scratch_bytes.restype = ctypes.c_size_t
         _lib = L
     return _lib
 
@@ -362,3 +391,68 @@ def nosa_quant_attend(q, store, sel, sel_slot, units, group, n_queries, max_bloc
 def nosa_debug_quant_wait(cycles: int) -> None:
     """Test hook: the wait limit of this thread's 4-bit attention calls (see include/nosa.h)."""
     _check(lib().nosa_debug_quant_wait(cycles), "nosa_debug_quant_wait")
+
+
+def nosa_byte_append(k, v, store, units, n_tokens, max_blocks, pos=None, count=None, slot_blk=None, err_out=None,
+                     stream=0) -> None:
+    """Quantises tokens k, v [units][n_tokens][d] into an 8-bit store [units][max_blocks][16512] (see include/nosa.h)."""
+    _check(lib().nosa_byte_append(_ptr(k), _ptr(v), _ptr(store), units, n_tokens, max_blocks, _ptr(pos), _ptr(count),
+                                  _ptr(slot_blk), _ptr(err_out), stream or None), "nosa_byte_append")
+
+
+def nosa_byte_read(store, units, max_blocks, blocks, n_blocks, kv, slots=None, lens=None, err_out=None, stream=0) -> None:
+    """Reads blocks of an 8-bit store back to bf16 kv [units][n_blocks][2][64][d] (see include/nosa.h)."""
+    _check(lib().nosa_byte_read(_ptr(store), units, max_blocks, _ptr(blocks), _ptr(slots), n_blocks, _ptr(lens),
+                                _ptr(kv), _ptr(err_out), stream or None), "nosa_byte_read")
+
+
+def nosa_byte_scratch_bytes(units, rows, blocks, mass=False) -> int:
+    return int(lib().nosa_byte_scratch_bytes(units, rows, blocks, int(bool(mass))))
+
+
+def nosa_byte_dense_attend(q, store, units, group, n_queries, max_blocks, lens, max_len, out, scratch, scratch_bytes,
+                           mass=None, softmax_scale=0.0, stream=0) -> None:
+    """Attention over every token of an 8-bit store, q/out [units][group][n_queries][d] (see include/nosa.h)."""
+    _check(lib().nosa_byte_dense_attend(_ptr(q), _ptr(store), units, group, n_queries, max_blocks, _ptr(lens), max_len,
+                                        softmax_scale, _ptr(out), _ptr(mass), _ptr(scratch), scratch_bytes,
+                                        stream or None), "nosa_byte_dense_attend")
+
+
+def nosa_byte_attend(q, store, sel, sel_slot, units, group, n_queries, max_blocks, max_sel, lens, out, scratch,
+                     scratch_bytes, mass=None, softmax_scale=0.0, stream=0) -> None:
+    """Attention over listed blocks sel [units][max_sel] of an 8-bit store (see include/nosa.h)."""
+    _check(lib().nosa_byte_attend(_ptr(q), _ptr(store), _ptr(sel), _ptr(sel_slot), units, group, n_queries, max_blocks,
+                                  max_sel, _ptr(lens), softmax_scale, _ptr(out), _ptr(mass), _ptr(scratch),
+                                  scratch_bytes, stream or None), "nosa_byte_attend")
+
+
+def nosa_evict(acc, slot_blk, mass, units, slots, lens, budget, sink_blocks, window_blocks, decay, acc_out,
+               slot_blk_out, next_block=None, next_slot=None, err_out=None, stream=0) -> None:
+    """Accumulates block masses and drops the rows of least weight, acc/slot_blk [units][slots] (see include/nosa.h)."""
+    _check(lib().nosa_evict(_ptr(acc), _ptr(slot_blk), _ptr(mass), units, slots, _ptr(lens), budget, sink_blocks,
+                            window_blocks, decay, _ptr(acc_out), _ptr(slot_blk_out), _ptr(next_block), _ptr(next_slot),
+                            _ptr(err_out), stream or None), "nosa_evict")
+
+
+def nosa_rope_make(rot_dims=128, interleaved=False, scaling=NOSA_ROPE_PLAIN, base=10000.0, factor=1.0, low=1.0,
+                   high=32.0, original=0.0, attention_factor=1.0) -> nosa_rope_table:
+    """The table nosa_rope takes (host only; see include/nosa.h)."""
+    cfg = nosa_rope_config(ctypes.sizeof(nosa_rope_config), rot_dims, int(interleaved), scaling, base, factor, low, high,
+                           original, attention_factor)
+    out = nosa_rope_table()
+    _check(lib().nosa_rope_make(ctypes.byref(cfg), ctypes.byref(out)), "nosa_rope_make")
+    return out
+
+
+def nosa_rope(table, views, pos=None, count=None, inverse=False, err_out=None, stream=0) -> None:
+    """Rotary positions of one or two pairs (x, y) of tensors [batch][heads][n_tokens][d] with any strides but the
+    last's 1; y may be x itself (see include/nosa.h)."""
+    batch, _, n, _ = views[0][0].shape
+    v = (nosa_rope_view * len(views))()
+    for w, (x, y) in zip(v, views):
+        if x.shape != y.shape or (x.shape[0], x.shape[2], x.shape[3]) != (batch, n, 128) or x.stride(3) != 1 or y.stride(3) != 1:
+            raise ValueError("views are pairs of tensors [batch][heads][n_tokens][128], contiguous along the last")
+        w.x, w.y, w.heads = x.data_ptr(), y.data_ptr(), x.shape[1]
+        w.x_stride[:], w.y_stride[:] = x.stride()[:3], y.stride()[:3]
+    _check(lib().nosa_rope(ctypes.byref(table), v, len(views), batch, n, _ptr(pos), _ptr(count), int(bool(inverse)),
+                           _ptr(err_out), stream or None), "nosa_rope")
