@@ -1,19 +1,20 @@
 // Attention over an 8-bit KV block store (nosa_byte_dense_attend, nosa_byte_attend).
 //
 // With codes c and one scale each for a block's K and V, the scores are s_K (q . c_t) and a block adds
-// s_V sum_t p_t c_t to the result: e4m3 codes are exact in f16, so a conversion per two codes feeds the tensor cores
-// (mma.sync m16n8k16, f16 in, float32 accumulate; with at most 32 rows a unit tcgen05's tiles of 64 rows and more would
-// be mostly empty), and the scales are one float32 factor each per block.
+// s_V sum_t p_t c_t to the result: e4m3 codes are exact in f16, two in a conversion, so they go to mma.sync m16n8k16 with f16
+// operands and float32 accumulators, and the scales are one float32 factor each per block.  (mma.sync takes e4m3 too, but
+// sm_103a converts it inside: 7.9 cycles an MMA with new operands against 2.7 of f16.  With at most 32 rows a unit
+// tcgen05's tiles of 64 rows and more would be mostly empty.)
 //
 // As for the 4-bit store, CTAs share the units' blocks in equal pieces, or a cluster of CTAs takes a unit (byte_plan), and a
-// warp takes half a block (two tiles of 16 tokens) at a time through a ring of its own of bulk copies.  Per half
-// block and tile of 8 query rows:
-//   S^T (2 x 16 tokens x 8 rows) = K codes . q^T       16 MMAs
+// warp takes half a block (two tiles of 16 tokens) at a time through a ring of its own of bulk copies.  Per half block
+// and 8 query rows:
+//   S^T (2 x 16 tokens x 8 rows) = K codes . q^T       16 MMAs in two chains
 //   P^T by movmatrix of the f16-packed weights
-//   O^T (128 dims x 8 rows) += s_V (V codes^T . P^T)    16 MMAs into fresh accumulators, 32 FMAs: results stay in
-//                                                      true units whatever the blocks' scales
+//   O^T (128 dims x 8 rows) += s_V (V codes^T . P^T)    16 MMAs into fresh accumulators, 32 FMAs: results stay in true
+//                                                  units whatever the blocks' scales
 // Weights are 2^(logit - R), R within 14 of the row's maximum, their sum float32.  Where masses are wanted a half block
-// stores its (R, sum) per row; the rows' final references and sums turn these into masses in a last kernel.
+// stores its (R, sum) per row; the rows' final references and sums turn these into masses in the end (in a kernel of their own after pieces).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -28,8 +29,8 @@ namespace nosa {
 namespace cg = cooperative_groups;
 
 constexpr int kHalfTokens = 32, kHalfBytes = 2 * kByteTile;
-constexpr int kHalfStage = kHalfBytes + 128;  // a stage: the tiles and, behind them, the scales
-constexpr int kWarps = 8, kStages = 3, kThreads = kWarps * 32;
+constexpr int kHalfStage = kHalfBytes + 128;  // a stage: half a block and, behind it, the block's scales
+constexpr int kWarps = 4, kStages = 3, kThreads = kWarps * 32, kCtasPerSm = 2;
 constexpr int kMassThreads = 128;
 constexpr float kTopLead = 10.f, kTopWeight = 14.f;  // a new reference weighs the best score 2^10; up to 2^14 it stays
 
@@ -95,8 +96,8 @@ __device__ __forceinline__ void load_byte_query(ByteQuery& Q, float (&alpha)[2],
   }
 }
 
-// Logits per score: alpha x s_K, kept where logits are finite (scores are below 2^26: 128 products of a q below 2^10 and
-// a code of at most 448) and differences between them are not lost.
+// Logits per score: alpha x s_K, kept where logits are finite (scores are below 2^26: 128 products of a q below 2^10 and a
+// code of at most 448).
 __device__ __forceinline__ float logit_factor(float alpha, float sk) {
   const float c = alpha * sk;
   return c > 0x1p100f ? 0x1p100f : c;  // (a NaN stays)
@@ -117,43 +118,56 @@ struct ByteRows {
 
 // Prepares a half block that not every row sees as a whole (left: tokens of the context from its first on, possibly
 // none).  Behind the context the store may hold anything, and 0 x NaN is a NaN, so those tokens' V codes are cleared.  So
-// is a NaN of a token that only some rows see: the rows that see it get a bit of `poison`, and a NaN in that dim in
-// the end.
+// is a NaN of a token that only some rows see: the rows that see it get a bit of `poison`, and a NaN in that dim in the
+// end.
 __device__ __noinline__ void clear_byte_tail(unsigned char* stage, uint32_t (*poison)[4], int left, int nq, int rows, int lane) {
+  const int g = lane >> 2, t = lane & 3;
 #pragma unroll 1
-  for (int i = lane; i < 2 * kByteV / 4; i += 32) {  // a word: two dims of two tokens
-    const int tile = i >> 9, at = i & 511;           // at: chunk, owner lane, word
-    uint32_t* w = reinterpret_cast<uint32_t*>(stage + tile * kByteTile + kByteV) + at;
-    uint32_t x = *w;
-    const int owner = (at >> 2) & 31, token = kByteTileTokens * tile + 2 * (owner & 3) + 8 * (at & 1);
-    const int dim = 16 * (owner >> 2) + 4 * (at >> 7) + 2 * ((at >> 1) & 1);
-#pragma unroll 1
-    for (int b = 0; b < 4; ++b) {
-      const int late = token + (b & 1) - (left - nq);  // rows of query tokens from `late` on see the token
-      const uint32_t mask = 0xffu << (8 * b);
-      if (late >= nq) {
-        x &= ~mask;
-      } else if (late > 0 && ((x >> (8 * b)) & 0x7fu) == 0x7fu) {
-        x &= ~mask;
-        const int d = dim + (b >> 1);
-        for (int row = 0; row < rows; ++row)
-          if (row % nq >= late) atomicOr(&poison[row][d >> 5], 1u << (d & 31));
-      }
+  for (int tile = 0; tile < 2; ++tile) {
+    const int late0 = kByteTileTokens * tile + 2 * t - (left - nq);  // rows of query tokens from there on see token 2t
+    // per half of the tile, the bytes of words (two dims of two tokens) that some row sees, and that not every row sees
+    uint32_t keep[2], part[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int late = late0 + 8 * h;
+      keep[h] = (late < nq ? 0x00ff00ffu : 0u) | (late + 1 < nq ? 0xff00ff00u : 0u);
+      part[h] = keep[h] & ((late > 0 ? 0x00ff00ffu : 0u) | (late >= 0 ? 0xff00ff00u : 0u));
     }
-    *w = x;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint4* at = reinterpret_cast<uint4*>(stage + tile * kByteTile + kByteV + 512 * c + 16 * lane);
+      const uint4 v = *at;
+      uint32_t w[4] = {v.x & keep[0], v.y & keep[1], v.z & keep[0], v.w & keep[1]};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t nan = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u & part[e & 1];
+        while (nan) {
+          const int b = (__ffs(nan) - 1) >> 3, d = 16 * g + 4 * c + 2 * (e >> 1) + (b >> 1);
+          const int late = late0 + 8 * (e & 1) + (b & 1);
+          for (int row = 0; row < rows; ++row)
+            if (row % nq >= late) atomicOr(&poison[row][d >> 5], 1u << (d & 31));
+          w[e] &= ~(0xffu << (8 * b));
+          nan &= nan - 1;
+        }
+      }
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
   fence_proxy_async_smem();  // the next bulk copy into the stage comes after these writes
   __syncwarp();
 }
 
-// One half block for all row tiles.  left: tokens of the context from its first on.
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// One half block, two tiles, for all row tiles.  left: tokens of the context from its first on; mass: where its sums
+// go, or null.
 template <int NT>
 __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery& Q, const float (&alpha1)[2],
                                              const ByteQueryShared* qs, unsigned char* stage, uint32_t (*poison)[4], int left,
-                                             const ByteArgs& a, float2* mass, int lane) {
-  const int g = lane >> 2, t = lane & 3, nq = a.nq;
+                                             int rows, int nq, float2* mass, int lane) {
+  const int g = lane >> 2, t = lane & 3;
   const bool tail = left - (nq - 1) < kHalfTokens;  // some row does not see the whole half
-  if (tail) clear_byte_tail(stage, poison, left, nq, a.rows, lane);
+  if (tail) clear_byte_tail(stage, poison, left, nq, rows, lane);
   const float2 s = *reinterpret_cast<const float2*>(stage + kHalfBytes);  // s_K, s_V
   float z[2][NT][4];
 #pragma unroll
@@ -169,30 +183,22 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
       uint32_t f[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t x0 = w == 0 ? k[i][0].x : w == 1 ? k[i][0].y : w == 2 ? k[i][0].z : k[i][0].w;
-        const uint32_t x1 = w == 0 ? k[i][1].x : w == 1 ? k[i][1].y : w == 2 ? k[i][1].z : k[i][1].w;
-        f[i][0] = codes_lo(x0);
-        f[i][1] = codes_lo(x1);
-        f[i][2] = codes_hi(x0);
-        f[i][3] = codes_hi(x1);
+        codes_to_half2(word_of(k[i][0], w), f[i][0], f[i][2]);
+        codes_to_half2(word_of(k[i][1], w), f[i][1], f[i][3]);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        uint32_t b0, b1;
-        if constexpr (NT == 1) {
-          b0 = Q.b[4 * c + w][0];
-          b1 = Q.b[4 * c + w][1];
-        } else {
-          const uint2 b = *reinterpret_cast<const uint2*>(reinterpret_cast<const char*>(&qs[nt].b[2 * c + (w >> 1)][lane]) + 8 * (w & 1));
-          b0 = b.x;
-          b1 = b.y;
-        }
+        uint2 b;
+        if constexpr (NT == 1)
+          b = make_uint2(Q.b[4 * c + w][0], Q.b[4 * c + w][1]);
+        else
+          b = *(reinterpret_cast<const uint2*>(&qs[nt].b[2 * c + (w >> 1)][lane]) + (w & 1));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (c == 0 && w == 0)
-            mma_f16_first(z[i][nt], f[i][0], f[i][1], f[i][2], f[i][3], b0, b1);
+            mma_f16_first(z[i][nt], f[i][0], f[i][1], f[i][2], f[i][3], b.x, b.y);
           else
-            mma_f16(z[i][nt], f[i][0], f[i][1], f[i][2], f[i][3], b0, b1);
+            mma_f16(z[i][nt], f[i][0], f[i][1], f[i][2], f[i][3], b.x, b.y);
         }
       }
     }
@@ -210,7 +216,7 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
         z[i][nt][e] *= e & 1 ? f1 : f0;
         if (tail) {
           const int row = 8 * nt + 2 * t + (e & 1), token = kByteTileTokens * i + g + 8 * (e >> 1);
-          if (row >= a.rows || token >= left - (nq - 1) + row % nq) z[i][nt][e] = -INFINITY;
+          if (row >= rows || token >= left - (nq - 1) + row % nq) z[i][nt][e] = -INFINITY;
         }
       }
 #pragma unroll
@@ -264,7 +270,7 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
         sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
       }
       const int row = 8 * nt + 2 * t;
-      if (g == 0 && row < a.rows)
+      if (g == 0 && row < rows)
         *reinterpret_cast<float4*>(mass + row) = make_float4(A[nt].top[0], sum[0], A[nt].top[1], sum[1]);
     }
   }
@@ -278,11 +284,8 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
       uint32_t f[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t x0 = jj ? v[i].z : v[i].x, x1 = jj ? v[i].w : v[i].y;
-        f[i][0] = codes_lo(x0);
-        f[i][1] = codes_hi(x0);
-        f[i][2] = codes_lo(x1);
-        f[i][3] = codes_hi(x1);
+        codes_to_half2(jj ? v[i].z : v[i].x, f[i][0], f[i][1]);
+        codes_to_half2(jj ? v[i].w : v[i].y, f[i][2], f[i][3]);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -305,8 +308,32 @@ constexpr int byte_smem_bytes() {
   return byte_ring_bytes(NT) + (NT > 1 ? NT * (int)sizeof(ByteQueryShared) : 0);
 }
 
+// The mass of entry i of unit u: per row, the sums of the block's halves at the row's final reference, over its final sum
+// (final: of each row the reference, and 1 / the sum, 0 where no token was seen).
+__device__ __forceinline__ float block_mass(const ByteArgs& a, int u, int i, const float2* final) {
+  const size_t at = (size_t)u * a.blocks + i;
+  const int len = a.sel ? max(a.lens[u], 0) : min(max(a.lens[u], 0), a.max_len);
+  int block = i;
+  if (a.sel) {
+    block = a.sel[at];
+    const int slot = block < 0 ? -1 : a.sel_slot ? a.sel_slot[at] : block;
+    if (slot < 0 || slot >= a.max_blocks) return 0.f;
+  }
+  float sum = 0.f;
+  if ((long long)block * kBlock < len) {
+    const float2* half = a.half + at * 2 * a.mass_rows;
+    for (int h = 0; h < 2; ++h)
+      for (int row = 0; row < a.rows; ++row) {
+        const float2 s = half[h * a.mass_rows + row], r = final[row];
+        if (r.y != 0.f) sum = fmaf(s.y * ex2(s.x - r.x), r.y, sum);
+      }
+  }
+  return sum;
+}
+__device__ __forceinline__ float2 final_of(float R, float L) { return make_float2(R, L == 0.f ? 0.f : 1.f / L); }
+
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_constant__ ByteArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) byte_attend_kernel(const __grid_constant__ ByteArgs a) {
   // the warps' rings, then [warp][8 NT rows][kQaRowStride], their partials; behind them the query operands
   extern __shared__ __align__(128) float smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
@@ -315,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_c
   __shared__ int scan[32], found[2];
   __shared__ uint32_t poison[kQaMaxRows][4];  // [row]: dims that end as NaN
   __shared__ float2 merged[8 * NT];           // a cluster CTA's references and sums
+  __shared__ float2 final[8 * NT];            // the unit's, for its masses
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (lane == 0) {
 #pragma unroll
@@ -333,12 +361,13 @@ __global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_c
   // unit u on, and unit u's begin at `begin` of `total`.
   const int ranks = a.split == kCluster ? (int)cg::this_cluster().num_blocks() : 1;
   const int rank = a.split == kCluster ? (int)cg::this_cluster().block_rank() : 0;
-  int u = blockIdx.x / ranks, at = 0, pieces = gridDim.x;
+  const int me = blockIdx.x / ranks;
+  int u = me, at = 0, pieces = gridDim.x;
   int todo = 1, total = 1, begin = 0;
   auto cut = [&]() {  // a half block per warp at least; further CTAs have nothing to do
-    pieces = min((int)gridDim.x, (total + kWarps / 2 - 1) / (kWarps / 2));
-    const int lo = blockIdx.x < pieces ? cta_first(total, blockIdx.x, pieces) : total;
-    todo = blockIdx.x < pieces ? cta_first(total, blockIdx.x + 1, pieces) - lo : 0;
+    pieces = min(pieces, (total + kWarps / 2 - 1) / (kWarps / 2));
+    const int lo = me < pieces ? cta_first(total, me, pieces) : total;
+    todo = me < pieces ? cta_first(total, me + 1, pieces) - lo : 0;
     return lo;
   };
   if (a.split == kPieces) {
@@ -387,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_c
     }
     if (threadIdx.x == 0 && first == 0 && rank == 0 && len != a.lens[u]) atomicOr(a.err, kErrBounds);
     if (a.nq > 1) {
-      if (threadIdx.x < kQaMaxRows * 4) poison[threadIdx.x >> 2][threadIdx.x & 3] = 0;
+      for (int i = threadIdx.x; i < kQaMaxRows * 4; i += kThreads) poison[i >> 2][i & 3] = 0;
       __syncthreads();
     }
     ByteQuery Q;
@@ -414,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_c
     };
 
     // The blocks, listed ones looked up kQaList at a time and those without a token left out.  Warp w takes half
-    // w % 2 of the blocks w / 2, w / 2 + 4, ...  (an empty second half of the last block too: it adds nothing).
+    // w % 2 of the blocks w / 2, w / 2 + kWarps / 2, ...  (an empty half of the last block too: it adds nothing).
     const int batch = a.sel ? kQaList : max(end - first, 1), half = warp & 1;
     const uint8_t* base = a.store + (size_t)u * a.max_blocks * kByteBlockBytes;
     for (int b0 = first; b0 < end || b0 == first; b0 += batch) {
@@ -445,12 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_c
         n = 0;
       }
       constexpr int step = kWarps / 2;
-      const int mine = (n - (warp >> 1) + step - 1) / step;  // the warp's halves
+      const int mine = (n - warp / 2 + step - 1) / step;  // the warp's halves
       int started = 0;
       auto issue = [&]() {  // the next half into the stage whose turn it is
         if (started >= mine || late) return;
         if (lane == 0) {
-          const int j = (warp >> 1) + started * step, row = a.sel ? list[j].x : b0 + j;
+          const int j = warp / 2 + started * step, row = a.sel ? list[j].x : b0 + j;
           const uint8_t* src = base + (size_t)row * kByteBlockBytes;
           const uint32_t to = smem_u32(ring + in * kHalfStage);
           mbar_arrive_expect_tx(&bars[warp][in], kHalfBytes + 16);
@@ -466,12 +495,12 @@ __global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_c
       for (int done = 0; done < started; ++done) {
         late |= !__all_sync(0xffffffffu, stage_wait(&bars[warp][out], phase, a.wait_limit));
         if (!late) {  // otherwise wait for what is in flight, and start no more
-          const int j = (warp >> 1) + done * step;
+          const int j = warp / 2 + done * step;
           const int left = (a.sel ? list[j].y : len - (b0 + j) * kBlock) - half * kHalfTokens;
           float2* mass = nullptr;
           if (a.mass)
             mass = a.half + (((size_t)u * a.blocks + (a.sel ? list[j].z : b0 + j)) * 2 + half) * a.mass_rows;
-          process_half<NT>(A, Q, alpha1, qs, ring + out * kHalfStage, poison, left, a, mass, lane);
+          process_half<NT>(A, Q, alpha1, qs, ring + out * kHalfStage, poison, left, a.rows, a.nq, mass, lane);
           __syncwarp();  // the stage is read
           issue();
         }
@@ -506,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_c
     }
     __syncthreads();
     const bool complete = first == 0 && end == whole;
-    const int part = blockIdx.x + u;  // a piece's end and a unit's each move on by one: no two segments share a part
+    const int part = me + u;  // a piece's end and a unit's each move on by one: no two segments share a part
+    const size_t out0 = (size_t)u * a.rows;  // the unit's first row of the result
     for (int idx = threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += kThreads) {
       const int row = idx >> 5, x = 4 * (idx & 31);
       float R = wr[0][row];
@@ -536,8 +566,11 @@ __global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_c
         *reinterpret_cast<float4*>(smem + row * kQaRowStride + x) = O;
         if (x == 0) merged[row] = make_float2(R, L);
       } else if (complete) {
-        store_out(a.out + ((size_t)u * a.rows + row) * kHeadDim + x, O, L);
-        if (x == 0 && a.mass) a.total[(size_t)u * a.rows + row] = make_float2(R, L);
+        store_out(a.out + (out0 + row) * kHeadDim + x, O, L);
+        if (x == 0) {
+          final[row] = final_of(R, L);
+          if (a.mass && a.split == kPieces) a.total[out0 + row] = make_float2(R, L);
+        }
       } else {
         const size_t i = (size_t)part * a.rows + row;
         if (x == 0) a.stats[i] = make_float2(R, L);
@@ -547,6 +580,20 @@ __global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_c
     if (ranks > 1) {  // each CTA of the cluster merges its share of the outputs through distributed shared memory
       cg::cluster_group cluster = cg::this_cluster();
       cluster.sync();
+      if (a.mass) {
+        if (threadIdx.x < a.rows) {
+          float R = kNoRef, L = 0.f;
+          for (int r = 0; r < ranks; ++r) R = fmaxf(R, cluster.map_shared_rank(&merged[threadIdx.x], r)->x);
+          for (int r = 0; r < ranks; ++r) {
+            const float2 m = *cluster.map_shared_rank(&merged[threadIdx.x], r);
+            L = fmaf(m.y, ex2(m.x - R), L);
+          }
+          final[threadIdx.x] = final_of(R, L);
+        }
+        __syncthreads();
+        for (int i = cta_first(a.blocks, rank, ranks) + threadIdx.x; i < cta_first(a.blocks, rank + 1, ranks); i += kThreads)
+          a.mass[(size_t)u * a.blocks + i] = block_mass(a, u, i, final);
+      }
       for (int idx = rank * kThreads + threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += ranks * kThreads) {
         const int row = idx >> 5, x = 4 * (idx & 31);
         float R = kNoRef, L = 0.f;
@@ -556,14 +603,17 @@ __global__ void __launch_bounds__(kThreads, 1) byte_attend_kernel(const __grid_c
           const float2 m = *cluster.map_shared_rank(&merged[row], r);
           merge_part(R, L, O, m.x, m.y, *reinterpret_cast<const float4*>(cluster.map_shared_rank(smem + row * kQaRowStride + x, r)));
         }
-        store_out(a.out + ((size_t)u * a.rows + row) * kHeadDim + x, O, L);
-        if (x == 0 && a.mass) a.total[(size_t)u * a.rows + row] = make_float2(R, L);
+        store_out(a.out + (out0 + row) * kHeadDim + x, O, L);
       }
       cluster.sync();  // keep every CTA's shared memory until all have read it
       return;
     }
+    if (a.split != kPieces && a.mass) {
+      __syncthreads();  // the warps' sums are written, and final
+      for (int i = threadIdx.x; i < a.blocks; i += kThreads) a.mass[(size_t)u * a.blocks + i] = block_mass(a, u, i, final);
+    }
     if (a.split == kPieces && first == 0 && threadIdx.x == 0)
-      a.meta[u] = make_int2(part, cta_of(total, begin + whole - 1, pieces) - blockIdx.x + 1);
+      a.meta[u] = make_int2(part, cta_of(total, begin + whole - 1, pieces) - me + 1);
     begin += whole;
     if (todo > 0) {
       fence_proxy_async_smem();  // the next segment's copies come after these reads and writes
@@ -602,38 +652,19 @@ __global__ void __launch_bounds__(kMergeWarps * 32) byte_merge_kernel(const __gr
   }
 }
 
-// The blocks' masses: per row, the sums of a block's halves at the row's final reference, over its final sum.
+// The blocks' masses, where the units were cut into pieces.
 __global__ void __launch_bounds__(kMassThreads) byte_mass_kernel(const __grid_constant__ ByteArgs a) {
-  __shared__ float2 total[kQaMaxRows];  // of each row: the final reference, and 1 / the final sum (0: no token seen)
+  __shared__ float2 final[kQaMaxRows];
   const int ctas = (a.blocks + kMassThreads - 1) / kMassThreads, u = blockIdx.x / ctas;
   const int i = blockIdx.x % ctas * kMassThreads + threadIdx.x;
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x < a.rows) {
     const float2 s = a.total[(size_t)u * a.rows + threadIdx.x];
-    total[threadIdx.x] = make_float2(s.x, s.y == 0.f ? 0.f : 1.f / s.y);
+    final[threadIdx.x] = final_of(s.x, s.y);
   }
   __syncthreads();
-  if (i >= a.blocks) return;
-  const size_t at = (size_t)u * a.blocks + i;
-  const int len = a.sel ? max(a.lens[u], 0) : min(max(a.lens[u], 0), a.max_len);
-  int block = i;
-  bool held = true;
-  if (a.sel) {
-    block = a.sel[at];
-    const int slot = block < 0 ? -1 : a.sel_slot ? a.sel_slot[at] : block;
-    held = slot >= 0 && slot < a.max_blocks;
-  }
-  float sum = 0.f;
-  if (held && (long long)block * kBlock < len) {
-    const float2* half = a.half + at * 2 * a.mass_rows;
-    for (int h = 0; h < 2; ++h)
-      for (int row = 0; row < a.rows; ++row) {
-        const float2 s = half[h * a.mass_rows + row], r = total[row];
-        if (r.y != 0.f) sum = fmaf(s.y * ex2(s.x - r.x), r.y, sum);
-      }
-  }
-  a.mass[at] = sum;
+  if (i < a.blocks) a.mass[(size_t)u * a.blocks + i] = block_mass(a, u, i, final);
 }
 
 // What the launches need of a device, looked up once (a call costs more in look-ups than in launching otherwise).
@@ -708,14 +739,14 @@ static int byte_cluster_size(int units, int blocks, int wave, int most) {
 }
 
 static BytePlan byte_plan(const ByteDevice& d, int units, int blocks, bool listed) {
-  const int rounds = (units + d.wave - 1) / d.wave;
-  if (units > kQaSplitUnits || (units > d.wave && (long long)(rounds * d.wave - units) * blocks <= 24ll * units))
+  const int wave = d.wave, rounds = (units + wave - 1) / wave;
+  if (units > kQaSplitUnits || (units > wave && (long long)(rounds * wave - units) * blocks <= 24ll * units))
     return {kWhole, units, 0};
-  const int cl = byte_cluster_size(units, blocks, d.wave, 16);
-  if (units * cl <= d.wave && 2 * units * cl > d.wave && blocks <= (listed ? 100 : 32) * cl) return {kCluster, units * cl, cl};
-  if (units * cl <= d.wave && blocks <= 6 * cl) return {kCluster, units * cl, cl};
+  const int cl = byte_cluster_size(units, blocks, wave, 32 * units <= wave ? 16 : 8);
+  if (units * cl <= wave && 2 * units * cl > wave && blocks <= (listed ? 160 : 32) * cl) return {kCluster, units * cl, cl};
+  if (units * cl <= wave && blocks <= 6 * cl) return {kCluster, units * cl, cl};
   const long long pieces = ((long long)units * blocks + kWarps / 2 - 1) / (kWarps / 2);
-  return {kPieces, (int)std::min<long long>(d.wave, pieces), 0};
+  return {kPieces, (int)std::min<long long>(wave, pieces), 0};
 }
 
 template <int NT>
@@ -745,7 +776,7 @@ static nosa_status byte_attend(ByteArgs& a, void* scratch, size_t scratch_bytes,
                                  : launch_byte_attend<4>(a, plan, st);
   if (e == cudaSuccess && plan.split == kPieces)
     e = launch_ex(byte_merge_kernel, dim3((unsigned)(a.units * a.rows)), dim3(kMergeWarps * 32), 0, st, true, 0, a);
-  if (e == cudaSuccess && a.mass)
+  if (e == cudaSuccess && plan.split == kPieces && a.mass)
     e = launch_ex(byte_mass_kernel, dim3((unsigned)(a.units * ((a.blocks + kMassThreads - 1) / kMassThreads))),
                   dim3(kMassThreads), 0, st, true, 0, a);
   if (e == cudaSuccess) return NOSA_OK;

@@ -42,7 +42,6 @@ struct RopeArgs {
 // Where a token's pair i is kept: in the order in which eight threads read four pairs each without bank conflicts.
 __device__ __forceinline__ int pair_place(int i) { return (i & 4 ? 32 : 0) + (i >> 3) * 4 + (i & 3); }
 
-// Rotates a pair of bf16 values and packs as is.
 __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
   const float x = a;
   a = fmaf(x, c, -(b * s));
@@ -68,12 +67,32 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   if (tokens <= 0) return;
   const int h0 = hd * kRopeHeads, heads = min(kRopeHeads, v.heads - h0), pairs = a.rot / 2;
   const long long p0 = (a.pos ? (long long)a.pos[b] : 0) + t0;
+  const int rows = tokens * heads, part = threadIdx.x & 7;
+  const uint16_t* xb = v.x + b * v.xs[0] + h0 * v.xs[1] + t0 * v.xs[2];
+  uint16_t* yb = v.y + b * v.ys[0] + h0 * v.ys[1] + t0 * v.ys[2];
+  // whole words: a thread's 16 dims, eight pairs or what is copied, of rows r0, r0 + kRopeRows, ...
+  const bool turns = 16 * part < a.rot, idle = !v.vec || (!turns && v.same);
+  const int d0 = turns && !a.interleaved ? 8 * part : 16 * part;
+  const int d1 = turns && !a.interleaved ? d0 + pairs : d0 + 8;
+  int r0 = threadIdx.x >> 3;
+  uint4 x[kRopeFlight][2];
+  auto load = [&]() {
+#pragma unroll
+    for (int k = 0; k < kRopeFlight; ++k) {
+      const int r = r0 + k * kRopeRows;
+      if (r >= rows) break;
+      const uint16_t* p = xb + r % heads * v.xs[1] + r / heads * v.xs[2];
+      x[k][0] = *reinterpret_cast<const uint4*>(p + d0);
+      x[k][1] = *reinterpret_cast<const uint4*>(p + d1);
+    }
+  };
+  if (!idle) load();  // while the angles are computed
   for (int k = threadIdx.x; k < tokens * kRopePairs; k += kRopeThreads) {
     const int t = k / kRopePairs, p = k % kRopePairs;
     if (p >= pairs) continue;
-    const uint64_t turns = (uint64_t)(p0 + t) * a.turn[p];
+    const uint64_t turns64 = (uint64_t)(p0 + t) * a.turn[p];
     float s, c;
-    sincospif((float)(int32_t)(uint32_t)(turns >> 32) * 0x1p-31f, &s, &c);
+    sincospif((float)(int32_t)(uint32_t)(turns64 >> 32) * 0x1p-31f, &s, &c);
     if (a.inverse) s = -s;
     const int at = pair_place(p);
     cosine[t][at] = c * a.factor;
@@ -81,25 +100,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
   __syncthreads();
 
-  const int rows = tokens * heads, part = threadIdx.x & 7;
-  const uint16_t* xb = v.x + b * v.xs[0] + h0 * v.xs[1] + t0 * v.xs[2];
-  uint16_t* yb = v.y + b * v.ys[0] + h0 * v.ys[1] + t0 * v.ys[2];
   if (v.vec) {
-    // a thread's 16 dims: eight pairs, or what is copied
-    const bool turns = 16 * part < a.rot;
-    if (!turns && v.same) return;
-    const int d0 = turns && !a.interleaved ? 8 * part : 16 * part;
-    const int d1 = turns && !a.interleaved ? d0 + pairs : d0 + 8;
-    for (int r0 = threadIdx.x >> 3; r0 < rows; r0 += kRopeRows * kRopeFlight) {
-      uint4 x[kRopeFlight][2];
-#pragma unroll
-      for (int k = 0; k < kRopeFlight; ++k) {
-        const int r = r0 + k * kRopeRows;
-        if (r >= rows) break;
-        const uint16_t* p = xb + r % heads * v.xs[1] + r / heads * v.xs[2];
-        x[k][0] = *reinterpret_cast<const uint4*>(p + d0);
-        x[k][1] = *reinterpret_cast<const uint4*>(p + d1);
-      }
+    if (idle) return;
+    for (; r0 < rows; r0 += kRopeRows * kRopeFlight, load()) {
 #pragma unroll
       for (int k = 0; k < kRopeFlight; ++k) {
         const int r = r0 + k * kRopeRows;

@@ -8,6 +8,7 @@ there is no fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -152,7 +153,7 @@ def lib() -> ctypes.CDLL:
             "nosa_byte_scratch_bytes": [i32, i32, i32, i32],
             "nosa_evict": [p, p, p, i32, i32, p, i32, i32, i32, ctypes.c_float, p, p, p, p, p, vp],
             "nosa_rope_make": [ctypes.POINTER(nosa_rope_config), ctypes.POINTER(nosa_rope_table)],
-            "nosa_rope": [ctypes.POINTER(nosa_rope_table), ctypes.POINTER(nosa_rope_view), i32, i32, i32, p, p, i32, p, vp],
+            "nosa_rope": [ctypes.POINTER(nosa_rope_table), p, i32, i32, i32, p, p, i32, p, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -448,11 +449,12 @@ def nosa_rope(table, views, pos=None, count=None, inverse=False, err_out=None, s
     """Rotary positions of one or two pairs (x, y) of tensors [batch][heads][n_tokens][d] with any strides but the
     last's 1; y may be x itself (see include/nosa.h)."""
     batch, _, n, _ = views[0][0].shape
-    v = (nosa_rope_view * len(views))()
-    for w, (x, y) in zip(v, views):
-        if x.shape != y.shape or (x.shape[0], x.shape[2], x.shape[3]) != (batch, n, 128) or x.stride(3) != 1 or y.stride(3) != 1:
+    flat = []  # the fields of nosa_rope_view as 64-bit words (heads and pad_ make one)
+    for x, y in views:
+        shape, xs, ys = x.shape, x.stride(), y.stride()
+        if y.shape != shape or shape[0] != batch or shape[2] != n or shape[3] != 128 or xs[3] != 1 or ys[3] != 1:
             raise ValueError("views are pairs of tensors [batch][heads][n_tokens][128], contiguous along the last")
-        w.x, w.y, w.heads = x.data_ptr(), y.data_ptr(), x.shape[1]
-        w.x_stride[:], w.y_stride[:] = x.stride()[:3], y.stride()[:3]
-    _check(lib().nosa_rope(ctypes.byref(table), v, len(views), batch, n, _ptr(pos), _ptr(count), int(bool(inverse)),
-                           _ptr(err_out), stream or None), "nosa_rope")
+        flat += (x.data_ptr(), y.data_ptr(), shape[1], xs[0], xs[1], xs[2], ys[0], ys[1], ys[2])
+    v = array.array("q", flat)
+    _check(lib().nosa_rope(ctypes.byref(table), v.buffer_info()[0], len(views), batch, n, _ptr(pos), _ptr(count),
+                           int(bool(inverse)), _ptr(err_out), stream or None), "nosa_rope")
