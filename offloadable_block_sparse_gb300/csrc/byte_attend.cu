@@ -30,7 +30,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kHalfTokens = 32, kHalfBytes = 2 * kByteTile;
 constexpr int kHalfStage = kHalfBytes + 128;  // a stage: half a block and, behind it, the block's scales
-constexpr int kWarps = 4, kStages = 3, kThreads = kWarps * 32, kCtasPerSm = 2;
+constexpr int kWarps = 4, kStages = 2, kThreads = kWarps * 32, kCtasPerSm = 2;
 constexpr int kMassThreads = 128;
 constexpr float kTopLead = 10.f, kTopWeight = 14.f;  // a new reference weighs the best score 2^10; up to 2^14 it stays
 
@@ -303,9 +303,13 @@ __host__ __device__ constexpr int byte_ring_bytes(int nt) {
   const int ring = kWarps * kStages * kHalfStage, partials = kWarps * 8 * nt * kQaRowStride * 4;
   return ring > partials ? ring : partials;
 }
+// Two CTAs an SM, by registers or by shared memory: a third with one row tile left 512 units of 64 blocks a round that was
+// nearly empty (102 us against 85).  Two stages a warp: with three, HBM is slower (256 units of 512 blocks 331 us against
+// 307), with one 364.
 template <int NT>
 constexpr int byte_smem_bytes() {
-  return byte_ring_bytes(NT) + (NT > 1 ? NT * (int)sizeof(ByteQueryShared) : 0);
+  const int need = byte_ring_bytes(NT) + (NT > 1 ? NT * (int)sizeof(ByteQueryShared) : 0);
+  return need > 80 * 1024 ? need : 80 * 1024;
 }
 
 // The mass of entry i of unit u: per row, the sums of the block's halves at the row's final reference, over its final sum

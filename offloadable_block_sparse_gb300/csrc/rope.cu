@@ -15,8 +15,8 @@
 
 namespace nosa {
 
-constexpr int kRopeThreads = 256, kRopeRows = kRopeThreads / 8;  // rows side by side
-constexpr int kRopeTokens = 32, kRopeHeads = 32, kRopeTile = 256;  // a tile: so many tokens and heads at most, rows about
+constexpr int kRopeThreads = 128, kRopeRows = kRopeThreads / 8;  // rows side by side
+constexpr int kRopeTokens = 32, kRopeHeads = 32, kRopeTile = 128;  // a tile: so many tokens and heads at most, rows about
 constexpr int kRopePairs = kHeadDim / 2;
 constexpr int kRopeFlight = 4;  // rows a thread has in flight
 
