@@ -15,44 +15,18 @@
 //                                                  units whatever the blocks' scales
 // Weights are 2^(logit - R), R within 14 of the row's maximum, their sum float32.  Where masses are wanted a half block
 // stores its (R, sum) per row; the rows' final references and sums turn these into masses in the end (in a kernel of their own after pieces).
-#include <cooperative_groups.h>
-
 #include <algorithm>
 #include <mutex>
 
-#include "byte_core.cuh"
+#include "byte_split.cuh"
 #include "host.h"
-#include "store_core.cuh"
 
 namespace nosa {
 
-namespace cg = cooperative_groups;
-
 constexpr int kHalfTokens = 32, kHalfBytes = 2 * kByteTile;
 constexpr int kHalfStage = kHalfBytes + 128;  // a stage: half a block and, behind it, the block's scales
-constexpr int kWarps = 4, kStages = 2, kThreads = kWarps * 32, kCtasPerSm = 2;
+constexpr int kWarps = kByteThreads / 32, kStages = 2, kCtasPerSm = 2;
 constexpr int kMassThreads = 128;
-constexpr float kTopLead = 10.f, kTopWeight = 14.f;  // a new reference weighs the best score 2^10; up to 2^14 it stays
-
-struct ByteArgs {
-  const uint16_t* q;
-  const uint8_t* store;
-  const int32_t* sel;       // null: every block (dense)
-  const int32_t* sel_slot;  // null: row b holds block b
-  const int32_t* lens;
-  uint16_t* out;
-  float* mass;    // null: not wanted
-  int* err;
-  int2* meta;     // [unit]: its first part and how many there are (1: the output is written already)
-  float2* stats;  // [part][row]: reference and softmax sum
-  float* part;    // [part][row][128]
-  float2* total;  // [unit][row]: final reference and sum, where masses are wanted
-  float2* half;   // [unit][block][half][mass_rows]: reference and sum of a half block
-  int units, nq, rows, mass_rows, max_blocks, max_sel, max_len, blocks;  // blocks: per unit, listed or up to max_len
-  int split;
-  float scale;    // softmax scale x log2(e)
-  long long wait_limit;  // SM cycles a wait for a staged half block may take before it gives up (< 0: none)
-};
 
 // Eight query rows as MMA operands: of row g, dims 32 t + 16 c + 4 w .. + 3 in [4 c + w].
 struct ByteQuery {
@@ -96,21 +70,14 @@ __device__ __forceinline__ void load_byte_query(ByteQuery& Q, float (&alpha)[2],
   }
 }
 
-// Logits per score: alpha x s_K, kept where logits are finite (scores are below 2^26: 128 products of a q below 2^10 and a
-// code of at most 448).
-__device__ __forceinline__ float logit_factor(float alpha, float sk) {
-  const float c = alpha * sk;
-  return c > 0x1p100f ? 0x1p100f : c;  // (a NaN stays)
-}
-
-// The query side in shared memory, for more than one row tile (registers hold it for one).
+// The query side in shared memory, for two row tiles (registers hold it for one).
 struct ByteQueryShared {
   uint4 b[4][32];  // [two operands][lane]
   float2 alpha[32];
 };
 
-// A warp's running state for a tile of 8 rows: of rows 2t, 2t + 1 the reference (a logit in base 2), the lane's part of
-// the softmax sum, and O^T: dims 16 g + 2 j and + 1 of those rows.
+// A warp's running state for a tile of 8 rows: of rows 2t, 2t + 1 the reference (a logit in base 2), the lane's part of the softmax sum, and O^T:
+// dims 16 g + 2 j and + 1 of those rows.
 struct ByteRows {
   float top[2], l[2];
   float o[8][4];
@@ -159,10 +126,10 @@ __device__ __noinline__ void clear_byte_tail(unsigned char* stage, uint32_t (*po
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// One half block, two tiles, for all row tiles.  left: tokens of the context from its first on; mass: where its sums
-// go, or null.
+// One half block for all row tiles: both tiles of tokens at once, so that their chains of dependent operations overlap.
+// left: tokens of the context from its first on; mass: where its sums go, or null.
 template <int NT>
-__device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery& Q, const float (&alpha1)[2],
+__device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery& Q, const float (&alpha)[2],
                                              const ByteQueryShared* qs, unsigned char* stage, uint32_t (*poison)[4], int left,
                                              int rows, int nq, float2* mass, int lane) {
   const int g = lane >> 2, t = lane & 3;
@@ -204,10 +171,11 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
     }
   }
   // logits, and whether a row's best would weigh more than its reference allows
+  float best[NT][2];
   bool raise = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const float2 al = NT == 1 ? make_float2(alpha1[0], alpha1[1]) : qs[nt].alpha[lane];
+    const float2 al = NT == 1 ? make_float2(alpha[0], alpha[1]) : qs[nt].alpha[lane];
     const float f0 = logit_factor(al.x, s.x), f1 = logit_factor(al.y, s.x);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -220,21 +188,21 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
         }
       }
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      raise |= fmaxf(fmaxf(z[0][nt][e], z[0][nt][e + 2]), fmaxf(z[1][nt][e], z[1][nt][e + 2])) - A[nt].top[e] > kTopWeight;
+    for (int e = 0; e < 2; ++e) {
+      best[nt][e] = fmaxf(fmaxf(z[0][nt][e], z[0][nt][e + 2]), fmaxf(z[1][nt][e], z[1][nt][e + 2]));
+      raise |= best[nt][e] - A[nt].top[e] > kTopWeight;
+    }
   }
   if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float best = fmaxf(fmaxf(z[0][nt][e], z[0][nt][e + 2]), fmaxf(z[1][nt][e], z[1][nt][e + 2]));
+        float b = best[nt][e];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-        if (best - A[nt].top[e] > kTopWeight) {  // the row's lanes agree; rows differ
-          // (the best itself where it is so large that the difference would not be what it should)
-          const float top = best - (best - kTopLead) > kTopWeight ? best : best - kTopLead;
-          const float f = ex2(A[nt].top[e] - top);
+        for (int o = 4; o < 32; o <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+        if (b - A[nt].top[e] > kTopWeight) {  // the row's lanes agree; rows differ
+          const float top = reference(b), f = ex2(A[nt].top[e] - top);
           A[nt].top[e] = top;
           A[nt].l[e] *= f;
 #pragma unroll
@@ -299,54 +267,22 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
   }
 }
 
-__host__ __device__ constexpr int byte_ring_bytes(int nt) {
-  const int ring = kWarps * kStages * kHalfStage, partials = kWarps * 8 * nt * kQaRowStride * 4;
-  return ring > partials ? ring : partials;
-}
-// Two CTAs an SM, by registers or by shared memory: a third with one row tile left 512 units of 64 blocks a round that was
-// nearly empty (102 us against 85).  Two stages a warp: with three, HBM is slower (256 units of 512 blocks 331 us against
-// 307), with one 364.
-template <int NT>
-constexpr int byte_smem_bytes() {
-  const int need = byte_ring_bytes(NT) + (NT > 1 ? NT * (int)sizeof(ByteQueryShared) : 0);
-  return need > 80 * 1024 ? need : 80 * 1024;
-}
-
-// The mass of entry i of unit u: per row, the sums of the block's halves at the row's final reference, over its final sum
-// (final: of each row the reference, and 1 / the sum, 0 where no token was seen).
-__device__ __forceinline__ float block_mass(const ByteArgs& a, int u, int i, const float2* final) {
-  const size_t at = (size_t)u * a.blocks + i;
-  const int len = a.sel ? max(a.lens[u], 0) : min(max(a.lens[u], 0), a.max_len);
-  int block = i;
-  if (a.sel) {
-    block = a.sel[at];
-    const int slot = block < 0 ? -1 : a.sel_slot ? a.sel_slot[at] : block;
-    if (slot < 0 || slot >= a.max_blocks) return 0.f;
-  }
-  float sum = 0.f;
-  if ((long long)block * kBlock < len) {
-    const float2* half = a.half + at * 2 * a.mass_rows;
-    for (int h = 0; h < 2; ++h)
-      for (int row = 0; row < a.rows; ++row) {
-        const float2 s = half[h * a.mass_rows + row], r = final[row];
-        if (r.y != 0.f) sum = fmaf(s.y * ex2(s.x - r.x), r.y, sum);
-      }
-  }
-  return sum;
-}
-__device__ __forceinline__ float2 final_of(float R, float L) { return make_float2(R, L == 0.f ? 0.f : 1.f / L); }
+// Two CTAs an SM by shared memory: a third left 512 units of 64 blocks a round that was nearly empty (102 us against 85).
+// Two stages a warp: with three, HBM is slower (256 units of 512 blocks 331 us against 307), with one 364.
+constexpr int kByteSmem = 80 * 1024, kRingBytes = kWarps * kStages * kHalfStage;
+static_assert(kRingBytes + 2 * (int)sizeof(ByteQueryShared) <= kByteSmem && kWarps * 16 * kQaRowStride * 4 <= kRingBytes, "");
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) byte_attend_kernel(const __grid_constant__ ByteArgs a) {
+__global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(const __grid_constant__ ByteArgs a) {
   // the warps' rings, then [warp][8 NT rows][kQaRowStride], their partials; behind them the query operands
   extern __shared__ __align__(128) float smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
-  __shared__ int4 list[kQaList];  // (row of the store, tokens of the context from the block on, the entry's index)
+  __shared__ int4 list[kQaList];
   __shared__ float wr[kWarps][8 * NT], wl[kWarps][8 * NT];
   __shared__ int scan[32], found[2];
-  __shared__ uint32_t poison[kQaMaxRows][4];  // [row]: dims that end as NaN
-  __shared__ float2 merged[8 * NT];           // a cluster CTA's references and sums
-  __shared__ float2 final[8 * NT];            // the unit's, for its masses
+  __shared__ uint32_t poison[8 * NT][4];  // [row]: dims that end as NaN
+  __shared__ float2 merged[8 * NT];       // a cluster CTA's references and sums
+  __shared__ float2 final[8 * NT];        // the unit's, for its masses
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (lane == 0) {
 #pragma unroll
@@ -356,125 +292,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) byte_attend_kernel(const
   __syncwarp();
   pdl_wait();
   pdl_launch_dependents();
+  ByteShare share = byte_share(a, kWarps / 2, scan, found);
 
-  auto length = [&](int u) { return a.sel ? max(a.lens[u], 0) : min(max(a.lens[u], 0), a.max_len); };
-  // blocks of a unit's work; an empty unit counts as one, so that somebody writes its zeros
-  auto blocks_of = [&](int u) { return a.sel ? a.max_sel : max((length(u) + kBlock - 1) / kBlock, 1); };
-
-  // The units' blocks in one line, cut into one piece per CTA: this CTA's are `todo` blocks from block `at` of
-  // unit u on, and unit u's begin at `begin` of `total`.
-  const int ranks = a.split == kCluster ? (int)cg::this_cluster().num_blocks() : 1;
-  const int rank = a.split == kCluster ? (int)cg::this_cluster().block_rank() : 0;
-  const int me = blockIdx.x / ranks;
-  int u = me, at = 0, pieces = gridDim.x;
-  int todo = 1, total = 1, begin = 0;
-  auto cut = [&]() {  // a half block per warp at least; further CTAs have nothing to do
-    pieces = min(pieces, (total + kWarps / 2 - 1) / (kWarps / 2));
-    const int lo = me < pieces ? cta_first(total, me, pieces) : total;
-    todo = me < pieces ? cta_first(total, me + 1, pieces) - lo : 0;
-    return lo;
-  };
-  if (a.split == kPieces) {
-    if (a.sel) {
-      total = a.units * a.max_sel;
-      begin = cut();
-      u = begin / a.max_sel;
-      at = begin % a.max_sel;
-    } else {
-      const int per = (a.units + kThreads - 1) / kThreads, u0 = threadIdx.x * per, u1 = min(u0 + per, a.units);
-      int mine = 0, sum;
-      for (int i = u0; i < u1; ++i) mine += blocks_of(i);
-      int before = block_scan_excl(mine, scan, &sum);
-      total = sum;
-      const int lo = begin = cut();
-      for (int i = u0; i < u1; ++i) {  // the one thread whose units hold block lo
-        const int n = blocks_of(i);
-        if (before <= lo && lo < before + n) {
-          found[0] = i;
-          found[1] = before;
-        }
-        before += n;
-      }
-      __syncthreads();
-      if (todo == 0) return;
-      u = found[0];
-      at = lo - found[1];
-    }
-    begin -= at;
-  }
-
-  ByteQueryShared* qs = reinterpret_cast<ByteQueryShared*>(reinterpret_cast<unsigned char*>(smem) + byte_ring_bytes(NT));
   unsigned char* ring = reinterpret_cast<unsigned char*>(smem) + warp * kStages * kHalfStage;
+  ByteQueryShared* qs = reinterpret_cast<ByteQueryShared*>(reinterpret_cast<unsigned char*>(smem) + kRingBytes);
   int in = 0, out = 0, phase = 0;  // the ring's next stage to fill and to use, and that one's phase
   bool late = false;
-  for (; todo > 0; ++u, at = 0) {
-    const int len = length(u), whole = blocks_of(u);
-    int first = at, end = whole;
-    if (a.split == kPieces) {
-      end = min(whole, at + todo);
-      todo -= end - first;
-    } else {
-      first = cta_first(whole, rank, ranks);
-      end = cta_first(whole, rank + 1, ranks);
-      todo = 0;
-    }
-    if (threadIdx.x == 0 && first == 0 && rank == 0 && len != a.lens[u]) atomicOr(a.err, kErrBounds);
+  while (share.todo > 0) {
+    const int u = share.u;
+    const ByteSegment seg = next_segment(a, share);
     if (a.nq > 1) {
-      for (int i = threadIdx.x; i < kQaMaxRows * 4; i += kThreads) poison[i >> 2][i & 3] = 0;
+      if (threadIdx.x < 32 * NT) poison[threadIdx.x >> 2][threadIdx.x & 3] = 0;
       __syncthreads();
     }
     ByteQuery Q;
     ByteRows A[NT];
-    float alpha1[2];
-    auto load_queries = [&]() {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (NT == 1 || warp == nt) {
-          load_byte_query(Q, alpha1, a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale);
-          if (NT > 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              qs[nt].b[i][lane] = make_uint4(Q.b[2 * i][0], Q.b[2 * i][1], Q.b[2 * i + 1][0], Q.b[2 * i + 1][1]);
-            qs[nt].alpha[lane] = make_float2(alpha1[0], alpha1[1]);
-          }
-        }
-        A[nt].top[0] = A[nt].top[1] = kNoRef;
-        A[nt].l[0] = A[nt].l[1] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) A[nt].o[j][0] = A[nt].o[j][1] = A[nt].o[j][2] = A[nt].o[j][3] = 0.f;
-      }
-      if (NT > 1) __syncthreads();
-    };
+    float alpha[2];
 
     // The blocks, listed ones looked up kQaList at a time and those without a token left out.  Warp w takes half
     // w % 2 of the blocks w / 2, w / 2 + kWarps / 2, ...  (an empty half of the last block too: it adds nothing).
-    const int batch = a.sel ? kQaList : max(end - first, 1), half = warp & 1;
+    const int batch = a.sel ? kQaList : max(seg.end - seg.first, 1), half = warp & 1;
     const uint8_t* base = a.store + (size_t)u * a.max_blocks * kByteBlockBytes;
-    for (int b0 = first; b0 < end || b0 == first; b0 += batch) {
-      int n = max(min(batch, end - b0), 0);
+    for (int b0 = seg.first; b0 < seg.end || b0 == seg.first; b0 += batch) {
+      int n = max(min(batch, seg.end - b0), 0);
       if (a.sel) {
-        if (b0 > first) __syncthreads();  // the list before is used up
-        int kept = 0;
-        for (int j0 = 0; j0 < n; j0 += kThreads) {
-          int4 e = make_int4(0, 0, b0 + j0 + threadIdx.x, 0);
-          if (j0 + (int)threadIdx.x < n) {
-            const size_t i = (size_t)u * a.max_sel + e.z;
-            const int block = a.sel[i];
-            const int slot = block < 0 ? 0 : a.sel_slot ? a.sel_slot[i] : block;
-            const bool held = slot >= 0 && slot < a.max_blocks;
-            if (!held) atomicOr(a.err, kErrBounds);
-            const long long left = block < 0 || !held ? 0 : (long long)len - (long long)block * kBlock;
-            e.x = slot;
-            e.y = (int)min(max(left, 0ll), 2ll * kBlock);  // 128 or more: every row sees the whole block
-          }
-          int sum;
-          const int to = block_scan_excl(e.y > 0, scan, &sum);
-          if (e.y > 0) list[kept + to] = e;
-          kept += sum;
-        }
-        n = kept;
-        __syncthreads();
-      } else if (len == 0) {
+        if (b0 > seg.first) __syncthreads();  // the list before is used up
+        n = byte_list(a, u, seg.len, b0, n, scan, list);
+      } else if (seg.len == 0) {
         n = 0;
       }
       constexpr int step = kWarps / 2;
@@ -495,16 +339,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) byte_attend_kernel(const
       };
 #pragma unroll
       for (int i = 0; i < kStages; ++i) issue();
-      if (b0 == first) load_queries();  // while the first stages arrive
+      if (b0 == seg.first) {  // while the first stages arrive
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (NT == 1 || warp == nt) {
+            load_byte_query(Q, alpha, a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale);
+            if (NT > 1) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                qs[nt].b[i][lane] = make_uint4(Q.b[2 * i][0], Q.b[2 * i][1], Q.b[2 * i + 1][0], Q.b[2 * i + 1][1]);
+              qs[nt].alpha[lane] = make_float2(alpha[0], alpha[1]);
+            }
+          }
+          A[nt].top[0] = A[nt].top[1] = kNoRef;
+          A[nt].l[0] = A[nt].l[1] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) A[nt].o[j][0] = A[nt].o[j][1] = A[nt].o[j][2] = A[nt].o[j][3] = 0.f;
+        }
+        if (NT > 1) __syncthreads();
+      }
       for (int done = 0; done < started; ++done) {
         late |= !__all_sync(0xffffffffu, stage_wait(&bars[warp][out], phase, a.wait_limit));
         if (!late) {  // otherwise wait for what is in flight, and start no more
           const int j = warp / 2 + done * step;
-          const int left = (a.sel ? list[j].y : len - (b0 + j) * kBlock) - half * kHalfTokens;
+          const int left = (a.sel ? list[j].y : seg.len - (b0 + j) * kBlock) - half * kHalfTokens;
           float2* mass = nullptr;
-          if (a.mass)
-            mass = a.half + (((size_t)u * a.blocks + (a.sel ? list[j].z : b0 + j)) * 2 + half) * a.mass_rows;
-          process_half<NT>(A, Q, alpha1, qs, ring + out * kHalfStage, poison, left, a.rows, a.nq, mass, lane);
+          if (a.mass) mass = a.half + (((size_t)u * a.blocks + (a.sel ? list[j].z : b0 + j)) * 2 + half) * a.mass_rows;
+          process_half<NT>(A, Q, alpha, qs, ring + out * kHalfStage, poison, left, a.rows, a.nq, mass, lane);
           __syncwarp();  // the stage is read
           issue();
         }
@@ -538,88 +399,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) byte_attend_kernel(const
       }
     }
     __syncthreads();
-    const bool complete = first == 0 && end == whole;
-    const int part = me + u;  // a piece's end and a unit's each move on by one: no two segments share a part
-    const size_t out0 = (size_t)u * a.rows;  // the unit's first row of the result
-    for (int idx = threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += kThreads) {
-      const int row = idx >> 5, x = 4 * (idx & 31);
-      float R = wr[0][row];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) R = fmaxf(R, wr[w][row]);
-      float L = 0.f;
-      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(wr[w][row] - R);
-        const float4 o = *reinterpret_cast<const float4*>(smem + (w * 8 * NT + row) * kQaRowStride + x);
-        L = fmaf(wl[w][row], f, L);
-        O.x = fmaf(o.x, f, O.x);
-        O.y = fmaf(o.y, f, O.y);
-        O.z = fmaf(o.z, f, O.z);
-        O.w = fmaf(o.w, f, O.w);
-      }
-      if (a.nq > 1) {
-        const uint32_t bad = poison[row][x >> 5] >> (x & 31) & 15u;
-        const float nan = __int_as_float(0x7fc00000);
-        if (bad & 1u) O.x = nan;
-        if (bad & 2u) O.y = nan;
-        if (bad & 4u) O.z = nan;
-        if (bad & 8u) O.w = nan;
-      }
-      if (ranks > 1) {  // in the place of warp 0's, which this thread alone has read
-        *reinterpret_cast<float4*>(smem + row * kQaRowStride + x) = O;
-        if (x == 0) merged[row] = make_float2(R, L);
-      } else if (complete) {
-        store_out(a.out + (out0 + row) * kHeadDim + x, O, L);
-        if (x == 0) {
-          final[row] = final_of(R, L);
-          if (a.mass && a.split == kPieces) a.total[out0 + row] = make_float2(R, L);
-        }
-      } else {
-        const size_t i = (size_t)part * a.rows + row;
-        if (x == 0) a.stats[i] = make_float2(R, L);
-        *reinterpret_cast<float4*>(a.part + i * kHeadDim + x) = O;
-      }
-    }
-    if (ranks > 1) {  // each CTA of the cluster merges its share of the outputs through distributed shared memory
-      cg::cluster_group cluster = cg::this_cluster();
-      cluster.sync();
-      if (a.mass) {
-        if (threadIdx.x < a.rows) {
-          float R = kNoRef, L = 0.f;
-          for (int r = 0; r < ranks; ++r) R = fmaxf(R, cluster.map_shared_rank(&merged[threadIdx.x], r)->x);
-          for (int r = 0; r < ranks; ++r) {
-            const float2 m = *cluster.map_shared_rank(&merged[threadIdx.x], r);
-            L = fmaf(m.y, ex2(m.x - R), L);
-          }
-          final[threadIdx.x] = final_of(R, L);
-        }
-        __syncthreads();
-        for (int i = cta_first(a.blocks, rank, ranks) + threadIdx.x; i < cta_first(a.blocks, rank + 1, ranks); i += kThreads)
-          a.mass[(size_t)u * a.blocks + i] = block_mass(a, u, i, final);
-      }
-      for (int idx = rank * kThreads + threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += ranks * kThreads) {
-        const int row = idx >> 5, x = 4 * (idx & 31);
-        float R = kNoRef, L = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int r = 0; r < ranks; ++r) {
-          const float2 m = *cluster.map_shared_rank(&merged[row], r);
-          merge_part(R, L, O, m.x, m.y, *reinterpret_cast<const float4*>(cluster.map_shared_rank(smem + row * kQaRowStride + x, r)));
-        }
-        store_out(a.out + (out0 + row) * kHeadDim + x, O, L);
-      }
-      cluster.sync();  // keep every CTA's shared memory until all have read it
-      return;
-    }
-    if (a.split != kPieces && a.mass) {
-      __syncthreads();  // the warps' sums are written, and final
-      for (int i = threadIdx.x; i < a.blocks; i += kThreads) a.mass[(size_t)u * a.blocks + i] = block_mass(a, u, i, final);
-    }
-    if (a.split == kPieces && first == 0 && threadIdx.x == 0)
-      a.meta[u] = make_int2(part, cta_of(total, begin + whole - 1, pieces) - me + 1);
-    begin += whole;
-    if (todo > 0) {
+    finish_segment<kWarps, 8 * NT>(a, share, seg, smem, wr, wl, poison, merged, final);
+    if (share.todo > 0) {
       fence_proxy_async_smem();  // the next segment's copies come after these reads and writes
       __syncthreads();
     }
@@ -674,20 +455,19 @@ __global__ void __launch_bounds__(kMassThreads) byte_mass_kernel(const __grid_co
 // What the launches need of a device, looked up once (a call costs more in look-ups than in launching otherwise).
 struct ByteDevice {
   int sms;
-  int wave;  // CTAs that are resident at once
+  int wave[3];  // CTAs that are resident at once: of this kernel's forms for 8 and 16 rows, of byte_attend_tc.cu's for 32
 };
 static std::mutex g_byte_mutex;
 static ByteDevice g_byte_device[64] = {};
 
 template <int NT>
 static cudaError_t set_up_byte_attend(int sms, int* wave) {
-  const int smem = byte_smem_bytes<NT>();
   int ctas = 0;
-  cudaError_t e = cudaFuncSetAttribute(byte_attend_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(byte_attend_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kByteSmem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(byte_attend_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, byte_attend_kernel<NT>, kThreads, smem);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, byte_attend_kernel<NT>, kByteThreads, kByteSmem);
   if (e == cudaSuccess && ctas < 1) e = cudaErrorInvalidConfiguration;
-  *wave = std::min(*wave, ctas * sms);
+  *wave = std::min(ctas, 8) * sms;
   return e;
 }
 
@@ -700,14 +480,13 @@ static bool byte_device(ByteDevice* out) {
   std::lock_guard<std::mutex> lock(g_byte_mutex);
   ByteDevice& d = g_byte_device[dev];
   if (!d.sms) {
-    ByteDevice n = {0, 1 << 30};
+    ByteDevice n = {};
     if (cudaDeviceGetAttribute(&n.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n.sms < 1 ||
-        set_up_byte_attend<1>(n.sms, &n.wave) != cudaSuccess || set_up_byte_attend<2>(n.sms, &n.wave) != cudaSuccess ||
-        set_up_byte_attend<4>(n.sms, &n.wave) != cudaSuccess) {
+        set_up_byte_attend<1>(n.sms, &n.wave[0]) != cudaSuccess || set_up_byte_attend<2>(n.sms, &n.wave[1]) != cudaSuccess ||
+        set_up_byte_attend_tc(n.sms, &n.wave[2]) != cudaSuccess) {
       (void)cudaGetLastError();
       return false;
     }
-    n.wave = std::min(n.wave, 8 * n.sms);
     d = n;
   }
   *out = d;
@@ -731,38 +510,34 @@ static size_t byte_parts_bytes(size_t units, size_t parts, int rows, size_t bloc
 // What a call wants for its scratch: enough for pieces whether it takes them or not, so that more units, rows or blocks never
 // want less, and a scratch made for the largest call serves them all.
 static size_t byte_bytes(const ByteDevice& d, int units, int rows, int blocks, bool mass) {
-  return byte_parts_bytes(units, (size_t)d.wave + units, rows, blocks, mass);
+  const int wave = std::max({d.wave[0], d.wave[1], d.wave[2]});
+  return byte_parts_bytes(units, (size_t)wave + units, rows, blocks, mass);
 }
 
-// The largest power of two of CTAs per unit, `most` at most, that fits all units into one wave and leaves each warp a half
-// block.
-static int byte_cluster_size(int units, int blocks, int wave, int most) {
+// The fewest blocks that keep a CTA of the kernel for so many rows busy: half a block a warp, or a chunk.
+static int byte_step(int rows) { return rows <= 16 ? kWarps / 2 : kTcChunkBlocks; }
+
+// The largest power of two of CTAs per unit, `most` at most, that fits all units into one wave and leaves each something to do.
+static int byte_cluster_size(int units, int blocks, int wave, int step, int most) {
   int cl = most;
-  while (cl > 1 && ((long long)units * cl > wave || (cl - 1) * (kWarps / 2) >= blocks)) cl /= 2;
+  while (cl > 1 && ((long long)units * cl > wave || (cl - 1) * step >= blocks)) cl /= 2;
   return cl;
 }
 
-static BytePlan byte_plan(const ByteDevice& d, int units, int blocks, bool listed) {
-  const int wave = d.wave, rounds = (units + wave - 1) / wave;
+static BytePlan byte_plan(const ByteDevice& d, int units, int rows, int blocks, bool listed) {
+  const int wave = d.wave[rows <= 8 ? 0 : rows <= 16 ? 1 : 2], rounds = (units + wave - 1) / wave, step = byte_step(rows);
   if (units > kQaSplitUnits || (units > wave && (long long)(rounds * wave - units) * blocks <= 24ll * units))
     return {kWhole, units, 0};
-  const int cl = byte_cluster_size(units, blocks, wave, 32 * units <= wave ? 16 : 8);
+  const int cl = byte_cluster_size(units, blocks, wave, step, 32 * units <= wave ? 16 : 8);
   if (units * cl <= wave && 2 * units * cl > wave && blocks <= (listed ? 160 : 32) * cl) return {kCluster, units * cl, cl};
   if (units * cl <= wave && blocks <= 6 * cl) return {kCluster, units * cl, cl};
-  const long long pieces = ((long long)units * blocks + kWarps / 2 - 1) / (kWarps / 2);
-  return {kPieces, (int)std::min<long long>(wave, pieces), 0};
-}
-
-template <int NT>
-static cudaError_t launch_byte_attend(const ByteArgs& a, const BytePlan& p, cudaStream_t st) {
-  return launch_ex(byte_attend_kernel<NT>, dim3((unsigned)p.ctas), dim3(kThreads), byte_smem_bytes<NT>(), st, true,
-                   p.cluster, a);
+  return {kPieces, (int)std::min<long long>(wave, ((long long)units * blocks + step - 1) / step), 0};
 }
 
 static nosa_status byte_attend(ByteArgs& a, void* scratch, size_t scratch_bytes, cudaStream_t st) {
   ByteDevice d;
   if (!byte_device(&d)) return NOSA_ERR_CUDA;
-  const BytePlan plan = byte_plan(d, a.units, a.blocks, a.sel != nullptr);
+  const BytePlan plan = byte_plan(d, a.units, a.rows, a.blocks, a.sel != nullptr);
   if (scratch_bytes < byte_bytes(d, a.units, a.rows, a.blocks, a.mass != nullptr)) return NOSA_ERR_CAPACITY;
   const size_t parts = (size_t)plan.ctas + a.units;
   unsigned char* p = static_cast<unsigned char*>(scratch);
@@ -775,9 +550,9 @@ static nosa_status byte_attend(ByteArgs& a, void* scratch, size_t scratch_bytes,
   a.total = reinterpret_cast<float2*>(a.part + (plan.split == kPieces ? parts * a.rows * kHeadDim : 0));
   a.stats = a.total + (size_t)a.units * a.rows;
   a.meta = reinterpret_cast<int2*>(a.stats + (plan.split == kPieces ? parts * a.rows : 0));
-  cudaError_t e = a.rows <= 8    ? launch_byte_attend<1>(a, plan, st)
-                  : a.rows <= 16 ? launch_byte_attend<2>(a, plan, st)
-                                 : launch_byte_attend<4>(a, plan, st);
+  cudaError_t e = a.rows > 16 ? launch_byte_attend_tc(a, plan.ctas, plan.cluster, st)
+                              : launch_ex(a.rows <= 8 ? byte_attend_kernel<1> : byte_attend_kernel<2>, dim3((unsigned)plan.ctas),
+                                          dim3(kByteThreads), kByteSmem, st, true, plan.cluster, a);
   if (e == cudaSuccess && plan.split == kPieces)
     e = launch_ex(byte_merge_kernel, dim3((unsigned)(a.units * a.rows)), dim3(kMergeWarps * 32), 0, st, true, 0, a);
   if (e == cudaSuccess && plan.split == kPieces && a.mass)

@@ -1,0 +1,451 @@
+// Attention over an 8-bit KV block store for 9 to 32 query rows a unit (several drafted tokens of a group of q heads): the same
+// sums as byte_attend.cu on the fifth-generation tensor cores.
+//
+// With so many rows mma.sync spends its time on fragments: two products of 16 x 8 values each an instruction, and a warp's
+// operands, accumulators and weights do not fit its registers (32 rows: 961 instructions for 32 tokens, 91 us for 16 units
+// of 65,521 tokens).  Here a CTA of 128 threads takes a chunk of two blocks, and a thread is a token, or a dim:
+//   S (128 tokens x rows) = K . q^T    tcgen05 kind::f8f6f4: K's codes as they are, moved from the store's order into the
+//                                      128-byte swizzle; q as two e4m3 codes a value (its columns twice), exact to 2^-21 of
+//                                      the row's largest
+//   weights of the thread's token, all rows: as f16 into shared memory, their sums float32 in registers
+//   O^T (128 dims x rows) += s_V (V^T . P)   kind::f16: V's codes converted to f16 and transposed by stmatrix, one product per
+//                                      block, read back and added in float32 with the block's scale
+// Chunks overlap between the two CTAs of an SM, and within one the copy of the next chunk and the products with the rest.
+// Row references are the CTA's: a thread whose score would weigh more than 2^14 says so at the barrier before the second
+// product, and then all raise and weigh again.
+#include "byte_split.cuh"
+#include "host.h"
+#include "tc.cuh"
+
+namespace nosa {
+
+constexpr int kTcTokens = kTcChunkBlocks * kBlock;
+constexpr int kTcThreads = 256, NR = 32;  // (rows a unit at most)
+static_assert(2 * kTcTokens == kTcThreads && kTcTokens == kHeadDim, "two threads a token, and a dim");
+// shared memory: K (128 tokens x 128 codes), P (128 tokens x 64 f16, of which the rows' are used), q (rows twice x 128
+// codes), all in the 128-byte swizzle, and two stages, each the codes of a chunk's blocks as they arrive, and then in their
+// place V^T (128 dims x 64 f16 a block, swizzled)
+constexpr int kTcK = 0, kTcP = 16384, kTcQ = kTcP + 16384, kTcStage = kTcQ + 8192, kTcStageBytes = kTcChunkBlocks * kByteScales;
+constexpr int kTcSmem = kTcStage + 2 * kTcStageBytes + 1024;
+static_assert(32 * kQaRowStride * 4 <= kTcQ, "the partial result takes the operands' place");
+static_assert(kByteScales == kHeadDim * kBlock * 2, "V^T in f16 takes a block's place");
+
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// The unit's query rows as operands: row r's codes in rows r (the values') and NR + r (16 times what these leave) of sq, and
+// the factors that turn its scores into logits in base 2 for a K scale of 1.  A warp takes every eighth row, a lane four
+// dims.  The largest magnitude of a row is brought into [2^7, 2^8), so that bf16's eight bits are two codes of four down to
+// 2^-13 of it.
+__device__ __forceinline__ void load_tc_queries(const ByteArgs& a, int u, unsigned char* sq, float* alpha, int warp, int lane) {
+  uint2 x[NR / 8];
+#pragma unroll
+  for (int i = 0; i < NR / 8; ++i) {
+    const int row = warp + 8 * i;
+    x[i] = row < a.rows ? *reinterpret_cast<const uint2*>(a.q + ((size_t)u * a.rows + row) * kHeadDim + 4 * lane) : make_uint2(0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < NR / 8; ++i) {
+    const int row = warp + 8 * i;
+    uint32_t big = max(max(x[i].x & 0x7fffu, (x[i].x >> 16) & 0x7fffu), max(x[i].y & 0x7fffu, (x[i].y >> 16) & 0x7fffu));
+    big = __reduce_max_sync(0xffffffffu, big);
+    const int shift = big == 0 || big >= 0x7f80u ? 0 : min(7 - ((int)(big >> 7) - 127), 126);
+    const float f = __uint_as_float((uint32_t)(127 + shift) << 23);
+    const float inv = big >= 0x7f80u ? __int_as_float(0x7fc00000) : __uint_as_float((uint32_t)(127 - shift) << 23);
+    const float v[4] = {__uint_as_float(x[i].x << 16) * f, __uint_as_float(x[i].x & 0xffff0000u) * f,
+                        __uint_as_float(x[i].y << 16) * f, __uint_as_float(x[i].y & 0xffff0000u) * f};
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t c = to_codes(v[2 * k], v[2 * k + 1]), h = codes_to_half2(c);
+      const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      hi |= c << (16 * k);
+      lo |= to_codes((v[2 * k] - got.x) * 16.f, (v[2 * k + 1] - got.y) * 16.f) << (16 * k);
+    }
+    const int at = 16 * ((lane >> 2) ^ (row & 7)) + 4 * (lane & 3);  // (NR is a multiple of 8)
+    *reinterpret_cast<uint32_t*>(sq + row * 128 + at) = hi;
+    *reinterpret_cast<uint32_t*>(sq + (NR + row) * 128 + at) = lo;
+    if (lane == 0) {
+      const float al = a.scale * inv;
+      alpha[row] = al > 0x1p127f ? 0x1p127f : al;  // finite: it may meet a zero s_K (a NaN stays)
+    }
+  }
+}
+
+// A warp moves a tile's K codes from the store's order into the swizzle: row by row of 128 bytes, 16-byte pieces of 16 dims.
+__device__ __forceinline__ void place_keys(unsigned char* sk, const unsigned char* tile, int token0, int lane) {
+  uint4 k[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // 8 tokens' half, half of 32 dims
+    k[i] = *reinterpret_cast<const uint4*>(tile + 512 * i + 16 * lane);
+  const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(sk + (token0 + 8 * (i >> 1) + g) * 128 + 16 * ((2 * q + (i & 1)) ^ g)) = k[i];
+}
+
+// A warp converts a tile's V codes to f16 and writes them transposed: dim 16 g + e is row 8 e + g, tokens in pieces of 8.
+// left: tokens of the context from the tile's first on.  Tokens that no row sees are cleared (the store may hold anything
+// there, and 0 x NaN is a NaN), and a NaN of one that only some rows see: those get a bit of `poison`, and a NaN in that dim
+// in the end.
+__device__ __forceinline__ void place_values(uint32_t sv, const uint4 (&v)[4], int piece, int left, uint32_t (*poison)[4], int nq,
+                                             int rows, int lane) {
+  const int g = lane & 7, m = lane >> 3;  // the address a lane gives: row g of matrix m
+  const bool tail = left - (nq - 1) < kByteTileTokens;  // some row does not see the whole tile
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+    if (tail) {
+      const int late0 = 2 * (lane & 3) - (left - nq);  // rows of query tokens from there on see token 2t
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // a word: two dims of tokens 2t + 8 (e % 2), + 1
+        const int late = late0 + 8 * (e & 1);
+        const uint32_t keep = (late < nq ? 0x00ff00ffu : 0u) | (late + 1 < nq ? 0xff00ff00u : 0u);
+        const uint32_t part = keep & ((late > 0 ? 0x00ff00ffu : 0u) | (late >= 0 ? 0xff00ff00u : 0u));
+        w[e] &= keep;
+        uint32_t nan = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u & part;
+        while (nan) {
+          const int b = (__ffs(nan) - 1) >> 3, d = 16 * (lane >> 2) + 4 * c + 2 * (e >> 1) + (b >> 1);
+          for (int row = 0; row < rows; ++row)
+            if (row % nq >= late + (b & 1)) atomicOr(&poison[row][d >> 5], 1u << (d & 31));
+          w[e] &= ~(0xffu << (8 * b));
+          nan &= nan - 1;
+        }
+      }
+      __syncwarp();
+    }
+    uint32_t f[2][4];  // [half][dim 4 c + ..]: tokens 2t + 8 half, + 1
+    codes_to_half2(w[0], f[0][0], f[0][1]);
+    codes_to_half2(w[2], f[0][2], f[0][3]);
+    codes_to_half2(w[1], f[1][0], f[1][1]);
+    codes_to_half2(w[3], f[1][2], f[1][3]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      stmatrix_x4(sv + (8 * (4 * c + m) + g) * 128 + 16 * ((piece + h) ^ g), f[h][0], f[h][1], f[h][2], f[h][3]);
+  }
+}
+
+// Sums of R values over a warp: lane r (mod R) gets value r's.
+template <int R>
+__device__ __forceinline__ float sum_rows(const float (&v)[R], int lane) {
+  float x[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    x[r] = v[r];
+#pragma unroll
+    for (int o = 16; o >= R; o >>= 1) x[r] += __shfl_xor_sync(0xffffffffu, x[r], o);
+  }
+#pragma unroll
+  for (int n = R / 2; n > 0; n >>= 1) {
+    const bool up = lane & n;
+#pragma unroll
+    for (int r = 0; r < n; ++r) {
+      const float keep = up ? x[r + n] : x[r], give = up ? x[r] : x[r + n];
+      x[r] = keep + __shfl_xor_sync(0xffffffffu, give, n);
+    }
+  }
+  return x[0];
+}
+
+// Four consecutive floats of shared memory that all lanes read.
+__device__ __forceinline__ void read4(float (&v)[4], const float* p) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+}
+
+__global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __grid_constant__ ByteArgs a) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bar_raw, bar_s, bar_o;  // a chunk's copies, its scores, its products with V
+  __shared__ __align__(16) float scales[2][kTcChunkBlocks][4];  // [stage][block]: s_K, s_V
+  __shared__ int4 list[kQaList];
+  __shared__ int scan[32], found[2];
+  __shared__ uint32_t tbase;
+  __shared__ __align__(16) float alpha[NR], top[NR], raised[NR], factor[kTcChunkBlocks][NR];
+  __shared__ uint32_t best[4][NR];
+  __shared__ float sums[4][NR], wr[1][NR], wl[1][NR];
+  __shared__ uint32_t poison[NR][4];
+  __shared__ float2 merged[NR], final[NR];
+  constexpr int R = NR / 2;           // a thread's rows
+  constexpr uint32_t kCols = 4 * NR;  // scores of both codes, and a block's result twice
+  constexpr uint32_t idS = tc::plain_idesc(128, 2 * NR, 0), idO = tc::plain_idesc(128, NR, 1);
+  unsigned char* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset, so that it stays a shared-memory address)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int quarter = warp & 3, r0 = warp >> 2 ? R : 0, at = 32 * quarter + lane;  // the thread's rows, token and dim's place
+  if (tid == 0) {
+    mbar_init(&bar_raw, 1);
+    mbar_init(&bar_s, 1);
+    mbar_init(&bar_o, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  ByteShare share = byte_share(a, kTcChunkBlocks, scan, found);
+  if (share.todo == 0) return;
+  if (warp == 0) tc::alloc(&tbase, kCols);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tm = tbase, trow = tm + ((uint32_t)(32 * quarter) << 16) + r0, sa = smem_u32(sm);
+
+  int ph_raw = 0, ph_s = 0, ph_o = 0, st = 0;  // the barriers' phases, and the stage of the chunk in work
+  bool late = false;
+  while (share.todo > 0) {
+    const int u = share.u;
+    const ByteSegment seg = next_segment(a, share);
+    float o[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) o[r] = l[r] = 0.f;
+    if (tid < NR) {
+      top[tid] = kNoRef;
+      poison[tid][0] = poison[tid][1] = poison[tid][2] = poison[tid][3] = 0;
+    }
+    float sv[kTcChunkBlocks] = {};  // the V scales of the chunk whose products are in flight
+    bool flying = false;
+    // waits are decided for the whole warp: the tensor-memory accesses behind them are warp-collective
+    auto wait_for = [&](uint64_t* bar, int phase) {
+      late |= !__all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, kWaitCycles));
+      tc::fence_after();
+    };
+    auto add_products = [&]() {  // O += s_V of the chunk before: the thread's dim, its rows
+      wait_for(&bar_o, ph_o);
+      ph_o ^= 1;
+      uint32_t d[kTcChunkBlocks][R];
+#pragma unroll
+      for (int b = 0; b < kTcChunkBlocks; ++b) tc::ld16(trow + 2 * NR + b * NR, d[b]);
+      tc::wait_ld();
+#pragma unroll
+      for (int b = 0; b < kTcChunkBlocks; ++b) tc::landed(d[b]);
+#pragma unroll
+      for (int b = 0; b < kTcChunkBlocks; ++b)
+#pragma unroll
+        for (int r = 0; r < R; ++r) o[r] = fmaf(__uint_as_float(d[b][r]), sv[b], o[r]);
+    };
+
+    const int batch = a.sel ? kQaList : max(seg.end - seg.first, 1);
+    const uint8_t* base = a.store + (size_t)u * a.max_blocks * kByteBlockBytes;
+    for (int b0 = seg.first; b0 < seg.end || b0 == seg.first; b0 += batch) {
+      int n = max(min(batch, seg.end - b0), 0);
+      if (a.sel) {
+        if (b0 > seg.first) __syncthreads();  // the list before is used up
+        n = byte_list(a, u, seg.len, b0, n, scan, list);
+      } else if (seg.len == 0) {
+        n = 0;
+      }
+      const int chunks = late ? 0 : (n + 1) / kTcChunkBlocks;
+      // One warp: the copies of chunk c into stage `to`, and a later chunk's way into L2; lanes b and 2 + b block b's codes and
+      // scales, 4 + b the later one's.
+      auto issue = [&](int c, int to, int later) {
+        const int m = min(n - kTcChunkBlocks * c, kTcChunkBlocks);
+        if (lane == 0 && m > 0) mbar_arrive_expect_tx(&bar_raw, m * (kByteScales + 16));
+        __syncwarp();
+        const int j = kTcChunkBlocks * (lane < 4 ? c : later) + (lane & 1);
+        if (lane < 6 && j < n) {
+          const uint8_t* src = base + (size_t)(a.sel ? list[j].x : b0 + j) * kByteBlockBytes;
+          if (lane < 4)
+            bulk_copy_g2s(lane < 2 ? sa + kTcStage + to * kTcStageBytes + lane * kByteScales : smem_u32(scales[to][lane & 1]),
+                          lane < 2 ? src : src + kByteScales, lane < 2 ? kByteScales : 16, &bar_raw);
+          else
+            bulk_prefetch(src, kByteScales + 16);
+        }
+        __syncwarp();
+      };
+      // tokens of the context from block j (of the list) on
+      auto left_of = [&](int j) { return j >= n ? 0 : a.sel ? list[j].y : seg.len - (b0 + j) * kBlock; };
+      if (chunks > 0 && warp == 2) issue(0, st, 1);
+      if (b0 == seg.first) {  // while the first chunk arrives
+        load_tc_queries(a, u, sm + kTcQ, alpha, warp, lane);
+        __syncthreads();
+      }
+      for (int c = 0; c < chunks; ++c) {
+        late |= !__all_sync(0xffffffffu, stage_wait(&bar_raw, ph_raw, a.wait_limit));
+        ph_raw ^= 1;
+        // a warp takes one of the chunk's eight tiles: K into its operand's place, V into registers
+        const int b_tile = warp >> 2, tile = warp & 3;
+        const unsigned char* codes = sm + kTcStage + st * kTcStageBytes + b_tile * kByteScales + tile * kByteTile;
+        place_keys(sm + kTcK, codes, kByteTileTokens * warp, lane);
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(codes + kByteV + 512 * i + 16 * lane);
+        float scale[kTcChunkBlocks];  // V's
+#pragma unroll
+        for (int b = 0; b < kTcChunkBlocks; ++b) {
+          const bool there = kTcChunkBlocks * c + b < n;
+          const float2 s = there ? *reinterpret_cast<const float2*>(scales[st][b]) : make_float2(0.f, 0.f);
+          scale[b] = s.y;
+          if (tid >= b * NR && tid < (b + 1) * NR) factor[b][tid - b * NR] = logit_factor(alpha[tid - b * NR], s.x);
+        }
+        fence_proxy_async_smem();  // K (generic stores) is read by the tensor core
+        tc::fence_before();
+        late = __syncthreads_or(late);
+        tc::fence_after();
+        if (late) break;
+        if (tid == 0) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // 32 dims each
+            tc::mma_f8(tm, tc::sw128_desc(sa + kTcK + 32 * k), tc::sw128_desc(sa + kTcQ + 32 * k), idS, k > 0);
+          tc::commit(&bar_s);
+        }
+        __syncwarp();
+        // V^T over the codes, which all warps have read
+        place_values(sa + kTcStage + st * kTcStageBytes + b_tile * kByteScales, v, 2 * tile,
+                     left_of(kTcChunkBlocks * c + b_tile) - kByteTileTokens * tile, poison, a.nq, a.rows, lane);
+        if (flying) add_products();  // then the other stage and P are free too
+#pragma unroll
+        for (int b = 0; b < kTcChunkBlocks; ++b) sv[b] = scale[b];
+        if (warp == 2) issue(c + 1, st ^ 1, c + 2);
+
+        // the thread's token: the logits of its rows
+        const int block = at / kBlock, j = kTcChunkBlocks * c + block, mine = left_of(j) - at % kBlock;  // rows of query tokens from nq - mine on see it
+        wait_for(&bar_s, ph_s);
+        ph_s ^= 1;
+        // Weights 2^(logit - top), as f16 into P.  Where one is more than its reference allows, all raise theirs and weigh again.
+        float y[R];
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          uint32_t d[R], e[R];
+          tc::ld16(trow, d);
+          tc::ld16(trow + NR, e);
+          tc::wait_ld();
+          tc::landed(d);
+          tc::landed(e);
+#pragma unroll
+          for (int r = 0; r < R; r += 4) {
+            float f[4];
+            read4(f, &factor[block][r0 + r]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[r + i] = fmaf(__uint_as_float(e[r + i]), 0.0625f, __uint_as_float(d[r + i])) * f[i];
+          }
+          if (mine < a.nq) {
+            int query = r0 % a.nq;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              if (query < a.nq - mine) y[r] = -INFINITY;
+              query = query + 1 == a.nq ? 0 : query + 1;
+            }
+          }
+          if (pass) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const uint32_t m = __reduce_max_sync(0xffffffffu, orderable(y[r]));
+              if (lane == 0) best[quarter][r0 + r] = m;
+            }
+            __syncthreads();
+            if (tid < NR) {
+              const uint32_t m = max(max(best[0][tid], best[1][tid]), max(best[2][tid], best[3][tid]));
+              const float b = __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m);
+              float f = 1.f;
+              if (b - top[tid] > kTopWeight) {
+                const float ref = reference(b);
+                f = ex2(top[tid] - ref);
+                top[tid] = ref;
+              }
+              raised[tid] = f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < R; r += 4) {
+              float f[4];
+              read4(f, &raised[r0 + r]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[r + i] *= f[i];
+                l[r + i] *= f[i];
+              }
+            }
+          }
+          float over = -INFINITY;
+          uint32_t p[R / 2];
+#pragma unroll
+          for (int r = 0; r < R; r += 4) {
+            float ref[4];
+            read4(ref, &top[r0 + r]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x = y[r + i] - ref[i];
+              over = fmaxf(over, x);
+              y[r + i] = ex2(x);
+            }
+            p[r / 2] = pack_half2(y[r], y[r + 1]);
+            p[r / 2 + 1] = pack_half2(y[r + 2], y[r + 3]);
+          }
+#pragma unroll
+          for (int i = 0; i < R / 8; ++i)
+            *reinterpret_cast<uint4*>(sm + kTcP + at * 128 + 16 * ((r0 / 8 + i) ^ (at & 7))) =
+                make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+          fence_proxy_async_smem();  // P and V^T are read by the tensor core
+          tc::fence_before();
+          const bool raise = __syncthreads_or(over > kTopWeight);
+          tc::fence_after();
+          if (!raise || pass) break;
+        }
+        if (tid == kTcThreads / 2) {
+#pragma unroll
+          for (int b = 0; b < kTcChunkBlocks; ++b)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // 16 tokens each
+              tc::mma_f16(tm + 2 * NR + b * NR, tc::sw128_desc(sa + kTcStage + st * kTcStageBytes + b * kByteScales + 32 * k),
+                          tc::sw128_desc_mn(sa + kTcP + b * 8192 + 2048 * k, 16384), idO, k > 0);
+          tc::commit(&bar_o);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < R; ++r) l[r] += y[r];
+        if (a.mass && j < n) {  // a warp's tokens are half a block
+          const float sum = sum_rows<R>(y, lane);
+          const size_t entry = (size_t)u * a.blocks + (a.sel ? list[j].z : b0 + j);
+          if (lane < R && r0 + lane < a.rows)
+            a.half[(entry * 2 + (quarter & 1)) * a.mass_rows + r0 + lane] = make_float2(top[r0 + lane], sum);
+        }
+        flying = true;
+        st ^= 1;
+      }
+      if (late) break;
+    }
+    if (flying) add_products();
+    late = __syncthreads_or(late);  // also: the operands' places are free
+    if (late && tid == 0) atomicOr(a.err, kErrTimeout);
+
+    // the partial: the thread's dim of its rows
+    float* part = reinterpret_cast<float*>(sm);
+    const int dim = 16 * (at & 7) + (at >> 3);
+#pragma unroll
+    for (int r = 0; r < R; ++r) part[(r0 + r) * kQaRowStride + dim] = o[r];
+    const float sum = sum_rows<R>(l, lane);
+    if (lane < R) sums[quarter][r0 + lane] = sum;
+    __syncthreads();
+    if (tid < NR) {
+      wr[0][tid] = top[tid];
+      wl[0][tid] = late ? __int_as_float(0x7fc00000) : (sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid]);
+    }
+    __syncthreads();
+    finish_segment<1, NR>(a, share, seg, part, wr, wl, poison, merged, final);
+    if (share.todo > 0) {
+      fence_proxy_async_smem();
+      __syncthreads();
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 0) tc::dealloc(tm, kCols);
+}
+
+// Two CTAs share an SM by registers, shared memory and tensor-memory columns.  (The occupancy query counts one for any kernel
+// that allocates tensor memory, whatever its shared memory.)
+cudaError_t set_up_byte_attend_tc(int sms, int* wave) {
+  cudaError_t e = cudaFuncSetAttribute(byte_attend_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(byte_attend_tc_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(byte_attend_tc_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  *wave = 2 * sms;
+  return e;
+}
+
+cudaError_t launch_byte_attend_tc(const ByteArgs& a, int ctas, int cluster, cudaStream_t st) {
+  return launch_ex(byte_attend_tc_kernel, dim3((unsigned)ctas), dim3(kTcThreads), kTcSmem, st, true, cluster, a);
+}
+
+}  // namespace nosa
