@@ -83,47 +83,6 @@ struct ByteRows {
   float o[8][4];
 };
 
-// Prepares a half block that not every row sees as a whole (left: tokens of the context from its first on, possibly
-// none).  Behind the context the store may hold anything, and 0 x NaN is a NaN, so those tokens' V codes are cleared.  So
-// is a NaN of a token that only some rows see: the rows that see it get a bit of `poison`, and a NaN in that dim in the
-// end.
-__device__ __noinline__ void clear_byte_tail(unsigned char* stage, uint32_t (*poison)[4], int left, int nq, int rows, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll 1
-  for (int tile = 0; tile < 2; ++tile) {
-    const int late0 = kByteTileTokens * tile + 2 * t - (left - nq);  // rows of query tokens from there on see token 2t
-    // per half of the tile, the bytes of words (two dims of two tokens) that some row sees, and that not every row sees
-    uint32_t keep[2], part[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int late = late0 + 8 * h;
-      keep[h] = (late < nq ? 0x00ff00ffu : 0u) | (late + 1 < nq ? 0xff00ff00u : 0u);
-      part[h] = keep[h] & ((late > 0 ? 0x00ff00ffu : 0u) | (late >= 0 ? 0xff00ff00u : 0u));
-    }
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      uint4* at = reinterpret_cast<uint4*>(stage + tile * kByteTile + kByteV + 512 * c + 16 * lane);
-      const uint4 v = *at;
-      uint32_t w[4] = {v.x & keep[0], v.y & keep[1], v.z & keep[0], v.w & keep[1]};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t nan = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u & part[e & 1];
-        while (nan) {
-          const int b = (__ffs(nan) - 1) >> 3, d = 16 * g + 4 * c + 2 * (e >> 1) + (b >> 1);
-          const int late = late0 + 8 * (e & 1) + (b & 1);
-          for (int row = 0; row < rows; ++row)
-            if (row % nq >= late) atomicOr(&poison[row][d >> 5], 1u << (d & 31));
-          w[e] &= ~(0xffu << (8 * b));
-          nan &= nan - 1;
-        }
-      }
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  fence_proxy_async_smem();  // the next bulk copy into the stage comes after these writes
-  __syncwarp();
-}
-
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // One half block for all row tiles: both tiles of tokens at once, so that their chains of dependent operations overlap.
@@ -134,7 +93,10 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
                                              int rows, int nq, float2* mass, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const bool tail = left - (nq - 1) < kHalfTokens;  // some row does not see the whole half
-  if (tail) clear_byte_tail(stage, poison, left, nq, rows, lane);
+  if (tail) {
+    clear_byte_tail(stage, poison, left, nq, rows, lane);
+    clear_byte_tail(stage + kByteTile, poison, left - kByteTileTokens, nq, rows, lane);
+  }
   const float2 s = *reinterpret_cast<const float2*>(stage + kHalfBytes);  // s_K, s_V
   float z[2][NT][4];
 #pragma unroll

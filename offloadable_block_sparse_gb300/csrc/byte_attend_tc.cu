@@ -87,40 +87,15 @@ __device__ __forceinline__ void place_keys(unsigned char* sk, const unsigned cha
 }
 
 // A warp converts a tile's V codes to f16 and writes them transposed: dim 16 g + e is row 8 e + g, tokens in pieces of 8.
-// left: tokens of the context from the tile's first on.  Tokens that no row sees are cleared (the store may hold anything
-// there, and 0 x NaN is a NaN), and a NaN of one that only some rows see: those get a bit of `poison`, and a NaN in that dim
-// in the end.
-__device__ __forceinline__ void place_values(uint32_t sv, const uint4 (&v)[4], int piece, int left, uint32_t (*poison)[4], int nq,
-                                             int rows, int lane) {
+__device__ __forceinline__ void place_values(uint32_t sv, const uint4 (&v)[4], int piece, int lane) {
   const int g = lane & 7, m = lane >> 3;  // the address a lane gives: row g of matrix m
-  const bool tail = left - (nq - 1) < kByteTileTokens;  // some row does not see the whole tile
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-    if (tail) {
-      const int late0 = 2 * (lane & 3) - (left - nq);  // rows of query tokens from there on see token 2t
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {  // a word: two dims of tokens 2t + 8 (e % 2), + 1
-        const int late = late0 + 8 * (e & 1);
-        const uint32_t keep = (late < nq ? 0x00ff00ffu : 0u) | (late + 1 < nq ? 0xff00ff00u : 0u);
-        const uint32_t part = keep & ((late > 0 ? 0x00ff00ffu : 0u) | (late >= 0 ? 0xff00ff00u : 0u));
-        w[e] &= keep;
-        uint32_t nan = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u & part;
-        while (nan) {
-          const int b = (__ffs(nan) - 1) >> 3, d = 16 * (lane >> 2) + 4 * c + 2 * (e >> 1) + (b >> 1);
-          for (int row = 0; row < rows; ++row)
-            if (row % nq >= late + (b & 1)) atomicOr(&poison[row][d >> 5], 1u << (d & 31));
-          w[e] &= ~(0xffu << (8 * b));
-          nan &= nan - 1;
-        }
-      }
-      __syncwarp();
-    }
     uint32_t f[2][4];  // [half][dim 4 c + ..]: tokens 2t + 8 half, + 1
-    codes_to_half2(w[0], f[0][0], f[0][1]);
-    codes_to_half2(w[2], f[0][2], f[0][3]);
-    codes_to_half2(w[1], f[1][0], f[1][1]);
-    codes_to_half2(w[3], f[1][2], f[1][3]);
+    codes_to_half2(v[c].x, f[0][0], f[0][1]);
+    codes_to_half2(v[c].z, f[0][2], f[0][3]);
+    codes_to_half2(v[c].y, f[1][0], f[1][1]);
+    codes_to_half2(v[c].w, f[1][2], f[1][3]);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       stmatrix_x4(sv + (8 * (4 * c + m) + g) * 128 + 16 * ((piece + h) ^ g), f[h][0], f[h][1], f[h][2], f[h][3]);
@@ -264,7 +239,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
         ph_raw ^= 1;
         // a warp takes one of the chunk's eight tiles: K into its operand's place, V into registers
         const int b_tile = warp >> 2, tile = warp & 3;
-        const unsigned char* codes = sm + kTcStage + st * kTcStageBytes + b_tile * kByteScales + tile * kByteTile;
+        unsigned char* codes = sm + kTcStage + st * kTcStageBytes + b_tile * kByteScales + tile * kByteTile;
+        const int left = left_of(kTcChunkBlocks * c + b_tile) - kByteTileTokens * tile;
+        if (left - (a.nq - 1) < kByteTileTokens) clear_byte_tail(codes, poison, left, a.nq, a.rows, lane);
         place_keys(sm + kTcK, codes, kByteTileTokens * warp, lane);
         uint4 v[4];
 #pragma unroll
@@ -290,8 +267,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
         }
         __syncwarp();
         // V^T over the codes, which all warps have read
-        place_values(sa + kTcStage + st * kTcStageBytes + b_tile * kByteScales, v, 2 * tile,
-                     left_of(kTcChunkBlocks * c + b_tile) - kByteTileTokens * tile, poison, a.nq, a.rows, lane);
+        place_values(sa + kTcStage + st * kTcStageBytes + b_tile * kByteScales, v, 2 * tile, lane);
         if (flying) add_products();  // then the other stage and P are free too
 #pragma unroll
         for (int b = 0; b < kTcChunkBlocks; ++b) sv[b] = scale[b];

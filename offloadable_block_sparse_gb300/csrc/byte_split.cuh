@@ -153,6 +153,43 @@ __device__ __forceinline__ int byte_list(const ByteArgs& a, int u, int len, int 
   return kept;
 }
 
+// Prepares a staged tile that not every row sees as a whole (left: tokens of the context from its first on, possibly
+// none).  Behind the context the store may hold anything, and 0 x NaN is a NaN, so those tokens' V codes are cleared.  So
+// is a NaN of a token that only some rows see: the rows that see it get a bit of `poison`, and a NaN in that dim in the
+// end.
+static __device__ __noinline__ void clear_byte_tail(unsigned char* tile, uint32_t (*poison)[4], int left, int nq, int rows, int lane) {
+  const int g = lane >> 2, t = lane & 3, late0 = 2 * t - (left - nq);  // rows of query tokens from there on see token 2t
+  // per half of the tile, the bytes of words (two dims of two tokens) that some row sees, and that not every row sees
+  uint32_t keep[2], part[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int late = late0 + 8 * h;
+    keep[h] = (late < nq ? 0x00ff00ffu : 0u) | (late + 1 < nq ? 0xff00ff00u : 0u);
+    part[h] = keep[h] & ((late > 0 ? 0x00ff00ffu : 0u) | (late >= 0 ? 0xff00ff00u : 0u));
+  }
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(tile + kByteV + 512 * c + 16 * lane);
+    const uint4 v = *at;
+    uint32_t w[4] = {v.x & keep[0], v.y & keep[1], v.z & keep[0], v.w & keep[1]};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t nan = ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u & part[e & 1];
+      while (nan) {
+        const int b = (__ffs(nan) - 1) >> 3, d = 16 * g + 4 * c + 2 * (e >> 1) + (b >> 1);
+        const int late = late0 + 8 * (e & 1) + (b & 1);
+        for (int row = 0; row < rows; ++row)
+          if (row % nq >= late) atomicOr(&poison[row][d >> 5], 1u << (d & 31));
+        w[e] &= ~(0xffu << (8 * b));
+        nan &= nan - 1;
+      }
+    }
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  fence_proxy_async_smem();  // the next bulk copy into the stage comes after these writes
+  __syncwarp();
+}
+
 // The mass of entry i of unit u: per row, the sums of the block's halves at the row's final reference, over its final sum
 // (final: of each row the reference, and 1 / the sum, 0 where no token was seen).
 __device__ __forceinline__ float block_mass(const ByteArgs& a, int u, int i, const float2* final) {
