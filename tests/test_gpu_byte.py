@@ -305,8 +305,9 @@ def _queries(rng, units, rows):
 
 
 # units, blocks a unit: how CTAs share them (few units with a cluster each, a wave of them, pieces, a unit a CTA, more than one)
-PLANS = {"cluster": (6, 24), "wave": (100, 12), "pieces": (12, 130), "unit-a-cta": (152, 9), "rounds": (310, 5), "many": (2100, 2)}
-FORMS = [(1, 1), (8, 1), (3, 2), (8, 2), (7, 3), (8, 4), (1, 32)]  # q heads and query tokens of a unit: 1 to 32 rows
+PLANS = {"cluster": (6, 24), "wave": (100, 12), "pieces": (12, 130), "units-in-pieces": (200, 40), "unit-a-cta": (152, 9),
+         "rounds": (310, 5), "many": (2100, 2)}
+FORMS = [(1, 1), (8, 1), (3, 2), (1, 9), (8, 2), (1, 17), (7, 3), (8, 4), (1, 32)]  # q heads and query tokens of a unit: 1 to 32 rows
 
 
 @pytest.fixture(scope="module")
@@ -609,3 +610,80 @@ def test_a_wait_that_gives_up_is_reported(plan, group, nq, listed, many_blocks):
     assert torch.isnan(out).all() and torch.isnan(mass).all()
     out, mass, err = call()
     assert err == 0 and torch.isfinite(out).all() and torch.isfinite(mass).all()
+
+
+@pytest.mark.parametrize("nq", range(1, 33))
+def test_any_number_of_rows(nq, many_blocks):
+    rng = np.random.default_rng(nq)
+    store = _store(rng, many_blocks, 2, 3)
+    _check(_queries(rng, 2, nq), store, [150, nq - 1], 1, nq, 3, max_len=160)
+
+
+def test_calls_from_two_threads_on_their_own_streams(many_blocks):
+    import threading
+    rng = np.random.default_rng(18)
+    cases, errors = [], []
+    for units, nb, group, nq in [(12, 130, 8, 1), (16, 40, 8, 4)]:
+        store, q = torch.from_numpy(_store(rng, many_blocks, units, nb)).cuda(), _queries(rng, units, group * nq)
+        lens = _i32(_lengths(units, nb, nq))
+        cases.append((q, store, lens, group, nq, nb, _attend(q, store, lens, group, nq, nb, max_len=64 * nb)))
+    torch.cuda.synchronize()
+
+    def work(case):
+        try:
+            q, store, lens, group, nq, nb, want = case
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    out, mass, err = _attend(q, store, lens, group, nq, nb, max_len=64 * nb)
+                    assert err == 0 and torch.equal(out, want[0]) and torch.equal(mass, want[1])
+        except BaseException as e:  # noqa: BLE001 - handed to the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+def test_first_calls_may_be_made_under_capture():
+    """A process whose first use of the store, of eviction and of rotary positions is inside a graph capture."""
+    code = """
+import torch
+from offloadable_block_sparse_gb300 import nosa as N
+k = torch.randn(3, 70, 128, device="cuda").to(torch.bfloat16)
+q, w = (torch.randn(3, r, 128, device="cuda").to(torch.bfloat16) for r in (8, 32))
+store = torch.zeros(3, 2, 16512, dtype=torch.uint8, device="cuda"); lens = torch.full((3,), 70, dtype=torch.int32, device="cuda")
+kv = torch.empty(3, 2, 2, 64, 128, dtype=torch.bfloat16, device="cuda"); sel = torch.tensor([[0, 1]] * 3, dtype=torch.int32, device="cuda")
+a, b, c = torch.empty_like(q), torch.empty_like(q), torch.empty_like(w)
+m, acc, sc = torch.empty(3, 2, device="cuda"), torch.zeros(3, 2, device="cuda"), torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+turned, back = torch.empty_like(k), torch.empty_like(k)
+t = N.nosa_rope_make()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    s = torch.cuda.current_stream().cuda_stream
+    N.nosa_rope(t, [(k[:, None], turned[:, None])], stream=s)
+    N.nosa_rope(t, [(turned[:, None], back[:, None])], inverse=True, stream=s)
+    N.nosa_byte_append(k, k, store, 3, 70, 2, stream=s)
+    N.nosa_byte_read(store, 3, 2, None, 2, kv, lens=lens, stream=s)
+    N.nosa_byte_dense_attend(q, store, 3, 8, 1, 2, lens, 70, a, sc, sc.numel(), stream=s)
+    N.nosa_byte_attend(q, store, sel, None, 3, 8, 1, 2, 2, lens, b, sc, sc.numel(), mass=m, stream=s)
+    N.nosa_byte_attend(w, store, sel, None, 3, 8, 4, 2, 2, lens, c, sc, sc.numel(), stream=s)
+    N.nosa_evict(acc, sel, m, 3, 2, lens, 1, 0, 0, 1.0, acc, sel, stream=s)
+g.replay()
+torch.cuda.synchronize()
+x = kv[:, :, 0].reshape(3, 128, 128)
+assert (x[:, :70].float() - k.float()).abs().max() < 0.3 and not x[:, 70:].any()
+assert torch.isfinite(a).all() and a.any() and (a.float() - b.float()).abs().max() < 0.1 and torch.isfinite(c).all() and c.any()
+assert (m.sum(1) - 8).abs().max() < 1e-3 and (sel == -1).sum() == 3 and (acc > 0).sum() == 3
+assert (back.float() - k.float()).abs().max() < 0.1 and not torch.equal(turned, k)
+print("ok")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
