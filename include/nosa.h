@@ -716,7 +716,7 @@ typedef struct {
  *            neither read nor written
  *   inverse  != 0: turns the other way, attention_factor as before: the gradient of the rotation
  * Angles are exact to 2^-24 of a half turn (and 2^-54 |p|, the table's own rounding), arithmetic is float32, the result
- * is rounded once.  Rows that begin at multiples of 16 bytes with r a multiple of 16 are fastest.
+ * is rounded once.  Rows that begin at multiples of 16 bytes are several times faster.
  * err_out (optional device int32, 4-byte aligned) gets bit 0 set when a count lies outside [0, n_tokens] (clamped);
  * it is not cleared.  Allocates nothing, keeps nothing of `table` or `views`; asynchronous on `stream`. */
 nosa_status nosa_rope(const nosa_rope_table* table, const nosa_rope_view* views, int n_views, int batch, int n_tokens,

@@ -25,7 +25,7 @@ struct RopeView {
   uint16_t* y;
   long long xs[3], ys[3];
   int heads, tokens, head_tiles;  // a tile's tokens; tiles of heads
-  int vec, same;                  // rows in whole 16-byte words; in place
+  int vec, same;                  // rows that begin at whole 16-byte words; in place
 };
 
 struct RopeArgs {
@@ -47,11 +47,35 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
   a = fmaf(x, c, -(b * s));
   b = fmaf(b, c, x * s);
 }
+// Sine and cosine of a fraction of 2^32 of a turn: the nearest quarter turn off, the Taylor series to the ninth and eighth power
+// on what is left, at most an eighth of a turn (the next terms are below 2^-25), in 22 instructions; sincospif takes about
+// twice as many, and one or two heads a token are then bound by them (2 heads of 65,536 tokens 38.6 us).
+__device__ __forceinline__ void turn_sincos(uint32_t turn, float& s, float& c) {
+  const uint32_t quarter = (turn + 0x20000000u) >> 30;
+  const float x = (float)(int32_t)(turn - (quarter << 30)) * 1.46291807926715968e-9f, x2 = x * x;  // 2 pi / 2^32
+  float a = fmaf(x2, 2.75573192e-6f, -1.98412698e-4f);  // 1 / 9!, 1 / 7!
+  a = fmaf(x2, a, 8.33333333e-3f);
+  a = fmaf(x2, a, -1.66666667e-1f);
+  a = fmaf(x2 * x, a, x);
+  float b = fmaf(x2, 2.48015873e-5f, -1.38888889e-3f);  // 1 / 8!, 1 / 6!
+  b = fmaf(x2, b, 4.16666667e-2f);
+  b = fmaf(x2, b, -0.5f);
+  b = fmaf(x2, b, 1.f);
+  s = quarter & 1 ? b : a;
+  c = quarter & 1 ? a : b;
+  if (quarter & 2) s = -s;
+  if ((quarter + 1) & 2) c = -c;
+}
 __device__ __forceinline__ float lo_float(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_float(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// kStaged: rows of whole words go through shared memory, for pairs half the rotated dims apart that do not lie in a thread's
+// words (the rotated dims are no multiple of 16).
+template <bool kStaged>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ __align__(16) float cosine[kRopeTokens][kRopePairs], sine[kRopeTokens][kRopePairs];
+  __shared__ __align__(16) uint16_t staged[kStaged ? kRopeRows : 1][kHeadDim + 8];
+  __shared__ uint64_t turn[kRopePairs];  // (a parameter that every lane reads at its own place is read lane by lane)
   pdl_wait();
   pdl_launch_dependents();
   const bool second = (int)blockIdx.x >= a.tiles0;
@@ -70,10 +94,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int rows = tokens * heads, part = threadIdx.x & 7;
   const uint16_t* xb = v.x + b * v.xs[0] + h0 * v.xs[1] + t0 * v.xs[2];
   uint16_t* yb = v.y + b * v.ys[0] + h0 * v.ys[1] + t0 * v.ys[2];
-  // whole words: a thread's 16 dims, eight pairs or what is copied, of rows r0, r0 + kRopeRows, ...
-  const bool turns = 16 * part < a.rot, idle = !v.vec || (!turns && v.same);
-  const int d0 = turns && !a.interleaved ? 8 * part : 16 * part;
-  const int d1 = turns && !a.interleaved ? d0 + pairs : d0 + 8;
+  // whole words: a thread's 16 dims, eight pairs (some of them, where the rotated dims end among interleaved ones) or what is
+  // copied, of rows r0, r0 + kRopeRows, ...
+  const bool turns = 16 * part < a.rot, idle = !v.vec || (!turns && v.same && !kStaged);
+  const bool apart = turns && !a.interleaved && !kStaged;
+  const int d0 = apart ? 8 * part : 16 * part, d1 = apart ? d0 + pairs : d0 + 8, mine = min(max(pairs - 8 * part, 0), 8);
   int r0 = threadIdx.x >> 3;
   uint4 x[kRopeFlight][2];
   auto load = [&]() {
@@ -87,12 +112,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     }
   };
   if (!idle) load();  // while the angles are computed
+  if (threadIdx.x < kRopePairs) turn[threadIdx.x] = a.turn[threadIdx.x];
+  __syncthreads();
   for (int k = threadIdx.x; k < tokens * kRopePairs; k += kRopeThreads) {
     const int t = k / kRopePairs, p = k % kRopePairs;
     if (p >= pairs) continue;
-    const uint64_t turns64 = (uint64_t)(p0 + t) * a.turn[p];
+    const uint64_t turns64 = (uint64_t)(p0 + t) * turn[p];
     float s, c;
-    sincospif((float)(int32_t)(uint32_t)(turns64 >> 32) * 0x1p-31f, &s, &c);
+    turn_sincos((uint32_t)(turns64 >> 32), s, c);
     if (a.inverse) s = -s;
     const int at = pair_place(p);
     cosine[t][at] = c * a.factor;
@@ -100,7 +127,55 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
   __syncthreads();
 
-  if (v.vec) {
+  if (kStaged && v.vec) {  // (a row's eight threads are in one warp; a thread rotates up to eight pairs, 8 part ..)
+    uint16_t* row = staged[kStaged ? threadIdx.x >> 3 : 0];
+    for (; r0 - (int)(threadIdx.x >> 3) < rows; r0 += kRopeRows * kRopeFlight, load()) {
+#pragma unroll
+      for (int k = 0; k < kRopeFlight; ++k) {
+        const int r = r0 + k * kRopeRows, t = r / heads;
+        const bool in = r < rows;
+        uint32_t w[4] = {}, z[4] = {};  // the first values of the pairs, and the second ones
+        if (in) {
+          *reinterpret_cast<uint4*>(row + d0) = x[k][0];
+          *reinterpret_cast<uint4*>(row + d1) = x[k][1];
+        }
+        __syncwarp();
+        if (in && mine > 0) {
+          const uint4 u = *reinterpret_cast<const uint4*>(row + 8 * part);
+          const uint32_t first[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // two pairs
+            const int at = (e & 2 ? 32 : 0) + 4 * part + 2 * (e & 1);
+            const float2 c = *reinterpret_cast<const float2*>(&cosine[t][at]), s = *reinterpret_cast<const float2*>(&sine[t][at]);
+            float f0 = lo_float(first[e]), f1 = bf16_to_float(row[pairs + 8 * part + 2 * e]);
+            float g0 = hi_float(first[e]), g1 = bf16_to_float(row[pairs + 8 * part + 2 * e + 1]);
+            rotate(f0, f1, c.x, s.x);
+            rotate(g0, g1, c.y, s.y);
+            w[e] = pack_bf16x2(f0, g0);
+            z[e] = pack_bf16x2(f1, g1);
+          }
+        }
+        __syncwarp();
+        if (in) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < mine) {
+              row[8 * part + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+              row[pairs + 8 * part + e] = (uint16_t)(z[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+        __syncwarp();
+        if (in) {
+          uint16_t* p = yb + r % heads * v.ys[1] + t * v.ys[2];
+          *reinterpret_cast<uint4*>(p + d0) = *reinterpret_cast<const uint4*>(row + d0);
+          *reinterpret_cast<uint4*>(p + d1) = *reinterpret_cast<const uint4*>(row + d1);
+        }
+        __syncwarp();
+      }
+    }
+    return;
+  }
+  if (!kStaged && v.vec) {
     if (idle) return;
     for (; r0 < rows; r0 += kRopeRows * kRopeFlight, load()) {
 #pragma unroll
@@ -120,7 +195,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
               for (int e = 0; e < 4; ++e) {
                 float f0 = lo_float(w[4 * q + e]), f1 = hi_float(w[4 * q + e]);
                 rotate(f0, f1, c[e], s[e]);
-                w[4 * q + e] = pack_bf16x2(f0, f1);
+                if (4 * q + e < mine) w[4 * q + e] = pack_bf16x2(f0, f1);
               }
             } else {
 #pragma unroll
@@ -225,7 +300,7 @@ extern "C" nosa_status nosa_rope(const nosa_rope_table* table, const nosa_rope_v
     RopeView& v = a.v[i];
     if (!w.x || !w.y || w.heads < 1 || off(w.x, 2) || off(w.y, 2)) return NOSA_ERR_INVALID_ARG;
     const long long extent[3] = {batch, w.heads, n_tokens};
-    bool same = w.x == w.y, whole = !off(w.x, 16) && !off(w.y, 16) && a.rot % 16 == 0;
+    bool same = w.x == w.y, whole = !off(w.x, 16) && !off(w.y, 16);
     for (int d = 0; d < 3; ++d) {
       if (extent[d] > 1) {
         if (w.x_stride[d] < 0 || w.y_stride[d] < kHeadDim) return NOSA_ERR_INVALID_ARG;
@@ -251,7 +326,8 @@ extern "C" nosa_status nosa_rope(const nosa_rope_table* table, const nosa_rope_v
     if (tiles >= (1ll << 31)) return NOSA_ERR_INVALID_ARG;
     if (i == 0) a.tiles0 = (int)tiles;
   }
-  const cudaError_t e = launch_ex(rope_kernel, dim3((unsigned)tiles), dim3(kRopeThreads), 0,
+  const bool staged = !a.interleaved && a.rot % 16 != 0;
+  const cudaError_t e = launch_ex(staged ? rope_kernel<true> : rope_kernel<false>, dim3((unsigned)tiles), dim3(kRopeThreads), 0,
                                   static_cast<cudaStream_t>(stream), true, 0, a);
   if (e == cudaSuccess) return NOSA_OK;
   (void)cudaGetLastError();
