@@ -586,9 +586,8 @@ nosa_status nosa_debug_quant_wait(long long cycles);
  *            table); a token's block is written to the lowest row that holds it.  NULL: row b holds block b
  * A call that writes a block's first token begins the block: its scales come from the new tokens alone, and rows
  * behind these hold nothing until they are written.  Otherwise the block keeps its scales, or takes larger ones
- * if the new tokens need them; then the codes c of all its other rows become e4m3(c s_old / s_new).  Each such step
- * halves s_old / s_new at least, so it rounds only codes whose values are below 2^-6 s_new.  Everything else
- * in the store is left as it was.
+ * if the new tokens need them; then the codes c of all its other rows become e4m3(c s_old / s_new), which rounds again
+ * only values that end below 2^-6 s_new.  Everything else in the store is left as it was.
  * err_out (optional device int32, 4-byte aligned) gets bit 0 set when a count lies outside [0, n_tokens] (clamped),
  * or a token's position is negative, at or behind 64 max_blocks (without slot_blk) or in a block that no row holds:
  * that token is not written.  It is not cleared.  Two calls that write the same block at the same time race.
@@ -620,8 +619,9 @@ nosa_status nosa_byte_read(const uint8_t* store, int units, int max_blocks, cons
  * A query that sees no token gets zeros; one with a value that is not finite, NaN.
  * The sums, the weights' among them, are float32.  q is exact but for values far below their row's largest: with up to 16
  * rows a unit those below 2^-22 of it, with more those below 2^-13, which are off by at most 2^-21 of it.
- * The weights exp(logit - reference) that multiply V are rounded to f16: 2^-11 relative each, 2^-35 of the row's
- * largest weight at least.  Logits of any size are fine: beyond float32 the largest takes all.
+ * The weights exp(logit - reference) that multiply V are rounded to f16: by 2^-11 of themselves, small ones by 2^-35 of
+ * the row's largest weight (2^-25 where logits are beyond 2^26).  Logits of any size are fine: beyond float32 the largest
+ * takes all.
  * Asynchronous on `stream`.  NOSA_ERR_CAPACITY if the scratch is too small. */
 nosa_status nosa_byte_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group, int n_queries,
                                    int max_blocks, const int32_t* lens, int max_len, float softmax_scale, uint16_t* out,

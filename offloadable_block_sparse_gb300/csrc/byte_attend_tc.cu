@@ -1,18 +1,24 @@
-// Attention over an 8-bit KV block store for 9 to 32 query rows a unit (several drafted tokens of a group of q heads): the same
+// Attention over an 8-bit KV block store for 17 to 32 query rows a unit (several drafted tokens of a group of q heads): the same
 // sums as byte_attend.cu on the fifth-generation tensor cores.
 //
-// With so many rows mma.sync spends its time on fragments: two products of 16 x 8 values each an instruction, and a warp's
-// operands, accumulators and weights do not fit its registers (32 rows: 961 instructions for 32 tokens, 91 us for 16 units
-// of 65,521 tokens).  Here a CTA of 128 threads takes a chunk of two blocks, and a thread is a token, or a dim:
-//   S (128 tokens x rows) = K . q^T    tcgen05 kind::f8f6f4: K's codes as they are, moved from the store's order into the
+// With so many rows mma.sync spends its time on fragments, and a warp's operands, accumulators and weights do not fit its
+// registers (32 rows of 16 units of 65,521 tokens: 961 instructions for 32 tokens, 91 us).  Here a CTA of 256 threads
+// takes a chunk of two blocks, 128 tokens; two threads, with half the rows each, are a token and later a dim:
+//   S (128 tokens x 2 x 32) = K . q^T   tcgen05 kind::f8f6f4: K's codes as they are, moved from the store's order into the
 //                                      128-byte swizzle; q as two e4m3 codes a value (its columns twice), exact to 2^-21 of
 //                                      the row's largest
-//   weights of the thread's token, all rows: as f16 into shared memory, their sums float32 in registers
-//   O^T (128 dims x rows) += s_V (V^T . P)   kind::f16: V's codes converted to f16 and transposed by stmatrix, one product per
-//                                      block, read back and added in float32 with the block's scale
-// Chunks overlap between the two CTAs of an SM, and within one the copy of the next chunk and the products with the rest.
-// Row references are the CTA's: a thread whose score would weigh more than 2^14 says so at the barrier before the second
-// product, and then all raise and weigh again.
+//   weights of the thread's token: as f16 into shared memory, their sums float32 in registers
+//   O^T (128 dims x 32) += s_V (V^T . P)   kind::f16: V's codes converted to f16 and transposed by stmatrix into their own
+//                                      place, one product per block, read back and added in float32 with the block's scale
+// The copies of the next chunk, the products with V and the next chunk's conversion overlap, and the two CTAs of an SM.  Row
+// references are the CTA's: a thread whose score would weigh more than 2^14 says so at the barrier before the second
+// product, and then all raise theirs and weigh again.
+//
+// 16 units of 65,521 tokens and 32 rows take 69.5 us against 40 of HBM (4,860 cycles a chunk and CTA, some 520 instructions a
+// warp at 1.8 an SM and cycle; tensor pipe 10 %, shared memory about 60 %): a chunk's chain of copies, products and barriers,
+// twice an SM.  64 units of 64 blocks 26.2 us (mma.sync 36.7), 256 of 32 43.5 (59.7), 2 of 32 10.1 (15.2).  With 16 rows
+// mma.sync is faster (54 against 69).  Tried without gain: tiles of V^T without a swizzle and one barrier fewer a chunk,
+// 128 threads (88 us with one stage; 88.5 with 256), the second product before the next chunk's conversion (82 with two stages).
 #include "byte_split.cuh"
 #include "host.h"
 #include "tc.cuh"

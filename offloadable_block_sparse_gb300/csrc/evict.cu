@@ -4,7 +4,9 @@
 // and writes the unit's table.  Rows are ordered by one 64-bit key (weight, then the block's number downwards), which a
 // radix selection takes eight bits at a time through a histogram in shared memory; for n = 1, the step of a full store,
 // a minimum does.  Counts are the only atomics, so the outcome does not depend on their order.  20 bytes a row: a call
-// is bound by its latency.
+// is bound by its latency, 2.3 us for 256 units of 128 rows of which one goes, 6.4 for 256 units of 1,025 of which three
+// quarters go (four rounds of the selection; counting a warp's equal digits before the histogram took 7.3), 34 for 256 of
+// 16,384.
 #include <algorithm>
 #include <mutex>
 
