@@ -554,8 +554,9 @@ nosa_status nosa_quant_attend(const uint16_t* q, const uint8_t* store, const int
 size_t nosa_quant_scratch_bytes(int units, int rows, int blocks);
 
 /* Test hook, as NOSA_F_TEST_ZERO_WAIT is for a context's calls: SM cycles that a wait for a staged tile may take in
- * the attention calls over 4-bit and 8-bit stores that this host thread makes from now on (negative: waits give up at once; 0: the built-in
- * limit, about a second, which is also the most).  Calls captured in a graph keep the limit of their capture. */
+ * the attention calls over 4-bit and 8-bit stores that this host thread makes from now on (negative: waits give up at
+ * once; 0: the built-in limit, about a second, which is also the most).  Calls captured in a graph keep the limit of their
+ * capture. */
 nosa_status nosa_debug_quant_wait(long long cycles);
 
 /* ------------------------------------------------------------ 8-bit KV block store
@@ -648,7 +649,7 @@ size_t nosa_byte_scratch_bytes(int units, int rows, int blocks, int mass);
  *      sink_blocks, the last window_blocks of the unit's ceil(lens / 64), those behind them, and next_block
  *   3. next_block, if no row holds it, takes the lowest empty row, with a_i = 0
  * acc, slot_blk   device float32, int32 [units][slots]: a_i, and the block of each row (negative: none); a block
- *                 has one row (of a block with several, all go or none)
+ *                 has one row (rows with the same block are as good as different ones: with equal a_i all go or none)
  * mass            device float32 [units][slots] (nosa_byte_attend's, with sel = slot_blk), or NULL: none
  * lens            device int32 [units]: tokens of each unit; may be NULL if window_blocks is 0
  * acc_out, slot_blk_out  as acc and slot_blk, which they may be (each its own; no other overlap)
@@ -704,13 +705,13 @@ nosa_status nosa_rope_make(const nosa_rope_config* cfg, nosa_rope_table* out);
 typedef struct {
   const uint16_t* x;  /* device bf16 */
   uint16_t* y;        /* device bf16; x itself with the same strides (in place), else no overlap */
-  int32_t heads;
+  int32_t heads;      /* 1 .. 2^20 */
   int32_t pad_;
   int64_t x_stride[3]; /* >= 0 */
   int64_t y_stride[3]; /* >= d where that extent is above 1 */
 } nosa_rope_view;
 
-/* Rotates one or two tensors (q and k of a layer) in one launch.
+/* Rotates one or two tensors (q and k of a layer) in one launch, of up to 2^30 tokens a sequence.
  *   pos      device int32 [batch]: position of each sequence's first token (NULL: 0 for all; any int32)
  *   count    device int32 [batch]: tokens of each sequence, 0 .. n_tokens (NULL: n_tokens); rows behind them are
  *            neither read nor written

@@ -262,7 +262,8 @@ extern "C" nosa_status nosa_rope_make(const nosa_rope_config* cfg, nosa_rope_tab
 extern "C" nosa_status nosa_rope(const nosa_rope_table* table, const nosa_rope_view* views, int n_views, int batch,
                                  int n_tokens, const int32_t* pos, const int32_t* count, int inverse, int32_t* err_out,
                                  void* stream) {
-  if (!table || !views || n_views < 1 || n_views > 2 || batch < 1 || n_tokens < 1) return NOSA_ERR_INVALID_ARG;
+  if (!table || !views || n_views < 1 || n_views > 2 || batch < 1 || n_tokens < 1 || n_tokens > (1 << 30))
+    return NOSA_ERR_INVALID_ARG;
   if (table->struct_size != sizeof(nosa_rope_table) || table->rot_dims < 2 || table->rot_dims > kHeadDim ||
       table->rot_dims % 2)
     return NOSA_ERR_INVALID_ARG;
@@ -282,7 +283,7 @@ extern "C" nosa_status nosa_rope(const nosa_rope_table* table, const nosa_rope_v
   for (int i = 0; i < n_views; ++i) {
     const nosa_rope_view& w = views[i];
     RopeView& v = a.v[i];
-    if (!w.x || !w.y || w.heads < 1 || off(w.x, 2) || off(w.y, 2)) return NOSA_ERR_INVALID_ARG;
+    if (!w.x || !w.y || w.heads < 1 || w.heads > (1 << 20) || off(w.x, 2) || off(w.y, 2)) return NOSA_ERR_INVALID_ARG;
     const long long extent[3] = {batch, w.heads, n_tokens};
     bool same = w.x == w.y, whole = !off(w.x, 16) && !off(w.y, 16);
     for (int d = 0; d < 3; ++d) {

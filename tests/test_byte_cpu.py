@@ -209,7 +209,9 @@ def test_evict_refusals(bad):
                                  dict(views=[_view(x_stride=(-1, 128, 128))]), dict(views=[_view(y_stride=(4096, 127, 128))]),
                                  dict(views=[_view(y_stride=(0, 1024, 128))]), dict(views=[_view(x_stride=(1 << 40, 1024, 128))]),
                                  dict(views=[_view(y=P, x_stride=(8192, 1024, 128))]),
-                                 dict(batch=2 ** 30, n_tokens=2 ** 30)])
+                                 dict(batch=2 ** 30, n_tokens=2 ** 30), dict(batch=1, n_tokens=2 ** 30 + 1),
+                                 dict(batch=1, n_tokens=2 ** 31 - 1), dict(views=[_view(heads=2 ** 20 + 1)]),
+                                 dict(views=[_view(), _view(heads=2 ** 31 - 1)])])
 def test_rope_refusals(bad):
     assert _rope(**bad) == N.NOSA_ERR_INVALID_ARG
 

@@ -103,6 +103,20 @@ def test_evict_protected_blocks_stay():
     _evict_check(acc, blk, None, [2 ** 31 - 1] * 2, 3, 0, 1, 1.0, [33554431, 33554431])
 
 
+def test_evict_rows_with_the_same_block():
+    rng = np.random.default_rng(7)
+    blk = rng.integers(-1, 40, (6, 200)).astype(np.int32)
+    acc = rng.permutation(1200).reshape(6, 200).astype(np.float32)
+    nxt = [int(blk[0].max()), 41, -1, 3, 44, int(blk[5, 5])]
+    for budget in (200, 199, 198, 90, 1):
+        _evict_check(acc, blk, None, [2560] * 6, budget, 1, 2, 0.5, nxt)
+    for budget in (3, 2):  # one or two rows have to go: of equal weights all three of block 9 do
+        b = torch.tensor([[4, 9, 9, 9]], dtype=torch.int32, device="cuda")
+        a = torch.ones(1, 4, device="cuda")
+        N.nosa_evict(a, b, None, 1, 4, None, budget, 0, 0, 1.0, a, b, stream=_stream())
+        assert b.tolist() == [[4, -1, -1, -1]] and a.tolist() == [[1, 0, 0, 0]]
+
+
 def test_evict_without_optional_outputs_and_many_units():
     rng = np.random.default_rng(5)
     units, slots = 3000, 40
