@@ -4,21 +4,20 @@
 // With so many rows mma.sync spends its time on fragments, and a warp's operands, accumulators and weights do not fit its
 // registers (32 rows of 16 units of 65,521 tokens: 961 instructions for 32 tokens, 91 us).  Here a CTA of 256 threads
 // takes a chunk of two blocks, 128 tokens; two threads, with half the rows each, are a token and later a dim:
-//   S (128 tokens x 2 x 32) = K . q^T   tcgen05 kind::f8f6f4: K's codes as they are, moved from the store's order into the
-//                                      128-byte swizzle; q as two e4m3 codes a value (its columns twice), exact to 2^-21 of
-//                                      the row's largest
+//   S (128 tokens x 2 x 32) = K . q^T   tcgen05 kind::f8f6f4: K's codes as they are, moved into tensor memory; q as two e4m3
+//                                      codes a value (its columns twice), exact to 2^-21 of the row's largest
 //   weights of the thread's token: as f16 into shared memory, their sums float32 in registers
-//   O^T (128 dims x 32) += s_V (V^T . P)   kind::f16: V's codes converted to f16 and transposed by stmatrix into their own
-//                                      place, one product per block, read back and added in float32 with the block's scale
-// The copies of the next chunk, the products with V and the next chunk's conversion overlap, and the two CTAs of an SM.  Row
-// references are the CTA's: a thread whose score would weigh more than 2^14 says so at the barrier before the second
-// product, and then all raise theirs and weigh again.
+//   O^T (128 dims x 32) += s_V (V^T . P)   kind::f16: V's codes converted to f16 and moved into tensor memory, one product per
+//                                      block, read back and added in float32 with the block's scale
+// The store's order is that of 8 x 4 words' fragments, which tcgen05.st 16x128b takes: both operands reach tensor memory
+// without a shuffle, and shared memory only sees the codes arrive and leave (with operands in its 128-byte swizzle, by plain
+// stores and stmatrix, 69.5 us where it is 62.8).  The copies of two chunks, the products with V and the next chunk's
+// conversion overlap, and the two CTAs of an SM.  Row references are the CTA's: a thread whose score would weigh more than
+// 2^14 says so at the barrier before the second product, and then all raise theirs and weigh again.
 //
-// 16 units of 65,521 tokens and 32 rows take 69.5 us against 40 of HBM (4,860 cycles a chunk and CTA, some 520 instructions a
-// warp at 1.8 an SM and cycle; tensor pipe 10 %, shared memory about 60 %): a chunk's chain of copies, products and barriers,
-// twice an SM.  64 units of 64 blocks 26.2 us (mma.sync 36.7), 256 of 32 43.5 (59.7), 2 of 32 10.1 (15.2).  With 16 rows
-// mma.sync is faster (54 against 69).  Tried without gain: tiles of V^T without a swizzle and one barrier fewer a chunk,
-// 128 threads (88 us with one stage; 88.5 with 256), the second product before the next chunk's conversion (82 with two stages).
+// 16 units of 65,521 tokens and 32 rows take 62.8 us against 40 of HBM: a chunk's chain of products and barriers, twice an
+// SM.  64 units of 64 blocks 23.8 us (mma.sync 36.7), 256 of 32 40.1 (59.7), 2 of 32 10.2 (15.2).  With 16 rows
+// mma.sync is faster.  Tried without gain: 128 threads (88 us with one stage; 88.5 with 256).
 #include "byte_split.cuh"
 #include "host.h"
 #include "tc.cuh"
@@ -28,18 +27,16 @@ namespace nosa {
 constexpr int kTcTokens = kTcChunkBlocks * kBlock;
 constexpr int kTcThreads = 256, NR = 32;  // (rows a unit at most)
 static_assert(2 * kTcTokens == kTcThreads && kTcTokens == kHeadDim, "two threads a token, and a dim");
-// shared memory: K (128 tokens x 128 codes), P (128 tokens x 64 f16, of which the rows' are used), q (rows twice x 128
-// codes), all in the 128-byte swizzle, and two stages, each the codes of a chunk's blocks as they arrive, and then in their
-// place V^T (128 dims x 64 f16 a block, swizzled)
-constexpr int kTcK = 0, kTcP = 16384, kTcQ = kTcP + 16384, kTcStage = kTcQ + 8192, kTcStageBytes = kTcChunkBlocks * kByteScales;
+// shared memory: P (128 tokens x 64 f16, of which the rows' are used) and q (rows twice x 128 codes), both in the 128-byte
+// swizzle, and two stages, each the codes of a chunk's blocks
+constexpr int kTcP = 0, kTcQ = kTcP + 16384, kTcStage = kTcQ + 8192, kTcStageBytes = kTcChunkBlocks * kByteScales;
 constexpr int kTcSmem = kTcStage + 2 * kTcStageBytes + 1024;
-static_assert(32 * kQaRowStride * 4 <= kTcQ, "the partial result takes the operands' place");
-static_assert(kByteScales == kHeadDim * kBlock * 2, "V^T in f16 takes a block's place");
-
-__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
-}
+static_assert(32 * kQaRowStride * 4 <= kTcStage, "the partial result takes the operands' place");
+// tensor memory: scores of both codes of q; a block's result twice; V^T of both blocks (128 dims x 64 f16 each); K (128 tokens
+// x 128 codes)
+constexpr uint32_t kTcO = 2 * NR, kTcV = kTcO + kTcChunkBlocks * NR, kTcK = kTcV + kTcChunkBlocks * kBlock / 2;
+constexpr uint32_t kTcCols = 256;
+static_assert(kTcK + kHeadDim / 4 <= kTcCols, "two CTAs share an SM's 512 columns");
 
 // The unit's query rows as operands: row r's codes in rows r (the values') and NR + r (16 times what these leave) of sq, and
 // the factors that turn its scores into logits in base 2 for a K scale of 1.  A warp takes every eighth row, a lane four
@@ -70,7 +67,7 @@ __device__ __forceinline__ void load_tc_queries(const ByteArgs& a, int u, unsign
       hi |= c << (16 * k);
       lo |= to_codes((v[2 * k] - got.x) * 16.f, (v[2 * k + 1] - got.y) * 16.f) << (16 * k);
     }
-    const int at = 16 * ((lane >> 2) ^ (row & 7)) + 4 * (lane & 3);  // (NR is a multiple of 8)
+    const int at = 16 * ((lane & 7) ^ (row & 7)) + 4 * (lane >> 3);  // K's order of dims (NR is a multiple of 8)
     *reinterpret_cast<uint32_t*>(sq + row * 128 + at) = hi;
     *reinterpret_cast<uint32_t*>(sq + (NR + row) * 128 + at) = lo;
     if (lane == 0) {
@@ -80,31 +77,32 @@ __device__ __forceinline__ void load_tc_queries(const ByteArgs& a, int u, unsign
   }
 }
 
-// A warp moves a tile's K codes from the store's order into the swizzle: row by row of 128 bytes, 16-byte pieces of 16 dims.
-__device__ __forceinline__ void place_keys(unsigned char* sk, const unsigned char* tile, int token0, int lane) {
-  uint4 k[4];
+// A warp moves a tile's K codes into tensor memory: lane i of its 16 is token i, column 16 c + 4 w + t the codes of dims
+// 32 t + 16 c + 4 w .. + 3.
+__device__ __forceinline__ void place_keys(uint32_t tk, const unsigned char* tile, int lane) {
+  uint32_t k[16];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)  // 8 tokens' half, half of 32 dims
-    k[i] = *reinterpret_cast<const uint4*>(tile + 512 * i + 16 * lane);
-  const int g = lane >> 2, q = lane & 3;
+  for (int c = 0; c < 2; ++c)
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<uint4*>(sk + (token0 + 8 * (i >> 1) + g) * 128 + 16 * ((2 * q + (i & 1)) ^ g)) = k[i];
+    for (int h = 0; h < 2; ++h) {  // tokens g + 8 h
+      const uint4 x = *reinterpret_cast<const uint4*>(tile + 1024 * h + 512 * c + 16 * lane);
+      k[8 * c + h] = x.x, k[8 * c + 2 + h] = x.y, k[8 * c + 4 + h] = x.z, k[8 * c + 6 + h] = x.w;
+    }
+  tc::st_rows16(tk, k);
 }
 
-// A warp converts a tile's V codes to f16 and writes them transposed: dim 16 g + e is row 8 e + g, tokens in pieces of 8.
-__device__ __forceinline__ void place_values(uint32_t sv, const uint4 (&v)[4], int piece, int lane) {
-  const int g = lane & 7, m = lane >> 3;  // the address a lane gives: row g of matrix m
+// A warp converts its quarter of the dims of a block's V codes to f16 and moves them, transposed, into tensor memory:
+// lane 8 k + g of the quarter q is dim 16 g + 4 q + k, a column two tokens.
+__device__ __forceinline__ void place_values(uint32_t tv, const uint4 (&v)[kByteTiles]) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t f[2][4];  // [half][dim 4 c + ..]: tokens 2t + 8 half, + 1
-    codes_to_half2(v[c].x, f[0][0], f[0][1]);
-    codes_to_half2(v[c].z, f[0][2], f[0][3]);
-    codes_to_half2(v[c].y, f[1][0], f[1][1]);
-    codes_to_half2(v[c].w, f[1][2], f[1][3]);
+  for (int i = 0; i < 2; ++i) {  // dims 4 q + 2 i, + 1
+    uint32_t f[16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      stmatrix_x4(sv + (8 * (4 * c + m) + g) * 128 + 16 * ((piece + h) ^ g), f[h][0], f[h][1], f[h][2], f[h][3]);
+    for (int tile = 0; tile < kByteTiles; ++tile) {
+      codes_to_half2(i ? v[tile].z : v[tile].x, f[4 * tile], f[4 * tile + 1]);
+      codes_to_half2(i ? v[tile].w : v[tile].y, f[4 * tile + 2], f[4 * tile + 3]);
+    }
+    tc::st_rows16(tv + ((uint32_t)(16 * i) << 16), f);
   }
 }
 
@@ -138,7 +136,7 @@ __device__ __forceinline__ void read4(float (&v)[4], const float* p) {
 
 __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __grid_constant__ ByteArgs a) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bar_raw, bar_s, bar_o;  // a chunk's copies, its scores, its products with V
+  __shared__ __align__(8) uint64_t bar_raw[2], bar_s, bar_o;  // a stage's copies, a chunk's scores, its products with V
   __shared__ __align__(16) float scales[2][kTcChunkBlocks][4];  // [stage][block]: s_K, s_V
   __shared__ int4 list[kQaList];
   __shared__ int scan[32], found[2];
@@ -149,13 +147,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   __shared__ uint32_t poison[NR][4];
   __shared__ float2 merged[NR], final[NR];
   constexpr int R = NR / 2;           // a thread's rows
-  constexpr uint32_t kCols = 4 * NR;  // scores of both codes, and a block's result twice
   constexpr uint32_t idS = tc::plain_idesc(128, 2 * NR, 0), idO = tc::plain_idesc(128, NR, 1);
   unsigned char* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset, so that it stays a shared-memory address)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quarter = warp & 3, r0 = warp >> 2 ? R : 0, at = 32 * quarter + lane;  // the thread's rows, token and dim's place
   if (tid == 0) {
-    mbar_init(&bar_raw, 1);
+    mbar_init(&bar_raw[0], 1);
+    mbar_init(&bar_raw[1], 1);
     mbar_init(&bar_s, 1);
     mbar_init(&bar_o, 1);
     fence_mbar_init();
@@ -165,13 +163,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   pdl_launch_dependents();
   ByteShare share = byte_share(a, kTcChunkBlocks, scan, found);
   if (share.todo == 0) return;
-  if (warp == 0) tc::alloc(&tbase, kCols);
+  if (warp == 0) tc::alloc(&tbase, kTcCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tm = tbase, trow = tm + ((uint32_t)(32 * quarter) << 16) + r0, sa = smem_u32(sm);
+  const uint32_t tm = tbase, tlane = tm + ((uint32_t)(32 * quarter) << 16), trow = tlane + r0, sa = smem_u32(sm);
 
-  int ph_raw = 0, ph_s = 0, ph_o = 0, st = 0;  // the barriers' phases, and the stage of the chunk in work
+  int ph_raw = 0, ph_s = 0, ph_o = 0, st = 0;  // the barriers' phases (a bit a stage), and the stage of the chunk in work
   bool late = false;
   while (share.todo > 0) {
     const int u = share.u;
@@ -195,7 +193,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
       ph_o ^= 1;
       uint32_t d[kTcChunkBlocks][R];
 #pragma unroll
-      for (int b = 0; b < kTcChunkBlocks; ++b) tc::ld16(trow + 2 * NR + b * NR, d[b]);
+      for (int b = 0; b < kTcChunkBlocks; ++b) tc::ld16(trow + kTcO + b * NR, d[b]);
       tc::wait_ld();
 #pragma unroll
       for (int b = 0; b < kTcChunkBlocks; ++b) tc::landed(d[b]);
@@ -220,14 +218,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
       // scales, 4 + b the later one's.
       auto issue = [&](int c, int to, int later) {
         const int m = min(n - kTcChunkBlocks * c, kTcChunkBlocks);
-        if (lane == 0 && m > 0) mbar_arrive_expect_tx(&bar_raw, m * (kByteScales + 16));
+        if (lane == 0 && m > 0) mbar_arrive_expect_tx(&bar_raw[to], m * (kByteScales + 16));
         __syncwarp();
         const int j = kTcChunkBlocks * (lane < 4 ? c : later) + (lane & 1);
         if (lane < 6 && j < n) {
           const uint8_t* src = base + (size_t)(a.sel ? list[j].x : b0 + j) * kByteBlockBytes;
           if (lane < 4)
             bulk_copy_g2s(lane < 2 ? sa + kTcStage + to * kTcStageBytes + lane * kByteScales : smem_u32(scales[to][lane & 1]),
-                          lane < 2 ? src : src + kByteScales, lane < 2 ? kByteScales : 16, &bar_raw);
+                          lane < 2 ? src : src + kByteScales, lane < 2 ? kByteScales : 16, &bar_raw[to]);
           else
             bulk_prefetch(src, kByteScales + 16);
         }
@@ -235,23 +233,27 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
       };
       // tokens of the context from block j (of the list) on
       auto left_of = [&](int j) { return j >= n ? 0 : a.sel ? list[j].y : seg.len - (b0 + j) * kBlock; };
-      if (chunks > 0 && warp == 2) issue(0, st, 1);
+      if (chunks > 0 && warp == 2) {
+        issue(0, st, 2);
+        issue(1, st ^ 1, n);
+      }
       if (b0 == seg.first) {  // while the first chunk arrives
         load_tc_queries(a, u, sm + kTcQ, alpha, warp, lane);
         __syncthreads();
       }
       for (int c = 0; c < chunks; ++c) {
-        late |= !__all_sync(0xffffffffu, stage_wait(&bar_raw, ph_raw, a.wait_limit));
-        ph_raw ^= 1;
-        // a warp takes one of the chunk's eight tiles: K into its operand's place, V into registers
-        const int b_tile = warp >> 2, tile = warp & 3;
-        unsigned char* codes = sm + kTcStage + st * kTcStageBytes + b_tile * kByteScales + tile * kByteTile;
-        const int left = left_of(kTcChunkBlocks * c + b_tile) - kByteTileTokens * tile;
+        auto wait_raw = [&](int stage) {
+          late |= !__all_sync(0xffffffffu, stage_wait(&bar_raw[stage], ph_raw >> stage & 1, a.wait_limit));
+          ph_raw ^= 1 << stage;
+        };
+        wait_raw(st);
+        // a warp takes one of the chunk's eight tiles, whose tokens are its lanes: of K all, of V what must not be looked at
+        const int own = 2 * quarter + (warp >> 2), half = warp >> 2;
+        unsigned char* stage = sm + kTcStage + st * kTcStageBytes;
+        unsigned char* codes = stage + own / kByteTiles * kByteScales + own % kByteTiles * kByteTile;
+        const int left = left_of(kTcChunkBlocks * c + own / kByteTiles) - kByteTileTokens * (own % kByteTiles);
         if (left - (a.nq - 1) < kByteTileTokens) clear_byte_tail(codes, poison, left, a.nq, a.rows, lane);
-        place_keys(sm + kTcK, codes, kByteTileTokens * warp, lane);
-        uint4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(codes + kByteV + 512 * i + 16 * lane);
+        place_keys(tlane + ((uint32_t)(16 * half) << 16) + kTcK, codes, lane);
         float scale[kTcChunkBlocks];  // V's
 #pragma unroll
         for (int b = 0; b < kTcChunkBlocks; ++b) {
@@ -260,24 +262,31 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           scale[b] = s.y;
           if (tid >= b * NR && tid < (b + 1) * NR) factor[b][tid - b * NR] = logit_factor(alpha[tid - b * NR], s.x);
         }
-        fence_proxy_async_smem();  // K (generic stores) is read by the tensor core
+        tc::wait_st();
+        fence_proxy_async_smem();  // q (generic stores) is read by the tensor core
         tc::fence_before();
         late = __syncthreads_or(late);
         tc::fence_after();
-        if (late) break;
+        if (late) {
+          if (c + 1 < chunks) wait_raw(st ^ 1);  // it is in flight
+          break;
+        }
         if (tid == 0) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 dims each
-            tc::mma_f8(tm, tc::sw128_desc(sa + kTcK + 32 * k), tc::sw128_desc(sa + kTcQ + 32 * k), idS, k > 0);
+            tc::mma_f8_ta(tm, tm + kTcK + 8 * k, tc::sw128_desc(sa + kTcQ + 32 * k), idS, k > 0);
           tc::commit(&bar_s);
         }
         __syncwarp();
-        // V^T over the codes, which all warps have read
-        place_values(sa + kTcStage + st * kTcStageBytes + b_tile * kByteScales, v, 2 * tile, lane);
-        if (flying) add_products();  // then the other stage and P are free too
+        // a quarter of the dims of block `half` of V
+        uint4 v[kByteTiles];
+#pragma unroll
+        for (int i = 0; i < kByteTiles; ++i)
+          v[i] = *reinterpret_cast<const uint4*>(stage + half * kByteScales + i * kByteTile + kByteV + 512 * quarter + 16 * lane);
+        if (flying) add_products();  // then V^T's place and P are free
+        place_values(tlane + kTcV + half * (kBlock / 2), v);
 #pragma unroll
         for (int b = 0; b < kTcChunkBlocks; ++b) sv[b] = scale[b];
-        if (warp == 2) issue(c + 1, st ^ 1, c + 2);
 
         // the thread's token: the logits of its rows
         const int block = at / kBlock, j = kTcChunkBlocks * c + block, mine = left_of(j) - at % kBlock;  // rows of query tokens from nq - mine on see it
@@ -357,7 +366,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           for (int i = 0; i < R / 8; ++i)
             *reinterpret_cast<uint4*>(sm + kTcP + at * 128 + 16 * ((r0 / 8 + i) ^ (at & 7))) =
                 make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-          fence_proxy_async_smem();  // P and V^T are read by the tensor core
+          tc::wait_st();             // V^T
+          fence_proxy_async_smem();  // P is read by the tensor core
           tc::fence_before();
           const bool raise = __syncthreads_or(over > kTopWeight);
           tc::fence_after();
@@ -368,11 +378,11 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           for (int b = 0; b < kTcChunkBlocks; ++b)
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // 16 tokens each
-              tc::mma_f16(tm + 2 * NR + b * NR, tc::sw128_desc(sa + kTcStage + st * kTcStageBytes + b * kByteScales + 32 * k),
-                          tc::sw128_desc_mn(sa + kTcP + b * 8192 + 2048 * k, 16384), idO, k > 0);
+              tc::mma_f16_ta(tm + kTcO + b * NR, tm + kTcV + b * (kBlock / 2) + 8 * k, tc::sw128_desc_mn(sa + kTcP + b * 8192 + 2048 * k, 16384), idO, k > 0);
           tc::commit(&bar_o);
         }
         __syncwarp();
+        if (warp == 2) issue(c + 2, st, c + 3);  // all have read the stage
 #pragma unroll
         for (int r = 0; r < R; ++r) l[r] += y[r];
         if (a.mass && j < n) {  // a warp's tokens are half a block
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == 0) tc::dealloc(tm, kCols);
+  if (warp == 0) tc::dealloc(tm, kTcCols);
 }
 
 // Two CTAs share an SM by registers, shared memory and tensor-memory columns.  (The occupancy query counts one for any kernel
