@@ -149,13 +149,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   constexpr int R = NR / 2;           // a thread's rows
   constexpr uint32_t idS = tc::plain_idesc(128, 2 * NR, 0), idO = tc::plain_idesc(128, NR, 1);
   unsigned char* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset, so that it stays a shared-memory address)
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int quarter = warp & 3, r0 = warp >> 2 ? R : 0, at = 32 * quarter + lane;  // the thread's rows, token and dim's place
   if (tid == 0) {
-    mbar_init(&bar_raw[0], 1);
-    mbar_init(&bar_raw[1], 1);
+    mbar_init(&bar_raw[0], kTcChunkBlocks);
+    mbar_init(&bar_raw[1], kTcChunkBlocks);
     mbar_init(&bar_s, 1);
-    mbar_init(&bar_o, 1);
+    mbar_init(&bar_o, 2);
     fence_mbar_init();
   }
   __syncthreads();
@@ -214,29 +214,27 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
         n = 0;
       }
       const int chunks = late ? 0 : (n + 1) / kTcChunkBlocks;
-      // One warp: the copies of chunk c into stage `to`, and a later chunk's way into L2; lanes b and 2 + b block b's codes and
-      // scales, 4 + b the later one's.
+      // The copies of chunk c into stage `to`, and a later chunk's way into L2: a warp a block each, as such an instruction takes
+      // a warp some hundred cycles, and six lanes of one warp take one after the other.
       auto issue = [&](int c, int to, int later) {
-        const int m = min(n - kTcChunkBlocks * c, kTcChunkBlocks);
-        if (lane == 0 && m > 0) mbar_arrive_expect_tx(&bar_raw[to], m * (kByteScales + 16));
-        __syncwarp();
-        const int j = kTcChunkBlocks * (lane < 4 ? c : later) + (lane & 1);
-        if (lane < 6 && j < n) {
-          const uint8_t* src = base + (size_t)(a.sel ? list[j].x : b0 + j) * kByteBlockBytes;
-          if (lane < 4)
-            bulk_copy_g2s(lane < 2 ? sa + kTcStage + to * kTcStageBytes + lane * kByteScales : smem_u32(scales[to][lane & 1]),
-                          lane < 2 ? src : src + kByteScales, lane < 2 ? kByteScales : 16, &bar_raw[to]);
-          else
-            bulk_prefetch(src, kByteScales + 16);
+        const bool copy = warp == 1 || warp == 2, prefetch = warp == 6 || warp == 7;
+        if (!(copy ? c < chunks : prefetch && later < chunks) || !tc::elect()) return;
+        const int b = copy ? warp - 1 : warp - 6, j = kTcChunkBlocks * (copy ? c : later) + b;
+        const uint8_t* src = base + (j < n ? (size_t)(a.sel ? list[j].x : b0 + j) * kByteBlockBytes : 0);
+        if (prefetch) {
+          if (j < n) bulk_prefetch(src, kByteScales + 16);
+        } else if (j < n) {
+          mbar_arrive_expect_tx(&bar_raw[to], kByteScales + 16);
+          bulk_copy_g2s(sa + kTcStage + to * kTcStageBytes + b * kByteScales, src, kByteScales, &bar_raw[to]);
+          bulk_copy_g2s(smem_u32(scales[to][b]), src + kByteScales, 16, &bar_raw[to]);
+        } else {
+          mbar_arrive(&bar_raw[to]);
         }
-        __syncwarp();
       };
       // tokens of the context from block j (of the list) on
       auto left_of = [&](int j) { return j >= n ? 0 : a.sel ? list[j].y : seg.len - (b0 + j) * kBlock; };
-      if (chunks > 0 && warp == 2) {
-        issue(0, st, 2);
-        issue(1, st ^ 1, n);
-      }
+      issue(0, st, 2);
+      issue(1, st ^ 1, chunks);
       if (b0 == seg.first) {  // while the first chunk arrives
         load_tc_queries(a, u, sm + kTcQ, alpha, warp, lane);
         __syncthreads();
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           if (c + 1 < chunks) wait_raw(st ^ 1);  // it is in flight
           break;
         }
-        if (tid == 0) {
+        if (warp == 0 && tc::elect()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // 32 dims each
             tc::mma_f8_ta(tm, tm + kTcK + 8 * k, tc::sw128_desc(sa + kTcQ + 32 * k), idS, k > 0);
@@ -373,16 +371,18 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           tc::fence_after();
           if (!raise || pass) break;
         }
-        if (tid == kTcThreads / 2) {
-#pragma unroll
-          for (int b = 0; b < kTcChunkBlocks; ++b)
+        if ((warp == 3 || warp == 5) && tc::elect()) {
+          const int b = warp == 5;
+          {
 #pragma unroll
             for (int k = 0; k < 4; ++k)  // 16 tokens each
               tc::mma_f16_ta(tm + kTcO + b * NR, tm + kTcV + b * (kBlock / 2) + 8 * k, tc::sw128_desc_mn(sa + kTcP + b * 8192 + 2048 * k, 16384), idO, k > 0);
+          }
           tc::commit(&bar_o);
         }
         __syncwarp();
-        if (warp == 2) issue(c + 2, st, c + 3);  // all have read the stage
+        issue(c + 2, st, c + 3);  // all have read the stage
+        __syncwarp();
 #pragma unroll
         for (int r = 0; r < R; ++r) l[r] += y[r];
         if (a.mass && j < n) {  // a warp's tokens are half a block

@@ -81,6 +81,14 @@ __device__ __forceinline__ void mma_f8_ta(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
+// True in one thread of the (whole) warp, which the compiler then knows to be one: with a comparison of the thread's index
+// instead it lets each instruction above look for its threads.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
 // The mbarrier receives one arrival when every MMA this thread issued before has completed.
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(
