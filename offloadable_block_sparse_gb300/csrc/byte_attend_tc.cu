@@ -42,13 +42,14 @@ static_assert(kTcK + kHeadDim / 4 <= kTcCols, "two CTAs share an SM's 512 column
 // the factors that turn its scores into logits in base 2 for a K scale of 1.  A warp takes every eighth row, a lane four
 // dims.  The largest magnitude of a row is brought into [2^7, 2^8), so that bf16's eight bits are two codes of four down to
 // 2^-13 of it.
-__device__ __forceinline__ void load_tc_queries(const ByteArgs& a, int u, unsigned char* sq, float* alpha, int warp, int lane) {
-  uint2 x[NR / 8];
+__device__ __forceinline__ void load_tc_queries(uint2 (&x)[NR / 8], const ByteArgs& a, int u, int warp, int lane) {
 #pragma unroll
   for (int i = 0; i < NR / 8; ++i) {
     const int row = warp + 8 * i;
     x[i] = row < a.rows ? *reinterpret_cast<const uint2*>(a.q + ((size_t)u * a.rows + row) * kHeadDim + 4 * lane) : make_uint2(0, 0);
   }
+}
+__device__ __forceinline__ void place_tc_queries(const uint2 (&x)[NR / 8], const ByteArgs& a, unsigned char* sq, float* alpha, int warp, int lane) {
 #pragma unroll
   for (int i = 0; i < NR / 8; ++i) {
     const int row = warp + 8 * i;
@@ -158,15 +159,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
     mbar_init(&bar_o, 2);
     fence_mbar_init();
   }
-  __syncthreads();
-  pdl_wait();
-  pdl_launch_dependents();
-  ByteShare share = byte_share(a, kTcChunkBlocks, scan, found);
-  if (share.todo == 0) return;
   if (warp == 0) tc::alloc(&tbase, kTcCols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  pdl_wait();
+  pdl_launch_dependents();
+  ByteShare share = byte_share(a, kTcChunkBlocks, scan, found);
   const uint32_t tm = tbase, tlane = tm + ((uint32_t)(32 * quarter) << 16), trow = tlane + r0, sa = smem_u32(sm);
 
   int ph_raw = 0, ph_s = 0, ph_o = 0, st = 0;  // the barriers' phases (a bit a stage), and the stage of the chunk in work
@@ -203,6 +202,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
         for (int r = 0; r < R; ++r) o[r] = fmaf(__uint_as_float(d[b][r]), sv[b], o[r]);
     };
 
+    uint2 q[NR / 8];
+    load_tc_queries(q, a, u, warp, lane);
     const int batch = a.sel ? kQaList : max(seg.end - seg.first, 1);
     const uint8_t* base = a.store + (size_t)u * a.max_blocks * kByteBlockBytes;
     for (int b0 = seg.first; b0 < seg.end || b0 == seg.first; b0 += batch) {
@@ -214,29 +215,26 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
         n = 0;
       }
       const int chunks = late ? 0 : (n + 1) / kTcChunkBlocks;
-      // The copies of chunk c into stage `to`, and a later chunk's way into L2: a warp a block each, as such an instruction takes
-      // a warp some hundred cycles, and six lanes of one warp take one after the other.
-      auto issue = [&](int c, int to, int later) {
-        const bool copy = warp == 1 || warp == 2, prefetch = warp == 6 || warp == 7;
-        if (!(copy ? c < chunks : prefetch && later < chunks) || !tc::elect()) return;
-        const int b = copy ? warp - 1 : warp - 6, j = kTcChunkBlocks * (copy ? c : later) + b;
-        const uint8_t* src = base + (j < n ? (size_t)(a.sel ? list[j].x : b0 + j) * kByteBlockBytes : 0);
-        if (prefetch) {
-          if (j < n) bulk_prefetch(src, kByteScales + 16);
-        } else if (j < n) {
-          mbar_arrive_expect_tx(&bar_raw[to], kByteScales + 16);
-          bulk_copy_g2s(sa + kTcStage + to * kTcStageBytes + b * kByteScales, src, kByteScales, &bar_raw[to]);
-          bulk_copy_g2s(smem_u32(scales[to][b]), src + kByteScales, 16, &bar_raw[to]);
-        } else {
+      // The copies of chunk c into stage `to`: a warp a block, as such an instruction takes a warp a hundred cycles or more, and
+      // several lanes of a warp take them one after the other.
+      auto issue = [&](int c, int to) {
+        if (c >= chunks || !(warp == 1 || warp == 2) || !tc::elect()) return;
+        const int b = warp - 1, j = kTcChunkBlocks * c + b;
+        if (j >= n) {
           mbar_arrive(&bar_raw[to]);
+          return;
         }
+        const uint8_t* src = base + (size_t)(a.sel ? list[j].x : b0 + j) * kByteBlockBytes;
+        mbar_arrive_expect_tx(&bar_raw[to], kByteScales + 16);
+        bulk_copy_g2s(sa + kTcStage + to * kTcStageBytes + b * kByteScales, src, kByteScales, &bar_raw[to]);
+        bulk_copy_g2s(smem_u32(scales[to][b]), src + kByteScales, 16, &bar_raw[to]);
       };
       // tokens of the context from block j (of the list) on
       auto left_of = [&](int j) { return j >= n ? 0 : a.sel ? list[j].y : seg.len - (b0 + j) * kBlock; };
-      issue(0, st, 2);
-      issue(1, st ^ 1, chunks);
+      issue(0, st);
+      issue(1, st ^ 1);
       if (b0 == seg.first) {  // while the first chunk arrives
-        load_tc_queries(a, u, sm + kTcQ, alpha, warp, lane);
+        place_tc_queries(q, a, sm + kTcQ, alpha, warp, lane);
         __syncthreads();
       }
       for (int c = 0; c < chunks; ++c) {
@@ -276,12 +274,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           tc::commit(&bar_s);
         }
         __syncwarp();
+        if (flying) add_products();  // then V^T's place and P are free
         // a quarter of the dims of block `half` of V
         uint4 v[kByteTiles];
 #pragma unroll
         for (int i = 0; i < kByteTiles; ++i)
           v[i] = *reinterpret_cast<const uint4*>(stage + half * kByteScales + i * kByteTile + kByteV + 512 * quarter + 16 * lane);
-        if (flying) add_products();  // then V^T's place and P are free
         place_values(tlane + kTcV + half * (kBlock / 2), v);
 #pragma unroll
         for (int b = 0; b < kTcChunkBlocks; ++b) sv[b] = scale[b];
@@ -381,7 +379,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           tc::commit(&bar_o);
         }
         __syncwarp();
-        issue(c + 2, st, c + 3);  // all have read the stage
+        issue(c + 2, st);  // all have read the stage
         __syncwarp();
 #pragma unroll
         for (int r = 0; r < R; ++r) l[r] += y[r];
