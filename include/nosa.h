@@ -618,7 +618,7 @@ nosa_status nosa_byte_read(const uint8_t* store, int units, int max_blocks, cons
  *   scratch  device memory of at least nosa_byte_scratch_bytes(units, group * n_queries, ceil(max_len / 64), mass != NULL)
  *            bytes, 256-byte aligned, its first 4 bytes as for nosa_quant_dense_attend
  * A query that sees no token gets zeros; one with a value that is not finite, NaN.
- * The sums, the weights' among them, are float32.  q is exact but for values far below their row's largest: with up to 16
+ * The sums, the weights' among them, are float32.  q is exact but for values far below their row's largest: with up to 8
  * rows a unit those below 2^-22 of it, with more those below 2^-13, which are off by at most 2^-21 of it.
  * The weights exp(logit - reference) that multiply V are rounded to f16: by 2^-11 of themselves, small ones by 2^-35 of
  * the row's largest weight (2^-25 where logits are beyond 2^26).  Logits of any size are fine: beyond float32 the largest

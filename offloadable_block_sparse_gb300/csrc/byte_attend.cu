@@ -32,6 +32,7 @@ namespace nosa {
 constexpr int kHalfTokens = 32, kHalfBytes = 2 * kByteTile;
 constexpr int kHalfStage = kHalfBytes + 128;  // a stage: half a block and, behind it, the block's scales
 constexpr int kWarps = kByteThreads / 32, kStages = 2, kCtasPerSm = 2;
+constexpr int kByteRows = 8;  // query rows a unit at most
 constexpr int kMassThreads = 128;
 
 // Eight query rows as MMA operands: of row g, dims 32 t + 16 c + 4 w .. + 3 in [4 c + w].
@@ -39,12 +40,12 @@ struct ByteQuery {
   uint32_t b[8][2];
 };
 
-// Rows 8 nt + g of q, scaled by a power of two that brings the row's largest magnitude into [2^9, 2^10) (bf16 values
+// Row g of q, scaled by a power of two that brings the row's largest magnitude into [2^9, 2^10) (bf16 values
 // down to 2^-22 of it stay exact in f16).  alpha: the factors that turn rows 2t, 2t + 1 of q . c into logits in base 2
 // for a K scale of 1.
-__device__ __forceinline__ void load_byte_query(ByteQuery& Q, float (&alpha)[2], const uint16_t* q, int row, int rows,
-                                                int lane, float scale) {
-  const int t = lane & 3;
+__device__ __forceinline__ void load_byte_query(ByteQuery& Q, float (&alpha)[2], const uint16_t* q, int rows, int lane,
+                                                float scale) {
+  const int row = lane >> 2, t = lane & 3;
   uint4 x[4];
   uint32_t big = 0;  // the largest magnitude's bf16 bits
 #pragma unroll
@@ -76,13 +77,7 @@ __device__ __forceinline__ void load_byte_query(ByteQuery& Q, float (&alpha)[2],
   }
 }
 
-// The query side in shared memory, for two row tiles (registers hold it for one).
-struct ByteQueryShared {
-  uint4 b[4][32];  // [two operands][lane]
-  float2 alpha[32];
-};
-
-// A warp's running state for a tile of 8 rows: of rows 2t, 2t + 1 the reference (a logit in base 2), the lane's part of the softmax sum, and O^T:
+// A warp's running state: of rows 2t, 2t + 1 the reference (a logit in base 2), the lane's part of the softmax sum, and O^T:
 // dims 16 g + 2 j and + 1 of those rows.
 struct ByteRows {
   float top[2], l[2];
@@ -91,12 +86,10 @@ struct ByteRows {
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// One half block for all row tiles: both tiles of tokens at once, so that their chains of dependent operations overlap.
+// One half block: both tiles of tokens at once, so that their chains of dependent operations overlap.
 // left: tokens of the context from its first on; mass: where its sums go, or null.
-template <int NT>
-__device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery& Q, const float (&alpha)[2],
-                                             const ByteQueryShared* qs, unsigned char* stage, uint32_t (*poison)[4], int left,
-                                             int rows, int nq, float2* mass, int lane) {
+__device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, const float (&alpha)[2], unsigned char* stage,
+                                             uint32_t (*poison)[4], int left, int rows, int nq, float2* mass, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const bool tail = left - (nq - 1) < kHalfTokens;  // some row does not see the whole half
   if (tail) {
@@ -104,7 +97,7 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
     clear_byte_tail(stage + kByteTile, poison, left - kByteTileTokens, nq, rows, lane);
   }
   const float2 s = *reinterpret_cast<const float2*>(stage + kHalfBytes);  // s_K, s_V
-  float z[2][NT][4];
+  float z[2][4];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     uint4 k[2][2];
@@ -115,100 +108,79 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
         k[i][h] = *reinterpret_cast<const uint4*>(stage + i * kByteTile + 1024 * h + 512 * c + 16 * lane);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      uint32_t f[2][4];
+      const uint32_t b0 = Q.b[4 * c + w][0], b1 = Q.b[4 * c + w][1];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        codes_to_half2(word_of(k[i][0], w), f[i][0], f[i][2]);
-        codes_to_half2(word_of(k[i][1], w), f[i][1], f[i][3]);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint2 b;
-        if constexpr (NT == 1)
-          b = make_uint2(Q.b[4 * c + w][0], Q.b[4 * c + w][1]);
+        uint32_t f[4];
+        codes_to_half2(word_of(k[i][0], w), f[0], f[2]);
+        codes_to_half2(word_of(k[i][1], w), f[1], f[3]);
+        if (c == 0 && w == 0)
+          mma_f16_first(z[i], f[0], f[1], f[2], f[3], b0, b1);
         else
-          b = *(reinterpret_cast<const uint2*>(&qs[nt].b[2 * c + (w >> 1)][lane]) + (w & 1));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (c == 0 && w == 0)
-            mma_f16_first(z[i][nt], f[i][0], f[i][1], f[i][2], f[i][3], b.x, b.y);
-          else
-            mma_f16(z[i][nt], f[i][0], f[i][1], f[i][2], f[i][3], b.x, b.y);
-        }
+          mma_f16(z[i], f[0], f[1], f[2], f[3], b0, b1);
       }
     }
   }
   // logits, and whether a row's best would weigh more than its reference allows
-  float best[NT][2];
+  float best[2];
   bool raise = false;
+  const float f0 = logit_factor(alpha[0], s.x), f1 = logit_factor(alpha[1], s.x);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const float2 al = NT == 1 ? make_float2(alpha[0], alpha[1]) : qs[nt].alpha[lane];
-    const float f0 = logit_factor(al.x, s.x), f1 = logit_factor(al.y, s.x);
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        z[i][nt][e] *= e & 1 ? f1 : f0;
-        if (tail) {
-          const int row = 8 * nt + 2 * t + (e & 1), token = kByteTileTokens * i + g + 8 * (e >> 1);
-          if (row >= rows || token >= left - (nq - 1) + row % nq) z[i][nt][e] = -INFINITY;
-        }
+    for (int e = 0; e < 4; ++e) {
+      z[i][e] *= e & 1 ? f1 : f0;
+      if (tail) {
+        const int row = 2 * t + (e & 1), token = kByteTileTokens * i + g + 8 * (e >> 1);
+        if (row >= rows || token >= left - (nq - 1) + row % nq) z[i][e] = -INFINITY;
       }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      best[nt][e] = fmaxf(fmaxf(z[0][nt][e], z[0][nt][e + 2]), fmaxf(z[1][nt][e], z[1][nt][e + 2]));
-      raise |= best[nt][e] - A[nt].top[e] > kTopWeight;
     }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    best[e] = fmaxf(fmaxf(z[0][e], z[0][e + 2]), fmaxf(z[1][e], z[1][e + 2]));
+    raise |= best[e] - A.top[e] > kTopWeight;
   }
   if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int e = 0; e < 2; ++e) {
+      float b = best[e];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float b = best[nt][e];
+      for (int o = 4; o < 32; o <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+      if (b - A.top[e] > kTopWeight) {  // the row's lanes agree; rows differ
+        const float top = reference(b), f = ex2(A.top[e] - top);
+        A.top[e] = top;
+        A.l[e] *= f;
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-        if (b - A[nt].top[e] > kTopWeight) {  // the row's lanes agree; rows differ
-          const float top = reference(b), f = ex2(A[nt].top[e] - top);
-          A[nt].top[e] = top;
-          A[nt].l[e] *= f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            A[nt].o[j][e] *= f;
-            A[nt].o[j][e + 2] *= f;
-          }
+        for (int j = 0; j < 8; ++j) {
+          A.o[j][e] *= f;
+          A.o[j][e + 2] *= f;
         }
       }
+    }
   }
   // weights of tokens g, g + 8 and rows 2t, 2t + 1; as f16, transposed: of row g and token pairs t, t + 4
-  uint32_t p[2][NT][2];
+  uint32_t p[2][2];
+  float sum[2] = {0.f, 0.f};
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float sum[2] = {0.f, 0.f};
+  for (int i = 0; i < 2; ++i) {
+    float w[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        w[e] = ex2(z[i][nt][e] - A[nt].top[e & 1]);
-        sum[e & 1] += w[e];
-      }
-      p[i][nt][0] = movmatrix_trans(pack_half2(w[0], w[1]));
-      p[i][nt][1] = movmatrix_trans(pack_half2(w[2], w[3]));
+    for (int e = 0; e < 4; ++e) {
+      w[e] = ex2(z[i][e] - A.top[e & 1]);
+      sum[e & 1] += w[e];
     }
-    A[nt].l[0] += sum[0];
-    A[nt].l[1] += sum[1];
-    if (mass) {
+    p[i][0] = movmatrix_trans(pack_half2(w[0], w[1]));
+    p[i][1] = movmatrix_trans(pack_half2(w[2], w[3]));
+  }
+  A.l[0] += sum[0];
+  A.l[1] += sum[1];
+  if (mass) {
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
-        sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
-      }
-      const int row = 8 * nt + 2 * t;
-      if (g == 0 && row < rows)
-        *reinterpret_cast<float4*>(mass + row) = make_float4(A[nt].top[0], sum[0], A[nt].top[1], sum[1]);
+    for (int o = 4; o < 32; o <<= 1) {
+      sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+      sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
     }
+    if (g == 0 && 2 * t < rows) *reinterpret_cast<float4*>(mass + 2 * t) = make_float4(A.top[0], sum[0], A.top[1], sum[1]);
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -217,20 +189,19 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
     for (int i = 0; i < 2; ++i) v[i] = *reinterpret_cast<const uint4*>(stage + i * kByteTile + kByteV + 512 * c + 16 * lane);
 #pragma unroll
     for (int jj = 0; jj < 2; ++jj) {
-      uint32_t f[2][4];
+      float d[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        codes_to_half2(jj ? v[i].z : v[i].x, f[i][0], f[i][1]);
-        codes_to_half2(jj ? v[i].w : v[i].y, f[i][2], f[i][3]);
+        uint32_t f[4];
+        codes_to_half2(jj ? v[i].z : v[i].x, f[0], f[1]);
+        codes_to_half2(jj ? v[i].w : v[i].y, f[2], f[3]);
+        if (i == 0)
+          mma_f16_first(d, f[0], f[1], f[2], f[3], p[0][0], p[0][1]);
+        else
+          mma_f16(d, f[0], f[1], f[2], f[3], p[1][0], p[1][1]);
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float d[4];
-        mma_f16_first(d, f[0][0], f[0][1], f[0][2], f[0][3], p[0][nt][0], p[0][nt][1]);
-        mma_f16(d, f[1][0], f[1][1], f[1][2], f[1][3], p[1][nt][0], p[1][nt][1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) A[nt].o[2 * c + jj][e] = fmaf(d[e], s.y, A[nt].o[2 * c + jj][e]);
-      }
+      for (int e = 0; e < 4; ++e) A.o[2 * c + jj][e] = fmaf(d[e], s.y, A.o[2 * c + jj][e]);
     }
   }
 }
@@ -238,19 +209,18 @@ __device__ __forceinline__ void process_half(ByteRows (&A)[NT], const ByteQuery&
 // Two CTAs an SM by shared memory: a third left 512 units of 64 blocks a round that was nearly empty (102 us against 85).
 // Two stages a warp: with three, HBM is slower (256 units of 512 blocks 331 us against 307), with one 364.
 constexpr int kByteSmem = 80 * 1024, kRingBytes = kWarps * kStages * kHalfStage;
-static_assert(kRingBytes + 2 * (int)sizeof(ByteQueryShared) <= kByteSmem && kWarps * 16 * kQaRowStride * 4 <= kRingBytes, "");
+static_assert(kRingBytes <= kByteSmem && kWarps * kByteRows * kQaRowStride * 4 <= kRingBytes, "");
 
-template <int NT>
 __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(const __grid_constant__ ByteArgs a) {
-  // the warps' rings, then [warp][8 NT rows][kQaRowStride], their partials; behind them the query operands
+  // the warps' rings, then [warp][row][kQaRowStride], their partials
   extern __shared__ __align__(128) float smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ int4 list[kQaList];
-  __shared__ float wr[kWarps][8 * NT], wl[kWarps][8 * NT];
+  __shared__ float wr[kWarps][kByteRows], wl[kWarps][kByteRows];
   __shared__ int scan[32], found[2];
-  __shared__ uint32_t poison[8 * NT][4];  // [row]: dims that end as NaN
-  __shared__ float2 merged[8 * NT];       // a cluster CTA's references and sums
-  __shared__ float2 final[8 * NT];        // the unit's, for its masses
+  __shared__ uint32_t poison[kByteRows][4];  // [row]: dims that end as NaN
+  __shared__ float2 merged[kByteRows];       // a cluster CTA's references and sums
+  __shared__ float2 final[kByteRows];        // the unit's, for its masses
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (lane == 0) {
 #pragma unroll
@@ -263,18 +233,17 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
   ByteShare share = byte_share(a, kWarps / 2, scan, found);
 
   unsigned char* ring = reinterpret_cast<unsigned char*>(smem) + warp * kStages * kHalfStage;
-  ByteQueryShared* qs = reinterpret_cast<ByteQueryShared*>(reinterpret_cast<unsigned char*>(smem) + kRingBytes);
   int in = 0, out = 0, phase = 0;  // the ring's next stage to fill and to use, and that one's phase
   bool late = false;
   while (share.todo > 0) {
     const int u = share.u;
     const ByteSegment seg = next_segment(a, share);
     if (a.nq > 1) {
-      if (threadIdx.x < 32 * NT) poison[threadIdx.x >> 2][threadIdx.x & 3] = 0;
+      if (threadIdx.x < 4 * kByteRows) poison[threadIdx.x >> 2][threadIdx.x & 3] = 0;
       __syncthreads();
     }
     ByteQuery Q;
-    ByteRows A[NT];
+    ByteRows A;
     float alpha[2];
 
     // The blocks, listed ones looked up kQaList at a time and those without a token left out.  Warp w takes half
@@ -308,23 +277,11 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
 #pragma unroll
       for (int i = 0; i < kStages; ++i) issue();
       if (b0 == seg.first) {  // while the first stages arrive
+        load_byte_query(Q, alpha, a.q + (size_t)u * a.rows * kHeadDim, a.rows, lane, a.scale);
+        A.top[0] = A.top[1] = kNoRef;
+        A.l[0] = A.l[1] = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (NT == 1 || warp == nt) {
-            load_byte_query(Q, alpha, a.q + (size_t)u * a.rows * kHeadDim, 8 * nt + g, a.rows, lane, a.scale);
-            if (NT > 1) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                qs[nt].b[i][lane] = make_uint4(Q.b[2 * i][0], Q.b[2 * i][1], Q.b[2 * i + 1][0], Q.b[2 * i + 1][1]);
-              qs[nt].alpha[lane] = make_float2(alpha[0], alpha[1]);
-            }
-          }
-          A[nt].top[0] = A[nt].top[1] = kNoRef;
-          A[nt].l[0] = A[nt].l[1] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) A[nt].o[j][0] = A[nt].o[j][1] = A[nt].o[j][2] = A[nt].o[j][3] = 0.f;
-        }
-        if (NT > 1) __syncthreads();
+        for (int j = 0; j < 8; ++j) A.o[j][0] = A.o[j][1] = A.o[j][2] = A.o[j][3] = 0.f;
       }
       for (int done = 0; done < started; ++done) {
         late |= !__all_sync(0xffffffffu, stage_wait(&bars[warp][out], phase, a.wait_limit));
@@ -333,7 +290,7 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
           const int left = (a.sel ? list[j].y : seg.len - (b0 + j) * kBlock) - half * kHalfTokens;
           float2* mass = nullptr;
           if (a.mass) mass = a.half + (((size_t)u * a.blocks + (a.sel ? list[j].z : b0 + j)) * 2 + half) * a.mass_rows;
-          process_half<NT>(A, Q, alpha, qs, ring + out * kHalfStage, poison, left, a.rows, a.nq, mass, lane);
+          process_half(A, Q, alpha, ring + out * kHalfStage, poison, left, a.rows, a.nq, mass, lane);
           __syncwarp();  // the stage is read
           issue();
         }
@@ -343,31 +300,27 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
     }
     if (late) {  // a wait gave up: poison the outputs
       if (lane == 0) atomicOr(a.err, kErrTimeout);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) A[nt].l[0] = A[nt].l[1] = __int_as_float(0x7fc00000);
+      A.l[0] = A.l[1] = __int_as_float(0x7fc00000);
     }
     __syncthreads();  // the rings become the warps' partials
 
     // the warp's partial: of rows 2t, 2t + 1, dims 16 g .. + 15
+    float* w = smem + (warp * kByteRows + 2 * t) * kQaRowStride + 16 * g;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float* w = smem + (warp * 8 * NT + 8 * nt + 2 * t) * kQaRowStride + 16 * g;
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<float4*>(w + i * kQaRowStride + 4 * j) =
+            make_float4(A.o[2 * j][i], A.o[2 * j][i + 2], A.o[2 * j + 1][i], A.o[2 * j + 1][i + 2]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<float4*>(w + i * kQaRowStride + 4 * j) = make_float4(
-              A[nt].o[2 * j][i], A[nt].o[2 * j][i + 2], A[nt].o[2 * j + 1][i], A[nt].o[2 * j + 1][i + 2]);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) A[nt].l[i] += __shfl_xor_sync(0xffffffffu, A[nt].l[i], o);
-        if (g == 0) {
-          wr[warp][8 * nt + 2 * t + i] = A[nt].top[i];
-          wl[warp][8 * nt + 2 * t + i] = A[nt].l[i];
-        }
+      for (int o = 4; o < 32; o <<= 1) A.l[i] += __shfl_xor_sync(0xffffffffu, A.l[i], o);
+      if (g == 0) {
+        wr[warp][2 * t + i] = A.top[i];
+        wl[warp][2 * t + i] = A.l[i];
       }
     }
     __syncthreads();
-    finish_segment<kWarps, 8 * NT>(a, share, seg, smem, wr, wl, poison, merged, final);
+    finish_segment<kWarps, kByteRows>(a, share, seg, smem, wr, wl, poison, merged, final);
     if (share.todo > 0) {
       fence_proxy_async_smem();  // the next segment's copies come after these reads and writes
       __syncthreads();
@@ -423,17 +376,16 @@ __global__ void __launch_bounds__(kMassThreads) byte_mass_kernel(const __grid_co
 // What the launches need of a device, looked up once (a call costs more in look-ups than in launching otherwise).
 struct ByteDevice {
   int sms;
-  int wave[3];  // CTAs that are resident at once: of this kernel's forms for 8 and 16 rows, of byte_attend_tc.cu's for 32
+  int wave[2];  // CTAs that are resident at once: of this kernel, of byte_attend_tc.cu's
 };
 static std::mutex g_byte_mutex;
 static ByteDevice g_byte_device[64] = {};
 
-template <int NT>
 static cudaError_t set_up_byte_attend(int sms, int* wave) {
   int ctas = 0;
-  cudaError_t e = cudaFuncSetAttribute(byte_attend_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kByteSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(byte_attend_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, byte_attend_kernel<NT>, kByteThreads, kByteSmem);
+  cudaError_t e = cudaFuncSetAttribute(byte_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kByteSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(byte_attend_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, byte_attend_kernel, kByteThreads, kByteSmem);
   if (e == cudaSuccess && ctas < 1) e = cudaErrorInvalidConfiguration;
   *wave = std::min(ctas, 8) * sms;
   return e;
@@ -450,8 +402,7 @@ static bool byte_device(ByteDevice* out) {
   if (!d.sms) {
     ByteDevice n = {};
     if (cudaDeviceGetAttribute(&n.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n.sms < 1 ||
-        set_up_byte_attend<1>(n.sms, &n.wave[0]) != cudaSuccess || set_up_byte_attend<2>(n.sms, &n.wave[1]) != cudaSuccess ||
-        set_up_byte_attend_tc(n.sms, &n.wave[2]) != cudaSuccess) {
+        set_up_byte_attend(n.sms, &n.wave[0]) != cudaSuccess || set_up_byte_attend_tc(n.sms, &n.wave[1]) != cudaSuccess) {
       (void)cudaGetLastError();
       return false;
     }
@@ -478,12 +429,12 @@ static size_t byte_parts_bytes(size_t units, size_t parts, int rows, size_t bloc
 // What a call wants for its scratch: enough for pieces whether it takes them or not, so that more units, rows or blocks never
 // want less, and a scratch made for the largest call serves them all.
 static size_t byte_bytes(const ByteDevice& d, int units, int rows, int blocks, bool mass) {
-  const int wave = std::max({d.wave[0], d.wave[1], d.wave[2]});
+  const int wave = std::max(d.wave[0], d.wave[1]);
   return byte_parts_bytes(units, (size_t)wave + units, rows, blocks, mass);
 }
 
 // The fewest blocks that keep a CTA of the kernel for so many rows busy: half a block a warp, or a chunk.
-static int byte_step(int rows) { return rows <= 16 ? kWarps / 2 : kTcChunkBlocks; }
+static int byte_step(int rows) { return rows <= kByteRows ? kWarps / 2 : kTcChunkBlocks; }
 
 // The largest power of two of CTAs per unit, `most` at most, that fits all units into one wave and leaves each something to do.
 static int byte_cluster_size(int units, int blocks, int wave, int step, int most) {
@@ -512,7 +463,7 @@ static int byte_cluster_size(int units, int blocks, int wave, int step, int most
 // So clusters where they fill most of a wave and the units are not long (listed blocks balance, lengths may not), and for
 // small calls; pieces otherwise.
 static BytePlan byte_plan(const ByteDevice& d, int units, int rows, int blocks, bool listed) {
-  const int wave = d.wave[rows <= 8 ? 0 : rows <= 16 ? 1 : 2], rounds = (units + wave - 1) / wave, step = byte_step(rows);
+  const int wave = d.wave[rows > kByteRows], rounds = (units + wave - 1) / wave, step = byte_step(rows);
   if (units > kQaSplitUnits || (units > wave && (long long)(rounds * wave - units) * blocks <= 24ll * units))
     return {kWhole, units, 0};
   const int cl = byte_cluster_size(units, blocks, wave, step, 32 * units <= wave ? 16 : 8);
@@ -537,9 +488,9 @@ static nosa_status byte_attend(ByteArgs& a, void* scratch, size_t scratch_bytes,
   a.total = reinterpret_cast<float2*>(a.part + (plan.split == kPieces ? parts * a.rows * kHeadDim : 0));
   a.stats = a.total + (size_t)a.units * a.rows;
   a.meta = reinterpret_cast<int2*>(a.stats + (plan.split == kPieces ? parts * a.rows : 0));
-  cudaError_t e = a.rows > 16 ? launch_byte_attend_tc(a, plan.ctas, plan.cluster, st)
-                              : launch_ex(a.rows <= 8 ? byte_attend_kernel<1> : byte_attend_kernel<2>, dim3((unsigned)plan.ctas),
-                                          dim3(kByteThreads), kByteSmem, st, true, plan.cluster, a);
+  cudaError_t e = a.rows > kByteRows ? launch_byte_attend_tc(a, plan.ctas, plan.cluster, st)
+                                     : launch_ex(byte_attend_kernel, dim3((unsigned)plan.ctas), dim3(kByteThreads), kByteSmem,
+                                                 st, true, plan.cluster, a);
   if (e == cudaSuccess && plan.split == kPieces)
     e = launch_ex(byte_merge_kernel, dim3((unsigned)(a.units * a.rows)), dim3(kMergeWarps * 32), 0, st, true, 0, a);
   if (e == cudaSuccess && plan.split == kPieces && a.mass)

@@ -25,7 +25,7 @@
 namespace nosa {
 
 constexpr int kTcTokens = kTcChunkBlocks * kBlock;
-constexpr int kTcThreads = 256, NR = 32;  // (rows a unit at most)
+constexpr int kTcThreads = 256;
 static_assert(2 * kTcTokens == kTcThreads && kTcTokens == kHeadDim, "two threads a token, and a dim");
 // shared memory: P (128 tokens x 64 f16, of which the rows' are used) and q (rows twice x 128 codes), both in the 128-byte
 // swizzle, and two stages, each the codes of a chunk's blocks
@@ -34,14 +34,14 @@ constexpr int kTcSmem = kTcStage + 2 * kTcStageBytes + 1024;
 static_assert(32 * kQaRowStride * 4 <= kTcStage, "the partial result takes the operands' place");
 // tensor memory: scores of both codes of q; a block's result twice; V^T of both blocks (128 dims x 64 f16 each); K (128 tokens
 // x 128 codes)
-constexpr uint32_t kTcO = 2 * NR, kTcV = kTcO + kTcChunkBlocks * NR, kTcK = kTcV + kTcChunkBlocks * kBlock / 2;
-constexpr uint32_t kTcCols = 256;
-static_assert(kTcK + kHeadDim / 4 <= kTcCols, "two CTAs share an SM's 512 columns");
+constexpr uint32_t kTcO = 64, kTcV = 128, kTcK = kTcV + kTcChunkBlocks * kBlock / 2, kTcCols = 256;
+static_assert(kTcChunkBlocks == 2 && kTcK + kHeadDim / 4 <= kTcCols, "two CTAs share an SM's 512 columns");
 
 // The unit's query rows as operands: row r's codes in rows r (the values') and NR + r (16 times what these leave) of sq, and
 // the factors that turn its scores into logits in base 2 for a K scale of 1.  A warp takes every eighth row, a lane four
 // dims.  The largest magnitude of a row is brought into [2^7, 2^8), so that bf16's eight bits are two codes of four down to
 // 2^-13 of it.
+template <int NR>
 __device__ __forceinline__ void load_tc_queries(uint2 (&x)[NR / 8], const ByteArgs& a, int u, int warp, int lane) {
 #pragma unroll
   for (int i = 0; i < NR / 8; ++i) {
@@ -49,7 +49,9 @@ __device__ __forceinline__ void load_tc_queries(uint2 (&x)[NR / 8], const ByteAr
     x[i] = row < a.rows ? *reinterpret_cast<const uint2*>(a.q + ((size_t)u * a.rows + row) * kHeadDim + 4 * lane) : make_uint2(0, 0);
   }
 }
-__device__ __forceinline__ void place_tc_queries(const uint2 (&x)[NR / 8], const ByteArgs& a, unsigned char* sq, float* alpha, int warp, int lane) {
+template <int NR>
+__device__ __forceinline__ void place_tc_queries(const uint2 (&x)[NR / 8], const ByteArgs& a, unsigned char* sq, float* alpha,
+                                                 int warp, int lane) {
 #pragma unroll
   for (int i = 0; i < NR / 8; ++i) {
     const int row = warp + 8 * i;
@@ -135,6 +137,8 @@ __device__ __forceinline__ void read4(float (&v)[4], const float* p) {
   v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
 }
 
+// NR: rows a unit at most, 16 or 32.
+template <int NR>
 __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __grid_constant__ ByteArgs a) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bar_raw[2], bar_s, bar_o;  // a stage's copies, a chunk's scores, its products with V
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
       ph_o ^= 1;
       uint32_t d[kTcChunkBlocks][R];
 #pragma unroll
-      for (int b = 0; b < kTcChunkBlocks; ++b) tc::ld16(trow + kTcO + b * NR, d[b]);
+      for (int b = 0; b < kTcChunkBlocks; ++b) tc::ld(trow + kTcO + b * NR, d[b]);
       tc::wait_ld();
 #pragma unroll
       for (int b = 0; b < kTcChunkBlocks; ++b) tc::landed(d[b]);
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
     };
 
     uint2 q[NR / 8];
-    load_tc_queries(q, a, u, warp, lane);
+    load_tc_queries<NR>(q, a, u, warp, lane);
     const int batch = a.sel ? kQaList : max(seg.end - seg.first, 1);
     const uint8_t* base = a.store + (size_t)u * a.max_blocks * kByteBlockBytes;
     for (int b0 = seg.first; b0 < seg.end || b0 == seg.first; b0 += batch) {
@@ -234,7 +238,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
       issue(0, st);
       issue(1, st ^ 1);
       if (b0 == seg.first) {  // while the first chunk arrives
-        place_tc_queries(q, a, sm + kTcQ, alpha, warp, lane);
+        place_tc_queries<NR>(q, a, sm + kTcQ, alpha, warp, lane);
         __syncthreads();
       }
       for (int c = 0; c < chunks; ++c) {
@@ -293,8 +297,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
 #pragma unroll 1
         for (int pass = 0;; ++pass) {
           uint32_t d[R], e[R];
-          tc::ld16(trow, d);
-          tc::ld16(trow + NR, e);
+          tc::ld(trow, d);
+          tc::ld(trow + NR, e);
           tc::wait_ld();
           tc::landed(d);
           tc::landed(e);
@@ -423,19 +427,26 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   if (warp == 0) tc::dealloc(tm, kTcCols);
 }
 
-// Two CTAs share an SM by registers, shared memory and tensor-memory columns.  (The occupancy query counts one for any kernel
-// that allocates tensor memory, whatever its shared memory.)
-cudaError_t set_up_byte_attend_tc(int sms, int* wave) {
-  cudaError_t e = cudaFuncSetAttribute(byte_attend_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(byte_attend_tc_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+template <int NR>
+static cudaError_t set_up_tc() {
+  cudaError_t e = cudaFuncSetAttribute(byte_attend_tc_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(byte_attend_tc_kernel<NR>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(byte_attend_tc_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-  *wave = 2 * sms;
+    e = cudaFuncSetAttribute(byte_attend_tc_kernel<NR>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   return e;
 }
 
+// Two CTAs share an SM by registers, shared memory and tensor-memory columns.  (The occupancy query counts one for any kernel
+// that allocates tensor memory, whatever its shared memory.)
+cudaError_t set_up_byte_attend_tc(int sms, int* wave) {
+  *wave = 2 * sms;
+  const cudaError_t e = set_up_tc<16>();
+  return e == cudaSuccess ? set_up_tc<32>() : e;
+}
+
 cudaError_t launch_byte_attend_tc(const ByteArgs& a, int ctas, int cluster, cudaStream_t st) {
-  return launch_ex(byte_attend_tc_kernel, dim3((unsigned)ctas), dim3(kTcThreads), kTcSmem, st, true, cluster, a);
+  return launch_ex(a.rows <= 16 ? byte_attend_tc_kernel<16> : byte_attend_tc_kernel<32>, dim3((unsigned)ctas), dim3(kTcThreads),
+                   kTcSmem, st, true, cluster, a);
 }
 
 }  // namespace nosa

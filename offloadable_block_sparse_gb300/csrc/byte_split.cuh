@@ -1,4 +1,4 @@
-// What the two attention kernels over an 8-bit store share (byte_attend.cu: up to 16 query rows a unit, byte_attend_tc.cu: up
+// What the two attention kernels over an 8-bit store share (byte_attend.cu: up to 8 query rows a unit, byte_attend_tc.cu: up
 // to 32): their arguments, how CTAs share the units' blocks, the lists of blocks, and what becomes of a CTA's part of a
 // unit's result.
 #pragma once
@@ -305,7 +305,7 @@ __device__ __forceinline__ void finish_segment(const ByteArgs& a, ByteShare& s, 
   s.at = 0;
 }
 
-// In byte_attend_tc.cu: the kernel for 17 to 32 rows a unit, its set-up (and how many of its CTAs are resident at once).
+// In byte_attend_tc.cu: the kernel for 9 to 32 rows a unit, its set-up (and how many of its CTAs are resident at once).
 cudaError_t launch_byte_attend_tc(const ByteArgs& a, int ctas, int cluster, cudaStream_t st);
 cudaError_t set_up_byte_attend_tc(int sms, int* wave);
 constexpr int kTcChunkBlocks = 2;  // blocks that it takes at a time

@@ -227,8 +227,8 @@ def _expect(q, k, v, at, length, nq, scale):
     """The oracle's result and masses of one unit, and how far the kernels' may be from them.
 
     With p_t a row's weights, o its result and S_t = scale sum |q| |k_t|: a logit is a float32 sum and a few products, in
-    some twenty steps of 2^-24 at most of S_t, taken as 2^-18 S_t, and with more than 16 rows small values of q are off
-    by 2^-21 of the row's largest, Q: 2^-21 Q scale sum |k_t|; it moves a weight by as much, relative.  A weight that
+    some twenty steps of 2^-24 at most of S_t, taken as 2^-18 S_t, and with more than 8 rows small values of q are off
+    by 2^-21 of the row's largest, Q (two e4m3 codes a value): 2^-21 Q scale sum |k_t|; it moves a weight by as much, relative.  A weight that
     multiplies V is rounded to f16, 2^-11, or is off by 2^-35 of the row's largest where it is small.  These are
     independent from token to token: with e_t the sum of both, V = sum (p_t e_t v_t)^2 + (p_t 2^-18 S_t o)^2 is at
     least three times the error's variance, so six roots of V is more than ten standard deviations, and more than the
@@ -247,7 +247,7 @@ def _expect(q, k, v, at, length, nq, scale):
         p = np.exp(z - z.max())
         p /= p.sum()
         d = 2.0 ** -18 * (np.abs(kk[see]) @ np.abs(q[r])) * scale
-        if q.shape[0] > 16:
+        if q.shape[0] > 8:
             d += 2.0 ** -21 * np.abs(q[r]).max() * np.abs(kk[see]).sum(1) * scale
         x, o = vv[see], out[r]
         var = ((p * (2.0 ** -11 + d))[:, None] * x) ** 2 + ((p * d)[:, None] * o) ** 2
