@@ -3,12 +3,11 @@
 // With codes c and one scale each for a block's K and V, the scores are s_K (q . c_t) and a block adds
 // s_V sum_t p_t c_t to the result: e4m3 codes are exact in f16, two in a conversion, so they go to mma.sync m16n8k16 with f16
 // operands and float32 accumulators, and the scales are one float32 factor each per block.  (mma.sync takes e4m3 too, at 7.9
-// cycles an MMA with new operands against 2.7 of f16; with at most 16 rows a unit tcgen05's tiles, which byte_attend_tc.cu
-// uses for more, are mostly empty.)
+// cycles an MMA with new operands against 2.7 of f16.)  For up to 8 query rows a unit; byte_attend_tc.cu, on tcgen05, takes
+// more.
 //
 // As for the 4-bit store, CTAs share the units' blocks in equal pieces, or a cluster of CTAs takes a unit (byte_plan), and a
-// warp takes half a block (two tiles of 16 tokens) at a time through a ring of its own of bulk copies.  Per half block
-// and 8 query rows:
+// warp takes half a block (two tiles of 16 tokens) at a time through a ring of its own of bulk copies.  Per half block:
 //   S^T (2 x 16 tokens x 8 rows) = K codes . q^T       16 MMAs in two chains
 //   P^T by movmatrix of the f16-packed weights
 //   O^T (128 dims x 8 rows) += s_V (V codes^T . P^T)    16 MMAs into fresh accumulators, 32 FMAs: results stay in true
@@ -20,7 +19,7 @@
 // Bound by HBM where a call is long: 256 units of 32,768 tokens and 4 rows (2.15 GB) in 306 us, 1.05 of measured HBM (a copy);
 // ragged 198 us, 1.01.  437 instructions a half block, of which 128 conversions and 32 MMAs, leave the issue slots two
 // thirds empty.  Shorter calls pay for their start and end: 256 units listing 81 blocks 57.4 us, 0.89, with the masses of 128
-// 90 us, 0.89.  16 rows: 16 units of 65,536 tokens 54 us, 0.74.
+// 90 us, 0.89.
 #include <algorithm>
 #include <mutex>
 
@@ -449,17 +448,17 @@ static int byte_cluster_size(int units, int blocks, int wave, int step, int most
 //    9.6 with 8.
 //  * equal pieces of all units' blocks over one wave, merged by a second kernel (3 to 5).
 //  * one CTA per unit, where they are more than a wave and the last round is not too empty for their length.
-// 4 or 8 rows a unit:          cluster   whole   pieces        17 to 32 rows:   cluster   whole   pieces
-//    2 units of 64 blocks         6.8               7.6           2 of 32          10.9               11.4
-//    8 units of 256              14.6              12.8           8 of 64          14.4               16.1
-//   16 units of 64                9.6               9.7          16 of 64          17.4               18.4
-//   16 units of 256              21.7              15.2          16 of 256         43.4               29.2
-//   32 units of 64               10.2              13.4          32 of 64          19.0               27.7
-//   64 units of 64               14.0              17.3          64 of 64          27.7               36.9
+// 4 or 8 rows a unit:          cluster   whole   pieces     32 rows (16):   cluster        whole          pieces
+//    2 units of 64 blocks         6.8               7.6        2 of 32        9.8 ( 8.1)                  10.4 ( 9.2)
+//    8 units of 256              14.6              12.8        8 of 64       12.8 (10.5)                  13.5 (10.8)
+//   16 units of 64                9.6               9.7       16 of 64       14.8 (12.1)                  14.8 (12.2)
+//   16 units of 256              21.7              15.2       16 of 256      33.7 (27.5)                  23.3 (19.1)
+//   32 units of 64               10.2              13.4       32 of 64       16.0 (13.0)                  22.3 (18.5)
+//   64 units of 64               14.0              17.3       64 of 64       21.9 (17.9)                  30.3 (23.6)
 //  128 units of 64               26.4              30.8
-//  256 units of 32               25.2              29.1         256 of 32          46.0               59.1
-//  256 units listing 128         86                90           256 listing 81    103.3              106.8
-//  512 units of 64                        83       91           512 of 16                    53.9     73.6
+//  256 units of 32               25.2              29.1      256 of 32       36.5 (30.0)                  49.9 (39.1)
+//  256 units listing 128         86                90        256 listing 81  80.3 (65.5)                  87.7 (70.7)
+//  512 units of 64                        83       91        512 of 16                     44.3 (36.3)    64.2 (47.2)
 // So clusters where they fill most of a wave and the units are not long (listed blocks balance, lengths may not), and for
 // small calls; pieces otherwise.
 static BytePlan byte_plan(const ByteDevice& d, int units, int rows, int blocks, bool listed) {

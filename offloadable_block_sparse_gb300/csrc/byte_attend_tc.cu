@@ -1,23 +1,26 @@
-// Attention over an 8-bit KV block store for 17 to 32 query rows a unit (several drafted tokens of a group of q heads): the same
+// Attention over an 8-bit KV block store for 9 to 32 query rows a unit (several drafted tokens of a group of q heads): the same
 // sums as byte_attend.cu on the fifth-generation tensor cores.
 //
 // With so many rows mma.sync spends its time on fragments, and a warp's operands, accumulators and weights do not fit its
-// registers (32 rows of 16 units of 65,521 tokens: 961 instructions for 32 tokens, 91 us).  Here a CTA of 256 threads
-// takes a chunk of two blocks, 128 tokens; two threads, with half the rows each, are a token and later a dim:
-//   S (128 tokens x 2 x 32) = K . q^T   tcgen05 kind::f8f6f4: K's codes as they are, moved into tensor memory; q as two e4m3
+// registers (32 rows of 16 units of 65,521 tokens: 961 instructions for 32 tokens, 91 us; 16 rows 54).  Here a CTA of 256
+// threads takes a chunk of two blocks, 128 tokens; two threads, with half the rows each, are a token and later a dim:
+//   S (128 tokens x 2 x NR) = K . q^T   tcgen05 kind::f8f6f4: K's codes as they are, moved into tensor memory; q as two e4m3
 //                                      codes a value (its columns twice), exact to 2^-21 of the row's largest
 //   weights of the thread's token: as f16 into shared memory, their sums float32 in registers
-//   O^T (128 dims x 32) += s_V (V^T . P)   kind::f16: V's codes converted to f16 and moved into tensor memory, one product per
+//   O^T (128 dims x NR) += s_V (V^T . P)   kind::f16: V's codes converted to f16 and moved into tensor memory, one product per
 //                                      block, read back and added in float32 with the block's scale
 // The store's order is that of 8 x 4 words' fragments, which tcgen05.st 16x128b takes: both operands reach tensor memory
 // without a shuffle, and shared memory only sees the codes arrive and leave (with operands in its 128-byte swizzle, by plain
-// stores and stmatrix, 69.5 us where it is 62.8).  The copies of two chunks, the products with V and the next chunk's
-// conversion overlap, and the two CTAs of an SM.  Row references are the CTA's: a thread whose score would weigh more than
-// 2^14 says so at the barrier before the second product, and then all raise theirs and weigh again.
+// stores and stmatrix, 69.5 us where it was then 62.8).  The copies of two chunks, the products with V and the next chunk's
+// keys overlap, and the two CTAs of an SM.  Row references are the CTA's: a thread whose score would weigh more than 2^14
+// says so at the barrier before the second product, and then all raise theirs and weigh again.
 //
-// 16 units of 65,521 tokens and 32 rows take 62.8 us against 40 of HBM: a chunk's chain of products and barriers, twice an
-// SM.  64 units of 64 blocks 23.8 us (mma.sync 36.7), 256 of 32 40.1 (59.7), 2 of 32 10.2 (15.2).  With 16 rows
-// mma.sync is faster.  Tried without gain: 128 threads (88 us with one stage; 88.5 with 256).
+// 16 units of 65,521 tokens take 57.4 us with 32 rows and 51.6 with 16, against 40 of HBM: a chunk's chain of waits and two
+// barriers, 2,750 cycles of a CTA alone, 3,200 of two on an SM, and some 12,000 cycles before and after the 27 chunks.
+// Instructions for one thread (products, copies) take it a hundred cycles each, so they are spread over the warps (one
+// warp's products and another's copies 62.8).  64 units of 64 blocks 21.9 us with 32 rows, 17.9 with 16 (mma.sync 36.7 and
+// 21.8), 256 of 32 36.5 and 30.0 (59.7 and 34.1), 2 of 32 9.8 and 8.1 (15.2 and 10.2).  Tried without gain: 128 threads;
+// one barrier a chunk, with the next chunk's keys and scores before this one's products (69); prefetching into L2.
 #include "byte_split.cuh"
 #include "host.h"
 #include "tc.cuh"
