@@ -17,14 +17,15 @@
 // own after pieces).
 //
 // Bound by HBM where a call is long: 256 units of 32,768 tokens and 4 rows (2.15 GB) in 306 us, 1.05 of measured HBM (a copy);
-// ragged 198 us, 1.01.  437 instructions a half block, of which 128 conversions and 32 MMAs, leave the issue slots two
-// thirds empty.  Shorter calls pay for their start and end: 256 units listing 81 blocks 57.4 us, 0.89, with the masses of 128
-// 90 us, 0.89.
+// ragged 194 us, 1.03.  437 instructions a half block, of which 128 conversions and 32 MMAs, leave the issue slots two
+// thirds empty.  Shorter calls pay for their start and end: 256 units listing 81 blocks 55.3 us, 0.92, with the masses of 128
+// 86.2 us, 0.93.  (With the copies by a thread that the compiler does not know to be one, 57.4 and 90.)
 #include <algorithm>
 #include <mutex>
 
 #include "byte_split.cuh"
 #include "host.h"
+#include "tc.cuh"
 
 namespace nosa {
 
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
   __shared__ uint32_t poison[kByteRows][4];  // [row]: dims that end as NaN
   __shared__ float2 merged[kByteRows];       // a cluster CTA's references and sums
   __shared__ float2 final[kByteRows];        // the unit's, for its masses
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (lane == 0) {
 #pragma unroll
     for (int st = 0; st < kStages; ++st) mbar_init(&bars[warp][st], 1);
@@ -262,13 +263,14 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
       int started = 0;
       auto issue = [&]() {  // the next half into the stage whose turn it is
         if (started >= mine || late) return;
-        if (lane == 0) {
+        if (tc::elect()) {
           const int j = warp / 2 + started * step, row = a.sel ? list[j].x : b0 + j;
           const uint8_t* src = base + (size_t)row * kByteBlockBytes;
           const uint32_t to = smem_u32(ring + in * kHalfStage);
           mbar_arrive_expect_tx(&bars[warp][in], kHalfBytes + 16);
-          bulk_copy_g2s(to, src + half * kHalfBytes, kHalfBytes, &bars[warp][in]);
-          bulk_copy_g2s(to + kHalfBytes, src + kByteScales, 16, &bars[warp][in]);
+          // (a half block's codes, and the scales, which lie behind the second half)
+          bulk_copy_g2s(to, src + half * kHalfBytes, kHalfBytes + 16 * half, &bars[warp][in]);
+          if (!half) bulk_copy_g2s(to + kHalfBytes, src + kByteScales, 16, &bars[warp][in]);
         }
         in = in + 1 == kStages ? 0 : in + 1;
         ++started;
