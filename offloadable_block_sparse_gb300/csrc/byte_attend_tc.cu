@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           const bool there = kTcChunkBlocks * c + b < n;
           const float2 s = there ? *reinterpret_cast<const float2*>(scales[st][b]) : make_float2(0.f, 0.f);
           scale[b] = s.y;
-          if (tid >= b * NR && tid < (b + 1) * NR) factor[b][tid - b * NR] = logit_factor(alpha[tid - b * NR], s.x);
+          if (warp == 6 + b && lane < NR) factor[b][lane] = logit_factor(alpha[lane], s.x);
         }
         tc::wait_st();
         fence_proxy_async_smem();  // q (generic stores) is read by the tensor core
