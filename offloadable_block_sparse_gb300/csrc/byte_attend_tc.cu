@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   const uint32_t tm = tbase, tlane = tm + ((uint32_t)(32 * quarter) << 16), trow = tlane + r0, sa = smem_u32(sm);
 
   int ph_raw = 0, ph_s = 0, ph_o = 0, st = 0;  // the barriers' phases (a bit a stage), and the stage of the chunk in work
-  bool late = false;
+  bool late = false, stuck = false;  // a wait gave up: known to all behind the next barrier; of this warp, for products
   while (share.todo > 0) {
     const int u = share.u;
     const ByteSegment seg = next_segment(a, share);
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
     bool flying = false;
     // waits are decided for the whole warp: the tensor-memory accesses behind them are warp-collective
     auto wait_for = [&](uint64_t* bar, int phase) {
-      late |= !__all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, kWaitCycles));
+      stuck |= !__all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, kWaitCycles));
       tc::fence_after();
     };
     auto add_products = [&]() {  // O += s_V of the chunk before: the thread's dim, its rows
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
         tc::wait_st();
         fence_proxy_async_smem();  // q (generic stores) is read by the tensor core
         tc::fence_before();
-        late = __syncthreads_or(late);
+        late = __syncthreads_or(late || stuck);
         tc::fence_after();
         if (late) {
           if (c + 1 < chunks) wait_raw(st ^ 1);  // it is in flight
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
       if (late) break;
     }
     if (flying) add_products();
-    late = __syncthreads_or(late);  // also: the operands' places are free
+    late = __syncthreads_or(late || stuck);  // also: the operands' places are free
     if (late && tid == 0) atomicOr(a.err, kErrTimeout);
 
     // the partial: the thread's dim of its rows
