@@ -17,9 +17,9 @@
 // own after pieces).
 //
 // Bound by HBM where a call is long: 256 units of 32,768 tokens and 4 rows (2.15 GB) in 306 us, 1.05 of measured HBM (a copy);
-// ragged 194 us, 1.03.  437 instructions a half block, of which 128 conversions and 32 MMAs, leave the issue slots two
-// thirds empty.  Shorter calls pay for their start and end: 256 units listing 81 blocks 55.3 us, 0.92, with the masses of 128
-// 86.2 us, 0.93.  (With the copies by a thread that the compiler does not know to be one, 57.4 and 90.)
+// ragged 196 us, 1.02.  437 instructions a half block, of which 128 conversions and 32 MMAs, leave the issue slots two
+// thirds empty.  Shorter calls pay for their start and end: 256 units listing 81 blocks 56 us, 0.91, with the masses of 128
+// 88 us, 0.91.  (With the copies by a thread that the compiler does not know to be one, 57.4 and 90.)
 #include <algorithm>
 #include <mutex>
 
