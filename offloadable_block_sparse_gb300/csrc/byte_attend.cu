@@ -11,7 +11,7 @@
 //   S^T (2 x 16 tokens x 8 rows) = K codes . q^T       16 MMAs in two chains
 //   P^T by movmatrix of the f16-packed weights
 //   O^T (128 dims x 8 rows) += s_V (V codes^T . P^T)    16 MMAs into fresh accumulators, 32 FMAs: results stay in true
-//                                                  units whatever the blocks' scales
+//                                                  units whatever the blocks' scales (or in units of 2^40: byte_split.cuh)
 // Weights are 2^(logit - R), R within 14 of the row's maximum, their sum float32.  Where masses are wanted a half block
 // stores its (R, sum) per row; the rows' final references and sums turn these into masses in the end (in a kernel of their
 // own after pieces).
@@ -78,10 +78,18 @@ __device__ __forceinline__ void load_byte_query(ByteQuery& Q, float (&alpha)[2],
 }
 
 // A warp's running state: of rows 2t, 2t + 1 the reference (a logit in base 2), the lane's part of the softmax sum, and O^T:
-// dims 16 g + 2 j and + 1 of those rows.
+// dims 16 g + 2 j and + 1 of those rows, in units of 1 / per.
 struct ByteRows {
-  float top[2], l[2];
+  float top[2], l[2], per;
   float o[8][4];
+
+  __device__ __forceinline__ void to_large() {
+    per = 1.f / kLargeUnit;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] *= 1.f / kLargeUnit;
+  }
 };
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -182,6 +190,8 @@ __device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, co
     }
     if (g == 0 && 2 * t < rows) *reinterpret_cast<float4*>(mass + 2 * t) = make_float4(A.top[0], sum[0], A.top[1], sum[1]);
   }
+  if (s.y * A.per > kLargeScale) A.to_large();
+  const float sv = s.y * A.per;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint4 v[2];
@@ -201,7 +211,7 @@ __device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, co
           mma_f16(d, f[0], f[1], f[2], f[3], p[1][0], p[1][1]);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) A.o[2 * c + jj][e] = fmaf(d[e], s.y, A.o[2 * c + jj][e]);
+      for (int e = 0; e < 4; ++e) A.o[2 * c + jj][e] = fmaf(d[e], sv, A.o[2 * c + jj][e]);
     }
   }
 }
@@ -281,6 +291,7 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
         load_byte_query(Q, alpha, a.q + (size_t)u * a.rows * kHeadDim, a.rows, lane, a.scale);
         A.top[0] = A.top[1] = kNoRef;
         A.l[0] = A.l[1] = 0.f;
+        A.per = 1.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) A.o[j][0] = A.o[j][1] = A.o[j][2] = A.o[j][3] = 0.f;
       }
@@ -303,7 +314,8 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
       if (lane == 0) atomicOr(a.err, kErrTimeout);
       A.l[0] = A.l[1] = __int_as_float(0x7fc00000);
     }
-    __syncthreads();  // the rings become the warps' partials
+    const bool large = __syncthreads_or(A.per != 1.f);  // also: the rings become the warps' partials
+    if (large && A.per == 1.f) A.to_large();
 
     // the warp's partial: of rows 2t, 2t + 1, dims 16 g .. + 15
     float* w = smem + (warp * kByteRows + 2 * t) * kQaRowStride + 16 * g;
@@ -321,7 +333,7 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
       }
     }
     __syncthreads();
-    finish_segment<kWarps, kByteRows>(a, share, seg, smem, wr, wl, poison, merged, final);
+    finish_segment<kWarps, kByteRows>(a, share, seg, smem, wr, wl, poison, merged, final, large);
     if (share.todo > 0) {
       fence_proxy_async_smem();  // the next segment's copies come after these reads and writes
       __syncthreads();
@@ -342,19 +354,19 @@ __global__ void __launch_bounds__(kMergeWarps * 32) byte_merge_kernel(const __gr
   if (m.y == 1) return;
   float R = kNoRef, L = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool large = false;
 #pragma unroll 4
   for (int c = warp; c < m.y; c += kMergeWarps) {
     const size_t i = (size_t)(m.x + c) * a.rows + row;
-    const float2 s = a.stats[i];
-    merge_part(R, L, O, s.x, s.y, *reinterpret_cast<const float4*>(a.part + i * kHeadDim + 4 * lane));
+    merge_byte_part(R, L, O, large, a.stats[i], *reinterpret_cast<const float4*>(a.part + i * kHeadDim + 4 * lane));
   }
   so[warp][lane] = O;
-  if (lane == 0) ss[warp] = make_float2(R, L);
+  if (lane == 0) ss[warp] = make_float2(R, large_sum(L, large));
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < kMergeWarps; ++w) merge_part(R, L, O, ss[w].x, ss[w].y, so[w][lane]);
-    store_out(a.out + ((size_t)u * a.rows + row) * kHeadDim + 4 * lane, O, L);
+    for (int w = 1; w < kMergeWarps; ++w) merge_byte_part(R, L, O, large, ss[w], so[w][lane]);
+    store_out(a.out + ((size_t)u * a.rows + row) * kHeadDim + 4 * lane, O, L, large ? kLargeUnit : 1.f);
     if (lane == 0 && a.mass) a.total[(size_t)u * a.rows + row] = make_float2(R, L);
   }
 }

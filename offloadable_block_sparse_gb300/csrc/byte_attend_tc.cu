@@ -175,7 +175,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   ByteShare share = byte_share(a, kTcChunkBlocks, scan, found);
   const uint32_t tm = tbase, tlane = tm + ((uint32_t)(32 * quarter) << 16), trow = tlane + r0, sa = smem_u32(sm);
 
-  int ph_raw = 0, ph_s = 0, ph_o = 0, st = 0;  // the barriers' phases (a bit a stage), and the stage of the chunk in work
+  // the barriers' phases (a bit a stage; and in ph_raw, for want of a register, kLargeBit: o is in units of kLargeUnit), and the
+  // stage of the chunk in work
+  int ph_raw = 0, ph_s = 0, ph_o = 0, st = 0;
+  constexpr int kLargeBit = 4;
   bool late = false, stuck = false;  // a wait gave up: known to all behind the next barrier; of this warp, for products
   while (share.todo > 0) {
     const int u = share.u;
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
       top[tid] = kNoRef;
       poison[tid][0] = poison[tid][1] = poison[tid][2] = poison[tid][3] = 0;
     }
-    float sv[kTcChunkBlocks] = {};  // the V scales of the chunk whose products are in flight
+    float sv[kTcChunkBlocks] = {};  // the V scales of the chunk whose products are in flight, in the units of o
     bool flying = false;
     // waits are decided for the whole warp: the tensor-memory accesses behind them are warp-collective
     auto wait_for = [&](uint64_t* bar, int phase) {
@@ -288,8 +291,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
         for (int i = 0; i < kByteTiles; ++i)
           v[i] = *reinterpret_cast<const uint4*>(stage + half * kByteScales + i * kByteTile + kByteV + 512 * quarter + 16 * lane);
         place_values(tlane + kTcV + half * (kBlock / 2), v);
+        if (!(ph_raw & kLargeBit) && fmaxf(scale[0], scale[1]) > kLargeScale) {  // (products of the chunks before are in o)
+          ph_raw |= kLargeBit;
 #pragma unroll
-        for (int b = 0; b < kTcChunkBlocks; ++b) sv[b] = scale[b];
+          for (int r = 0; r < R; ++r) o[r] *= 1.f / kLargeUnit;
+        }
+#pragma unroll
+        for (int b = 0; b < kTcChunkBlocks; ++b) sv[b] = ph_raw & kLargeBit ? scale[b] * (1.f / kLargeUnit) : scale[b];
 
         // the thread's token: the logits of its rows
         const int block = at / kBlock, j = kTcChunkBlocks * c + block, mine = left_of(j) - at % kBlock;  // rows of query tokens from nq - mine on see it
@@ -418,7 +426,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
       wl[0][tid] = late ? __int_as_float(0x7fc00000) : (sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid]);
     }
     __syncthreads();
-    finish_segment<1, NR>(a, share, seg, part, wr, wl, poison, merged, final);
+    finish_segment<1, NR>(a, share, seg, part, wr, wl, poison, merged, final, ph_raw & kLargeBit);
+    ph_raw &= ~kLargeBit;
     if (share.todo > 0) {
       fence_proxy_async_smem();
       __syncthreads();

@@ -15,6 +15,28 @@ namespace cg = cooperative_groups;
 constexpr int kByteThreads = 128;
 constexpr float kTopLead = 10.f, kTopWeight = 14.f;  // a new reference weighs the best score 2^10; up to 2^14 it stays
 
+// Results are kept in true units as long as no block's s_V is above kLargeScale: of 2^20 tokens with weights of up to 2^14
+// and codes of up to 448 their sum is below 2^123.  From the first such block on a part's are kept in units of 2^40, below
+// 2^122 with the largest scale of 2^119; a step then loses up to 2^-110 of a result (half of float32's 2^-149 in those units,
+// over a sum of weights of at least 1).  The sign bit of a part's softmax sum says so (large_sum).
+constexpr float kLargeScale = 0x1p80f, kLargeUnit = 0x1p40f;
+
+__device__ __forceinline__ float large_sum(float l, bool large) { return large ? -l : l; }
+
+// Adds a part (reference and marked sum s, four dims o) to a running one in units that `large` tells.
+__device__ __forceinline__ void merge_byte_part(float& R, float& L, float4& O, bool& large, const float2& s, float4 o) {
+  const bool part = __float_as_int(s.y) < 0;
+  if (part != large) {
+    float4& x = large ? o : O;
+    x.x *= 1.f / kLargeUnit;
+    x.y *= 1.f / kLargeUnit;
+    x.z *= 1.f / kLargeUnit;
+    x.w *= 1.f / kLargeUnit;
+    large = true;
+  }
+  merge_part(R, L, O, s.x, fabsf(s.y), o);
+}
+
 struct ByteArgs {
   const uint16_t* q;
   const uint8_t* store;
@@ -25,7 +47,7 @@ struct ByteArgs {
   float* mass;    // null: not wanted
   int* err;
   int2* meta;     // [unit]: its first part and how many there are (1: the output is written already)
-  float2* stats;  // [part][row]: reference and softmax sum
+  float2* stats;  // [part][row]: reference and softmax sum (large_sum)
   float* part;    // [part][row][128]
   float2* total;  // [unit][row]: final reference and sum, where masses are wanted
   float2* half;   // [unit][block][half][mass_rows]: reference and sum of a half block
@@ -216,11 +238,11 @@ __device__ __forceinline__ float2 final_of(float R, float L) { return make_float
 
 // What becomes of a CTA's part of unit s.u: part[worker][rows_alloc][kQaRowStride] holds N workers' results, wr and wl
 // [worker][rows_alloc] their references and sums, poison the dims that end as NaN (where there is more than one query
-// token).  They go into the result where the CTA has the whole unit, through the cluster, or to the merge kernel.
+// token), large whether they are in units of kLargeUnit.  They go into the result where the CTA has the whole unit, through the cluster, or to the merge kernel.
 template <int N, int kRows>
 __device__ __forceinline__ void finish_segment(const ByteArgs& a, ByteShare& s, const ByteSegment& g, float* part,
                                                const float (*wr)[kRows], const float (*wl)[kRows], const uint32_t (*poison)[4],
-                                               float2* merged, float2* final) {
+                                               float2* merged, float2* final, bool large) {
   const int p = blockIdx.x + s.u;  // a piece's end and a unit's each move on by one: no two segments share a part
   const size_t out0 = (size_t)s.u * a.rows;  // the unit's first row of the result
   for (int idx = threadIdx.x; idx < a.rows * (kHeadDim / 4); idx += (int)blockDim.x) {
@@ -250,16 +272,16 @@ __device__ __forceinline__ void finish_segment(const ByteArgs& a, ByteShare& s, 
     }
     if (s.ranks > 1) {  // in the place of worker 0's, which this thread alone has read
       *reinterpret_cast<float4*>(part + row * kQaRowStride + x) = O;
-      if (x == 0) merged[row] = make_float2(R, L);
+      if (x == 0) merged[row] = make_float2(R, large_sum(L, large));
     } else if (g.complete()) {
-      store_out(a.out + (out0 + row) * kHeadDim + x, O, L);
+      store_out(a.out + (out0 + row) * kHeadDim + x, O, L, large ? kLargeUnit : 1.f);
       if (x == 0) {
         final[row] = final_of(R, L);
         if (a.mass && a.split == kPieces) a.total[out0 + row] = make_float2(R, L);
       }
     } else {
       const size_t i = (size_t)p * a.rows + row;
-      if (x == 0) a.stats[i] = make_float2(R, L);
+      if (x == 0) a.stats[i] = make_float2(R, large_sum(L, large));
       *reinterpret_cast<float4*>(a.part + i * kHeadDim + x) = O;
     }
   }
@@ -272,7 +294,7 @@ __device__ __forceinline__ void finish_segment(const ByteArgs& a, ByteShare& s, 
         for (int r = 0; r < s.ranks; ++r) R = fmaxf(R, cluster.map_shared_rank(&merged[threadIdx.x], r)->x);
         for (int r = 0; r < s.ranks; ++r) {
           const float2 m = *cluster.map_shared_rank(&merged[threadIdx.x], r);
-          L = fmaf(m.y, ex2(m.x - R), L);
+          L = fmaf(fabsf(m.y), ex2(m.x - R), L);
         }
         final[threadIdx.x] = final_of(R, L);
       }
@@ -284,12 +306,13 @@ __device__ __forceinline__ void finish_segment(const ByteArgs& a, ByteShare& s, 
       const int row = idx >> 5, x = 4 * (idx & 31);
       float R = kNoRef, L = 0.f;
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+      bool any_large = false;
 #pragma unroll 4
       for (int r = 0; r < s.ranks; ++r) {
         const float2 m = *cluster.map_shared_rank(&merged[row], r);
-        merge_part(R, L, O, m.x, m.y, *reinterpret_cast<const float4*>(cluster.map_shared_rank(part + row * kQaRowStride + x, r)));
+        merge_byte_part(R, L, O, any_large, m, *reinterpret_cast<const float4*>(cluster.map_shared_rank(part + row * kQaRowStride + x, r)));
       }
-      store_out(a.out + (out0 + row) * kHeadDim + x, O, L);
+      store_out(a.out + (out0 + row) * kHeadDim + x, O, L, any_large ? kLargeUnit : 1.f);
     }
     cluster.sync();  // keep every CTA's shared memory until all have read it
     return;

@@ -71,10 +71,10 @@ __device__ __forceinline__ void merge_part(float& R, float& L, float4& O, float 
   O.w = O.w * f + o.w * h;
 }
 
-// Four dims of an output row: zeros where no token was seen.
-__device__ __forceinline__ void store_out(uint16_t* out, const float4& o, float l) {
+// Four dims of an output row, o in units of `unit`: zeros where no token was seen.
+__device__ __forceinline__ void store_out(uint16_t* out, const float4& o, float l, float unit = 1.f) {
   uint2 v = make_uint2(0, 0);
-  if (l != 0.f) v = make_uint2(pack_bf16x2(o.x / l, o.y / l), pack_bf16x2(o.z / l, o.w / l));
+  if (l != 0.f) v = make_uint2(pack_bf16x2(o.x / l * unit, o.y / l * unit), pack_bf16x2(o.z / l * unit, o.w / l * unit));
   *reinterpret_cast<uint2*>(out) = v;
 }
 

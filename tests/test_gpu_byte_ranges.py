@@ -1,0 +1,105 @@
+"""The attention over the 8-bit store at the ends of what the store, the queries and the lists may hold, with 8, 16 and 32
+query rows a unit: the kernel of up to 8 rows and both forms of the one for more."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import byte_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+from tests.test_gpu_byte import (_attend, _expect, _f64, _i32, _lengths, _queries, _some, _store,  # noqa: E402
+                                 many_blocks)  # noqa: F401 (a fixture)
+
+FORMS = [(8, 1), (8, 2), (8, 4)]  # q heads and query tokens of a unit
+WAVE = 2 * torch.cuda.get_device_properties(0).multi_processor_count  # CTAs that are resident at once
+# units, blocks a unit: a cluster a unit, equal pieces of few and of many units, a CTA a unit
+PLANS = {"cluster": (6, 24), "pieces": (12, 130), "pieces-of-units": (WAVE + 16, 40), "unit-a-cta": (2 * WAVE, 5)}
+
+
+def _set_scales(store, ks=None, vs=None):
+    """Replaces blocks' scales: ks, vs broadcast over [units][blocks]."""
+    for x, at in ((ks, O.SCALES), (vs, O.SCALES + 4)):
+        if x is not None:
+            s = np.ascontiguousarray(np.broadcast_to(np.asarray(x, np.float32), store.shape[:2]))
+            store[..., at:at + 4] = s[..., None].view(np.uint8)
+
+
+def _check(q, store, lens, group, nq, *, units=None, sel=None, slots=None, max_len=None, scale=0.0):
+    """Compares the units listed (all by default) with the oracle within _expect's bounds; returns the result and the masses.
+
+    One term more for a mass: it is a float32 sum of 2 rows terms (a half block's sum times two factors, a row at a time)
+    by multiply-add.  All are positive, so no partial sum is above the mass, and each step rounds by at most 2^-24 of it:
+    2 rows 2^-24 of the mass.  _expect's 2^-21 has room for that with random roundings, not with rows whose terms are all
+    equal and round the same way."""
+    nb, rows = store.shape[1], group * nq
+    st, ln = torch.from_numpy(store).cuda(), _i32(lens)
+    s, sl = (None if x is None else _i32(x) for x in (sel, slots))
+    out, mass, err = _attend(q, st, ln, group, nq, nb, sel=s, slots=sl, max_len=max_len, scale=scale)
+    again, _, _ = _attend(q, st, ln, group, nq, nb, sel=s, slots=sl, max_len=max_len, scale=scale, mass=False)
+    assert err == 0 and torch.equal(out.view(torch.int16), again.view(torch.int16))
+    got, gm, qq = _f64(out), _f64(mass), _f64(q)
+    for u in range(q.shape[0]) if units is None else units:
+        at = np.arange(-(-max_len // 64)) if sel is None else np.asarray(sel[u])
+        row = at if slots is None else np.asarray(slots[u])
+        k, v = O.unpack(store[u, np.where(at >= 0, row, 0)])
+        ref, m, tol, off = _expect(qq[u], k, v, at, lens[u], nq, scale or 1 / math.sqrt(128))
+        assert np.isfinite(got[u]).all() and np.isfinite(gm[u]).all()
+        assert (np.abs(got[u] - ref) <= tol).all(), (u, np.max(np.abs(got[u] - ref) / (tol + 1e-300)))
+        off = off + 2 * rows * 2.0 ** -24 * m
+        assert (np.abs(gm[u] - m) <= off).all(), (u, np.max(np.abs(gm[u] - m) / (off + 1e-300)))
+    return out, mass
+
+
+# ------------------------------------------------------------------------------------------ V
+@pytest.mark.parametrize("group,nq", FORMS)
+@pytest.mark.parametrize("plan", PLANS)
+@pytest.mark.parametrize("kind", ["mixed", "equal"])
+def test_values_to_the_end_of_the_range(kind, plan, group, nq, many_blocks):
+    """V up to 448 2^119, of both signs beside smaller blocks, and of one sign with equal weights: finite as the sum is."""
+    units, nb = PLANS[plan]
+    rng = np.random.default_rng(50 + units)
+    store, q = _store(rng, many_blocks, units, nb), _queries(rng, units, group * nq)
+    if kind == "mixed":
+        _set_scales(store, vs=np.exp2(rng.choice([119, 118, 100, 81, 80, 60, -6], (units, nb))))
+    else:
+        store[..., O.AT["v"].ravel()] &= 0x7F
+        _set_scales(store, vs=2.0 ** 119)
+        q.zero_()
+    out, _ = _check(q, store, _lengths(units, nb, nq), group, nq, units=_some(units), max_len=64 * nb)
+    assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("group,nq", FORMS)
+@pytest.mark.parametrize("plan", PLANS)
+def test_large_values_without_weight_leave_the_others_exact(plan, group, nq, many_blocks):
+    """Blocks of 448 2^119 whose logits are thousands below: their weight is 0 in 64 bits too, so the result and its bound
+    are those of the other blocks alone."""
+    units, nb = PLANS[plan]
+    rng = np.random.default_rng(60 + units)
+    store, q = _store(rng, many_blocks, units, nb), _queries(rng, units, group * nq)
+    q[..., 0] = 8.0
+    store[..., O.AT["k"][:, 0]] = 0                       # ordinary blocks do not look at that dim
+    big = rng.random((units, nb)) < 0.2
+    big[:, 0] = False
+    big[0], big[1, -1], big[2, 1:] = False, True, True
+    x = np.zeros((64, 128))
+    x[:, 0] = -448
+    where = np.argwhere(big)
+    for u, b in where:
+        store[u, b, O.AT["k"].ravel()] = O.encode(x).ravel()
+        store[u, b, O.SCALES:O.SCALES + 8] = np.array([8.0, 2.0 ** 119], np.float32).view(np.uint8)
+    lens = np.full(units, 64 * nb - 5)
+    out, mass, err = _attend(q, torch.from_numpy(store).cuda(), _i32(lens), group, nq, nb, max_len=64 * nb)
+    got, gm = _f64(out), _f64(mass)
+    assert err == 0 and np.isfinite(got).all()
+    for u in _some(units):
+        k, v = O.unpack(store[u])
+        ref, m, tol, off = _expect(_f64(q)[u], k, v, np.where(big[u], -1, np.arange(nb)), lens[u], nq, 1 / math.sqrt(128))
+        assert (np.abs(got[u] - ref) <= tol).all(), (u, (np.abs(got[u] - ref) / tol).max())
+        assert (np.abs(gm[u] - m) <= off).all()
