@@ -621,8 +621,8 @@ nosa_status nosa_byte_read(const uint8_t* store, int units, int max_blocks, cons
  * The sums, the weights' among them, are float32.  q is exact but for values far below their row's largest: with up to 8
  * rows a unit those below 2^-22 of it, with more those below 2^-13, which are off by at most 2^-21 of it.
  * The weights exp(logit - reference) that multiply V are rounded to f16: by 2^-11 of themselves, small ones by 2^-35 of
- * the row's largest weight (2^-25 where logits are beyond 2^26).  Logits of any size are fine: beyond float32 the largest
- * takes all.  So are values of any size: only in a unit with an s_V above 2^80 are results off by up to 2^-90 besides.
+ * the row's largest weight (2^-25 where logits are beyond 2^26).  Logits of any size are fine, beyond float32 too: there the
+ * largest takes all (beyond 2^90 those within 2^-19 of it share).  So are values of any size: only in a unit with an s_V above 2^80 are results off by up to 2^-90 besides.
  * Asynchronous on `stream`.  NOSA_ERR_CAPACITY if the scratch is too small. */
 nosa_status nosa_byte_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group, int n_queries,
                                    int max_blocks, const int32_t* lens, int max_len, float softmax_scale, uint16_t* out,

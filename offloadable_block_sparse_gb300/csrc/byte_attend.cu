@@ -40,10 +40,15 @@ struct ByteQuery {
   uint32_t b[8][2];
 };
 
+// What turns the scores q . c of rows 2t, 2t + 1 into logits: row_factor, the row's own power of two in it, and the largest
+// factor of all eight rows.
+struct ByteFactors {
+  float alpha[2], inv[2], most;
+};
+
 // Row g of q, scaled by a power of two that brings the row's largest magnitude into [2^9, 2^10) (bf16 values
-// down to 2^-22 of it stay exact in f16).  alpha: the factors that turn rows 2t, 2t + 1 of q . c into logits in base 2
-// for a K scale of 1.
-__device__ __forceinline__ void load_byte_query(ByteQuery& Q, float (&alpha)[2], const uint16_t* q, int rows, int lane,
+// down to 2^-22 of it stay exact in f16).
+__device__ __forceinline__ void load_byte_query(ByteQuery& Q, ByteFactors& F, const uint16_t* q, int rows, int lane,
                                                 float scale) {
   const int row = lane >> 2, t = lane & 3;
   uint4 x[4];
@@ -70,10 +75,12 @@ __device__ __forceinline__ void load_byte_query(ByteQuery& Q, float (&alpha)[2],
     for (int k = 0; k < 4; ++k)
       Q.b[2 * i + (k >> 1)][k & 1] = pack_half2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
   }
+  const float al = row_factor(scale, inv);
+  F.most = __uint_as_float(__reduce_max_sync(0xffffffffu, al == al ? __float_as_uint(al) : 0u));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float al = scale * __shfl_sync(0xffffffffu, inv, 8 * t + 4 * i);  // row 2t's lanes: 8t ..
-    alpha[i] = al > 0x1p127f ? 0x1p127f : al;  // finite: it may meet a zero s_K (a NaN stays)
+  for (int i = 0; i < 2; ++i) {  // row 2t's lanes: 8t ..
+    F.alpha[i] = __shfl_sync(0xffffffffu, al, 8 * t + 4 * i);
+    F.inv[i] = __shfl_sync(0xffffffffu, inv, 8 * t + 4 * i);
   }
 }
 
@@ -96,8 +103,9 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i ==
 
 // One half block: both tiles of tokens at once, so that their chains of dependent operations overlap.
 // left: tokens of the context from its first on; mass: where its sums go, or null.
-__device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, const float (&alpha)[2], unsigned char* stage,
-                                             uint32_t (*poison)[4], int left, int rows, int nq, float2* mass, int lane) {
+__device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, const ByteFactors& F, double scale64,
+                                             unsigned char* stage, uint32_t (*poison)[4], int left, int rows, int nq,
+                                             float2* mass, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const bool tail = left - (nq - 1) < kHalfTokens;  // some row does not see the whole half
   if (tail) {
@@ -132,12 +140,13 @@ __device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, co
   // logits, and whether a row's best would weigh more than its reference allows
   float best[2];
   bool raise = false;
-  const float f0 = logit_factor(alpha[0], s.x), f1 = logit_factor(alpha[1], s.x);
+  const float f0 = F.alpha[0] * s.x, f1 = F.alpha[1] * s.x;
+  const bool wide = !(F.most * s.x <= kWideFactor);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      z[i][e] *= e & 1 ? f1 : f0;
+      z[i][e] = wide ? wide_logit(z[i][e], F.inv[e & 1], s.x, scale64) : z[i][e] * (e & 1 ? f1 : f0);
       if (tail) {
         const int row = 2 * t + (e & 1), token = kByteTileTokens * i + g + 8 * (e >> 1);
         if (row >= rows || token >= left - (nq - 1) + row % nq) z[i][e] = -INFINITY;
@@ -254,7 +263,7 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
     }
     ByteQuery Q;
     ByteRows A;
-    float alpha[2];
+    ByteFactors F;
 
     // The blocks, listed ones looked up kQaList at a time and those without a token left out.  Warp w takes half
     // w % 2 of the blocks w / 2, w / 2 + kWarps / 2, ...  (an empty half of the last block too: it adds nothing).
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
 #pragma unroll
       for (int i = 0; i < kStages; ++i) issue();
       if (b0 == seg.first) {  // while the first stages arrive
-        load_byte_query(Q, alpha, a.q + (size_t)u * a.rows * kHeadDim, a.rows, lane, a.scale);
+        load_byte_query(Q, F, a.q + (size_t)u * a.rows * kHeadDim, a.rows, lane, a.scale);
         A.top[0] = A.top[1] = kNoRef;
         A.l[0] = A.l[1] = 0.f;
         A.per = 1.f;
@@ -302,7 +311,7 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
           const int left = (a.sel ? list[j].y : seg.len - (b0 + j) * kBlock) - half * kHalfTokens;
           float2* mass = nullptr;
           if (a.mass) mass = a.half + (((size_t)u * a.blocks + (a.sel ? list[j].z : b0 + j)) * 2 + half) * a.mass_rows;
-          process_half(A, Q, alpha, ring + out * kHalfStage, poison, left, a.rows, a.nq, mass, lane);
+          process_half(A, Q, F, a.scale64, ring + out * kHalfStage, poison, left, a.rows, a.nq, mass, lane);
           __syncwarp();  // the stage is read
           issue();
         }
@@ -485,6 +494,14 @@ static BytePlan byte_plan(const ByteDevice& d, int units, int rows, int blocks, 
   return {kPieces, (int)std::min<long long>(wave, ((long long)units * blocks + step - 1) / step), 0};
 }
 
+static void set_scale(ByteArgs& a, float softmax_scale) {
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.f / sqrtf((float)kHeadDim);
+  const double exact = scale * 1.4426950408889634;
+  const bool normal = exact >= 0x1p-126 && exact <= 0x1p127;
+  a.scale = normal ? scale * 1.4426950408889634f : INFINITY;
+  a.scale64 = normal ? a.scale : exact;
+}
+
 static nosa_status byte_attend(ByteArgs& a, void* scratch, size_t scratch_bytes, cudaStream_t st) {
   ByteDevice d;
   if (!byte_device(&d)) return NOSA_ERR_CUDA;
@@ -557,7 +574,7 @@ extern "C" nosa_status nosa_byte_dense_attend(const uint16_t* q, const uint8_t* 
   a.max_blocks = max_blocks;
   a.max_len = max_len;
   a.blocks = (max_len + kBlock - 1) / kBlock;
-  a.scale = (softmax_scale > 0.f ? softmax_scale : 1.f / sqrtf((float)kHeadDim)) * 1.4426950408889634f;
+  set_scale(a, softmax_scale);
   return byte_attend(a, scratch, scratch_bytes, static_cast<cudaStream_t>(stream));
 }
 
@@ -583,6 +600,6 @@ extern "C" nosa_status nosa_byte_attend(const uint16_t* q, const uint8_t* store,
   a.rows = group * n_queries;
   a.max_blocks = max_blocks;
   a.max_sel = a.blocks = max_sel;
-  a.scale = (softmax_scale > 0.f ? softmax_scale : 1.f / sqrtf((float)kHeadDim)) * 1.4426950408889634f;
+  set_scale(a, softmax_scale);
   return byte_attend(a, scratch, scratch_bytes, static_cast<cudaStream_t>(stream));
 }

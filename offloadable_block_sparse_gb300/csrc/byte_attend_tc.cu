@@ -41,7 +41,7 @@ constexpr uint32_t kTcO = 64, kTcV = 128, kTcK = kTcV + kTcChunkBlocks * kBlock 
 static_assert(kTcChunkBlocks == 2 && kTcK + kHeadDim / 4 <= kTcCols, "two CTAs share an SM's 512 columns");
 
 // The unit's query rows as operands: row r's codes in rows r (the values') and NR + r (16 times what these leave) of sq, and
-// the factors that turn its scores into logits in base 2 for a K scale of 1.  A warp takes every eighth row, a lane four
+// row_factor and the row's own power of two in it.  A warp takes every eighth row, a lane four
 // dims.  The largest magnitude of a row is brought into [2^7, 2^8), so that bf16's eight bits are two codes of four down to
 // 2^-13 of it.
 template <int NR>
@@ -53,7 +53,7 @@ __device__ __forceinline__ void load_tc_queries(uint2 (&x)[NR / 8], const ByteAr
   }
 }
 template <int NR>
-__device__ __forceinline__ void place_tc_queries(const uint2 (&x)[NR / 8], const ByteArgs& a, unsigned char* sq, float* alpha,
+__device__ __forceinline__ void place_tc_queries(const uint2 (&x)[NR / 8], const ByteArgs& a, unsigned char* sq, float* alpha, float* invs,
                                                  int warp, int lane) {
 #pragma unroll
   for (int i = 0; i < NR / 8; ++i) {
@@ -77,8 +77,8 @@ __device__ __forceinline__ void place_tc_queries(const uint2 (&x)[NR / 8], const
     *reinterpret_cast<uint32_t*>(sq + row * 128 + at) = hi;
     *reinterpret_cast<uint32_t*>(sq + (NR + row) * 128 + at) = lo;
     if (lane == 0) {
-      const float al = a.scale * inv;
-      alpha[row] = al > 0x1p127f ? 0x1p127f : al;  // finite: it may meet a zero s_K (a NaN stays)
+      alpha[row] = row_factor(a.scale, inv);
+      invs[row] = inv;
     }
   }
 }
@@ -134,6 +134,21 @@ __device__ __forceinline__ float sum_rows(const float (&v)[R], int lane) {
   return x[0];
 }
 
+// Turns a thread's scores y into logits: one by one, through places in P that no other thread writes, which are the 16-byte
+// words of its f16 weights (the first at `word`) and those 64 bytes from there in the unswizzled order, which hold none.
+template <int R>
+__device__ __forceinline__ float4* other_word(float4* word, int i) {
+  return reinterpret_cast<float4*>(reinterpret_cast<uintptr_t>(word) ^ (16 * (i % (R / 8)) + 64 * (i / (R / 8))));
+}
+template <int R>
+__device__ __noinline__ void wide_logits(float4* word, const float* invs, const float* sk, double scale) {
+#pragma unroll 1
+  for (int r = 0; r < R; ++r) {
+    float& y = reinterpret_cast<float*>(other_word<R>(word, r / 4))[r % 4];
+    y = wide_logit(y, invs[r], *sk, scale);
+  }
+}
+
 // Four consecutive floats of shared memory that all lanes read.
 __device__ __forceinline__ void read4(float (&v)[4], const float* p) {
   const float4 x = *reinterpret_cast<const float4*>(p);
@@ -149,7 +164,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   __shared__ int4 list[kQaList];
   __shared__ int scan[32], found[2];
   __shared__ uint32_t tbase;
-  __shared__ __align__(16) float alpha[NR], top[NR], raised[NR], factor[kTcChunkBlocks][NR];
+  __shared__ int wide[kTcChunkBlocks];  // whether the block's logits are wide_logit's
+  __shared__ __align__(16) float alpha[NR], invs[NR], top[NR], raised[NR], factor[kTcChunkBlocks][NR];
   __shared__ uint32_t best[4][NR];
   __shared__ float sums[4][NR], wr[1][NR], wl[1][NR];
   __shared__ uint32_t poison[NR][4];
@@ -175,9 +191,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   ByteShare share = byte_share(a, kTcChunkBlocks, scan, found);
   const uint32_t tm = tbase, tlane = tm + ((uint32_t)(32 * quarter) << 16), trow = tlane + r0, sa = smem_u32(sm);
 
-  // the barriers' phases (a bit a stage; and in ph_raw, for want of a register, kLargeBit: o is in units of kLargeUnit), and the
-  // stage of the chunk in work
-  int ph_raw = 0, ph_s = 0, ph_o = 0, st = 0;
+  // The stage of the chunk in work, which is also its phase of bar_s (and of bar_o, whose chunk before has the other), and the
+  // phases of the stages' copies (a bit each; there too, for want of a register, kLargeBit: o is in units of kLargeUnit).
+  int st = 0, ph_raw = 0;
   constexpr int kLargeBit = 4;
   bool late = false, stuck = false;  // a wait gave up: known to all behind the next barrier; of this warp, for products
   while (share.todo > 0) {
@@ -198,8 +214,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
       tc::fence_after();
     };
     auto add_products = [&]() {  // O += s_V of the chunk before: the thread's dim, its rows
-      wait_for(&bar_o, ph_o);
-      ph_o ^= 1;
+      wait_for(&bar_o, st ^ 1);
       uint32_t d[kTcChunkBlocks][R];
 #pragma unroll
       for (int b = 0; b < kTcChunkBlocks; ++b) tc::ld(trow + kTcO + b * NR, d[b]);
@@ -244,7 +259,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
       issue(0, st);
       issue(1, st ^ 1);
       if (b0 == seg.first) {  // while the first chunk arrives
-        place_tc_queries<NR>(q, a, sm + kTcQ, alpha, warp, lane);
+        place_tc_queries<NR>(q, a, sm + kTcQ, alpha, invs, warp, lane);
         __syncthreads();
       }
       for (int c = 0; c < chunks; ++c) {
@@ -266,7 +281,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           const bool there = kTcChunkBlocks * c + b < n;
           const float2 s = there ? *reinterpret_cast<const float2*>(scales[st][b]) : make_float2(0.f, 0.f);
           scale[b] = s.y;
-          if (warp == 6 + b && lane < NR) factor[b][lane] = logit_factor(alpha[lane], s.x);
+          if (warp == 6 + b) {
+            const float al = lane < NR ? alpha[lane] : 0.f, f = al * s.x;
+            if (lane < NR) factor[b][lane] = f;
+            const bool any = __any_sync(0xffffffffu, isinf(al) || f > kWideFactor);
+            if (lane == 0) wide[b] = any;
+          }
         }
         tc::wait_st();
         fence_proxy_async_smem();  // q (generic stores) is read by the tensor core
@@ -301,8 +321,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
 
         // the thread's token: the logits of its rows
         const int block = at / kBlock, j = kTcChunkBlocks * c + block, mine = left_of(j) - at % kBlock;  // rows of query tokens from nq - mine on see it
-        wait_for(&bar_s, ph_s);
-        ph_s ^= 1;
+        wait_for(&bar_s, st);
         // Weights 2^(logit - top), as f16 into P.  Where one is more than its reference allows, all raise theirs and weigh again.
         float y[R];
 #pragma unroll 1
@@ -314,11 +333,25 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           tc::landed(d);
           tc::landed(e);
 #pragma unroll
-          for (int r = 0; r < R; r += 4) {
-            float f[4];
-            read4(f, &factor[block][r0 + r]);
+          for (int r = 0; r < R; ++r) y[r] = fmaf(__uint_as_float(e[r]), 0.0625f, __uint_as_float(d[r]));
+          if (!wide[block]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[r + i] = fmaf(__uint_as_float(e[r + i]), 0.0625f, __uint_as_float(d[r + i])) * f[i];
+            for (int r = 0; r < R; r += 4) {
+              float f[4];
+              read4(f, &factor[block][r0 + r]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) y[r + i] *= f[i];
+            }
+          } else {  // one by one, through the place of the thread's weights
+            float4* word = reinterpret_cast<float4*>(sm + kTcP + at * 128 + 16 * (r0 / 8 ^ (at & 7)));
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i) *other_word<R>(word, i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            wide_logits<R>(word, invs + r0, scales[st][block], a.scale64);
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i) {
+              const float4 v = *other_word<R>(word, i);
+              y[4 * i] = v.x, y[4 * i + 1] = v.y, y[4 * i + 2] = v.z, y[4 * i + 3] = v.w;
+            }
           }
           if (mine < a.nq) {
             int query = r0 % a.nq;

@@ -53,15 +53,27 @@ struct ByteArgs {
   float2* half;   // [unit][block][half][mass_rows]: reference and sum of a half block
   int units, nq, rows, mass_rows, max_blocks, max_sel, max_len, blocks;  // blocks: per unit, listed or up to max_len
   int split;
-  float scale;    // softmax scale x log2(e)
+  float scale;    // softmax scale x log2(e); infinite where float32's normal range does not hold it
+  double scale64;
   long long wait_limit;  // SM cycles a wait for a staged half block may take before it gives up (< 0: none)
 };
 
-// Logits per score: alpha x s_K, kept where logits are finite (scores are below 2^26: 128 products of a q below 2^10 and
-// a code of at most 448).
-__device__ __forceinline__ float logit_factor(float alpha, float sk) {
-  const float c = alpha * sk;
-  return c > 0x1p100f ? 0x1p100f : c;  // (a NaN stays)
+// A logit is a score (below 2^26: 128 products of a q below 2^10 and a code of at most 448) x alpha x s_K, alpha = scale x inv
+// being what turns the row's scores into logits in base 2.  All but s_K is one float32 where that neither overflows nor loses
+// bits, infinity elsewhere; and where alpha s_K is above kWideFactor for some row, infinity among them, all of a block's logits
+// are computed by wide_logit.
+constexpr float kWideFactor = 0x1p64f;
+__device__ __forceinline__ float row_factor(float scale, float inv) {
+  const float alpha = scale * inv;
+  return alpha != alpha || (alpha >= 0x1p-100f && alpha <= 0x1p100f) ? alpha : INFINITY;
+}
+// In 64 bits, and for sizes beyond 2^90, which the others stay below, as 2^90 (size / 2^90)^(1/16): at most 2^111, in the same
+// order, with differences as far beyond any softmax's reach.  (Cut at a largest factor or logit, unequal ones would be equal or
+// change places.)
+static __device__ __noinline__ float wide_logit(float score, float inv, float sk, double scale) {
+  const double x = scale * inv * sk * score, size = fabs(x);
+  if (!(size > 0x1p90)) return (float)x;  // (a NaN stays)
+  return copysignf((float)(0x1p90 * sqrt(sqrt(sqrt(sqrt(size * 0x1p-90))))), (float)(x > 0) - 0.5f);
 }
 // A row's new reference for its best logit: the best itself where it is so large that the difference would not be what
 // it should.

@@ -103,3 +103,79 @@ def test_large_values_without_weight_leave_the_others_exact(plan, group, nq, man
         ref, m, tol, off = _expect(_f64(q)[u], k, v, np.where(big[u], -1, np.arange(nb)), lens[u], nq, 1 / math.sqrt(128))
         assert (np.abs(got[u] - ref) <= tol).all(), (u, (np.abs(got[u] - ref) / tol).max())
         assert (np.abs(gm[u] - m) <= off).all()
+
+
+# ------------------------------------------------------------------------------------------ K
+def _codes_of(rng, units, nb, k, v=1.0):
+    """A store with the codes of N(0, 1) times k and v, and scales of 1."""
+    store = np.zeros((units, nb, O.BLOCK_BYTES), np.uint8)
+    for kind, size in (("k", k), ("v", v)):
+        x = rng.standard_normal((units, nb, 64, 128)) * size
+        store[..., O.AT[kind].ravel()] = O.encode(x).reshape(units, nb, -1)
+    _set_scales(store, ks=1.0, vs=1.0)
+    return store
+
+
+@pytest.mark.parametrize("group,nq", FORMS)
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -60, 1.0, 2.0 ** 33, 3e38])
+def test_the_largest_of_logits_beyond_float32_takes_all(scale, group, nq):
+    """Blocks with different K scales, the larger ones with the smaller codes, so that codes alone mislead.  A logit is off
+    by 2^-17 of S = scale sum |q| |k| at most (the sums, the roundings and what 2^90 and beyond keep), so a token that leads
+    by that of both and by 40 has a weight of 1 in f16 and float32, the others 0, and the result is its V, which bf16
+    holds exactly."""
+    rng = np.random.default_rng(70)
+    units, blocks = 6, 12
+    ks = np.array([119, 118, 114, 112, 107, 98, 90, 80, 60, 20, -20, -118])
+    size = np.exp2(rng.uniform(0, 1, (units, blocks)) * np.minimum(119 - ks, 13) - 6)
+    store = _codes_of(rng, units, blocks, size[..., None, None])
+    order = np.argsort(rng.random((units, blocks)), 1)
+    _set_scales(store, ks=np.exp2(ks))
+    store = np.take_along_axis(store, order[..., None], 1)
+    lens = np.array([64 * blocks] * 3 + [64 * blocks - 37] * 3)
+    q = _queries(rng, units, group * nq)
+    out, mass, err = _attend(q, torch.from_numpy(store).cuda(), _i32(lens), group, nq, blocks, max_len=64 * blocks, scale=scale)
+    got, gm, qq, held = _f64(out), _f64(mass), _f64(q), 0
+    assert err == 0 and np.isfinite(got).all() and np.isfinite(gm).all()
+    assert (np.abs(gm.sum(1) - group * nq) <= 1e-4).all()
+    scale = scale or 1 / math.sqrt(128)
+    for u in range(units):
+        k, v = (x.reshape(-1, 128) for x in O.unpack(store[u]))
+        for r in range(group * nq):
+            n = lens[u] - (nq - 1 - r % nq)
+            z, s = k[:n] @ qq[u, r] * scale, np.abs(k[:n]) @ np.abs(qq[u, r]) * scale
+            top = z.argmax()
+            lead = z[top] - z - 2.0 ** -17 * (s[top] + s)
+            lead[top] = np.inf
+            if lead.min() > 40:
+                held += 1
+                assert np.array_equal(got[u, r], v[top]), (u, r)
+    assert held >= units * group * nq // 2
+
+
+@pytest.mark.parametrize("group,nq", FORMS)
+@pytest.mark.parametrize("scale,size,ks,codes", [
+    (3e38, -9, -118, 0.25),            # the scale in base 2 is beyond float32, the logits are ordinary
+    (2.0 ** 100, 0, -110, 2.0 ** 6),    # ... and with larger codes
+    (2.0 ** -40, -80, 116, 4.0),       # its product with the row's power of two is below float32's normal range
+    (2.0 ** -16, -110, 119, 64.0),
+    (2.0 ** -140, 20, 119, 4.0),       # the scale itself is
+    (0.0, 120, -118, 2.0),             # rows of q near bf16's largest
+    (0.0, -120, 119, 4.0),             # and smallest
+], ids=["scale-inf", "scale-large", "alpha-tiny", "alpha-tiniest", "scale-tiny", "q-large", "q-small"])
+def test_factors_of_any_size(scale, size, ks, codes, group, nq):
+    rng = np.random.default_rng(71)
+    store = _codes_of(rng, 3, 5, codes)
+    _set_scales(store, ks=2.0 ** ks)
+    q = (_queries(rng, 3, group * nq).double() * 2.0 ** size).to(torch.bfloat16)
+    _check(q, store, np.array([320, 200, 33]), group, nq, max_len=320, scale=scale)
+
+
+@pytest.mark.parametrize("group,nq", FORMS)
+def test_blocks_of_ordinary_logits_beside_a_huge_scale(group, nq, many_blocks):
+    """A block with the largest s_K and codes of zero has logits of zero, also where its factor is beyond float32."""
+    rng = np.random.default_rng(72)
+    store = _store(rng, many_blocks, 3, 6)
+    for b in (0, 3):
+        store[:, b, O.AT["k"].ravel()] = 0
+    _set_scales(store, ks=np.array([2.0 ** 119, 2.0 ** -8, 2.0 ** -9, 2.0 ** 119, 2.0 ** -7, 2.0 ** -8]))
+    _check(_queries(rng, 3, group * nq), store, np.array([384, 300, 250]), group, nq, max_len=384)
