@@ -21,6 +21,7 @@
 // thirds empty.  Shorter calls pay for their start and end: 256 units listing 81 blocks 56 us, 0.91, with the masses of 128
 // 88 us, 0.91.  (With the copies by a thread that the compiler does not know to be one, 57.4 and 90.)
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "byte_split.cuh"
@@ -101,9 +102,15 @@ struct ByteRows {
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
+// A score x to a logit where the block's factor is beyond kWideFactor for some row.  (Eight in line made the shortest calls 2 %
+// slower.)
+static __device__ __noinline__ float wide_one(float x, float inv, float sk, float scale_m, int scale_e) {
+  const float y = wide_logit(sk == 0.f ? 0.f : x * scale_m, scale_e + exponent_of(inv) + exponent_of(sk));
+  return inv != inv ? inv : y;
+}
 // One half block: both tiles of tokens at once, so that their chains of dependent operations overlap.
 // left: tokens of the context from its first on; mass: where its sums go, or null.
-__device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, const ByteFactors& F, double scale64,
+__device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, const ByteFactors& F, float scale_m, int scale_e,
                                              unsigned char* stage, uint32_t (*poison)[4], int left, int rows, int nq,
                                              float2* mass, int lane) {
   const int g = lane >> 2, t = lane & 3;
@@ -137,30 +144,39 @@ __device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, co
       }
     }
   }
-  // logits, and whether a row's best would weigh more than its reference allows
-  float best[2];
-  bool raise = false;
-  const float f0 = F.alpha[0] * s.x, f1 = F.alpha[1] * s.x;
-  const bool wide = !(F.most * s.x <= kWideFactor);
+  // logits; whether a row's best would weigh more than its reference allows, or something else wants care
+  float y[2][4];
+  const float sk = F.most * s.x <= kWideFactor ? s.x : __int_as_float(0x7fc00000), f0 = F.alpha[0] * sk, f1 = F.alpha[1] * sk;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      z[i][e] = wide ? wide_logit(z[i][e], F.inv[e & 1], s.x, scale64) : z[i][e] * (e & 1 ? f1 : f0);
-      if (tail) {
+    for (int e = 0; e < 4; ++e) y[i][e] = z[i][e] * (e & 1 ? f1 : f0);
+  auto hide = [&]() {  // what a row does not see
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
         const int row = 2 * t + (e & 1), token = kByteTileTokens * i + g + 8 * (e >> 1);
-        if (row >= rows || token >= left - (nq - 1) + row % nq) z[i][e] = -INFINITY;
+        if (row >= rows || token >= left - (nq - 1) + row % nq) y[i][e] = -INFINITY;
       }
+  };
+  if (tail) hide();
+  bool raise = s.y * A.per > kLargeScale;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    raise |= !(max_or_nan(max_or_nan(y[0][e], y[0][e + 2]), max_or_nan(y[1][e], y[1][e + 2])) - A.top[e] <= kTopWeight);
+  if (__any_sync(0xffffffffu, raise)) {
+    if (s.y * A.per > kLargeScale) A.to_large();
+    if (!(F.most * s.x <= kWideFactor)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[i][e] = wide_one(z[i][e], F.inv[e & 1], s.x, scale_m, scale_e);
+      if (tail) hide();
     }
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    best[e] = fmaxf(fmaxf(z[0][e], z[0][e + 2]), fmaxf(z[1][e], z[1][e + 2]));
-    raise |= best[e] - A.top[e] > kTopWeight;
-  }
-  if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float b = best[e];
+      float b = fmaxf(fmaxf(y[0][e], y[0][e + 2]), fmaxf(y[1][e], y[1][e + 2]));
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
       if (b - A.top[e] > kTopWeight) {  // the row's lanes agree; rows differ
@@ -183,7 +199,7 @@ __device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, co
     float w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      w[e] = ex2(z[i][e] - A.top[e & 1]);
+      w[e] = ex2(y[i][e] - A.top[e & 1]);
       sum[e & 1] += w[e];
     }
     p[i][0] = movmatrix_trans(pack_half2(w[0], w[1]));
@@ -199,7 +215,6 @@ __device__ __forceinline__ void process_half(ByteRows& A, const ByteQuery& Q, co
     }
     if (g == 0 && 2 * t < rows) *reinterpret_cast<float4*>(mass + 2 * t) = make_float4(A.top[0], sum[0], A.top[1], sum[1]);
   }
-  if (s.y * A.per > kLargeScale) A.to_large();
   const float sv = s.y * A.per;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -311,7 +326,7 @@ __global__ void __launch_bounds__(kByteThreads, kCtasPerSm) byte_attend_kernel(c
           const int left = (a.sel ? list[j].y : seg.len - (b0 + j) * kBlock) - half * kHalfTokens;
           float2* mass = nullptr;
           if (a.mass) mass = a.half + (((size_t)u * a.blocks + (a.sel ? list[j].z : b0 + j)) * 2 + half) * a.mass_rows;
-          process_half(A, Q, F, a.scale64, ring + out * kHalfStage, poison, left, a.rows, a.nq, mass, lane);
+          process_half(A, Q, F, a.scale_m, a.scale_e, ring + out * kHalfStage, poison, left, a.rows, a.nq, mass, lane);
           __syncwarp();  // the stage is read
           issue();
         }
@@ -499,7 +514,7 @@ static void set_scale(ByteArgs& a, float softmax_scale) {
   const double exact = scale * 1.4426950408889634;
   const bool normal = exact >= 0x1p-126 && exact <= 0x1p127;
   a.scale = normal ? scale * 1.4426950408889634f : INFINITY;
-  a.scale64 = normal ? a.scale : exact;
+  a.scale_m = (float)std::frexp(normal ? (double)a.scale : exact, &a.scale_e);
 }
 
 static nosa_status byte_attend(ByteArgs& a, void* scratch, size_t scratch_bytes, cudaStream_t st) {

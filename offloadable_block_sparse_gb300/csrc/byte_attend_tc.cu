@@ -21,6 +21,8 @@
 // products by one warp and all copies by another: 62.8).  64 units of 64 blocks 21.8 us with 32 rows, 17.9 with 16 (mma.sync 36.7 and
 // 21.8), 256 of 32 36.1 and 30.0 (59.7 and 34.1), 2 of 32 9.8 and 8.1 (15.2 and 10.2).  Tried without gain: 128 threads;
 // one barrier a chunk, with the next chunk's keys and scores before this one's products (69); prefetching into L2.
+#include <type_traits>
+
 #include "byte_split.cuh"
 #include "host.h"
 #include "tc.cuh"
@@ -134,21 +136,6 @@ __device__ __forceinline__ float sum_rows(const float (&v)[R], int lane) {
   return x[0];
 }
 
-// Turns a thread's scores y into logits: one by one, through places in P that no other thread writes, which are the 16-byte
-// words of its f16 weights (the first at `word`) and those 64 bytes from there in the unswizzled order, which hold none.
-template <int R>
-__device__ __forceinline__ float4* other_word(float4* word, int i) {
-  return reinterpret_cast<float4*>(reinterpret_cast<uintptr_t>(word) ^ (16 * (i % (R / 8)) + 64 * (i / (R / 8))));
-}
-template <int R>
-__device__ __noinline__ void wide_logits(float4* word, const float* invs, const float* sk, double scale) {
-#pragma unroll 1
-  for (int r = 0; r < R; ++r) {
-    float& y = reinterpret_cast<float*>(other_word<R>(word, r / 4))[r % 4];
-    y = wide_logit(y, invs[r], *sk, scale);
-  }
-}
-
 // Four consecutive floats of shared memory that all lanes read.
 __device__ __forceinline__ void read4(float (&v)[4], const float* p) {
   const float4 x = *reinterpret_cast<const float4*>(p);
@@ -164,7 +151,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   __shared__ int4 list[kQaList];
   __shared__ int scan[32], found[2];
   __shared__ uint32_t tbase;
-  __shared__ int wide[kTcChunkBlocks];  // whether the block's logits are wide_logit's
   __shared__ __align__(16) float alpha[NR], invs[NR], top[NR], raised[NR], factor[kTcChunkBlocks][NR];
   __shared__ uint32_t best[4][NR];
   __shared__ float sums[4][NR], wr[1][NR], wl[1][NR];
@@ -194,7 +180,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
   // The stage of the chunk in work, which is also its phase of bar_s (and of bar_o, whose chunk before has the other), and the
   // phases of the stages' copies (a bit each; there too, for want of a register, kLargeBit: o is in units of kLargeUnit).
   int st = 0, ph_raw = 0;
-  constexpr int kLargeBit = 4;
+  constexpr int kLargeBit = 4, kOddBias = 1024;
   bool late = false, stuck = false;  // a wait gave up: known to all behind the next barrier; of this warp, for products
   while (share.todo > 0) {
     const int u = share.u;
@@ -281,11 +267,11 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           const bool there = kTcChunkBlocks * c + b < n;
           const float2 s = there ? *reinterpret_cast<const float2*>(scales[st][b]) : make_float2(0.f, 0.f);
           scale[b] = s.y;
-          if (warp == 6 + b) {
-            const float al = lane < NR ? alpha[lane] : 0.f, f = al * s.x;
-            if (lane < NR) factor[b][lane] = f;
-            const bool any = __any_sync(0xffffffffu, isinf(al) || f > kWideFactor);
-            if (lane == 0) wide[b] = any;
+          if (warp == 6 + b && lane < NR) {  // (a large V scale makes its block's factors odd too, so that it is looked at)
+            const float al = alpha[lane], f = al * s.x;
+            uint32_t odd = 0x7fffffffu;  // a NaN whose low bits are the exponent and kOddBias (0: no scale), or all set
+            if (al == al) odd = 0x7fc00000u + (s.x == 0.f ? 0 : kOddBias + a.scale_e + exponent_of(invs[lane]) + exponent_of(s.x));
+            factor[b][lane] = f <= kWideFactor && s.y <= kLargeScale ? f : __uint_as_float(odd);
           }
         }
         tc::wait_st();
@@ -311,21 +297,39 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
         for (int i = 0; i < kByteTiles; ++i)
           v[i] = *reinterpret_cast<const uint4*>(stage + half * kByteScales + i * kByteTile + kByteV + 512 * quarter + 16 * lane);
         place_values(tlane + kTcV + half * (kBlock / 2), v);
-        if (!(ph_raw & kLargeBit) && fmaxf(scale[0], scale[1]) > kLargeScale) {  // (products of the chunks before are in o)
-          ph_raw |= kLargeBit;
-#pragma unroll
-          for (int r = 0; r < R; ++r) o[r] *= 1.f / kLargeUnit;
-        }
 #pragma unroll
         for (int b = 0; b < kTcChunkBlocks; ++b) sv[b] = ph_raw & kLargeBit ? scale[b] * (1.f / kLargeUnit) : scale[b];
 
         // the thread's token: the logits of its rows
         const int block = at / kBlock, j = kTcChunkBlocks * c + block, mine = left_of(j) - at % kBlock;  // rows of query tokens from nq - mine on see it
         wait_for(&bar_s, st);
-        // Weights 2^(logit - top), as f16 into P.  Where one is more than its reference allows, all raise theirs and weigh again.
+        // Weights 2^(logit - top), as f16 into P.  Where one is more than its reference allows (or a factor or a V scale wants
+        // care), all raise theirs and weigh again.
         float y[R];
+        auto weigh = [&](auto again) {
+          const bool pass = again;
+          if (pass) {  // where a factor is odd, but for rows of q that hold a NaN, all scores become logits in their place first
+            uint32_t odd = __float_as_uint(factor[0][tid % (kTcChunkBlocks * NR)]);
+            if (__syncthreads_or(odd > 0x7f800000u && odd != 0x7fffffffu)) {
 #pragma unroll 1
-        for (int pass = 0;; ++pass) {
+              for (int r = 0; r < R; ++r) {
+                uint32_t v[2] = {tc::ld1(trow + r), tc::ld1(trow + NR + r)};
+                tc::wait_ld();
+                tc::landed(v);
+                float x = fmaf(__uint_as_float(v[1]), 0.0625f, __uint_as_float(v[0]));
+                const float f = factor[block][r0 + r];
+                odd = __float_as_uint(f);
+                const bool wide = odd > 0x7f800000u && odd != 0x7fffffffu;
+                x = wide ? wide_logit(x * a.scale_m, (int)(odd - 0x7fc00000u) - kOddBias) : x * f;
+                tc::st1(trow + r, __float_as_uint(x));
+                tc::st1(trow + NR + r, 0u);
+              }
+              tc::wait_st();
+              __syncthreads();
+              if (tid < kTcChunkBlocks * NR) factor[0][tid] = 1.f;
+              __syncthreads();
+            }
+          }
           uint32_t d[R], e[R];
           tc::ld(trow, d);
           tc::ld(trow + NR, e);
@@ -333,25 +337,11 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           tc::landed(d);
           tc::landed(e);
 #pragma unroll
-          for (int r = 0; r < R; ++r) y[r] = fmaf(__uint_as_float(e[r]), 0.0625f, __uint_as_float(d[r]));
-          if (!wide[block]) {
+          for (int r = 0; r < R; r += 4) {
+            float f[4];
+            read4(f, &factor[block][r0 + r]);
 #pragma unroll
-            for (int r = 0; r < R; r += 4) {
-              float f[4];
-              read4(f, &factor[block][r0 + r]);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) y[r + i] *= f[i];
-            }
-          } else {  // one by one, through the place of the thread's weights
-            float4* word = reinterpret_cast<float4*>(sm + kTcP + at * 128 + 16 * (r0 / 8 ^ (at & 7)));
-#pragma unroll
-            for (int i = 0; i < R / 4; ++i) *other_word<R>(word, i) = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-            wide_logits<R>(word, invs + r0, scales[st][block], a.scale64);
-#pragma unroll
-            for (int i = 0; i < R / 4; ++i) {
-              const float4 v = *other_word<R>(word, i);
-              y[4 * i] = v.x, y[4 * i + 1] = v.y, y[4 * i + 2] = v.z, y[4 * i + 3] = v.w;
-            }
+            for (int i = 0; i < 4; ++i) y[r + i] = fmaf(__uint_as_float(e[r + i]), 0.0625f, __uint_as_float(d[r + i])) * f[i];
           }
           if (mine < a.nq) {
             int query = r0 % a.nq;
@@ -380,13 +370,20 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
               raised[tid] = f;
             }
             __syncthreads();
+            float unit = 1.f;
+            if (!(ph_raw & kLargeBit) && fmaxf(sv[0], sv[1]) > kLargeScale) {  // (the products of the chunks before are in o)
+              ph_raw |= kLargeBit;
+              unit = 1.f / kLargeUnit;
+              sv[0] *= unit;
+              sv[1] *= unit;
+            }
 #pragma unroll
             for (int r = 0; r < R; r += 4) {
               float f[4];
               read4(f, &raised[r0 + r]);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                o[r + i] *= f[i];
+                o[r + i] *= f[i] * unit;
                 l[r + i] *= f[i];
               }
             }
@@ -400,7 +397,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float x = y[r + i] - ref[i];
-              over = fmaxf(over, x);
+              over = max_or_nan(over, x);
               y[r + i] = ex2(x);
             }
             p[r / 2] = pack_half2(y[r], y[r + 1]);
@@ -413,9 +410,16 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           tc::wait_st();             // V^T
           fence_proxy_async_smem();  // P is read by the tensor core
           tc::fence_before();
-          const bool raise = __syncthreads_or(over > kTopWeight);
+          const bool raise = __syncthreads_or(!(over <= kTopWeight));
           tc::fence_after();
-          if (!raise || pass) break;
+          return raise;
+        };
+        if constexpr (NR == 16) {  // (64 units of 64 blocks: 19.9 us so, 20.2 as below; 32 rows 24.3 and 23.9)
+          if (weigh(std::false_type{})) weigh(std::true_type{});
+        } else {
+#pragma unroll 1
+          for (bool pass = false; weigh(pass) && !pass; pass = true) {
+          }
         }
         if ((warp == 3 || warp == 5) && tc::elect()) {
           const int b = warp == 5;

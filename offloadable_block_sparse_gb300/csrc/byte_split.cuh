@@ -24,17 +24,17 @@ constexpr float kLargeScale = 0x1p80f, kLargeUnit = 0x1p40f;
 __device__ __forceinline__ float large_sum(float l, bool large) { return large ? -l : l; }
 
 // Adds a part (reference and marked sum s, four dims o) to a running one in units that `large` tells.
-__device__ __forceinline__ void merge_byte_part(float& R, float& L, float4& O, bool& large, const float2& s, float4 o) {
+__device__ __forceinline__ void merge_byte_part(float& R, float& L, float4& O, bool& large, const float2& s, const float4& o) {
   const bool part = __float_as_int(s.y) < 0;
-  if (part != large) {
-    float4& x = large ? o : O;
-    x.x *= 1.f / kLargeUnit;
-    x.y *= 1.f / kLargeUnit;
-    x.z *= 1.f / kLargeUnit;
-    x.w *= 1.f / kLargeUnit;
-    large = true;
-  }
-  merge_part(R, L, O, s.x, fabsf(s.y), o);
+  const float top = fmaxf(R, s.x), f = ex2(R - top), h = ex2(s.x - top);
+  const float fo = part && !large ? f / kLargeUnit : f, ho = large && !part ? h / kLargeUnit : h;
+  R = top;
+  L = L * f + fabsf(s.y) * h;
+  O.x = O.x * fo + o.x * ho;
+  O.y = O.y * fo + o.y * ho;
+  O.z = O.z * fo + o.z * ho;
+  O.w = O.w * fo + o.w * ho;
+  large |= part;
 }
 
 struct ByteArgs {
@@ -54,26 +54,37 @@ struct ByteArgs {
   int units, nq, rows, mass_rows, max_blocks, max_sel, max_len, blocks;  // blocks: per unit, listed or up to max_len
   int split;
   float scale;    // softmax scale x log2(e); infinite where float32's normal range does not hold it
-  double scale64;
+  float scale_m;  // the same as scale_m 2^scale_e, in any case
+  int scale_e;
   long long wait_limit;  // SM cycles a wait for a staged half block may take before it gives up (< 0: none)
 };
 
 // A logit is a score (below 2^26: 128 products of a q below 2^10 and a code of at most 448) x alpha x s_K, alpha = scale x inv
-// being what turns the row's scores into logits in base 2.  All but s_K is one float32 where that neither overflows nor loses
-// bits, infinity elsewhere; and where alpha s_K is above kWideFactor for some row, infinity among them, all of a block's logits
-// are computed by wide_logit.
+// being what turns the row's scores into logits in base 2, inv a power of two.  alpha is one float32 where that neither
+// overflows nor loses bits, infinity elsewhere.  A factor alpha s_K above kWideFactor, infinity among them, is a NaN to the
+// kernels; where they raise references they look for these and take wide_logit with the factor's own exponent.
 constexpr float kWideFactor = 0x1p64f;
 __device__ __forceinline__ float row_factor(float scale, float inv) {
   const float alpha = scale * inv;
   return alpha != alpha || (alpha >= 0x1p-100f && alpha <= 0x1p100f) ? alpha : INFINITY;
 }
-// In 64 bits, and for sizes beyond 2^90, which the others stay below, as 2^90 (size / 2^90)^(1/16): at most 2^111, in the same
-// order, with differences as far beyond any softmax's reach.  (Cut at a largest factor or logit, unequal ones would be equal or
-// change places.)
-static __device__ __noinline__ float wide_logit(float score, float inv, float sk, double scale) {
-  const double x = scale * inv * sk * score, size = fabs(x);
-  if (!(size > 0x1p90)) return (float)x;  // (a NaN stays)
-  return copysignf((float)(0x1p90 * sqrt(sqrt(sqrt(sqrt(size * 0x1p-90))))), (float)(x > 0) - 0.5f);
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23 & 0xff) - 127; }
+// x 2^e for x = score x (scale's mantissa).  Sizes from 2^90 on, which the others stay below, are drawn together, sixteen powers
+// of two to one and evenly between them: below 2^110 then, in the same order and with differences as far beyond any softmax's
+// reach.  (Cut at a largest factor or logit, unequal ones would be equal or change places.)
+__device__ __forceinline__ float wide_logit(float x, int e) {
+  const uint32_t bits = __float_as_uint(x), size = bits & 0x7fffffffu;
+  if (size == 0 || size > 0x7f800000u) return x;
+  const int to = (int)(size >> 23) - 127 + e;
+  if (to < -126) return 0.f;
+  const uint32_t drawn = ((uint32_t)(90 + 127) << 23) + (((uint32_t)(to - 90) << 23 | (size & 0x7fffffu)) >> 4);
+  return __uint_as_float((bits & 0x80000000u) | (to < 90 ? size + ((uint32_t)e << 23) : drawn));
+}
+// The larger, or a NaN if one is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 // A row's new reference for its best logit: the best itself where it is so large that the difference would not be what
 // it should.
