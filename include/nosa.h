@@ -636,8 +636,8 @@ nosa_status nosa_byte_attend(const uint16_t* q, const uint8_t* store, const int3
                              void* stream);
 
 /* Scratch bytes of the two attention calls for `rows` = group * n_queries query rows per unit and at most `blocks`
- * blocks per unit, with their masses (mass != 0) or without: never more than 512 + 536 rows (units + 16 SMs), and
- * 16 (rows + 1) units blocks more with masses; never less for more units, rows or blocks or with masses.  0 on a
+ * blocks per unit, with their masses (mass != 0) or without: never more than 512 + 536 rows (units + 16 SMs) (or, if less,
+ * 512 + 536 rows (2048 + 16 SMs) + 16 rows units), and 16 (rows + 1) units blocks more with masses; never less for more units, rows or blocks or with masses.  0 on a
  * bad argument or without a device. */
 size_t nosa_byte_scratch_bytes(int units, int rows, int blocks, int mass);
 

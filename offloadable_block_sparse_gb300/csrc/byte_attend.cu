@@ -463,11 +463,12 @@ static size_t byte_parts_bytes(size_t units, size_t parts, int rows, size_t bloc
          (mass ? units * blocks * 2 * mass_rows(rows) * sizeof(float2) : 0) + 16;
 }
 
-// What a call wants for its scratch: enough for pieces whether it takes them or not, so that more units, rows or blocks never
-// want less, and a scratch made for the largest call serves them all.
+// What a call wants for its scratch: enough for pieces whether it takes them or not (of the most units that pieces are made
+// of, where there are more), so that more units, rows or blocks never want less, and a scratch made for the largest call serves
+// them all.
 static size_t byte_bytes(const ByteDevice& d, int units, int rows, int blocks, bool mass) {
   const int wave = std::max(d.wave[0], d.wave[1]);
-  return byte_parts_bytes(units, (size_t)wave + units, rows, blocks, mass);
+  return byte_parts_bytes(units, (size_t)wave + std::min(units, kQaSplitUnits), rows, blocks, mass);
 }
 
 // The fewest blocks that keep a CTA of the kernel for so many rows busy: half a block a warp, or a chunk.

@@ -13,6 +13,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no CUDA device", allow_module_level=True)
 
+from offloadable_block_sparse_gb300 import nosa as N  # noqa: E402
 from tests.test_gpu_byte import (_attend, _expect, _f64, _i32, _lengths, _queries, _some, _store,  # noqa: E402
                                  many_blocks)  # noqa: F401 (a fixture)
 
@@ -179,3 +180,33 @@ def test_blocks_of_ordinary_logits_beside_a_huge_scale(group, nq, many_blocks):
         store[:, b, O.AT["k"].ravel()] = 0
     _set_scales(store, ks=np.array([2.0 ** 119, 2.0 ** -8, 2.0 ** -9, 2.0 ** 119, 2.0 ** -7, 2.0 ** -8]))
     _check(_queries(rng, 3, group * nq), store, np.array([384, 300, 250]), group, nq, max_len=384)
+
+
+# ------------------------------------------------------------------------------------------ scratch
+@pytest.mark.parametrize("mass", [False, True])
+def test_many_units_want_no_scratch_for_pieces(mass):
+    """Beyond 2,048 units a CTA takes a unit: no parts to keep, but the scratch still never shrinks with more units."""
+    last, most = 0, 536 * 32 * (2048 + 8 * WAVE)
+    for units in (2047, 2048, 2049, 5000, 1 << 20):
+        n = N.nosa_byte_scratch_bytes(units, 32, 1, mass)
+        assert last <= n <= 512 + most + 16 * 32 * units + (16 * 33 * units if mass else 0)
+        last = n
+
+
+@pytest.mark.parametrize("group,nq", FORMS)
+def test_many_units_stay_within_their_scratch(group, nq, many_blocks):
+    rng = np.random.default_rng(80)
+    units, nb, rows = 2500, 3, group * nq
+    store, q = torch.from_numpy(_store(rng, many_blocks, units, nb)).cuda(), _queries(rng, units, rows)
+    need = N.nosa_byte_scratch_bytes(units, rows, nb, True)
+    scratch = torch.full((need + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    scratch[:4] = 0
+    lens = _i32(_lengths(units, nb, nq))
+    want = _attend(q, store, lens, group, nq, nb, max_len=64 * nb,
+                   scratch=torch.zeros(4 * need + (1 << 26), dtype=torch.uint8, device="cuda"))
+    out, mass = torch.empty_like(q), torch.empty_like(want[1])
+    N.nosa_byte_dense_attend(q, store, units, group, nq, nb, lens, 64 * nb, out, scratch, need, mass=mass,
+                             stream=torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert (scratch[need:] == 0xA5).all() and scratch[:4].sum() == 0
+    assert torch.equal(out, want[0]) and torch.equal(mass, want[1])
