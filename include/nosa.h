@@ -555,7 +555,8 @@ size_t nosa_quant_scratch_bytes(int units, int rows, int blocks);
 
 /* Test hook, as NOSA_F_TEST_ZERO_WAIT is for a context's calls: SM cycles that a wait for a staged tile may take in
  * the attention calls over 4-bit and 8-bit stores that this host thread makes from now on (negative: waits give up at
- * once; 0: the built-in limit, about a second, which is also the most).  Calls captured in a graph keep the limit of their
+ * once, those for tensor-core products among them; -2: over 8-bit stores only the latter, which calls with more than 8 rows
+ * make; 0: the built-in limit, about a second, which is also the most).  Calls captured in a graph keep the limit of their
  * capture. */
 nosa_status nosa_debug_quant_wait(long long cycles);
 

@@ -526,7 +526,8 @@ static nosa_status byte_attend(ByteArgs& a, void* scratch, size_t scratch_bytes,
   const size_t parts = (size_t)plan.ctas + a.units;
   unsigned char* p = static_cast<unsigned char*>(scratch);
   a.split = plan.split;
-  a.wait_limit = g_wait_limit;
+  a.wait_limit = g_wait_limit == kProductsGiveUp ? kWaitCycles : g_wait_limit;
+  a.products_late = g_wait_limit < 0;
   a.mass_rows = mass_rows(a.rows);
   a.err = reinterpret_cast<int*>(p);
   a.half = reinterpret_cast<float2*>(p + kQaErrBytes);

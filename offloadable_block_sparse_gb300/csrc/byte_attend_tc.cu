@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
     bool flying = false;
     // waits are decided for the whole warp: the tensor-memory accesses behind them are warp-collective
     auto wait_for = [&](uint64_t* bar, int phase) {
-      stuck |= !__all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, kWaitCycles));
+      stuck |= !__all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, kWaitCycles)) || a.products_late;
       tc::fence_after();
     };
     auto add_products = [&]() {  // O += s_V of the chunk before: the thread's dim, its rows

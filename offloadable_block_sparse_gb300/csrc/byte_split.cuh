@@ -56,7 +56,8 @@ struct ByteArgs {
   float scale;    // softmax scale x log2(e); infinite where float32's normal range does not hold it
   float scale_m;  // the same as scale_m 2^scale_e, in any case
   int scale_e;
-  long long wait_limit;  // SM cycles a wait for a staged half block may take before it gives up (< 0: none)
+  long long wait_limit;  // SM cycles a wait for staged blocks may take before it gives up (< 0: none)
+  bool products_late;    // count those for products as given up
 };
 
 // A logit is a score (below 2^26: 128 products of a q below 2^10 and a code of at most 448) x alpha x s_K, alpha = scale x inv

@@ -48,6 +48,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 // SM cycles that a wait of this host thread's attention calls may take (nosa_debug_quant_wait; in quant_attend.cu).
 extern thread_local long long g_wait_limit;
+constexpr long long kProductsGiveUp = -2;  // of the 8-bit store's waits only those for products
 
 // Waits for a staged half block.  Returns whether it came within `limit` cycles; waits on for those that did not, as long
 // again as the longest limit, so that the copy has landed before the ring has another use or the CTA ends.

@@ -390,7 +390,7 @@ def nosa_quant_attend(q, store, sel, sel_slot, units, group, n_queries, max_bloc
 
 
 def nosa_debug_quant_wait(cycles: int) -> None:
-    """Test hook: the wait limit of this thread's 4-bit attention calls (see include/nosa.h)."""
+    """Test hook: the wait limit of this thread's 4-bit and 8-bit attention calls (see include/nosa.h)."""
     _check(lib().nosa_debug_quant_wait(cycles), "nosa_debug_quant_wait")
 
 

@@ -210,3 +210,31 @@ def test_many_units_stay_within_their_scratch(group, nq, many_blocks):
     torch.cuda.synchronize()
     assert (scratch[need:] == 0xA5).all() and scratch[:4].sum() == 0
     assert torch.equal(out, want[0]) and torch.equal(mass, want[1])
+
+
+# ------------------------------------------------------------------------------------------ waits
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("group,nq", FORMS)
+@pytest.mark.parametrize("plan", PLANS)
+def test_a_wait_for_products_that_gives_up_is_reported(plan, group, nq, listed, many_blocks):
+    """The copies come in time, the products do not (they are waited for all the same): NaN and bit 1, and the next call is
+    whole.  Up to 8 rows there is no such wait."""
+    units, nb = PLANS[plan]
+    rng = np.random.default_rng(81)
+    store, q = torch.from_numpy(_store(rng, many_blocks, units, nb)).cuda(), _queries(rng, units, group * nq)
+    lens = _i32(np.full(units, 64 * nb))
+    sel = _i32(np.tile(np.arange(nb), (units, 1))) if listed else None
+    call = lambda: _attend(q, store, lens, group, nq, nb, sel=sel, max_len=64 * nb)  # noqa: E731
+    want = call()
+    assert want[2] == 0
+    N.nosa_debug_quant_wait(-2)
+    try:
+        out, mass, err = call()
+    finally:
+        N.nosa_debug_quant_wait(0)
+    if group * nq > 8:
+        assert err == 2 and torch.isnan(out).all() and torch.isnan(mass).all()
+    else:
+        assert err == 0 and torch.equal(out, want[0]) and torch.equal(mass, want[1])
+    out, mass, err = call()
+    assert err == 0 and torch.equal(out, want[0]) and torch.equal(mass, want[1])
