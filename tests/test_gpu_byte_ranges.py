@@ -238,3 +238,181 @@ def test_a_wait_for_products_that_gives_up_is_reported(plan, group, nq, listed, 
         assert err == 0 and torch.equal(out, want[0]) and torch.equal(mass, want[1])
     out, mass, err = call()
     assert err == 0 and torch.equal(out, want[0]) and torch.equal(mass, want[1])
+
+
+# ------------------------------------------------------------------------------------------ lists
+# units, listed blocks: more than the 256 entries that a CTA looks up at a time, in a CTA a unit and in a piece
+LISTS = {"unit-a-cta": (2049, 300), "pieces": (17 * WAVE // 20, 512)}
+
+
+@pytest.mark.parametrize("group,nq", FORMS + [(5, 1), (3, 3)])
+@pytest.mark.parametrize("plan", LISTS)
+def test_lists_longer_than_a_lookup(plan, group, nq, many_blocks):
+    """Lists of which the first 256 entries hold nothing, the others nothing, one block, odd numbers of blocks; through
+    slots of a small store."""
+    units, n = LISTS[plan]
+    rng = np.random.default_rng(90)
+    store = _store(rng, many_blocks, units, 5)
+    sel = rng.integers(0, 2000, (units, n)).astype(np.int32)
+    slots = rng.integers(0, 5, (units, n)).astype(np.int32)
+    sel[rng.random((units, n)) < 0.1] = -1
+    lens = np.full(units, 64 * 2000)
+    sel[0, :256], sel[1, 256:] = -1, -1
+    sel[2, 257:] = -1
+    sel[2, 256] = 1999
+    sel[3] = -1
+    sel[3, [7, 255, 256]] = [4, 1000, 9]
+    lens[4:8] = [0, 1, 64 * 900 + 33, 64 * 1500]  # entries behind the context are left out
+    sel[5, 299] = 0
+    sel[8] = np.arange(n)
+    _check(_queries(rng, units, group * nq), store, lens, group, nq, units=[0, 1, 2, 3, 4, 5, 6, 7, 8, units // 2, units - 1],
+           sel=sel, slots=slots)
+
+
+@pytest.mark.parametrize("group,nq", FORMS[1:])
+def test_listed_rows_past_4_gib(group, nq):
+    """4,688 blocks of one unit at the end of a store of more than 4 GiB, values repeated so that the oracle stays small."""
+    rng = np.random.default_rng(91)
+    nb = 2 ** 32 // O.BLOCK_BYTES + 40
+    blocks = _codes_of(rng, 1, 7, 60.0, 60.0)[0]
+    blocks[:, O.SCALES:O.SCALES + 8] = np.array([2.0 ** -6, 2.0 ** -6], np.float32).view(np.uint8)
+    store = torch.from_numpy(blocks).cuda().repeat(nb // 7 + 1, 1)[:nb].contiguous()
+    q, n = _queries(rng, 1, group * nq), 4688
+    sel = torch.arange(nb - n, nb, dtype=torch.int32, device="cuda")[None].contiguous()
+    out, mass, err = _attend(q, store, _i32([64 * nb]), group, nq, nb, sel=sel)
+    k, v = (x[(np.arange(n) + nb - n) % 7] for x in O.unpack(blocks))
+    ref, m, tol, off = _expect(_f64(q)[0], k, v, np.arange(nb - n, nb), 64 * nb, nq, 1 / math.sqrt(128))
+    assert err == 0 and (np.abs(_f64(out)[0] - ref) <= tol).all() and (np.abs(_f64(mass)[0] - m) <= off).all()
+
+
+@pytest.mark.parametrize("group", [2, 8])
+def test_a_context_selects_and_the_8_bit_store_is_attended(group):
+    """nosa_select's own list, -1 entries and all, over a store that got the same tokens."""
+    torch.cuda.set_device(0)
+    B, Hkv, T0, steps = 2, 2, 1500, 3
+    U = B * Hkv
+    cfg = N.make_config(num_layers=1, batch=B, num_q_heads=group * Hkv, num_kv_heads=Hkv, k_q=4, k_e=6, window_tokens=128,
+                        max_context=T0 + steps)
+    sizes = N.nosa_query_sizes(cfg)
+    cap, nb = sizes.select_slots, sizes.max_blocks
+    stream = torch.cuda.current_stream().cuda_stream
+    ctx = N.nosa_create(cfg, stream)
+    try:
+        rng = np.random.default_rng(92)
+        K, V = (torch.from_numpy(rng.standard_normal((B, Hkv, T0 + steps, 128))).to(torch.bfloat16).cuda() for _ in range(2))
+        W1 = (rng.standard_normal((Hkv, 128, 128)) / math.sqrt(128)).astype(np.float32)
+        W2 = (rng.standard_normal((Hkv, 128)) / math.sqrt(128)).astype(np.float32)
+        N.nosa_set_eviction_head(ctx, 0, W1, W2)
+        store = torch.zeros((U, nb, O.BLOCK_BYTES), dtype=torch.uint8, device="cuda")
+        k0, v0 = K[:, :, :T0].contiguous(), V[:, :, :T0].contiguous()
+        N.nosa_append_kv(ctx, 0, k0, v0, T0)
+        N.nosa_byte_append(k0, v0, store, U, T0, nb, stream=stream)
+        sel = torch.empty((U, cap), dtype=torch.int32, device="cuda")
+        for t in range(steps):
+            T = T0 + t + 1
+            k, v = K[:, :, T - 1].contiguous(), V[:, :, T - 1].contiguous()
+            q = _queries(rng, U, group)
+            N.nosa_append_kv(ctx, 0, k, v, 1)
+            N.nosa_byte_append(k, v, store, U, 1, nb, pos=_i32([T - 1] * U), stream=stream)
+            N.nosa_select(ctx, 0, q, sel_out=sel)
+            out, mass, err = _attend(q, store, _i32([T] * U), group, 1, nb, sel=sel)
+            assert N.nosa_sync(ctx) == N.NOSA_OK and err == 0
+            host, s = store.cpu().numpy(), sel.cpu().numpy()
+            assert (s >= 0).any(1).all()
+            for u in range(U):
+                kk, vv = O.unpack(host[u, np.maximum(s[u], 0)])
+                ref, m, tol, off = _expect(_f64(q)[u], kk, vv, s[u], T, 1, 1 / math.sqrt(128))
+                assert (np.abs(_f64(out)[u] - ref) <= tol).all() and (np.abs(_f64(mass)[u] - m) <= off).all()
+    finally:
+        N.nosa_destroy(ctx)
+
+
+# ------------------------------------------------------------------------------------------ q, and the other ranges
+@pytest.mark.parametrize("group,nq", FORMS)
+@pytest.mark.parametrize("above", [6, 12, 13, 16, 20])
+def test_small_values_of_q_beside_a_large_one_decide(above, group, nq):
+    """One value of each row is 2^above times the others' size, in a dim where K is zero: the logits are the small values'.
+    _expect counts what is off by 2^-21 of the row's largest with more than 8 rows."""
+    rng = np.random.default_rng(93)
+    store = _codes_of(rng, 4, 6, 2.0)
+    q = _queries(rng, 4, group * nq)
+    dims = rng.integers(0, 128, (4, group * nq))
+    store[..., O.AT["k"][:, np.unique(dims)].ravel()] = 0
+    for u in range(4):
+        q[u, torch.arange(group * nq), torch.from_numpy(dims[u])] = 2.0 ** above * (1 if u % 2 else -1.375)
+    _check(q, store, np.array([384, 383, 200, 65]), group, nq, max_len=384)
+
+
+@pytest.mark.parametrize("group,nq", FORMS[1:])
+def test_v_and_k_scales_far_apart_with_many_rows(group, nq, many_blocks):
+    """As test_blocks_of_very_different_scales, for the kernel of more than 8 rows."""
+    rng = np.random.default_rng(94)
+    units, nb = 4, 12
+    store = _store(rng, many_blocks, units, nb)
+    for b in range(nb):
+        for u, (ks, vs) in enumerate([(2.0 ** -8, 2.0 ** rng.integers(-100, 100)), (2.0 ** (b % 5 - 8), 2.0 ** -6),
+                                      (2.0 ** rng.integers(-20, -8), 2.0 ** rng.integers(-12, 12)), (0.0, 0.0)]):
+            store[u, b, O.SCALES:O.SCALES + 8] = np.array([ks, vs], np.float32).view(np.uint8)
+    _check(_queries(rng, units, group * nq), store, np.full(units, 64 * nb - 5), group, nq, max_len=64 * nb)
+
+
+@pytest.mark.parametrize("group,nq", FORMS[1:])
+@pytest.mark.parametrize("ks", [2.0 ** -118, 2.0 ** -30, 2.0 ** 6, 2.0 ** 20, 2.0 ** 60, 2.0 ** 119])
+@pytest.mark.parametrize("scale", [1e-30, 1.0, 2.0 ** 21, 2.0 ** 25, 2.0 ** 27, 2.0 ** 29, 2.0 ** 33, 1e30, 3e38])
+def test_logits_of_any_size_with_many_rows(ks, scale, group, nq, many_blocks):
+    """A token that leads by more than its logit and the others may be off (2^-17 of S, as above) and by 40 has all the weight;
+    logits below 2^-12 weigh the same within 2^-11 (twice 2^-12 / ln 2, half a step of f16's 2^-11 besides: 2^-10 of the
+    largest |v| covers both)."""
+    rng = np.random.default_rng(95)
+    store = _store(rng, many_blocks, 2, 6)
+    _set_scales(store, ks=ks)
+    q = _queries(rng, 2, group * nq)
+    lens = [384, 377]
+    out, mass, err = _attend(q, torch.from_numpy(store).cuda(), _i32(lens), group, nq, 6, max_len=384, scale=scale)
+    got, gm, qq = _f64(out), _f64(mass), _f64(q)
+    assert err == 0 and np.isfinite(got).all() and np.isfinite(gm).all()
+    for u in range(2):
+        k, v = (x.reshape(-1, 128) for x in O.unpack(store[u]))
+        for r in range(group * nq):
+            n = lens[u] - (nq - 1 - r % nq)
+            z, s = k[:n] @ qq[u, r] * scale, np.abs(k[:n]) @ np.abs(qq[u, r]) * scale
+            if s.max() < 2.0 ** -12:
+                o = v[:n].mean(0)
+                assert (np.abs(got[u, r] - o) <= 2.0 ** -8 * np.abs(o) + 2.0 ** -10 * np.abs(v).max()).all()
+                continue
+            top = z.argmax()
+            lead = z[top] - z - 2.0 ** -17 * (s[top] + s)
+            lead[top] = np.inf
+            if lead.min() > 40:
+                assert np.array_equal(got[u, r], v[top])
+
+
+@pytest.mark.parametrize("group,nq", FORMS[1:])
+def test_rows_of_q_that_are_not_finite_or_tiny_or_zero_with_many_rows(group, nq, many_blocks):
+    rng = np.random.default_rng(96)
+    store = _store(rng, many_blocks, 2, 3)
+    q = _queries(rng, 2, group * nq)
+    q[0, 1] = 0
+    q[0, 2] *= 2.0 ** -120
+    q[0, 3] *= 2.0 ** 100
+    q[0, 4, 100] = math.inf
+    q[0, 5, 3] = math.nan
+    q[0, 6, 17] = 1e4  # one value far above the others
+    q[0, 9] = 1e-40    # below bf16's normal range
+    st = torch.from_numpy(store).cuda()
+    out, mass, err = _attend(q, st, _i32([150, 150]), group, nq, 3, max_len=192)
+    rows = [r for r in range(group * nq) if r not in (4, 5)]
+    assert torch.isnan(out[0, 4:6]).all() and torch.isfinite(out[0, rows]).all() and torch.isnan(mass[0]).all()
+    assert err == 0 and torch.isfinite(out[1]).all() and torch.isfinite(mass[1]).all()
+    v = O.unpack(store[0])[1].reshape(-1, 128)
+    for r in (1, 2, 9):
+        o = v[:150 - (nq - 1 - r % nq)].mean(0)
+        assert (np.abs(_f64(out)[0, r] - o) <= 2.0 ** -8 * np.abs(o) + 2.0 ** -10 * np.abs(v).max()).all()
+    q[0, 3:6] = 1.0  # the rows beside those, against the oracle
+    _check(q, store, np.array([150, 0]), group, nq, max_len=192)
+    want = out[0, rows[7:]]
+    out, _, _ = _attend(q, st, _i32([150, 150]), group, nq, 3, max_len=192)
+    assert torch.equal(out[0, rows[7:]], want)  # what other rows hold changes nothing
+    q[1, 2, 5] = math.nan  # a row that sees nothing is zeros whatever it holds
+    out, mass, _ = _attend(q, st, _i32([150, 0]), group, nq, 3, max_len=192)
+    assert not out[1].any() and not mass[1].any()
