@@ -623,7 +623,8 @@ nosa_status nosa_byte_read(const uint8_t* store, int units, int max_blocks, cons
  * rows a unit those below 2^-22 of it, with more those below 2^-13, which are off by at most 2^-21 of it.
  * The weights exp(logit - reference) that multiply V are rounded to f16: by 2^-11 of themselves, small ones by 2^-35 of
  * the row's largest weight (2^-25 where logits are beyond 2^26).  Logits of any size are fine, beyond float32 too: there the
- * largest takes all (beyond 2^90 those within 2^-19 of it share).  So are values of any size: only in a unit with an s_V above 2^80 are results off by up to 2^-90 besides.
+ * largest takes all (beyond 2^90 those within 2^-19 of it share).  So are values of any size: only in a unit with an s_V
+ * above 2^80 are results off by up to 2^-90 besides.
  * Asynchronous on `stream`.  NOSA_ERR_CAPACITY if the scratch is too small. */
 nosa_status nosa_byte_dense_attend(const uint16_t* q, const uint8_t* store, int units, int group, int n_queries,
                                    int max_blocks, const int32_t* lens, int max_len, float softmax_scale, uint16_t* out,
@@ -638,13 +639,14 @@ nosa_status nosa_byte_attend(const uint16_t* q, const uint8_t* store, const int3
 
 /* Scratch bytes of the two attention calls for `rows` = group * n_queries query rows per unit and at most `blocks`
  * blocks per unit, with their masses (mass != 0) or without: never more than 512 + 536 rows (units + 16 SMs) (or, if less,
- * 512 + 536 rows (2048 + 16 SMs) + 16 rows units), and 16 (rows + 1) units blocks more with masses; never less for more units, rows or blocks or with masses.  0 on a
- * bad argument or without a device. */
+ * 512 + 536 rows (2048 + 16 SMs) + 16 rows units), and 16 (rows + 1) units blocks more with masses; never less for more
+ * units, rows or blocks or with masses.  0 on a bad argument or without a device. */
 size_t nosa_byte_scratch_bytes(int units, int rows, int blocks, int mass);
 
 /* Eviction from a store by accumulated attention weight, for stores whose rows hold any block (slot_blk).  For
  * each unit, with a_i the accumulated weight of row i:
- *   1. a_i = decay a_i + mass_i (two float32 roundings; a NaN counts as 0) for rows that hold a block, 0 for the others
+ *   1. a_i = decay a_i + mass_i (two float32 roundings; a sum that is NaN counts as 0) for rows that hold a block, 0 for
+ *      the others.  A unit whose masses are NaN, as a query that is not finite makes them, starts again from nothing
  *   2. while more than `budget` rows would hold a block, next_block's among them, the block with the smallest a_i goes
  *      (of equal ones the one with the higher number): its row is empty, a_i = 0.  Never dropped are the blocks below
  *      sink_blocks, the last window_blocks of the unit's ceil(lens / 64), those behind them, and next_block

@@ -17,9 +17,9 @@
 // own after pieces).
 //
 // Bound by HBM where a call is long: 256 units of 32,768 tokens and 4 rows (2.15 GB) in 306 us, 1.05 of measured HBM (a copy);
-// ragged 196 us, 1.02.  437 instructions a half block, of which 128 conversions and 32 MMAs, leave the issue slots two
-// thirds empty.  Shorter calls pay for their start and end: 256 units listing 81 blocks 56 us, 0.91, with the masses of 128
-// 88 us, 0.91.  (With the copies by a thread that the compiler does not know to be one, 57.4 and 90.)
+// ragged 196 us, 1.02.  400 instructions a half block (423 with masses), of which 128 conversions and 32 MMAs, leave the issue
+// slots 70 % empty.  Shorter calls pay for their start and end: 256 units listing 81 blocks 54.5 us, 0.94, with the masses of
+// 128 87 us, 0.92.  (With the copies by a thread that the compiler does not know to be one, 57.4 and 90.)
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -481,7 +481,8 @@ static int byte_cluster_size(int units, int blocks, int wave, int step, int most
   return cl;
 }
 
-// Three ways, by what a call pays (microseconds on GB300, back to back in a graph, all units of one length):
+// Three ways, by what a call pays (microseconds on GB300, back to back in a graph, all units of one length, one store: up to
+// 64 units of 64 blocks partly from L2, without which they take 2 to 3 more):
 //  * a cluster per unit, merged through distributed shared memory: no second kernel, but a unit cannot spread further, and
 //    ragged lengths do not balance.  Clusters of 16 fit an eighth of the device or so: 16 units of 64 blocks 15.4 with 16,
 //    9.6 with 8.
