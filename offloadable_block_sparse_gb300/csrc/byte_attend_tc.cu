@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
     bool flying = false;
     // waits are decided for the whole warp: the tensor-memory accesses behind them are warp-collective
     auto wait_for = [&](uint64_t* bar, int phase) {
-      stuck |= !__all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, kWaitCycles)) || a.products_late;
+      stuck |= !__all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, kWaitCycles));
       tc::fence_after();
     };
     auto add_products = [&]() {  // O += s_V of the chunk before: the thread's dim, its rows
@@ -269,10 +269,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
           const float2 s = there ? *reinterpret_cast<const float2*>(scales[st][b]) : make_float2(0.f, 0.f);
           scale[b] = s.y;
           if (warp == 6 + b && lane < NR) {  // (a large V scale makes its block's factors odd too, so that it is looked at)
-            const float al = alpha[lane], f = al * s.x;
-            uint32_t odd = 0x7fffffffu;  // a NaN whose low bits are the exponent and kOddBias (0: no scale), or all set
-            if (al == al) odd = 0x7fc00000u + (s.x == 0.f ? 0 : kOddBias + a.scale_e + exponent_of(invs[lane]) + exponent_of(s.x));
-            factor[b][lane] = f <= kWideFactor && s.y <= kLargeScale ? f : __uint_as_float(odd);
+            float f = alpha[lane] * s.x;
+            if (!(f <= kWideFactor && s.y <= kLargeScale)) {
+              uint32_t odd = 0x7fffffffu;  // a NaN whose low bits are the exponent and kOddBias (0: no scale), or all set
+              if (!isnan(alpha[lane])) odd = 0x7fc00000u + (s.x == 0.f ? 0 : kOddBias + a.scale_e + exponent_of(invs[lane]) + exponent_of(s.x));
+              f = __uint_as_float(odd);
+            }
+            factor[b][lane] = f;
           }
         }
         tc::wait_st();
@@ -309,7 +312,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) byte_attend_tc_kernel(const __g
         float y[R];
         auto weigh = [&](auto again) {
           const bool pass = again;
-          if (pass) {  // where a factor is odd, but for rows of q that hold a NaN, all scores become logits in their place first
+          if (pass) {
+            stuck |= a.products_late;  // (here it costs nothing; every unit's first chunk comes by)
+            // Where a factor is odd, but for rows of q that hold a NaN, all scores become logits in their place first.
             uint32_t odd = __float_as_uint(factor[0][tid % (kTcChunkBlocks * NR)]);
             if (__syncthreads_or(odd > 0x7f800000u && odd != 0x7fffffffu)) {
 #pragma unroll 1
