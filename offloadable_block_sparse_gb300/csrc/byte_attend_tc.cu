@@ -15,11 +15,11 @@
 // keys overlap, and the two CTAs of an SM.  Row references are the CTA's: a thread whose score would weigh more than 2^14
 // says so at the barrier before the second product, and then all raise theirs and weigh again.
 //
-// 16 units of 65,521 tokens take 57 us with 32 rows and 52 with 16, against 40 of HBM: a chunk's chain of waits and two
+// 16 units of 65,521 tokens take 56.2 us with 32 rows and 51.4 with 16, against 40 of HBM: a chunk's chain of waits and two
 // barriers, 2,750 cycles of a CTA alone, 3,200 of two on an SM, and some 12,000 cycles before and after the 27 chunks.
 // Instructions for one thread (products, copies) take it a hundred cycles each, so they are spread over the warps (all
 // products by one warp and all copies by another: 62.8).  64 units of 64 blocks 22.1 us with 32 rows, 18.0 with 16 (mma.sync 36.7 and
-// 21.8; 23.9 and 20.2 where the store is not in L2), 256 of 32 35.7 and 30.1 (59.7 and 34.1), 256 listing 81 76.7 and 65.9, 2 of 32
+// 21.8; 23.7 and 19.8 where the store is not in L2), 256 of 32 35.4 and 29.7 (59.7 and 34.1), 256 listing 81 75.9 and 65.0, 2 of 32
 // 9.8 and 8.1 (15.2 and 10.2).  Tried without gain: 128 threads;
 // one barrier a chunk, with the next chunk's keys and scores before this one's products (69); prefetching into L2.
 #include <type_traits>
